@@ -502,3 +502,18 @@ def quantize_rows(A):
 
 def version() -> int:
     return _lib.q8mv_version()
+
+
+# the Q8_0 key/value cache and its operators: torch is imported here, where they are first asked for
+_KV = ("Cache", "TreeAttention", "TreeVerify")
+
+
+def __getattr__(name):
+    if name in _KV:
+        from . import kv
+
+        kv.bind(_lib)
+        for n in _KV:
+            globals()[n] = getattr(kv, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -2,8 +2,8 @@
 
 Compiles the translation units under ``csrc/`` (``q8mv.cu``: the single-row
 kernels and the C ABI; ``batched.cu``: the batched kernel; ``pair.cu``: the
-feed-forward pair kernel) in parallel with
-nvcc and links them into ``libq8mv.so`` inside the package directory.  Run
+feed-forward pair kernel; ``kv_*.cu``: the Q8_0 cache and its operators) in
+parallel with nvcc and links them into ``libq8mv.so`` inside the package directory.  Run
 ``python -m q8_matrix_vector_gb300._build`` or call ``build_library()``;
 nothing here needs a GPU.
 """
@@ -17,9 +17,11 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-UNITS = [os.path.join(CSRC, "q8mv.cu"), os.path.join(CSRC, "batched.cu"), os.path.join(CSRC, "pair.cu")]
+UNITS = [os.path.join(CSRC, name) for name in ("q8mv.cu", "batched.cu", "pair.cu", "kv_cache.cu", "kv_attend.cu",
+                                               "kv_verify.cu")]
 SRC = UNITS[0]
 HDR = os.path.join(ROOT, "include", "q8mv.h")
+HDRS = [HDR, os.path.join(ROOT, "include", "q8kv.h")]
 LIB = os.path.join(PKG, "libq8mv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,7 +43,7 @@ def nvcc() -> str:
 
 def sources() -> list:
     """Every file the library is built from."""
-    files = [HDR]
+    files = list(HDRS)
     for name in sorted(os.listdir(CSRC)):
         if name.endswith((".cu", ".cuh", ".h")):
             files.append(os.path.join(CSRC, name))

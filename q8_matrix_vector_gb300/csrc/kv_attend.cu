@@ -1,0 +1,172 @@
+// Plan, checks and launch of the draft-tree attention (kv_attend.cuh).
+#include "kv_attend.cuh"
+
+#include <algorithm>
+#include <new>
+
+namespace kv {
+
+namespace {
+
+using Fn = void (*)(AttendParams);
+
+struct Variant {
+    Fn fn = nullptr;
+    int smem = 0;
+};
+
+template <typename T, int QP, int PP>
+Variant variant_for(int dim) {
+    if (dim <= 64) return {q8kv_attend_kernel<T, 64, QP, PP>, Smem<64>::total(QP)};
+    if (dim <= 128) return {q8kv_attend_kernel<T, 128, QP, PP>, Smem<128>::total(QP)};
+    return {q8kv_attend_kernel<T, 256, QP, PP>, Smem<256>::total(QP)};
+}
+
+// Parts of q and of the weights per type: see q8kv.h.
+Variant variant(int dim, int type) {
+    if (type == Q8KV_F32) return variant_for<float, 2, 2>(dim);
+    if (type == Q8KV_F16) return variant_for<__half, 1, 2>(dim);
+    return variant_for<__nv_bfloat16, 1, 1>(dim);
+}
+
+}  // namespace
+
+cudaError_t attend_occupancy(int dim, int type, int *ctas) {
+    const Variant v = variant(dim, type);
+    cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, v.fn, kWarps * 32, v.smem);
+}
+
+cudaError_t attend_launch(const AttendParams &p, int type, int grid, cudaStream_t stream) {
+    const Variant v = variant(p.c.dim, type);
+    v.fn<<<grid, kWarps * 32, v.smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace kv
+
+struct q8kv_attend_s {
+    int device = 0;
+    int heads_q = 0, heads_kv = 0, dim = 0;
+    int max_requests = 0;
+    int64_t max_rows = 0;
+    int grid[3] = {0, 0, 0};  // CTAs per type: every SM full
+    int64_t max_items = 0;
+    float *partial = nullptr;
+    unsigned *tickets = nullptr;
+};
+
+extern "C" {
+
+q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+                               int32_t max_requests, int64_t max_rows, int device) {
+    if (out == nullptr) return Q8MV_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (heads_kv < 1 || heads_kv > 65535 || heads_q < heads_kv || heads_q > 65535 || heads_q % heads_kv != 0)
+        return Q8MV_ERR_INVALID_ARG;
+    if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return Q8MV_ERR_INVALID_ARG;
+    if (max_requests < 1 || max_requests > 65536 || max_rows < 1 || max_rows > (1 << 20)) return Q8MV_ERR_INVALID_ARG;
+    const int64_t group = heads_q / heads_kv;
+    // each request's rows round up to whole tiles
+    const int64_t items = (max_rows * group / kv::kTileRows + max_requests) * heads_kv;
+    if (items > (1LL << 28)) return Q8MV_ERR_INVALID_ARG;
+
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(device);
+    if (st != Q8MV_OK) return st;
+    q8kv_attend_s *p = new (std::nothrow) q8kv_attend_s();
+    if (p == nullptr) return Q8MV_ERR_OUT_OF_MEMORY;
+    p->device = scope.device();
+    p->heads_q = heads_q;
+    p->heads_kv = heads_kv;
+    p->dim = head_dim;
+    p->max_requests = max_requests;
+    p->max_rows = max_rows;
+    p->max_items = items;
+    int sms = 0, grid = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device);
+    for (int t = 0; t < 3 && e == cudaSuccess; ++t) {
+        int ctas = 0;
+        e = kv::attend_occupancy(head_dim, t, &ctas);
+        p->grid[t] = sms * std::max(1, ctas);
+        grid = std::max(grid, p->grid[t]);
+    }
+    if (e == cudaSuccess)
+        e = cudaMalloc(&p->partial, sizeof(float) * 2 * grid * kv::kTileRows * static_cast<size_t>(head_dim + 2));
+    if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(items));
+    if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(items));
+    // the tickets' zeros, before any stream may use them
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        if (p->partial) cudaFree(p->partial);
+        if (p->tickets) cudaFree(p->tickets);
+        delete p;
+        return q8i::cuda_status(e);
+    }
+    *out = p;
+    return Q8MV_OK;
+}
+
+q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, const q8kv_attend_args_t *a,
+                          cudaStream_t stream) {
+    kv::AttendParams p = {};
+    if (plan == nullptr || a == nullptr || !kv::make_cache(cache, &p.c)) return Q8MV_ERR_INVALID_ARG;
+    if (p.c.heads != plan->heads_kv || p.c.dim != plan->dim || !kv::valid_type(a->type)) return Q8MV_ERR_INVALID_ARG;
+    if (a->requests < 0 || a->requests > plan->max_requests || a->rows < 0 || a->rows > plan->max_rows)
+        return Q8MV_ERR_INVALID_ARG;
+    if (a->table_cols < 0 || a->table_row < 0 || a->mask_words < 0 || a->mask_row < 0) return Q8MV_ERR_INVALID_ARG;
+    const int64_t most = 1LL << 40;
+    if (a->q_row < 0 || a->q_row > most || a->q_head < 0 || a->q_head > most || a->out_row < 0 || a->out_row > most ||
+        a->out_head < 0 || a->out_head > most || a->table_row > most || a->mask_row > most)
+        return Q8MV_ERR_INVALID_ARG;
+    // positions are counted in 32 bits
+    if (static_cast<int64_t>(a->table_cols) * p.c.page_size > (1LL << 31) - 2 * kv::kTileKeys * kv::kStages)
+        return Q8MV_ERR_INVALID_ARG;
+    if (a->rows == 0 || a->requests == 0) return Q8MV_OK;
+    if (a->starts == nullptr && a->rows % a->requests != 0) return Q8MV_ERR_INVALID_ARG;
+    const int size = kv::type_size(a->type);
+    if (!a->q || !a->out || !a->lengths || (!a->table && a->table_cols > 0)) return Q8MV_ERR_INVALID_ARG;
+    if (!kv::aligned(a->q, size) || !kv::aligned(a->out, size) || !kv::aligned(a->lse, 4) ||
+        !kv::aligned(a->lengths, 4) || !kv::aligned(a->table, 4) || !kv::aligned(a->mask, 4) ||
+        !kv::aligned(a->starts, 4))
+        return Q8MV_ERR_INVALID_ARG;
+    p.q = a->q;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.q_row = a->q_row;
+    p.q_head = a->q_head;
+    p.out_row = a->out_row;
+    p.out_head = a->out_head;
+    p.starts = a->starts;
+    p.lengths = a->lengths;
+    p.table = a->table;
+    p.table_row = a->table_row;
+    p.table_cols = a->table_cols;
+    p.mask = a->mask;
+    p.mask_row = a->mask_row;
+    p.mask_words = a->mask_words;
+    p.rows = a->rows;
+    p.requests = a->requests;
+    p.heads_q = plan->heads_q;
+    p.group = plan->heads_q / plan->heads_kv;
+    p.scale_log2 = a->scale * 1.44269504088896341f;
+    p.partial = plan->partial;
+    p.tickets = plan->tickets;
+    p.tickets_n = static_cast<int>(plan->max_items);
+    return q8i::cuda_status(kv::attend_launch(p, a->type, plan->grid[a->type], stream));
+}
+
+q8mv_status_t q8kv_attend_destroy(q8kv_attend_plan_t p) {
+    if (p == nullptr) return Q8MV_OK;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(p->device);
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    if (p->partial) cudaFree(p->partial);
+    if (p->tickets) cudaFree(p->tickets);
+    delete p;
+    return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,523 @@
+// Verification of drafted tokens (../../include/q8kv.h).
+//
+// Per visited node: the row's maximum, its whole-number weights w = trunc(2^40
+// exp(z - max)) and their sums, then the tests of the node's children; at the end
+// one prefix search.  Everything that is summed is a 64-bit whole number, so the
+// split over threads and CTAs cannot change a result.
+//
+// One cluster of 8 CTAs walks one request and only reads the rows that the walk
+// visits: a tree of many nodes costs its accepted path, not its size.  A CTA owns
+// a contiguous eighth of the vocabulary and each of its 16 warps a contiguous part
+// of that, so the search at the end goes cluster -> CTA -> warp -> 128 tokens.  A
+// lane keeps its first 32 logits of the row in registers between the maximum and
+// the sum (all of a 131072-token vocabulary), so a row is read once.  Maxima and
+// sums cross the cluster through distributed shared memory; every CTA runs the
+// children's tests itself, on the same numbers, and reaches the same verdict.
+#include "kv_common.cuh"
+
+#include <cooperative_groups.h>
+
+#include <new>
+
+namespace cg = cooperative_groups;
+
+namespace kv {
+
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kVerifyWarps = 16;
+constexpr int kHeld = 8;                   // groups of 4 logits a lane holds
+constexpr float kOne = 1099511627776.0f;   // 2^40, the weight of a row's largest logit
+
+struct VerifyParams {
+    const void *logits;
+    const float *draft;
+    const int32_t *tokens, *parents;
+    const float *uniforms, *temperature;
+    const int32_t *starts;
+    int32_t *path, *count, *next;
+    int64_t logits_row, draft_row, rows;
+    int requests, vocab, seg;  // seg: tokens of a warp, a multiple of 4
+    int vec;                   // four logits (and draft probabilities) may be loaded at once
+};
+
+// The row that the walk stands on: what its weights are made of.
+struct Row {
+    float inv;       // 1 / temperature
+    float top;       // largest z
+    int best;        // its first index
+    bool greedy;
+    float per;       // f32(2^40 / W), drafts only
+    float less;      // a
+};
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+// z of one logit: NaN counts as -inf, -0 as 0
+__device__ __forceinline__ float scaled(float l, float inv) {
+    const float z = __fadd_rn(__fmul_rn(l, inv), 0.0f);
+    return z == z ? z : -INFINITY;
+}
+
+__device__ __forceinline__ float share(const Row &r, float z, int i) {
+    if (r.top == -INFINITY) return 0.0f;
+    if (r.greedy) return i == r.best ? 1.0f : 0.0f;
+    return z == r.top ? 1.0f : expf(z - r.top);
+}
+
+__device__ __forceinline__ int64_t weight(float e) { return __float2ll_rz(e * kOne); }
+
+__device__ __forceinline__ float residual(const Row &r, float e, float q) {
+    return fmaxf(__fsub_rn(__fmul_rn(e, r.per), __fmul_rn(r.less, q)), 0.0f);
+}
+
+template <typename T>
+__device__ __forceinline__ void load4(const T *p, int i, int n, bool vec, float (&x)[4], float fill) {
+    if (vec && i + 4 <= n) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        } else {
+            union {
+                uint2 u;
+                T t[4];
+            } v;
+            v.u = __ldg(reinterpret_cast<const uint2 *>(p + i));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = to_f32(v.t[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = i + k < n ? to_f32(p[i + k]) : fill;
+    }
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(~0u, x, d);
+    return x;
+}
+
+template <typename T, bool DRAFTS>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps * 32, 1)
+    q8kv_verify_kernel(const VerifyParams p) {
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ uint64_t x_max[2];
+    __shared__ int64_t x_sum[2];
+    __shared__ uint64_t warp_max[kVerifyWarps];
+    __shared__ int64_t warp_w[kVerifyWarps];   // sums of the warps' weights as they stand
+    __shared__ int64_t cta_w[kCluster];        // and of all CTAs'
+    __shared__ int verdict, child;             // of the last test
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int b = blockIdx.x / kCluster;
+    int64_t row0, row1;
+    if (p.starts) {
+        row0 = min(max(static_cast<int64_t>(p.starts[b]), static_cast<int64_t>(0)), p.rows);
+        row1 = min(max(static_cast<int64_t>(p.starts[b + 1]), row0), p.rows);
+    } else {
+        row0 = p.rows / p.requests * b;
+        row1 = row0 + p.rows / p.requests;
+    }
+    const int nodes = static_cast<int>(row1 - row0);
+    if (nodes == 0) {  // the whole cluster
+        if (rank == 0 && tid == 0) {
+            p.count[b] = 0;
+            p.next[b] = -1;
+        }
+        return;
+    }
+    const int32_t *tokens = p.tokens + row0, *parents = p.parents + row0;
+    const float *uniforms = p.uniforms + row0;
+    int32_t *path = p.path + row0;
+    if (rank == 0)
+        for (int i = tid; i < nodes; i += blockDim.x) path[i] = i == 0 ? 0 : -1;
+
+    Row r;
+    const float t = p.temperature ? p.temperature[b] : 1.0f;
+    r.greedy = !(t > 0.0f);
+    r.inv = r.greedy ? 1.0f : __frcp_rn(t);
+    const int seg = p.seg, chunk = seg * kVerifyWarps;
+    const int64_t lo64 = static_cast<int64_t>(rank) * chunk + static_cast<int64_t>(warp) * seg;
+    const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(p.vocab)));
+    const int hi = static_cast<int>(min(lo64 + seg, static_cast<int64_t>(p.vocab)));
+
+    int parity = 0;
+    // sums the lanes' numbers: warp_w, cta_w, and the total
+    auto exchange = [&](int64_t mine) -> int64_t {
+        mine = warp_sum(mine);
+        if (lane == 0) warp_w[warp] = mine;
+        __syncthreads();
+        if (tid == 0) {
+            int64_t s = 0;
+#pragma unroll
+            for (int i = 0; i < kVerifyWarps; ++i) s += warp_w[i];
+            x_sum[parity] = s;
+        }
+        cluster.sync();
+        if (tid < kCluster) cta_w[tid] = *cluster.map_shared_rank(&x_sum[parity], tid);
+        __syncthreads();
+        int64_t s = 0;
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) s += cta_w[i];
+        parity ^= 1;
+        return s;
+    };
+
+    int cur = 0, count = 0;
+    int64_t total = 0;
+    bool rest = false;  // drafts: the weights are the residual's
+    for (;;) {
+        const T *l = static_cast<const T *>(p.logits) + (row0 + cur) * p.logits_row;
+        const float *q = DRAFTS ? p.draft + (row0 + cur) * p.draft_row : nullptr;
+        // ---- the row's maximum
+        float z[kHeld][4];
+        float top = -INFINITY;
+        int best = lo;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) load4(l, lo + k * 128 + lane * 4, hi, p.vec, z[k], -INFINITY);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[k][j] = scaled(z[k][j], r.inv);
+                if (z[k][j] > top) {
+                    top = z[k][j];
+                    best = lo + k * 128 + lane * 4 + j;
+                }
+            }
+        for (int i = lo + kHeld * 128 + lane * 4; i < hi; i += 128) {
+            float x[4];
+            load4(l, i, hi, p.vec, x, -INFINITY);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float y = scaled(x[j], r.inv);
+                if (y > top) {
+                    top = y;
+                    best = i + j;
+                }
+            }
+        }
+        uint64_t key = static_cast<uint64_t>(ordered(top)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(best));
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) key = max(key, static_cast<uint64_t>(__shfl_xor_sync(~0u, key, d)));
+        if (lane == 0) warp_max[warp] = key;
+        __syncthreads();
+        if (tid == 0) {
+#pragma unroll
+            for (int i = 1; i < kVerifyWarps; ++i) key = max(key, warp_max[i]);
+            x_max[parity] = key;
+        }
+        cluster.sync();
+        key = 0;
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) key = max(key, *cluster.map_shared_rank(&x_max[parity], i));
+        parity ^= 1;
+        r.top = unordered(static_cast<uint32_t>(key >> 32));
+        r.best = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+        r.less = 0.0f;
+
+        // sum of the lane's weights (of the residual's once `rest`)
+        auto sum = [&]() -> int64_t {
+            int64_t s = 0;
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                const int i = lo + k * 128 + lane * 4;
+                if (i < hi) {
+                    float y[4];
+                    if (DRAFTS && rest) load4(q, i, hi, p.vec, y, 0.0f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float e = i + j < hi ? share(r, z[k][j], i + j) : 0.0f;
+                        s += weight(DRAFTS && rest && i + j < hi ? residual(r, e, y[j]) : e);
+                    }
+                }
+            }
+            for (int i = lo + kHeld * 128 + lane * 4; i < hi; i += 128) {
+                float x[4], y[4];
+                load4(l, i, hi, p.vec, x, -INFINITY);
+                if (DRAFTS && rest) load4(q, i, hi, p.vec, y, 0.0f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = i + j < hi ? share(r, scaled(x[j], r.inv), i + j) : 0.0f;
+                    s += weight(DRAFTS && rest && i + j < hi ? residual(r, e, y[j]) : e);
+                }
+            }
+            return s;
+        };
+        rest = false;
+        total = exchange(sum());
+        if (DRAFTS) r.per = static_cast<float>(1099511627776.0 / static_cast<double>(total));
+
+        // ---- the children, in index order.  Warp 0 tests until one is accepted (verdict 1), none is
+        // left (0) or, with draft probabilities, one is refused (2)
+        float norm = 1.0f;
+        int from = cur + 1;
+        bool open = true;
+        for (;;) {
+            if (warp == 0) {
+                int said = 0, who = nodes;
+                for (int i0 = from; i0 < nodes && said == 0 && open && total > 0; i0 += 32) {
+                    const int mine = i0 + lane;
+                    const bool is_child = mine < nodes && parents[mine] == cur;
+                    uint32_t todo = __ballot_sync(~0u, is_child);
+                    while (todo != 0 && said == 0) {
+                        const int i = i0 + __ffs(todo) - 1;
+                        todo &= todo - 1;
+                        const int x = tokens[i];
+                        const bool valid = x >= 0 && x < p.vocab;
+                        const float e = valid ? share(r, scaled(to_f32(l[x]), r.inv), x) : 0.0f;
+                        if constexpr (DRAFTS) {
+                            const float qx = valid ? q[x] : 0.0f;
+                            const float left = residual(r, e, qx);
+                            const bool ok = valid && __fmul_rn(__fmul_rn(uniforms[i], qx), norm) < left;
+                            who = i;
+                            said = ok ? 1 : valid ? 2 : 0;  // an invalid token was not drawn: nothing to take out
+                        } else {
+                            // a sibling with the same token has been refused: its weight is gone
+                            bool twin = false;
+                            for (int j = cur + 1 + lane; j < i; j += 32) twin |= parents[j] == cur && tokens[j] == x;
+                            const int64_t wx = __any_sync(~0u, twin) ? 0 : weight(e);
+                            if (static_cast<double>(uniforms[i]) * static_cast<double>(total) < static_cast<double>(wx)) {
+                                who = i;
+                                said = 1;
+                            } else {
+                                total -= wx;
+                                if (valid && lane == 0) {
+                                    cta_w[x / chunk] -= wx;
+                                    if (x / chunk == rank) warp_w[x % chunk / seg] -= wx;
+                                }
+                            }
+                        }
+                    }
+                }
+                if (lane == 0) {
+                    verdict = said;
+                    child = who;
+                }
+            }
+            __syncthreads();
+            const int said = verdict, who = child;
+            __syncthreads();
+            if (!DRAFTS || said != 2) {
+                if (said == 1) {
+                    cur = who;
+                    ++count;
+                    if (rank == 0 && tid == 0) path[count] = who;
+                }
+                open = said == 1;  // goes on with the accepted child's row
+                break;
+            }
+            // refused: take the draft's share out, once more
+            r.less = __fadd_rn(r.less, norm);
+            rest = true;
+            const int64_t left = exchange(sum());
+            from = who + 1;
+            if (left == 0) {
+                // nothing is left: the target's own weights, and no other child
+                rest = false;
+                r.less = 0.0f;
+                total = exchange(sum());
+                open = false;
+            } else {
+                total = left;
+                norm = static_cast<float>(static_cast<double>(left) * (1.0 / 1099511627776.0));
+            }
+        }
+        if (open) continue;
+
+        // ---- the next token: the first whose prefix sum exceeds the target
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) total += cta_w[i];
+        if (total == 0) {
+            if (rank == 0 && tid == 0) p.next[b] = -1;
+        } else {
+            int64_t want = __double2ll_rz(static_cast<double>(uniforms[0]) * static_cast<double>(total));
+            want = max(static_cast<int64_t>(0), min(want, total - 1));
+            int owner = 0;
+            while (owner < kCluster - 1 && want >= cta_w[owner]) want -= cta_w[owner++];
+            if (owner == rank) {
+                int ow = 0;
+                while (ow < kVerifyWarps - 1 && want >= warp_w[ow]) want -= warp_w[ow++];
+                if (ow == warp) {
+                    for (int i = lo + lane * 4;; i += 128) {  // ends: the warp's weights exceed `want`
+                        float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        int64_t w[4];
+                        load4(l, i, hi, p.vec, x, -INFINITY);
+                        if (DRAFTS && rest) load4(q, i, hi, p.vec, y, 0.0f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float e = i + j < hi ? share(r, scaled(x[j], r.inv), i + j) : 0.0f;
+                            w[j] = weight(DRAFTS && rest && i + j < hi ? residual(r, e, y[j]) : e);
+                        }
+                        if (!DRAFTS) {
+                            // refused children have no weight
+                            for (int j0 = cur + 1; j0 < nodes; j0 += 32) {
+                                const bool is_child = j0 + lane < nodes && parents[j0 + lane] == cur;
+                                const int tok = is_child ? tokens[j0 + lane] : -1;
+                                uint32_t todo = __ballot_sync(~0u, is_child);
+                                while (todo != 0) {
+                                    const int x0 = __shfl_sync(~0u, tok, __ffs(todo) - 1);
+                                    todo &= todo - 1;
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) w[j] = i + j == x0 ? 0 : w[j];
+                                }
+                            }
+                        }
+                        const int64_t mine = w[0] + w[1] + w[2] + w[3];
+                        int64_t upto = mine;
+#pragma unroll
+                        for (int d = 1; d < 32; d *= 2) {
+                            const int64_t a = __shfl_up_sync(~0u, upto, d);
+                            if (lane >= d) upto += a;
+                        }
+                        const uint32_t over = __ballot_sync(~0u, upto > want);
+                        if (over != 0) {
+                            if (lane == __ffs(over) - 1) {
+                                int64_t at = upto - mine;
+                                int j = 0;
+                                while (j < 3 && at + w[j] <= want) at += w[j++];
+                                p.next[b] = i + j;
+                            }
+                            break;
+                        }
+                        want -= __shfl_sync(~0u, upto, 31);
+                        if (i - lane * 4 + 128 >= hi) break;  // not reached: the sums are exact
+                    }
+                }
+            }
+        }
+        if (rank == 0 && tid == 0) p.count[b] = count;
+        break;
+    }
+    cluster.sync();  // no CTA leaves while another may read its shared memory
+}
+
+template <typename T>
+cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>(p.requests) * kCluster;
+    if (p.draft)
+        q8kv_verify_kernel<T, true><<<grid, kVerifyWarps * 32, 0, stream>>>(p);
+    else
+        q8kv_verify_kernel<T, false><<<grid, kVerifyWarps * 32, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace kv
+
+struct q8kv_verify_s {
+    int device = 0;
+    int max_requests = 0, vocab = 0;
+    int64_t max_rows = 0;
+};
+
+extern "C" {
+
+q8mv_status_t q8kv_verify_plan(q8kv_verify_plan_t *out, int32_t max_requests, int64_t max_rows, int32_t vocab,
+                               int device) {
+    if (out == nullptr) return Q8MV_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (max_requests < 1 || max_requests > 65535 || max_rows < 1 || max_rows > (1 << 20) || vocab < 1 ||
+        vocab > (1 << 22))
+        return Q8MV_ERR_INVALID_ARG;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(device);
+    if (st != Q8MV_OK) return st;
+    q8kv_verify_s *p = new (std::nothrow) q8kv_verify_s();
+    if (p == nullptr) return Q8MV_ERR_OUT_OF_MEMORY;
+    p->device = scope.device();
+    p->max_requests = max_requests;
+    p->max_rows = max_rows;
+    p->vocab = vocab;
+    *out = p;
+    return Q8MV_OK;
+}
+
+q8mv_status_t q8kv_verify(q8kv_verify_plan_t plan, const q8kv_verify_args_t *a, cudaStream_t stream) {
+    if (plan == nullptr || a == nullptr) return Q8MV_ERR_INVALID_ARG;
+    if (a->reserved != 0 || !kv::valid_type(a->type) || a->vocab != plan->vocab) return Q8MV_ERR_INVALID_ARG;
+    if (a->requests < 0 || a->requests > plan->max_requests || a->rows < 0 || a->rows > plan->max_rows)
+        return Q8MV_ERR_INVALID_ARG;
+    const int64_t most = 1LL << 40;
+    if (a->logits_row < 0 || a->logits_row > most || a->draft_row < 0 || a->draft_row > most)
+        return Q8MV_ERR_INVALID_ARG;
+    if (a->requests == 0) return Q8MV_OK;
+    if (a->starts == nullptr && a->rows % a->requests != 0) return Q8MV_ERR_INVALID_ARG;
+    if (!a->count || !a->next_token) return Q8MV_ERR_INVALID_ARG;
+    const int size = kv::type_size(a->type);
+    if (a->rows > 0) {
+        if (!a->logits || !a->tokens || !a->parents || !a->uniforms || !a->path) return Q8MV_ERR_INVALID_ARG;
+        if (!kv::aligned(a->logits, size)) return Q8MV_ERR_INVALID_ARG;
+    }
+    if (!kv::aligned(a->draft_probs, 4) || !kv::aligned(a->tokens, 4) || !kv::aligned(a->parents, 4) ||
+        !kv::aligned(a->uniforms, 4) || !kv::aligned(a->temperature, 4) || !kv::aligned(a->starts, 4) ||
+        !kv::aligned(a->path, 4) || !kv::aligned(a->count, 4) || !kv::aligned(a->next_token, 4))
+        return Q8MV_ERR_INVALID_ARG;
+    // every CTA of a cluster decides from the inputs: none of them may be written meanwhile
+    {
+        const int64_t R = a->rows, B = a->requests;
+        const kv::Range in[] = {
+            {a->logits, R > 0 ? ((R - 1) * a->logits_row + a->vocab) * size : 0},
+            {a->draft_probs, a->draft_probs && R > 0 ? ((R - 1) * a->draft_row + a->vocab) * 4 : 0},
+            {a->tokens, 4 * R}, {a->parents, 4 * R}, {a->uniforms, 4 * R},
+            {a->temperature, a->temperature ? 4 * B : 0}, {a->starts, a->starts ? 4 * (B + 1) : 0}};
+        const kv::Range outs[] = {{a->path, 4 * R}, {a->count, 4 * B}, {a->next_token, 4 * B}};
+        for (int i = 0; i < 3; ++i) {
+            for (const kv::Range &x : in)
+                if (kv::overlap(outs[i], x)) return Q8MV_ERR_INVALID_ARG;
+            for (int j = 0; j < i; ++j)
+                if (kv::overlap(outs[i], outs[j])) return Q8MV_ERR_INVALID_ARG;
+        }
+    }
+    kv::VerifyParams p = {};
+    p.logits = a->logits;
+    p.draft = a->draft_probs;
+    p.tokens = a->tokens;
+    p.parents = a->parents;
+    p.uniforms = a->uniforms;
+    p.temperature = a->temperature;
+    p.starts = a->starts;
+    p.path = a->path;
+    p.count = a->count;
+    p.next = a->next_token;
+    p.logits_row = a->logits_row;
+    p.draft_row = a->draft_row;
+    p.rows = a->rows;
+    p.requests = a->requests;
+    p.vocab = a->vocab;
+    const int parts = kv::kCluster * kv::kVerifyWarps;
+    p.seg = static_cast<int>(kv::ceil_div(kv::ceil_div(a->vocab, parts), 4) * 4);
+    p.vec = kv::aligned(a->logits, 4 * size) && a->logits_row % 4 == 0 && kv::aligned(a->draft_probs, 16) &&
+            a->draft_row % 4 == 0;
+    cudaError_t e;
+    if (a->type == Q8KV_F32)
+        e = kv::launch<float>(p, stream);
+    else if (a->type == Q8KV_F16)
+        e = kv::launch<__half>(p, stream);
+    else
+        e = kv::launch<__nv_bfloat16>(p, stream);
+    return q8i::cuda_status(e);
+}
+
+q8mv_status_t q8kv_verify_destroy(q8kv_verify_plan_t p) {
+    if (p == nullptr) return Q8MV_OK;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(p->device);
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    delete p;
+    return st;
+}
+
+}  // extern "C"

@@ -42,6 +42,7 @@
 #include <new>
 
 #include "batched.h"
+#include "kv.h"
 #include "mma_kernel.cuh"
 #include "pair.h"
 #include "regs_kernel.cuh"
@@ -68,6 +69,13 @@ q8mv_status_t cuda_status(cudaError_t e) {
         return Q8MV_ERR_UNSUPPORTED_DEVICE;
     return Q8MV_ERR_CUDA;
 }
+
+}  // namespace
+
+// the same conversion and record for the q8kv translation units
+q8mv_status_t q8i::cuda_status(cudaError_t e) { return ::cuda_status(e); }
+
+namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
