@@ -17,8 +17,9 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-UNITS = [os.path.join(CSRC, name) for name in ("q8mv.cu", "batched.cu", "pair.cu", "kv_cache.cu", "kv_attend.cu",
-                                               "kv_verify.cu")]
+UNITS = [os.path.join(CSRC, name) for name in
+         ("q8mv.cu", "batched.cu", "pair.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_f32.cu", "kv_attend_f16.cu",
+          "kv_attend_bf16.cu", "kv_verify.cu")]
 SRC = UNITS[0]
 HDR = os.path.join(ROOT, "include", "q8mv.h")
 HDRS = [HDR, os.path.join(ROOT, "include", "q8kv.h")]

@@ -1,5 +1,5 @@
 // Plan, checks and launch of the draft-tree attention (kv_attend.cuh).
-#include "kv_attend.cuh"
+#include "kv_attend.h"
 
 #include <algorithm>
 #include <new>
@@ -8,41 +8,13 @@ namespace kv {
 
 namespace {
 
-using Fn = void (*)(AttendParams);
-
-struct Variant {
-    Fn fn = nullptr;
-    int smem = 0;
-};
-
-template <typename T, int QP, int PP>
-Variant variant_for(int dim) {
-    if (dim <= 64) return {q8kv_attend_kernel<T, 64, QP, PP>, Smem<64>::total(QP)};
-    if (dim <= 128) return {q8kv_attend_kernel<T, 128, QP, PP>, Smem<128>::total(QP)};
-    return {q8kv_attend_kernel<T, 256, QP, PP>, Smem<256>::total(QP)};
-}
-
-// Parts of q and of the weights per type: see q8kv.h.
-Variant variant(int dim, int type) {
-    if (type == Q8KV_F32) return variant_for<float, 2, 2>(dim);
-    if (type == Q8KV_F16) return variant_for<__half, 1, 2>(dim);
-    return variant_for<__nv_bfloat16, 1, 1>(dim);
+AttendVariant variant(int dim, int type, int row_tiles) {
+    return type == Q8KV_F32   ? attend_variant_f32(dim, row_tiles)
+           : type == Q8KV_F16 ? attend_variant_f16(dim, row_tiles)
+                              : attend_variant_bf16(dim, row_tiles);
 }
 
 }  // namespace
-
-cudaError_t attend_occupancy(int dim, int type, int *ctas) {
-    const Variant v = variant(dim, type);
-    cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
-    if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, v.fn, kWarps * 32, v.smem);
-}
-
-cudaError_t attend_launch(const AttendParams &p, int type, int grid, cudaStream_t stream) {
-    const Variant v = variant(p.c.dim, type);
-    v.fn<<<grid, kWarps * 32, v.smem, stream>>>(p);
-    return cudaGetLastError();
-}
 
 }  // namespace kv
 
@@ -51,7 +23,8 @@ struct q8kv_attend_s {
     int heads_q = 0, heads_kv = 0, dim = 0;
     int max_requests = 0;
     int64_t max_rows = 0;
-    int grid[3] = {0, 0, 0};  // CTAs per type: every SM full
+    kv::AttendVariant variant[3][3];  // per type and row tiles
+    int grid[3][3] = {};              // and their CTAs: every SM full
     int64_t max_items = 0;
     float *partial = nullptr;
     unsigned *tickets = nullptr;
@@ -69,7 +42,7 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
     if (max_requests < 1 || max_requests > 65536 || max_rows < 1 || max_rows > (1 << 20)) return Q8MV_ERR_INVALID_ARG;
     const int64_t group = heads_q / heads_kv;
     // each request's rows round up to whole tiles
-    const int64_t items = (max_rows * group / kv::kTileRows + max_requests) * heads_kv;
+    const int64_t items = (max_rows * group / 8 + max_requests) * heads_kv;
     if (items > (1LL << 28)) return Q8MV_ERR_INVALID_ARG;
 
     kv::DeviceScope scope;
@@ -84,16 +57,20 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
     p->max_requests = max_requests;
     p->max_rows = max_rows;
     p->max_items = items;
-    int sms = 0, grid = 0;
+    int sms = 0;
+    int64_t slots = 0;  // rows of partial results
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device);
-    for (int t = 0; t < 3 && e == cudaSuccess; ++t) {
-        int ctas = 0;
-        e = kv::attend_occupancy(head_dim, t, &ctas);
-        p->grid[t] = sms * std::max(1, ctas);
-        grid = std::max(grid, p->grid[t]);
-    }
-    if (e == cudaSuccess)
-        e = cudaMalloc(&p->partial, sizeof(float) * 2 * grid * kv::kTileRows * static_cast<size_t>(head_dim + 2));
+    for (int t = 0; t < 3; ++t)
+        for (int v = 0; v < 3 && e == cudaSuccess; ++v) {
+            int ctas = 0;
+            const kv::AttendVariant k = p->variant[t][v] = kv::variant(head_dim, t, kv::kRowTiles[v]);
+            e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, k.fn, kv::kWarps * 32, k.smem);
+            p->grid[t][v] = sms * std::max(1, ctas);
+            slots = std::max<int64_t>(slots, 2LL * p->grid[t][v] * 8 * kv::kRowTiles[v]);
+        }
+    if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * slots * static_cast<size_t>(head_dim + 2));
     if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(items));
     if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(items));
     // the tickets' zeros, before any stream may use them
@@ -121,7 +98,11 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     if (a->q_row < 0 || a->q_row > most || a->q_head < 0 || a->q_head > most || a->out_row < 0 || a->out_row > most ||
         a->out_head < 0 || a->out_head > most || a->table_row > most || a->mask_row > most)
         return Q8MV_ERR_INVALID_ARG;
-    // positions are counted in 32 bits
+    // rows of the cache are numbered in 32 bits here
+    if (p.c.pages > 0 && (p.c.pages - 1) * p.c.stride_page + (p.c.heads - 1) * p.c.stride_head +
+                                 (p.c.page_size - 1) * p.c.stride_token >= 0xFFFFFFFFLL)
+        return Q8MV_ERR_INVALID_ARG;
+    // and positions in 31
     if (static_cast<int64_t>(a->table_cols) * p.c.page_size > (1LL << 31) - 2 * kv::kTileKeys * kv::kStages)
         return Q8MV_ERR_INVALID_ARG;
     if (a->rows == 0 || a->requests == 0) return Q8MV_OK;
@@ -155,7 +136,12 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.partial = plan->partial;
     p.tickets = plan->tickets;
     p.tickets_n = static_cast<int>(plan->max_items);
-    return q8i::cuda_status(kv::attend_launch(p, a->type, plan->grid[a->type], stream));
+    // 8, 16 or 32 query rows at a time, by the mean of a request's: the fewest that hold them
+    const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
+    const int v = mean <= 8 ? 0 : mean <= 16 || p.c.dim > 128 ? 1 : 2;
+    const kv::AttendVariant &k = plan->variant[a->type][v];
+    k.fn<<<plan->grid[a->type][v], kv::kWarps * 32, k.smem, stream>>>(p);
+    return q8i::cuda_status(cudaGetLastError());
 }
 
 q8mv_status_t q8kv_attend_destroy(q8kv_attend_plan_t p) {

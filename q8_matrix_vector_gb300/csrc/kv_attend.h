@@ -6,7 +6,7 @@
 
 namespace kv {
 
-constexpr int kTileRows = 16;    // query rows (node, head of the group) of one item
+constexpr int kRowTiles[] = {1, 2, 4};  // variants: an item has 8, 16 or 32 query rows (node, head of the group)
 constexpr int kWarps = 4;        // warps of a CTA, each with its own keys
 constexpr int kStepKeys = 32;    // keys a warp takes at a time
 constexpr int kTileKeys = kWarps * kStepKeys;
@@ -28,14 +28,19 @@ struct AttendParams {
     int table_cols, mask_words;
     int requests, heads_q, group;
     float scale_log2;   // scale * log2(e)
-    float *partial;     // 2 per CTA: [16 rows][dim + 2]
+    float *partial;     // 2 per CTA: [rows of an item][dim + 2]
     unsigned *tickets;  // one per item
     int tickets_n;
 };
 
-// Launches the kernel for `type`; grid = the CTAs that the plan sized its workspace for.
-cudaError_t attend_launch(const AttendParams &p, int type, int grid, cudaStream_t stream);
-// Resident CTAs per SM of the variant for (dim, type).
-cudaError_t attend_occupancy(int dim, int type, int *ctas);
+// One variant of the kernel: dim up to 64, 128 or 256, and row tiles.  The parts
+// of q and of the weights go by the type (see q8kv.h), a translation unit each.
+struct AttendVariant {
+    void (*fn)(AttendParams) = nullptr;
+    int smem = 0;
+};
+AttendVariant attend_variant_f32(int dim, int row_tiles);
+AttendVariant attend_variant_f16(int dim, int row_tiles);
+AttendVariant attend_variant_bf16(int dim, int row_tiles);
 
 }  // namespace kv

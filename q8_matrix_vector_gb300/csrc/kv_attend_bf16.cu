@@ -1,0 +1,8 @@
+// The draft-tree attention kernels of bf16 queries and outputs.
+#include "kv_attend.cuh"
+
+namespace kv {
+
+AttendVariant attend_variant_bf16(int dim, int row_tiles) { return attend_variant_of<__nv_bfloat16, 1, 1>(dim, row_tiles); }
+
+}  // namespace kv

@@ -1,0 +1,8 @@
+// The draft-tree attention kernels of f16 queries and outputs.
+#include "kv_attend.cuh"
+
+namespace kv {
+
+AttendVariant attend_variant_f16(int dim, int row_tiles) { return attend_variant_of<__half, 1, 2>(dim, row_tiles); }
+
+}  // namespace kv
