@@ -133,6 +133,8 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.heads_q = plan->heads_q;
     p.group = plan->heads_q / plan->heads_kv;
     p.scale_log2 = a->scale * 1.44269504088896341f;
+    while ((1u << p.page_shift) < static_cast<uint32_t>(p.c.page_size)) ++p.page_shift;
+    p.page_mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << p.page_shift) - p.c.page_size)) / p.c.page_size + 1);
     p.partial = plan->partial;
     p.tickets = plan->tickets;
     p.tickets_n = static_cast<int>(plan->max_items);

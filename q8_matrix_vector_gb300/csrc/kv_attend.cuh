@@ -99,17 +99,17 @@ struct Smem {
     static constexpr int kScaleBytes = kStepKeys * kBlocks * 4;
     static constexpr int kStage = kStepKeys * (kKPitch + kVPitch) + 2 * kScaleBytes;
     static constexpr int kRing = kStage * kStages * kWarps;
-    // the ring is reused by the join of the warps: O, then m and l
+    // the join of the warps, 8 rows at a time: O, then m and l
     static constexpr int kJoinPitch = DP + 4;
-    static constexpr int kJoin = kWarps * kRows * kJoinPitch * 4;
-    static constexpr int kMain = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kJoin = kWarps * 8 * kJoinPitch * 4;
     static constexpr int kQPitch = 2 * DP + ((2 * DP) % 128 == 64 ? 0 : 64);
     static constexpr int kQ = QP * kRows * kQPitch;
     static constexpr int kBias = kRows * kBlocks * 4;  // -128 * 2^-24 * the block's sum of q
-    static constexpr int kTotal = kMain + kQ + kBias;
+    static constexpr int kTotal = kRing + kJoin + kQ + kBias;
 };
 
-// Where a CTA is on the line of units.
+// Where a CTA is on the line of units.  An item is kItemUnits units of its fixed
+// cost, then its tiles.
 struct Place {
     int b;            // request
     int nodes;        // T_b
@@ -119,7 +119,7 @@ struct Place {
     int64_t tiles_k;  // key tiles
     int h, rt;
     int64_t item;     // number of the item over all requests
-    int64_t first;    // its first unit
+    int64_t first;    // the unit of its first tile
 };
 
 template <int ROWS>
@@ -147,7 +147,7 @@ __device__ __forceinline__ void load_request(const AttendParams &p, int b, Place
 }
 
 __device__ __forceinline__ int64_t units_of(const AttendParams &p, const Place &w) {
-    return static_cast<int64_t>(p.c.heads) * w.tiles_r * w.tiles_k;
+    return static_cast<int64_t>(p.c.heads) * w.tiles_r * (w.tiles_k + kItemUnits);
 }
 
 // What joining needs of an item's parts.
@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    unsigned char *q_sm = smem + S::kMain;
+    float *jo = reinterpret_cast<float *>(smem + S::kRing);  // [warp][8 rows][kJoinPitch]
+    unsigned char *q_sm = smem + S::kRing + S::kJoin;
     float *bias_sm = reinterpret_cast<float *>(q_sm + S::kQ);  // [row / 2][block][row % 2]
 
     // ---- the CTA's share of the line of units
@@ -269,39 +270,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         }
         __syncthreads();
         load_request<ROWS>(p, static_cast<int>(start_b), w);
-        const int64_t k = (u - start_unit) / w.tiles_k;  // item within the request
+        const int64_t k = (u - start_unit) / (w.tiles_k + kItemUnits);  // item within the request
         w.h = static_cast<int>(k / w.tiles_r);
         w.rt = static_cast<int>(k - static_cast<int64_t>(w.h) * w.tiles_r);
         w.item = start_item + k;
-        w.first = start_unit + k * w.tiles_k;
+        w.first = start_unit + k * (w.tiles_k + kItemUnits) + kItemUnits;
     }
+    // the item after w
+    auto advance = [&](Place &x) {
+        x.first += x.tiles_k + kItemUnits;
+        ++x.item;
+        if (++x.rt == x.tiles_r) {
+            x.rt = 0;
+            if (++x.h == p.c.heads) {
+                x.h = 0;
+                do load_request<ROWS>(p, x.b + 1, x);
+                while (x.tiles_r == 0);
+            }
+        }
+    };
     const bool wide_scales = (p.c.blocks & 3) == 0;
 
-    for (bool first_item = true; u < u_end; first_item = false) {
-        const int64_t item_end = w.first + w.tiles_k;
-        const int64_t kt0 = u - w.first, kt1 = min(u_end, item_end) - w.first;
-        const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
-        const int keys = static_cast<int>(min(static_cast<int64_t>(w.prefix) + w.nodes,
-                                              static_cast<int64_t>(p.table_cols) * p.c.page_size));
-
-        // ---- the warp's keys: steps of 32 from tile to tile
-        const int base0 = static_cast<int>(kt0) * kTileKeys + warp * kStepKeys;
-        const int n_steps = static_cast<int>(kt1 - kt0);
-        unsigned char *ring = smem + warp * (S::kStage * kStages);
-        const int32_t *table = p.table + static_cast<int64_t>(w.b) * p.table_row;
-
-        // row number of the lane's key of step i, or kNoRow
-        auto find = [&](int i) -> uint32_t {
-            const int pos = base0 + i * kTileKeys + lane;
-            if (i >= n_steps || pos >= keys) return kNoRow;
-            const int col = static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.c.page_size));
-            const int page = __ldg(table + col);
-            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
-            return static_cast<uint32_t>(row_of(p.c, page, w.h, pos - col * p.c.page_size));
-        };
-        auto issue = [&](int i, uint32_t row) {
-            if (i < n_steps) {
-                unsigned char *st = ring + (i % kStages) * S::kStage;
+    // ---- the warp's ring: stage `slot` takes 32 keys, of which the lane's is row `row`
+    unsigned char *ring = smem + warp * (S::kStage * kStages);
+    // scales past the cache's blocks are never copied: they stay 0
+    for (int i = lane; i < S::kStage * kStages / 16; i += 32) reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    auto issue = [&](bool any, int slot, uint32_t row) {
+            if (any) {
+                unsigned char *st = ring + slot * S::kStage;
                 const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(st));
                 const uint32_t sv = sk + kStepKeys * S::kKPitch;
                 const uint32_t ss = sv + kStepKeys * S::kVPitch;
@@ -352,14 +349,51 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             cp_commit();
         };
 
-        uint32_t row_cur[kStages];  // rows of the steps in the ring: their lanes' keys are there
+    // What a CTA does of one item: key tiles kt0 .. kt1 - 1, one step of the warp in each.
+    struct Work {
+        int64_t kt0, kt1;
+        int base0, n_steps, keys, h;
+        const int32_t *table;
+    };
+    auto work_of = [&](const Place &x) -> Work {
+        Work k;
+        k.kt0 = max(u, x.first) - x.first;
+        k.kt1 = max(min(u_end, x.first + x.tiles_k) - x.first, k.kt0);
+        k.base0 = static_cast<int>(k.kt0) * kTileKeys + warp * kStepKeys;
+        k.n_steps = static_cast<int>(k.kt1 - k.kt0);
+        k.keys = static_cast<int>(min(static_cast<int64_t>(x.prefix) + x.nodes,
+                                      static_cast<int64_t>(p.table_cols) * p.c.page_size));
+        k.h = x.h;
+        k.table = p.table + static_cast<int64_t>(x.b) * p.table_row;
+        return k;
+    };
+    // row number of the lane's key of step i, or kNoRow
+    auto find = [&](const Work &k, int i) -> uint32_t {
+        const int pos = k.base0 + i * kTileKeys + lane;
+        if (i >= k.n_steps || pos >= k.keys) return kNoRow;
+        const uint32_t col = (__umulhi(pos, p.page_mul) + pos) >> p.page_shift;  // pos / page_size
+        const int page = __ldg(k.table + col);
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
+        return static_cast<uint32_t>(row_of(p.c, page, k.h, pos - static_cast<int>(col) * p.c.page_size));
+    };
+    uint32_t row_cur[kStages];  // rows of the steps in the ring: their lanes' keys are there
+    uint32_t row_next;
+    int slot0 = 0;              // stage of the item's first step
+    auto begin = [&](const Work &k) {
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            row_cur[i] = find(i);
-            issue(i, row_cur[i]);
+            row_cur[i] = find(k, i);
+            issue(i < k.n_steps, (slot0 + i) % kStages, row_cur[i]);
         }
-        uint32_t row_next = find(kStages - 1);
+        row_next = find(k, kStages - 1);
+    };
 
+    Work k = work_of(w);
+    begin(k);
+    bool first_item = true;  // that has tiles here
+    for (;;) {
+        const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
+        if (k.n_steps > 0) {
         // ---- q rows to shared memory: a power of two per row, then f16 parts
         for (int r = tid >> 3; r < ROWS; r += kWarps * 4) {
             const int l8 = tid & 7;
@@ -425,24 +459,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                 mul[t][r] = row_mul[8 * t + 2 * c + r];
             }
 
-        for (int i = 0; i < n_steps; ++i) {
+        int slot = slot0;
+        for (int i = 0; i < k.n_steps; ++i) {
             // row_cur[0] is step i's; the next free stage takes step i + kStages - 1
             row_cur[kStages - 1] = row_next;
-            issue(i + kStages - 1, row_next);
-            row_next = find(i + kStages);
+            issue(i + kStages - 1 < k.n_steps, slot == 0 ? kStages - 1 : slot - 1, row_next);
+            row_next = find(k, i + kStages);
             cp_wait<kStages - 1>();
             __syncwarp();
-            const unsigned char *sk = ring + (i % kStages) * S::kStage, *sv = sk + kStepKeys * S::kKPitch;
+            const unsigned char *sk = ring + slot * S::kStage, *sv = sk + kStepKeys * S::kKPitch;
             const float *ks = reinterpret_cast<const float *>(sv + kStepKeys * S::kVPitch);
             const float *vs = ks + kStepKeys * NB;
             const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow);
-            const int base = base0 + i * kTileKeys;
+            const int base = k.base0 + i * kTileKeys;
             if (there != 0) {
                 // 2^(E + 14) is above the scales of the lane's key, and of all keys
                 uint32_t top_bits = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if (b < p.c.blocks) top_bits = max(top_bits, __float_as_uint(vs[lane * NB + b]) & 0x7FFFFFFFu);
+                for (int b = 0; b < NB; ++b) top_bits = max(top_bits, __float_as_uint(vs[lane * NB + b]) & 0x7FFFFFFFu);
                 const float e_key = static_cast<float>(max(min(static_cast<int>(top_bits >> 23) - 127 + 1 - 14, 114), -100));
                 const float e_all = static_cast<float>(
                     max(min(static_cast<int>(__reduce_max_sync(~0u, top_bits) >> 23) - 127 + 1 - 14, 114), -100));
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                         for (int r = 0; r < 2; ++r) s[t][2 * j][r] = s[t][2 * j + 1][r] = 0.0f;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        if (b < p.c.blocks) {
+                        {
                             const uint2 x = *reinterpret_cast<const uint2 *>(sk + (16 * j + g) * S::kKPitch + b * 32 + c * 8);
                             const uint2 y = *reinterpret_cast<const uint2 *>(sk + (16 * j + 8 + g) * S::kKPitch + b * 32 + c * 8);
                             const uint32_t x0 = x.x ^ 0x80808080u, x1 = x.y ^ 0x80808080u;
@@ -563,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                 for (int k = 0; k < 4; ++k) load_scales<NB>(vs + (8 * k + g) * NB, dv[k]);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    if (b < p.c.blocks) {
+                    {
                         // The tensor cores cut their f32 sums toward zero.  Over thousands of keys that bias is
                         // 1e-5 of the sum: with f32 or f16 outputs a step's 32 keys are summed apart, and added
                         // with rounding.
@@ -630,18 +664,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                 }
             }
             __syncwarp();
+            slot = slot + 1 == kStages ? 0 : slot + 1;
 #pragma unroll
-            for (int k = 0; k + 1 < kStages; ++k) row_cur[k] = row_cur[k + 1];
+            for (int j = 0; j + 1 < kStages; ++j) row_cur[j] = row_cur[j + 1];
         }
-        cp_wait<0>();
-        // ---- join the warps
-        __syncthreads();  // every warp is done with its ring
-        float *jo = reinterpret_cast<float *>(smem);  // [warp][row][kJoinPitch]
+        slot0 = slot;
+        // ---- the next item's first keys are on their way while the warps of this one are joined
+        const Place done = w;
+        const Work did = k;
+        const bool more = w.first + w.tiles_k < u_end;
+        if (more) {
+            advance(w);
+            k = work_of(w);
+            begin(k);
+        }
+        const bool whole = did.kt0 == 0 && did.kt1 == done.tiles_k;
+        const int pitch = p.c.dim + 2;
+        const int64_t slot_p = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
+        first_item = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+            if (t > 0) __syncthreads();
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float *at = jo + (warp * ROWS + 8 * t + 2 * c + r) * S::kJoinPitch;
+                float *at = jo + (warp * 8 + 2 * c + r) * S::kJoinPitch;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
                     *reinterpret_cast<float4 *>(at + 32 * b + 4 * g) =
@@ -653,76 +699,77 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                     at[DP + 1] = l[t][r];
                 }
             }
-        __syncthreads();
-        const bool whole = kt0 == 0 && kt1 == w.tiles_k;
-        const int pitch = p.c.dim + 2;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
-        for (int r = tid >> 3; r < rows; r += kWarps * 4) {  // 8 threads a row
-            const int l8 = tid & 7;
+            __syncthreads();
+            // kWarps * 4 threads a row
+            constexpr int TPR = kWarps * 4;
+            const int r8 = tid / TPR, lr = tid % TPR, r = 8 * t + r8;
             float f[kWarps], top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) top = fmaxf(top, jo[(k * ROWS + r) * S::kJoinPitch + DP]);
+            for (int q = 0; q < kWarps; ++q) top = fmaxf(top, jo[(q * 8 + r8) * S::kJoinPitch + DP]);
             const float z = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float *x = jo + (k * ROWS + r) * S::kJoinPitch;
-                f[k] = ex2(x[DP] - z);
-                sum = fmaf(f[k], x[DP + 1], sum);
+            for (int q = 0; q < kWarps; ++q) {
+                const float *x = jo + (q * 8 + r8) * S::kJoinPitch;
+                f[q] = ex2(x[DP] - z);
+                sum = fmaf(f[q], x[DP + 1], sum);
             }
-            const int idx = w.rt * ROWS + r, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
-            const int64_t row = static_cast<int64_t>(w.row0) + node;
-            T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
-            float *part = p.partial + (slot * ROWS + r) * pitch;
-            const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
+            if (r < rows) {
+                const int idx = done.rt * ROWS + r, node = idx / p.group, hq = done.h * p.group + idx - node * p.group;
+                const int64_t row = static_cast<int64_t>(done.row0) + node;
+                T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                float *part = p.partial + (slot_p * ROWS + r) * pitch;
+                const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
 #pragma unroll
-            for (int k = 0; k < DP / 8; ++k) {
-                const int e = l8 + 8 * k;
-                if (e < p.c.dim) {
-                    float x = 0.0f;
+                for (int q = 0; q < DP / TPR; ++q) {
+                    const int e = lr + TPR * q;
+                    if (e < p.c.dim) {
+                        float x = 0.0f;
 #pragma unroll
-                    for (int q = 0; q < kWarps; ++q) x = fmaf(f[q], jo[(q * ROWS + r) * S::kJoinPitch + e], x);
-                    if (whole)
-                        out[e] = from_f32<T>(x * inv);
-                    else
-                        part[e] = x;
+                        for (int v = 0; v < kWarps; ++v) x = fmaf(f[v], jo[(v * 8 + r8) * S::kJoinPitch + e], x);
+                        if (whole)
+                            out[e] = from_f32<T>(x * inv);
+                        else
+                            part[e] = x;
+                    }
                 }
-            }
-            if (l8 == 0) {
-                if (!whole) {
-                    part[p.c.dim] = top;
-                    part[p.c.dim + 1] = sum;
-                } else if (p.lse) {
-                    p.lse[row * p.heads_q + hq] = (z + log2f(sum)) * 0.693147180559945f;
+                if (lr == 0) {
+                    if (!whole) {
+                        part[p.c.dim] = top;
+                        part[p.c.dim + 1] = sum;
+                    } else if (p.lse) {
+                        p.lse[row * p.heads_q + hq] = (z + log2f(sum)) * 0.693147180559945f;
+                    }
                 }
             }
         }
         // (an item past the tickets exists only if `starts` is not ascending: it has no output)
-        if (!whole && w.item < p.tickets_n) {
-            const int64_t c0 = split.owner(w.first), c1 = split.owner(item_end - 1);
+        if (!whole && done.item < p.tickets_n) {
+            const int64_t c0 = split.owner(done.first), c1 = split.owner(done.first + done.tiles_k - 1);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const unsigned t = atomicAdd(p.tickets + w.item, 1u);
+                const unsigned t = atomicAdd(p.tickets + done.item, 1u);
                 is_last = t == static_cast<unsigned>(c1 - c0);
-                if (is_last) p.tickets[w.item] = 0;
+                if (is_last) p.tickets[done.item] = 0;
             }
             __syncthreads();
             if (is_last) {
                 __threadfence();
                 for (int r = tid >> 3; r < rows; r += kWarps * 4) {
                     const int l8 = tid & 7;
-                    auto part_of = [&](int64_t k) {
-                        const int64_t sl = k > c0 || split.begin(k) == w.first ? 2 * k : 2 * k + 1;
+                    // the part of CTA q: its first item with tiles, unless it begins before this item
+                    auto part_of = [&](int64_t q) {
+                        const int64_t sl = split.begin(q) >= done.first - kItemUnits ? 2 * q : 2 * q + 1;
                         return p.partial + (sl * ROWS + r) * pitch;
                     };
                     float top = -INFINITY, sum = 0.0f;
-                    for (int64_t k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part_of(k) + p.c.dim));
+                    for (int64_t q = c0; q <= c1; ++q) top = fmaxf(top, __ldcg(part_of(q) + p.c.dim));
                     const float z = top == -INFINITY ? 0.0f : top;
                     float x[DP / 8];
 #pragma unroll
                     for (int k = 0; k < DP / 8; ++k) x[k] = 0.0f;
-                    for (int64_t k = c0; k <= c1; ++k) {
-                        const float *part = part_of(k);
+                    for (int64_t v = c0; v <= c1; ++v) {
+                        const float *part = part_of(v);
                         const float f = ex2(__ldcg(part + p.c.dim) - z);
                         sum = fmaf(f, __ldcg(part + p.c.dim + 1), sum);
 #pragma unroll
@@ -730,8 +777,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                             if (l8 + 8 * q < p.c.dim) x[q] = fmaf(f, __ldcg(part + l8 + 8 * q), x[q]);
                     }
                     const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
-                    const int idx = w.rt * ROWS + r, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
-                    const int64_t row = static_cast<int64_t>(w.row0) + node;
+                    const int idx = done.rt * ROWS + r, node = idx / p.group, hq = done.h * p.group + idx - node * p.group;
+                    const int64_t row = static_cast<int64_t>(done.row0) + node;
                     T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
 #pragma unroll
                     for (int q = 0; q < DP / 8; ++q)
@@ -740,21 +787,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                 }
             }
         }
-        // ---- the next item
-        u = w.first + kt1;
-        if (u < u_end) {
-            w.first = item_end;
-            ++w.item;
-            if (++w.rt == w.tiles_r) {
-                w.rt = 0;
-                if (++w.h == p.c.heads) {
-                    w.h = 0;
-                    do load_request<ROWS>(p, w.b + 1, w);
-                    while (w.tiles_r == 0);
-                }
-            }
+        if (!more) break;
+        } else {
+            // only units of the item's fixed cost are here
+            if (w.first + w.tiles_k >= u_end) break;
+            advance(w);
+            k = work_of(w);
+            begin(k);
         }
-        __syncthreads();  // the join's reads, before the next item fills the ring and q
+        __syncthreads();  // the join's reads, before the next item's q
     }
 }
 

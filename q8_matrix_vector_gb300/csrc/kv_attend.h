@@ -11,6 +11,7 @@ constexpr int kWarps = 4;        // warps of a CTA, each with its own keys
 constexpr int kStepKeys = 32;    // keys a warp takes at a time
 constexpr int kTileKeys = kWarps * kStepKeys;
 constexpr int kStages = 2;       // steps in flight per warp
+constexpr int kItemUnits = 2;    // an item's fixed cost (start of its keys, q, join) in tiles
 
 struct AttendParams {
     Cache c;
@@ -28,6 +29,7 @@ struct AttendParams {
     int table_cols, mask_words;
     int requests, heads_q, group;
     float scale_log2;   // scale * log2(e)
+    uint32_t page_mul, page_shift;  // position / page_size = (umulhi(position, mul) + position) >> shift
     float *partial;     // 2 per CTA: [rows of an item][dim + 2]
     unsigned *tickets;  // one per item
     int tickets_n;
