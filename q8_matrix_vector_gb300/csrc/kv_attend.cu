@@ -70,7 +70,7 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
             p->grid[t][v] = sms * std::max(1, ctas);
             slots = std::max<int64_t>(slots, 2LL * p->grid[t][v] * 8 * kv::kRowTiles[v]);
         }
-    if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * slots * static_cast<size_t>(head_dim + 2));
+    if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * slots * static_cast<size_t>(head_dim + kv::kPartExtra));
     if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(items));
     if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(items));
     // the tickets' zeros, before any stream may use them

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             begin(k);
         }
         const bool whole = did.kt0 == 0 && did.kt1 == done.tiles_k;
-        const int pitch = p.c.dim + 2;
+        const int pitch = p.c.dim + kPartExtra;
         const int64_t slot_p = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
         first_item = false;
 #pragma unroll
@@ -755,35 +755,78 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             __syncthreads();
             if (is_last) {
                 __threadfence();
-                for (int r = tid >> 3; r < rows; r += kWarps * 4) {
-                    const int l8 = tid & 7;
-                    // the part of CTA q: its first item with tiles, unless it begins before this item
-                    auto part_of = [&](int64_t q) {
-                        const int64_t sl = split.begin(q) >= done.first - kItemUnits ? 2 * q : 2 * q + 1;
-                        return p.partial + (sl * ROWS + r) * pitch;
-                    };
-                    float top = -INFINITY, sum = 0.0f;
-                    for (int64_t q = c0; q <= c1; ++q) top = fmaxf(top, __ldcg(part_of(q) + p.c.dim));
-                    const float z = top == -INFINITY ? 0.0f : top;
-                    float x[DP / 8];
+                // parts by 32: their maxima and sums through shared memory, then their rows, 8 loads in flight
+                constexpr int TPR = kWarps * 4, V = DP / 4 / TPR > 0 ? DP / 4 / TPR : 1;
+                const int r8 = tid / TPR, lr = tid % TPR;
+                const int parts = static_cast<int>(c1 - c0) + 1;
+                // part 0 is its CTA's second result if that CTA began before this item
+                const int64_t base = 2 * c0, skew = split.begin(c0) >= done.first - kItemUnits ? 0 : 1;
+                float *part_m = jo, *part_l = jo + 32 * 8;
+#pragma unroll 1
+                for (int t = 0; t < NT; ++t) {
+                    const int r = 8 * t + r8;
+                    const float *mine = p.partial + (base * ROWS + r) * pitch;
+                    const int64_t step = 2 * static_cast<int64_t>(ROWS) * pitch, first = skew * ROWS * pitch;
+                    float top = -INFINITY, sum = 0.0f, x[V][4];
 #pragma unroll
-                    for (int k = 0; k < DP / 8; ++k) x[k] = 0.0f;
-                    for (int64_t v = c0; v <= c1; ++v) {
-                        const float *part = part_of(v);
-                        const float f = ex2(__ldcg(part + p.c.dim) - z);
-                        sum = fmaf(f, __ldcg(part + p.c.dim + 1), sum);
+                    for (int q = 0; q < V; ++q)
 #pragma unroll
-                        for (int q = 0; q < DP / 8; ++q)
-                            if (l8 + 8 * q < p.c.dim) x[q] = fmaf(f, __ldcg(part + l8 + 8 * q), x[q]);
+                        for (int e = 0; e < 4; ++e) x[q][e] = 0.0f;
+#pragma unroll 1
+                    for (int q0 = 0; q0 < parts; q0 += 32) {
+                        const int n = min(32, parts - q0);
+                        __syncthreads();
+                        for (int i = tid; i < n * 8; i += kWarps * 32) {
+                            const int q = q0 + (i >> 3);
+                            const float *at = p.partial + (base * ROWS + 8 * t + (i & 7)) * pitch + q * step +
+                                              (q == 0 ? first : 0) + p.c.dim;
+                            const bool live = 8 * t + (i & 7) < rows;
+                            part_m[i] = live ? __ldcg(at) : -INFINITY;
+                            part_l[i] = live ? __ldcg(at + 1) : 0.0f;
+                        }
+                        __syncthreads();
+                        float up = top;
+                        for (int q = 0; q < n; ++q) up = fmaxf(up, part_m[8 * q + r8]);
+                        const float z = up == -INFINITY ? 0.0f : up, back = ex2(top - z);
+                        top = up;
+                        sum *= back;
+#pragma unroll
+                        for (int q = 0; q < V; ++q)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[q][e] *= back;
+                        if (r < rows) {
+#pragma unroll 8
+                            for (int q = 0; q < n; ++q) {
+                                const float *at = mine + (q0 + q) * step + (q0 + q == 0 ? first : 0);
+                                const float f = ex2(part_m[8 * q + r8] - z);
+                                sum = fmaf(f, part_l[8 * q + r8], sum);
+#pragma unroll
+                                for (int k4 = 0; k4 < V; ++k4) {
+                                    const int e0 = 4 * (lr + TPR * k4);
+                                    if (e0 < p.c.dim) {
+                                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(at + e0));
+                                        x[k4][0] = fmaf(f, y.x, x[k4][0]);
+                                        x[k4][1] = fmaf(f, y.y, x[k4][1]);
+                                        x[k4][2] = fmaf(f, y.z, x[k4][2]);
+                                        x[k4][3] = fmaf(f, y.w, x[k4][3]);
+                                    }
+                                }
+                            }
+                        }
                     }
-                    const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
-                    const int idx = done.rt * ROWS + r, node = idx / p.group, hq = done.h * p.group + idx - node * p.group;
-                    const int64_t row = static_cast<int64_t>(done.row0) + node;
-                    T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                    if (r < rows) {
+                        const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+                        const int idx = done.rt * ROWS + r, node = idx / p.group, hq = done.h * p.group + idx - node * p.group;
+                        const int64_t row = static_cast<int64_t>(done.row0) + node;
+                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
 #pragma unroll
-                    for (int q = 0; q < DP / 8; ++q)
-                        if (l8 + 8 * q < p.c.dim) out[l8 + 8 * q] = from_f32<T>(x[q] * inv);
-                    if (l8 == 0 && p.lse) p.lse[row * p.heads_q + hq] = (z + log2f(sum)) * 0.693147180559945f;
+                        for (int k4 = 0; k4 < V; ++k4)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (4 * (lr + TPR * k4) < p.c.dim) out[4 * (lr + TPR * k4) + e] = from_f32<T>(x[k4][e] * inv);
+                        if (lr == 0 && p.lse)
+                            p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
+                    }
                 }
             }
         }

@@ -11,6 +11,7 @@ constexpr int kWarps = 4;        // warps of a CTA, each with its own keys
 constexpr int kStepKeys = 32;    // keys a warp takes at a time
 constexpr int kTileKeys = kWarps * kStepKeys;
 constexpr int kStages = 2;       // steps in flight per warp
+constexpr int kPartExtra = 4;    // of a partial row: its maximum and sum, and 16-byte alignment
 constexpr int kItemUnits = 2;    // an item's fixed cost (start of its keys, q, join) in tiles
 
 struct AttendParams {
@@ -30,7 +31,7 @@ struct AttendParams {
     int requests, heads_q, group;
     float scale_log2;   // scale * log2(e)
     uint32_t page_mul, page_shift;  // position / page_size = (umulhi(position, mul) + position) >> shift
-    float *partial;     // 2 per CTA: [rows of an item][dim + 2]
+    float *partial;     // 2 per CTA: [rows of an item][dim + kPartExtra]
     unsigned *tickets;  // one per item
     int tickets_n;
 };
