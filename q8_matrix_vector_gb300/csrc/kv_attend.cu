@@ -8,10 +8,10 @@ namespace kv {
 
 namespace {
 
-AttendVariant variant(int dim, int type, int row_tiles) {
-    return type == Q8KV_F32   ? attend_variant_f32(dim, row_tiles)
-           : type == Q8KV_F16 ? attend_variant_f16(dim, row_tiles)
-                              : attend_variant_bf16(dim, row_tiles);
+AttendVariant variant(int dim, int type, AttendShape shape) {
+    return type == Q8KV_F32   ? attend_variant_f32(dim, shape)
+           : type == Q8KV_F16 ? attend_variant_f16(dim, shape)
+                              : attend_variant_bf16(dim, shape);
 }
 
 }  // namespace
@@ -23,8 +23,8 @@ struct q8kv_attend_s {
     int heads_q = 0, heads_kv = 0, dim = 0;
     int max_requests = 0;
     int64_t max_rows = 0;
-    kv::AttendVariant variant[3][3];  // per type and row tiles
-    int grid[3][3] = {};              // and their CTAs: every SM full
+    kv::AttendVariant variant[3][kv::kAttendShapes];  // per type
+    int grid[3][kv::kAttendShapes] = {};              // and their CTAs: every SM full
     int64_t max_items = 0;
     float *partial = nullptr;
     unsigned *tickets = nullptr;
@@ -59,20 +59,24 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
     p->max_items = items;
     int sms = 0;
     int64_t slots = 0;  // rows of partial results
+    int64_t tickets = items;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device);
     for (int t = 0; t < 3; ++t)
-        for (int v = 0; v < 3 && e == cudaSuccess; ++v) {
+        for (int v = 0; v < kv::kAttendShapes && e == cudaSuccess; ++v) {
             int ctas = 0;
-            const kv::AttendVariant k = p->variant[t][v] = kv::variant(head_dim, t, kv::kRowTiles[v]);
+            const kv::AttendVariant k = p->variant[t][v] = kv::variant(head_dim, t, static_cast<kv::AttendShape>(v));
+            if (k.fn == nullptr) continue;
             e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
             if (e == cudaSuccess)
                 e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, k.fn, kv::kWarps * 32, k.smem);
             p->grid[t][v] = sms * std::max(1, ctas);
-            slots = std::max<int64_t>(slots, 2LL * p->grid[t][v] * 8 * kv::kRowTiles[v]);
+            tickets = std::max(tickets, items + 2 * kv::ceil_div(p->grid[t][v], kv::kJoinGroup));
+            const int rows = v == kv::kRows8 ? 8 : v == kv::kRows16 ? 16 : 32;
+            slots = std::max<int64_t>(slots, 2LL * p->grid[t][v] * rows);
         }
     if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * slots * static_cast<size_t>(head_dim + kv::kPartExtra));
-    if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(items));
-    if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(items));
+    if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(tickets));
+    if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(tickets));
     // the tickets' zeros, before any stream may use them
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
@@ -103,7 +107,7 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
                                  (p.c.page_size - 1) * p.c.stride_token >= 0xFFFFFFFFLL)
         return Q8MV_ERR_INVALID_ARG;
     // and positions in 31
-    if (static_cast<int64_t>(a->table_cols) * p.c.page_size > (1LL << 31) - 2 * kv::kTileKeys * kv::kStages)
+    if (static_cast<int64_t>(a->table_cols) * p.c.page_size > (1LL << 31) - 2 * kv::kWarps * kv::kStepKeys * kv::kStages)
         return Q8MV_ERR_INVALID_ARG;
     if (a->rows == 0 || a->requests == 0) return Q8MV_OK;
     if (a->starts == nullptr && a->rows % a->requests != 0) return Q8MV_ERR_INVALID_ARG;
@@ -138,9 +142,19 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.partial = plan->partial;
     p.tickets = plan->tickets;
     p.tickets_n = static_cast<int>(plan->max_items);
-    // 8, 16 or 32 query rows at a time, by the mean of a request's: the fewest that hold them
+    p.group_tickets = plan->tickets + plan->max_items;
+    // 8, 16 or 32 query rows at a time, by the mean of a request's: the fewest that hold them.
+    // With 8, and a token's heads side by side, each warp can take a head of its own, so that a CTA reads longer
+    // stretches: DRAM gives 128-byte pieces of 1 KB rows slowly (1.2 GB of cache, f32: 318 us with one head a CTA,
+    // 240 us with four; 0.59 GB: 143 and 119 us).  But four heads' partial results are to be joined instead of one's
+    // (0.28 GB of two requests: 68 and 81 us; 5 MB: 11.6 and 16.3 us), so only where the tables reach 0.5 GB.
     const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
-    const int v = mean <= 8 ? 0 : mean <= 16 || p.c.dim > 128 ? 1 : 2;
+    const double reach = static_cast<double>(a->requests) * a->table_cols * p.c.page_size * p.c.heads *
+                         (2.0 * p.c.dim + 8.0 * p.c.blocks);
+    const bool side_by_side = p.c.stride_head < p.c.stride_token && p.c.heads % kv::kWarps == 0 && reach >= 5e8;
+    const kv::AttendShape v = mean <= 8                            ? side_by_side ? kv::kHeads4 : kv::kRows8
+                              : mean <= 16 || p.c.dim > 128 ? kv::kRows16
+                                                            : kv::kRows32;
     const kv::AttendVariant &k = plan->variant[a->type][v];
     k.fn<<<plan->grid[a->type][v], kv::kWarps * 32, k.smem, stream>>>(p);
     return q8i::cuda_status(cudaGetLastError());

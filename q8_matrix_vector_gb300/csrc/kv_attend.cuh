@@ -86,13 +86,15 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Shared memory of one variant: dim up to DP, NT tiles of 8 query rows, QP parts of q.
+// Shared memory of one variant: dim up to DP, NT tiles of 8 query rows, QP parts of
+// q, HW kv heads (the warps' own, or one for all warps).
 // Row pitches are chosen so that the fragment loads hit 32 banks: keys (8 bytes
 // per lane, rows 0..3 per half warp) need a pitch of 32 mod 64 bytes, values (4
 // bytes, every second row) 16 mod 64, q (16 bytes, 2 rows a phase) 64 mod 128.
-template <int DP, int NT, int QP>
+template <int DP, int NT, int QP, int HW>
 struct Smem {
     static constexpr int kRows = 8 * NT;
+    static constexpr int kTileKeys = kStepKeys * kWarps / HW;
     static constexpr int kBlocks = DP / 32;
     static constexpr int kKPitch = (DP / 32) % 2 ? DP : DP + 32;
     static constexpr int kVPitch = DP + 16;
@@ -101,10 +103,12 @@ struct Smem {
     static constexpr int kRing = kStage * kStages * kWarps;
     // the join of the warps, 8 rows at a time: O, then m and l
     static constexpr int kJoinPitch = DP + 4;
-    static constexpr int kJoin = kWarps * 8 * kJoinPitch * 4;
+    static constexpr int kJoin = HW == 1 ? kWarps * 8 * kJoinPitch * 4 : 0;
     static constexpr int kQPitch = 2 * DP + ((2 * DP) % 128 == 64 ? 0 : 64);
-    static constexpr int kQ = QP * kRows * kQPitch;
-    static constexpr int kBias = kRows * kBlocks * 4;  // -128 * 2^-24 * the block's sum of q
+    static constexpr int kQHead = QP * kRows * kQPitch;
+    static constexpr int kQ = HW * kQHead;
+    static constexpr int kBiasHead = kRows * kBlocks * 4;
+    static constexpr int kBias = HW * kBiasHead;  // -128 * 2^-24 * the block's sum of q
     static constexpr int kTotal = kRing + kJoin + kQ + kBias;
 };
 
@@ -117,12 +121,12 @@ struct Place {
     int row0;         // first row of the request
     int tiles_r;      // row tiles
     int64_t tiles_k;  // key tiles
-    int h, rt;
+    int h, rt;        // head (of the first warp), row tile
     int64_t item;     // number of the item over all requests
     int64_t first;    // the unit of its first tile
 };
 
-template <int ROWS>
+template <int ROWS, int KEYS>
 __device__ __forceinline__ void load_request(const AttendParams &p, int b, Place &w) {
     w.b = b;
     int64_t s, e;
@@ -143,11 +147,12 @@ __device__ __forceinline__ void load_request(const AttendParams &p, int b, Place
     const int64_t reach = static_cast<int64_t>(p.table_cols) * p.c.page_size;
     const int64_t keys = min(static_cast<int64_t>(w.prefix) + w.nodes, reach);
     w.tiles_r = static_cast<int>((static_cast<int64_t>(w.nodes) * p.group + ROWS - 1) / ROWS);
-    w.tiles_k = max(static_cast<int64_t>(1), (keys + kTileKeys - 1) / kTileKeys);
+    w.tiles_k = max(static_cast<int64_t>(1), (keys + KEYS - 1) / KEYS);
 }
 
+template <int HW>
 __device__ __forceinline__ int64_t units_of(const AttendParams &p, const Place &w) {
-    return static_cast<int64_t>(p.c.heads) * w.tiles_r * (w.tiles_k + kItemUnits);
+    return static_cast<int64_t>(p.c.heads / HW) * w.tiles_r * (w.tiles_k + kItemUnits);
 }
 
 // What joining needs of an item's parts.
@@ -195,14 +200,16 @@ static __device__ __noinline__ uint32_t sees(const uint32_t *mask, int64_t mask_
     return (word(0) << -j0) | ((1u << -j0) - 1u);  // keys below -j0 are prefix
 }
 
-template <typename T, int DP, int NT, int QP, int PP>
-__global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const AttendParams p) {
-    using S = Smem<DP, NT, QP>;
-    constexpr int NB = S::kBlocks, ROWS = S::kRows;
+template <typename T, int DP, int NT, int QP, int PP, int HW>
+__global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv_attend_kernel(const AttendParams p) {
+    using S = Smem<DP, NT, QP, HW>;
+    static_assert(HW == 1 || (HW == kWarps && NT == 1), "one head for all warps, or one each with 8 rows");
+    constexpr int NB = S::kBlocks, ROWS = S::kRows, KEYS = S::kTileKeys;
+    constexpr int TILES = HW == 1 ? NT : HW;  // of 8 rows in a partial result
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t scan_units[kWarps], scan_items[kWarps];
     __shared__ int64_t start_b, start_item, start_unit;
-    __shared__ float row_mul[ROWS];
+    __shared__ float row_mul[HW * ROWS];
     __shared__ int is_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -220,9 +227,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
         int64_t units = 0, items = 0;
         for (int b = b0; b < b1; ++b) {
-            load_request<ROWS>(p, b, w);
-            units += units_of(p, w);
-            items += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+            load_request<ROWS, KEYS>(p, b, w);
+            units += units_of<HW>(p, w);
+            items += static_cast<int64_t>(p.c.heads / HW) * w.tiles_r;
         }
         int64_t iu = units, ii = items;  // inclusive over the warp
 #pragma unroll
@@ -258,21 +265,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         if (u >= before_u && u < before_u + units) {  // exactly one thread
             int b = b0;
             for (; b < b1; ++b) {
-                load_request<ROWS>(p, b, w);
-                const int64_t n = units_of(p, w);
+                load_request<ROWS, KEYS>(p, b, w);
+                const int64_t n = units_of<HW>(p, w);
                 if (u < before_u + n) break;
                 before_u += n;
-                before_i += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+                before_i += static_cast<int64_t>(p.c.heads / HW) * w.tiles_r;
             }
             start_b = b;
             start_unit = before_u;
             start_item = before_i;
         }
         __syncthreads();
-        load_request<ROWS>(p, static_cast<int>(start_b), w);
+        load_request<ROWS, KEYS>(p, static_cast<int>(start_b), w);
         const int64_t k = (u - start_unit) / (w.tiles_k + kItemUnits);  // item within the request
         w.h = static_cast<int>(k / w.tiles_r);
         w.rt = static_cast<int>(k - static_cast<int64_t>(w.h) * w.tiles_r);
+        w.h *= HW;
         w.item = start_item + k;
         w.first = start_unit + k * (w.tiles_k + kItemUnits) + kItemUnits;
     }
@@ -282,9 +290,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         ++x.item;
         if (++x.rt == x.tiles_r) {
             x.rt = 0;
-            if (++x.h == p.c.heads) {
+            if ((x.h += HW) == p.c.heads) {
                 x.h = 0;
-                do load_request<ROWS>(p, x.b + 1, x);
+                do load_request<ROWS, KEYS>(p, x.b + 1, x);
                 while (x.tiles_r == 0);
             }
         }
@@ -359,17 +367,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         Work k;
         k.kt0 = max(u, x.first) - x.first;
         k.kt1 = max(min(u_end, x.first + x.tiles_k) - x.first, k.kt0);
-        k.base0 = static_cast<int>(k.kt0) * kTileKeys + warp * kStepKeys;
+        k.base0 = static_cast<int>(k.kt0) * KEYS + (HW == 1 ? warp * kStepKeys : 0);
         k.n_steps = static_cast<int>(k.kt1 - k.kt0);
         k.keys = static_cast<int>(min(static_cast<int64_t>(x.prefix) + x.nodes,
                                       static_cast<int64_t>(p.table_cols) * p.c.page_size));
-        k.h = x.h;
+        k.h = x.h + (HW == 1 ? 0 : warp);
         k.table = p.table + static_cast<int64_t>(x.b) * p.table_row;
         return k;
     };
     // row number of the lane's key of step i, or kNoRow
     auto find = [&](const Work &k, int i) -> uint32_t {
-        const int pos = k.base0 + i * kTileKeys + lane;
+        const int pos = k.base0 + i * KEYS + lane;
         if (i >= k.n_steps || pos >= k.keys) return kNoRow;
         const uint32_t col = (__umulhi(pos, p.page_mul) + pos) >> p.page_shift;  // pos / page_size
         const int page = __ldg(k.table + col);
@@ -395,9 +403,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
         if (k.n_steps > 0) {
         // ---- q rows to shared memory: a power of two per row, then f16 parts
-        for (int r = tid >> 3; r < ROWS; r += kWarps * 4) {
-            const int l8 = tid & 7;
-            const int idx = w.rt * ROWS + r, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
+        for (int rr = tid >> 3; rr < HW * ROWS; rr += kWarps * 4) {
+            const int l8 = tid & 7, hw = rr / ROWS, r = rr % ROWS;
+            const int idx = w.rt * ROWS + r, node = idx / p.group, hq = (w.h + hw) * p.group + idx - node * p.group;
             const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
             float x[DP / 8];
             float top = 0.0f;
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             for (int i = 0; i < DP / 8; ++i) {
                 const float y = x[i] * down;
                 const __half hi = __float2half_rn(y);
-                __half *dst = reinterpret_cast<__half *>(q_sm + r * S::kQPitch) + l8 + 8 * i;
+                __half *dst = reinterpret_cast<__half *>(q_sm + hw * S::kQHead + r * S::kQPitch) + l8 + 8 * i;
                 *dst = hi;
                 float used = __half2float(hi);
                 if constexpr (QP == 2) {
@@ -433,11 +441,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
                 for (int d = 1; d < 8; d *= 2) sum[b] += __shfl_xor_sync(~0u, sum[b], d);
-                if (l8 == 0) bias_sm[((r >> 1) * NB + b) * 2 + (r & 1)] = -128.0f / 16777216.0f * sum[b];
+                if (l8 == 0) bias_sm[hw * (ROWS * NB) + ((r >> 1) * NB + b) * 2 + (r & 1)] = -128.0f / 16777216.0f * sum[b];
             }
             // not 0: a score of -inf has to stay that
             if (l8 == 0)
-                row_mul[r] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex + 24) << 23) * fabsf(p.scale_log2), 1e-37f);
+                row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex + 24) << 23) * fabsf(p.scale_log2), 1e-37f);
         }
         __syncthreads();
 
@@ -456,9 +464,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             for (int r = 0; r < 2; ++r) {
                 m[t][r] = -INFINITY;
                 l[t][r] = 0.0f;
-                mul[t][r] = row_mul[8 * t + 2 * c + r];
+                mul[t][r] = row_mul[(HW == 1 ? 0 : warp * ROWS) + 8 * t + 2 * c + r];
             }
 
+        const unsigned char *my_q = q_sm + (HW == 1 ? 0 : warp * S::kQHead);
+        const float *my_bias = bias_sm + (HW == 1 ? 0 : warp * (ROWS * NB));
         int slot = slot0;
         for (int i = 0; i < k.n_steps; ++i) {
             // row_cur[0] is step i's; the next free stage takes step i + kStages - 1
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             const float *ks = reinterpret_cast<const float *>(sv + kStepKeys * S::kVPitch);
             const float *vs = ks + kStepKeys * NB;
             const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow);
-            const int base = k.base0 + i * kTileKeys;
+            const int base = k.base0 + i * KEYS;
             if (there != 0) {
                 // 2^(E + 14) is above the scales of the lane's key, and of all keys
                 uint32_t top_bits = 0;
@@ -505,12 +515,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                                                     __byte_perm(x1, 0, 0x4342u), __byte_perm(y1, 0, 0x4342u)};
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const float2 z = *reinterpret_cast<const float2 *>(bias_sm + ((4 * t + c) * NB + b) * 2);
+                                const float2 z = *reinterpret_cast<const float2 *>(my_bias + ((4 * t + c) * NB + b) * 2);
                                 float part[4] = {z.x, z.y, z.x, z.y};
 #pragma unroll
                                 for (int q = 0; q < QP; ++q) {
                                     const uint4 qq = *reinterpret_cast<const uint4 *>(
-                                        q_sm + (q * ROWS + 8 * t + g) * S::kQPitch + b * 64 + c * 16);
+                                        my_q + (q * ROWS + 8 * t + g) * S::kQPitch + b * 64 + c * 16);
                                     mma_f16(part, a0, qq.x, qq.y, part);
                                     mma_f16(part, a1, qq.z, qq.w, part);
                                 }
@@ -682,6 +692,54 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
         const int pitch = p.c.dim + kPartExtra;
         const int64_t slot_p = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
         first_item = false;
+        // tile t, row r8 of the item's results: its output row and query head
+        auto place_row = [&](int t, int r8, int64_t *row, int *hq) -> bool {
+            const int r = HW == 1 ? 8 * t + r8 : r8;
+            const int idx = done.rt * ROWS + r, node = idx / p.group;
+            *row = static_cast<int64_t>(done.row0) + node;
+            *hq = (done.h + (HW == 1 ? 0 : t)) * p.group + idx - node * p.group;
+            return r < rows;
+        };
+        if constexpr (HW > 1) {
+            // each warp has whole results of its head
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int r8 = 2 * c + r;
+                int64_t row;
+                int hq;
+                const bool live = place_row(warp, r8, &row, &hq);
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) l[0][r] += __shfl_xor_sync(~0u, l[0][r], d);
+                if (live) {
+                    T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                    float *part = p.partial + (slot_p * (8 * TILES) + warp * 8 + r8) * pitch;
+                    const float sum = l[0][r], inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const int e = 32 * b + 4 * g;
+                        const float4 x = make_float4(o[0][2 * b][r], o[0][2 * b][2 + r], o[0][2 * b + 1][r], o[0][2 * b + 1][2 + r]);
+                        if (e < p.c.dim) {
+                            if (whole) {
+                                out[e] = from_f32<T>(x.x * inv);
+                                out[e + 1] = from_f32<T>(x.y * inv);
+                                out[e + 2] = from_f32<T>(x.z * inv);
+                                out[e + 3] = from_f32<T>(x.w * inv);
+                            } else {
+                                *reinterpret_cast<float4 *>(part + e) = x;
+                            }
+                        }
+                    }
+                    if (g == 0) {
+                        if (!whole) {
+                            part[p.c.dim] = m[0][r];
+                            part[p.c.dim + 1] = sum;
+                        } else if (p.lse) {
+                            p.lse[row * p.heads_q + hq] = ((m[0][r] == -INFINITY ? 0.0f : m[0][r]) + log2f(sum)) * 0.693147180559945f;
+                        }
+                    }
+                }
+            }
+        } else {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t > 0) __syncthreads();
@@ -702,7 +760,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
             __syncthreads();
             // kWarps * 4 threads a row
             constexpr int TPR = kWarps * 4;
-            const int r8 = tid / TPR, lr = tid % TPR, r = 8 * t + r8;
+            const int r8 = tid / TPR, lr = tid % TPR;
             float f[kWarps], top = -INFINITY, sum = 0.0f;
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) top = fmaxf(top, jo[(q * 8 + r8) * S::kJoinPitch + DP]);
@@ -713,11 +771,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                 f[q] = ex2(x[DP] - z);
                 sum = fmaf(f[q], x[DP + 1], sum);
             }
-            if (r < rows) {
-                const int idx = done.rt * ROWS + r, node = idx / p.group, hq = done.h * p.group + idx - node * p.group;
-                const int64_t row = static_cast<int64_t>(done.row0) + node;
+            int64_t row;
+            int hq;
+            if (place_row(t, r8, &row, &hq)) {
                 T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
-                float *part = p.partial + (slot_p * ROWS + r) * pitch;
+                float *part = p.partial + (slot_p * (8 * TILES) + 8 * t + r8) * pitch;
                 const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
 #pragma unroll
                 for (int q = 0; q < DP / TPR; ++q) {
@@ -742,91 +800,97 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
                 }
             }
         }
+        }
         // (an item past the tickets exists only if `starts` is not ascending: it has no output)
         if (!whole && done.item < p.tickets_n) {
-            const int64_t c0 = split.owner(done.first), c1 = split.owner(done.first + done.tiles_k - 1);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const unsigned t = atomicAdd(p.tickets + done.item, 1u);
-                is_last = t == static_cast<unsigned>(c1 - c0);
-                if (is_last) p.tickets[done.item] = 0;
-            }
-            __syncthreads();
-            if (is_last) {
-                __threadfence();
-                // parts by 32: their maxima and sums through shared memory, then their rows, 8 loads in flight
-                constexpr int TPR = kWarps * 4, V = DP / 4 / TPR > 0 ? DP / 4 / TPR : 1;
-                const int r8 = tid / TPR, lr = tid % TPR;
-                const int parts = static_cast<int>(c1 - c0) + 1;
-                // part 0 is its CTA's second result if that CTA began before this item
-                const int64_t base = 2 * c0, skew = split.begin(c0) >= done.first - kItemUnits ? 0 : 1;
-                float *part_m = jo, *part_l = jo + 32 * 8;
-#pragma unroll 1
-                for (int t = 0; t < NT; ++t) {
-                    const int r = 8 * t + r8;
-                    const float *mine = p.partial + (base * ROWS + r) * pitch;
-                    const int64_t step = 2 * static_cast<int64_t>(ROWS) * pitch, first = skew * ROWS * pitch;
-                    float top = -INFINITY, sum = 0.0f, x[V][4];
+            constexpr int PR = 8 * TILES, TPR = kWarps * 32 / PR, V = DP / 4 / TPR;  // rows, threads a row, float4 a thread
+            const int pr = tid / TPR, lr = tid % TPR;
+            int64_t row;
+            int hq;
+            const bool live = place_row(pr / 8, pr % 8, &row, &hq);
+            // Adds n parts, the first at slot `head`, the i-th at slot `at + i * step`: to the output, or to the
+            // first part's place.
+            auto join = [&](int n, int64_t head, int64_t at, int64_t step, bool last) {
+                const float *from = p.partial + (at * PR + pr) * pitch, *from0 = p.partial + (head * PR + pr) * pitch;
+                step *= PR * pitch;
+                float top = -INFINITY, sum = 0.0f, x[V][4];
 #pragma unroll
-                    for (int q = 0; q < V; ++q)
+                for (int q = 0; q < V; ++q)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[q][e] = 0.0f;
-#pragma unroll 1
-                    for (int q0 = 0; q0 < parts; q0 += 32) {
-                        const int n = min(32, parts - q0);
-                        __syncthreads();
-                        for (int i = tid; i < n * 8; i += kWarps * 32) {
-                            const int q = q0 + (i >> 3);
-                            const float *at = p.partial + (base * ROWS + 8 * t + (i & 7)) * pitch + q * step +
-                                              (q == 0 ? first : 0) + p.c.dim;
-                            const bool live = 8 * t + (i & 7) < rows;
-                            part_m[i] = live ? __ldcg(at) : -INFINITY;
-                            part_l[i] = live ? __ldcg(at + 1) : 0.0f;
-                        }
-                        __syncthreads();
-                        float up = top;
-                        for (int q = 0; q < n; ++q) up = fmaxf(up, part_m[8 * q + r8]);
-                        const float z = up == -INFINITY ? 0.0f : up, back = ex2(top - z);
-                        top = up;
-                        sum *= back;
+                    for (int e = 0; e < 4; ++e) x[q][e] = 0.0f;
+                if (live) {
+                    for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg((i == 0 ? from0 : from + i * step) + p.c.dim));
+                    const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll (V <= 2 ? 8 : 4)
+                    for (int i = 0; i < n; ++i) {
+                        const float *part = i == 0 ? from0 : from + i * step;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + p.c.dim));
+                        const float f = ex2(ml.x - z);
+                        sum = fmaf(f, ml.y, sum);
 #pragma unroll
-                        for (int q = 0; q < V; ++q)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[q][e] *= back;
-                        if (r < rows) {
-#pragma unroll 8
-                            for (int q = 0; q < n; ++q) {
-                                const float *at = mine + (q0 + q) * step + (q0 + q == 0 ? first : 0);
-                                const float f = ex2(part_m[8 * q + r8] - z);
-                                sum = fmaf(f, part_l[8 * q + r8], sum);
-#pragma unroll
-                                for (int k4 = 0; k4 < V; ++k4) {
-                                    const int e0 = 4 * (lr + TPR * k4);
-                                    if (e0 < p.c.dim) {
-                                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(at + e0));
-                                        x[k4][0] = fmaf(f, y.x, x[k4][0]);
-                                        x[k4][1] = fmaf(f, y.y, x[k4][1]);
-                                        x[k4][2] = fmaf(f, y.z, x[k4][2]);
-                                        x[k4][3] = fmaf(f, y.w, x[k4][3]);
-                                    }
-                                }
+                        for (int q = 0; q < V; ++q) {
+                            const int e0 = 4 * (lr + TPR * q);
+                            if (e0 < p.c.dim) {
+                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + e0));
+                                x[q][0] = fmaf(f, y.x, x[q][0]);
+                                x[q][1] = fmaf(f, y.y, x[q][1]);
+                                x[q][2] = fmaf(f, y.z, x[q][2]);
+                                x[q][3] = fmaf(f, y.w, x[q][3]);
                             }
                         }
                     }
-                    if (r < rows) {
-                        const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
-                        const int idx = done.rt * ROWS + r, node = idx / p.group, hq = done.h * p.group + idx - node * p.group;
-                        const int64_t row = static_cast<int64_t>(done.row0) + node;
-                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                }
+                __syncwarp();  // a row's threads have read the first part
+                if (live && last) {
+                    const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+                    T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
 #pragma unroll
-                        for (int k4 = 0; k4 < V; ++k4)
+                    for (int q = 0; q < V; ++q)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (4 * (lr + TPR * k4) < p.c.dim) out[4 * (lr + TPR * k4) + e] = from_f32<T>(x[k4][e] * inv);
-                        if (lr == 0 && p.lse)
-                            p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
+                        for (int e = 0; e < 4; ++e)
+                            if (4 * (lr + TPR * q) < p.c.dim) out[4 * (lr + TPR * q) + e] = from_f32<T>(x[q][e] * inv);
+                    if (lr == 0 && p.lse)
+                        p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
+                } else if (live) {
+                    float *to = p.partial + (head * PR + pr) * pitch;
+#pragma unroll
+                    for (int q = 0; q < V; ++q)
+                        if (4 * (lr + TPR * q) < p.c.dim)
+                            *reinterpret_cast<float4 *>(to + 4 * (lr + TPR * q)) = make_float4(x[q][0], x[q][1], x[q][2], x[q][3]);
+                    if (lr == 0) {
+                        to[p.c.dim] = top;
+                        to[p.c.dim + 1] = sum;
                     }
+                }
+            };
+            // true in the CTA that is the last of n to come
+            auto arrive = [&](unsigned *ticket, unsigned n) -> bool {
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const unsigned t = atomicAdd(ticket, 1u);
+                    is_last = t == n - 1;
+                    if (is_last) *ticket = 0;
+                }
+                __syncthreads();
+                const bool yes = is_last;
+                if (yes) __threadfence();
+                return yes;
+            };
+            // Parts c0 .. c1.  Up to kJoinGroup of them are joined at once; more are joined in groups of CTAs
+            // whose numbers agree but for the last bits, by each group's last, and then the groups.
+            const int c0 = static_cast<int>(split.owner(done.first)), c1 = static_cast<int>(split.owner(done.first + done.tiles_k - 1));
+            const int slot_c0 = split.begin(c0) >= done.first - kItemUnits ? 2 * c0 : 2 * c0 + 1;
+            if (c1 - c0 < kJoinGroup) {
+                if (arrive(p.tickets + done.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
+            } else {
+                const int grp = blockIdx.x / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
+                const int lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
+                // one item may come into a group from its left, and one may begin in it and leave it
+                if (arrive(p.group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1)) {
+                    join(hi - lo + 1, lo == c0 ? slot_c0 : 2 * lo, 2 * lo, 2, false);
+                    if (arrive(p.tickets + done.item, g1 - g0 + 1))
+                        join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
                 }
             }
         }
@@ -843,19 +907,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) q8kv_attend_kernel(const Atten
 }
 
 // The variants of one type; 32 rows of a dim above 128 do not fit the registers.
-template <typename T, int QP, int PP, int NT>
+template <typename T, int QP, int PP, int NT, int HW>
 AttendVariant attend_variant_of(int dim) {
-    if (dim <= 64) return {q8kv_attend_kernel<T, 64, NT, QP, PP>, Smem<64, NT, QP>::kTotal};
-    if (dim <= 128) return {q8kv_attend_kernel<T, 128, NT, QP, PP>, Smem<128, NT, QP>::kTotal};
-    if constexpr (NT <= 2) return {q8kv_attend_kernel<T, 256, NT, QP, PP>, Smem<256, NT, QP>::kTotal};
+    if (dim <= 64) return {q8kv_attend_kernel<T, 64, NT, QP, PP, HW>, Smem<64, NT, QP, HW>::kTotal};
+    if (dim <= 128) return {q8kv_attend_kernel<T, 128, NT, QP, PP, HW>, Smem<128, NT, QP, HW>::kTotal};
+    if constexpr (NT <= 2) return {q8kv_attend_kernel<T, 256, NT, QP, PP, HW>, Smem<256, NT, QP, HW>::kTotal};
     return {};
 }
 
 template <typename T, int QP, int PP>
-AttendVariant attend_variant_of(int dim, int row_tiles) {
-    if (row_tiles == 1) return attend_variant_of<T, QP, PP, 1>(dim);
-    if (row_tiles == 2 || dim > 128) return attend_variant_of<T, QP, PP, 2>(dim);
-    return attend_variant_of<T, QP, PP, 4>(dim);
+AttendVariant attend_variant_of(int dim, AttendShape shape) {
+    switch (shape) {
+        case kRows8: return attend_variant_of<T, QP, PP, 1, 1>(dim);
+        case kRows16: return attend_variant_of<T, QP, PP, 2, 1>(dim);
+        case kRows32: return attend_variant_of<T, QP, PP, 4, 1>(dim);
+        default: return attend_variant_of<T, QP, PP, 1, kWarps>(dim);
+    }
 }
 
 }  // namespace kv

@@ -6,13 +6,13 @@
 
 namespace kv {
 
-constexpr int kRowTiles[] = {1, 2, 4};  // variants: an item has 8, 16 or 32 query rows (node, head of the group)
 constexpr int kWarps = 4;        // warps of a CTA, each with its own keys
 constexpr int kStepKeys = 32;    // keys a warp takes at a time
-constexpr int kTileKeys = kWarps * kStepKeys;
 constexpr int kStages = 2;       // steps in flight per warp
 constexpr int kPartExtra = 4;    // of a partial row: its maximum and sum, and 16-byte alignment
-constexpr int kItemUnits = 2;    // an item's fixed cost (start of its keys, q, join) in tiles
+constexpr int kJoinGroup = 8;    // parts of a cut item that one CTA joins at once
+constexpr int kItemUnits = 3;    // an item's fixed cost (start of its keys, q, join) in tiles: of 0, 1, 2, 3, 4, 6 the best
+                                 // for 32 requests of 180 .. 8100 tokens (84.4, 72.4, 67.5, 67.3, 67.6, 70.3 us)
 
 struct AttendParams {
     Cache c;
@@ -34,16 +34,22 @@ struct AttendParams {
     float *partial;     // 2 per CTA: [rows of an item][dim + kPartExtra]
     unsigned *tickets;  // one per item
     int tickets_n;
+    unsigned *group_tickets;  // two per kJoinGroup CTAs
 };
 
-// One variant of the kernel: dim up to 64, 128 or 256, and row tiles.  The parts
-// of q and of the weights go by the type (see q8kv.h), a translation unit each.
+// What an item is: 8, 16 or 32 query rows (node, head of the group) of one kv head
+// whose keys the warps share, or 8 rows of four kv heads, one for each warp.
+enum AttendShape { kRows8 = 0, kRows16, kRows32, kHeads4, kAttendShapes };
+
+// One variant of the kernel: dim up to 64, 128 or 256, and a shape (kRows32: dim up
+// to 128).  The parts of q and of the weights go by the type (see q8kv.h), a
+// translation unit each.
 struct AttendVariant {
     void (*fn)(AttendParams) = nullptr;
     int smem = 0;
 };
-AttendVariant attend_variant_f32(int dim, int row_tiles);
-AttendVariant attend_variant_f16(int dim, int row_tiles);
-AttendVariant attend_variant_bf16(int dim, int row_tiles);
+AttendVariant attend_variant_f32(int dim, AttendShape shape);
+AttendVariant attend_variant_f16(int dim, AttendShape shape);
+AttendVariant attend_variant_bf16(int dim, AttendShape shape);
 
 }  // namespace kv

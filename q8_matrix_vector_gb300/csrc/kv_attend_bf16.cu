@@ -3,6 +3,6 @@
 
 namespace kv {
 
-AttendVariant attend_variant_bf16(int dim, int row_tiles) { return attend_variant_of<__nv_bfloat16, 1, 1>(dim, row_tiles); }
+AttendVariant attend_variant_bf16(int dim, AttendShape shape) { return attend_variant_of<__nv_bfloat16, 1, 1>(dim, shape); }
 
 }  // namespace kv

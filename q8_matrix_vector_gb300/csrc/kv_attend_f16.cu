@@ -3,6 +3,6 @@
 
 namespace kv {
 
-AttendVariant attend_variant_f16(int dim, int row_tiles) { return attend_variant_of<__half, 1, 2>(dim, row_tiles); }
+AttendVariant attend_variant_f16(int dim, AttendShape shape) { return attend_variant_of<__half, 1, 2>(dim, shape); }
 
 }  // namespace kv

@@ -104,6 +104,30 @@ def test_pages_that_end_inside_a_tile(q8mv, page):
     Case(q8mv, page, [257, 90], [6, 6], dim=64, page=page, dtype="bfloat16").check()
 
 
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("dim", [48, 64, 112, 128, 256])
+@pytest.mark.parametrize("heads,group,nodes", [(4, 2, [1, 3, 0, 2]), (8, 1, [5, 1, 1, 8]), (4, 8, [1, 1, 1, 1])])
+def test_heads_side_by_side(q8mv, dtype, dim, heads, group, nodes):
+    """A token's heads next to each other, eight query rows at most."""
+    Case(q8mv, dim, [0, 35, 64, 500], nodes, heads=heads, group=group, dim=dim, dtype=dtype, layout="token", page=9).check()
+
+
+def test_heads_side_by_side_in_a_long_table(q8mv):
+    """Tables that reach far, of which little is used: the shape for long sequences at short lengths."""
+    for dim, dtype, heads, group, nodes in ((64, "float32", 4, 2, [1, 3, 0, 2]), (128, "bfloat16", 8, 1, [5, 1, 1, 8]),
+                                            (80, "float16", 4, 8, [1, 1, 1, 1]), (256, "float32", 4, 1, [2, 2, 8, 1]),
+                                            (128, "float32", 12, 1, [1, 4, 6, 2])):
+        c = Case(q8mv, dim, [0, 35, 64, 3000], nodes, heads=heads, group=group, dim=dim, dtype=dtype, layout="token", page=9,
+                 cols=80000)
+        c.check()
+
+
+def test_heads_side_by_side_cut_between_ctas(q8mv):
+    Case(q8mv, 7, [20001], [1], heads=4, group=2, dim=64, page=64, tree=False, layout="token").check()
+    Case(q8mv, 8, [9000, 20011, 1, 5, 3000], [2, 1, 1, 2, 1], heads=8, group=4, dim=128, page=32, dtype="bfloat16",
+         layout="token", cols=9000).check()
+
+
 def test_items_cut_between_ctas(q8mv):
     """Few heads, long sequences: many CTAs share an item, and a CTA has two parts."""
     Case(q8mv, 1, [40001], [1], heads=1, group=2, dim=64, page=64, tree=False).check()
