@@ -5,14 +5,24 @@
 // one prefix search.  Everything that is summed is a 64-bit whole number, so the
 // split over threads and CTAs cannot change a result.
 //
-// One cluster of 8 CTAs walks one request and only reads the rows that the walk
-// visits: a tree of many nodes costs its accepted path, not its size.  A CTA owns
-// a contiguous eighth of the vocabulary and each of its 16 warps a contiguous part
-// of that, so the search at the end goes cluster -> CTA -> warp -> 128 tokens.  A
-// lane keeps its first 32 logits of the row in registers between the maximum and
-// the sum (all of a 131072-token vocabulary), so a row is read once.  Maxima and
-// sums cross the cluster through distributed shared memory; every CTA runs the
-// children's tests itself, on the same numbers, and reaches the same verdict.
+// One cluster of up to 16 CTAs walks one request and only reads the rows that the
+// walk visits: a tree of many nodes costs its accepted path, not its size.  What
+// bounds it is the longest path of the batch, a chain of rows each with a load, two
+// exchanges and the tests; so a row is spread over 128 warps, and the CTAs are small
+// (256 threads, 32 KB) so that the clusters of 30 and more requests are resident
+// together and those that go on get the SMs of those that have ended.  A CTA owns a
+// contiguous part of the vocabulary and each of its 8 warps a contiguous part of
+// that, so the search at the end goes cluster -> CTA -> warp -> 128 tokens.  A lane
+// keeps the row's first logits in shared memory between the maximum and the sum
+// (all of a 131072-token vocabulary), so a row is read once.  Maxima and sums cross
+// the cluster through distributed shared memory; every CTA runs the children's
+// tests itself, on the same numbers, and reaches the same verdict.
+//
+// A 64-bit conversion per logit runs at the few-per-cycle rate of the FP64 pipe
+// (4 us for an eighth of a 128256-token row).  The weight is split by two f32
+// fused multiply-adds rounded toward zero instead: e 2^20 + 2^23 has the upper 20
+// bits in its mantissa, the remainder gives the lower 20 the same way, and lanes
+// add both as 32-bit numbers.
 #include "kv_common.cuh"
 
 #include <cooperative_groups.h>
@@ -25,10 +35,10 @@ namespace kv {
 
 namespace {
 
-constexpr int kCluster = 8;
-constexpr int kVerifyWarps = 16;
-constexpr int kHeld = 8;                   // groups of 4 logits a lane holds
-constexpr float kOne = 1099511627776.0f;   // 2^40, the weight of a row's largest logit
+constexpr int kMaxCluster = 16;
+constexpr int kNodes = 256;                // of a request, that fit the shared copy
+constexpr int kVerifyWarps = 8;
+constexpr int kHeld = 1024;                // logits of a warp's part that are kept
 
 struct VerifyParams {
     const void *logits;
@@ -39,6 +49,7 @@ struct VerifyParams {
     int32_t *path, *count, *next;
     int64_t logits_row, draft_row, rows;
     int requests, vocab, seg;  // seg: tokens of a warp, a multiple of 4
+    int cluster;               // CTAs of a request
     int vec;                   // four logits (and draft probabilities) may be loaded at once
 };
 
@@ -72,7 +83,20 @@ __device__ __forceinline__ float share(const Row &r, float z, int i) {
     return z == r.top ? 1.0f : expf(z - r.top);
 }
 
-__device__ __forceinline__ int64_t weight(float e) { return __float2ll_rz(e * kOne); }
+// Whole-number weight trunc(2^40 e), 0 <= e <= 1, as 2^20 hi + lo.
+struct Weight {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Weight split_weight(float e) {
+    const float y = __fmaf_rz(e, 1048576.0f, 8388608.0f);
+    const float r = __fmaf_rn(e, 1048576.0f, 8388608.0f - y);  // exact, in [0, 1)
+    const float x = __fmaf_rz(r, 1048576.0f, 8388608.0f);
+    return {__float_as_uint(y) - 0x4B000000u, __float_as_uint(x) - 0x4B000000u};
+}
+__device__ __forceinline__ int64_t weight(float e) {
+    const Weight w = split_weight(e);
+    return (static_cast<int64_t>(w.hi) << 20) + w.lo;
+}
 
 __device__ __forceinline__ float residual(const Row &r, float e, float q) {
     return fmaxf(__fsub_rn(__fmul_rn(e, r.per), __fmul_rn(r.less, q)), 0.0f);
@@ -106,19 +130,21 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 }
 
 template <typename T, bool DRAFTS>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps * 32, 1)
-    q8kv_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const VerifyParams p) {
     cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ float4 held[];           // [warp][kHeld / 128][lane]
     __shared__ uint64_t x_max[2];
     __shared__ int64_t x_sum[2];
     __shared__ uint64_t warp_max[kVerifyWarps];
     __shared__ int64_t warp_w[kVerifyWarps];   // sums of the warps' weights as they stand
-    __shared__ int64_t cta_w[kCluster];        // and of all CTAs'
+    __shared__ int64_t cta_w[kMaxCluster];     // and of all CTAs'
+    __shared__ int32_t s_tokens[kNodes], s_parents[kNodes];
+    __shared__ float s_uniforms[kNodes];
     __shared__ int verdict, child;             // of the last test
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster.block_rank());
-    const int b = blockIdx.x / kCluster;
+    const int ctas = p.cluster, b = blockIdx.x / ctas;
     int64_t row0, row1;
     if (p.starts) {
         row0 = min(max(static_cast<int64_t>(p.starts[b]), static_cast<int64_t>(0)), p.rows);
@@ -138,6 +164,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
     const int32_t *tokens = p.tokens + row0, *parents = p.parents + row0;
     const float *uniforms = p.uniforms + row0;
     int32_t *path = p.path + row0;
+    if (nodes <= kNodes) {
+        for (int i = tid; i < nodes; i += kVerifyWarps * 32) {
+            s_tokens[i] = tokens[i];
+            s_parents[i] = parents[i];
+            s_uniforms[i] = uniforms[i];
+        }
+        tokens = s_tokens;
+        parents = s_parents;
+        uniforms = s_uniforms;
+    }
     if (rank == 0)
         for (int i = tid; i < nodes; i += blockDim.x) path[i] = i == 0 ? 0 : -1;
 
@@ -148,7 +184,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
     const int seg = p.seg, chunk = seg * kVerifyWarps;
     const int64_t lo64 = static_cast<int64_t>(rank) * chunk + static_cast<int64_t>(warp) * seg;
     const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(p.vocab)));
-    const int hi = static_cast<int>(min(lo64 + seg, static_cast<int64_t>(p.vocab)));
+    const int hi_end = static_cast<int>(min(lo64 + seg, static_cast<int64_t>(p.vocab)));
 
     int parity = 0;
     // sums the lanes' numbers: warp_w, cta_w, and the total
@@ -163,11 +199,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
             x_sum[parity] = s;
         }
         cluster.sync();
-        if (tid < kCluster) cta_w[tid] = *cluster.map_shared_rank(&x_sum[parity], tid);
+        if (tid < ctas) cta_w[tid] = *cluster.map_shared_rank(&x_sum[parity], tid);
         __syncthreads();
         int64_t s = 0;
-#pragma unroll
-        for (int i = 0; i < kCluster; ++i) s += cta_w[i];
+        for (int i = 0; i < ctas; ++i) s += cta_w[i];
         parity ^= 1;
         return s;
     };
@@ -179,33 +214,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
         const T *l = static_cast<const T *>(p.logits) + (row0 + cur) * p.logits_row;
         const float *q = DRAFTS ? p.draft + (row0 + cur) * p.draft_row : nullptr;
         // ---- the row's maximum
-        float z[kHeld][4];
         float top = -INFINITY;
         int best = lo;
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) load4(l, lo + k * 128 + lane * 4, hi, p.vec, z[k], -INFINITY);
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                z[k][j] = scaled(z[k][j], r.inv);
-                if (z[k][j] > top) {
-                    top = z[k][j];
-                    best = lo + k * 128 + lane * 4 + j;
-                }
-            }
-        for (int i = lo + kHeld * 128 + lane * 4; i < hi; i += 128) {
+        float4 *mine = held + warp * (kHeld / 4) + lane;
+        auto look = [&](int i) -> float4 {
             float x[4];
-            load4(l, i, hi, p.vec, x, -INFINITY);
+            load4(l, i, hi_end, p.vec, x, -INFINITY);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float y = scaled(x[j], r.inv);
-                if (y > top) {
-                    top = y;
+                x[j] = scaled(x[j], r.inv);
+                if (x[j] > top) {
+                    top = x[j];
                     best = i + j;
                 }
             }
-        }
+            return make_float4(x[0], x[1], x[2], x[3]);
+        };
+        const int held_end = min(hi_end, lo + kHeld);
+#pragma unroll 8
+        for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
+#pragma unroll 4
+        for (int i = lo + kHeld; i < hi_end; i += 128) look(i + lane * 4);
         uint64_t key = static_cast<uint64_t>(ordered(top)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(best));
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) key = max(key, static_cast<uint64_t>(__shfl_xor_sync(~0u, key, d)));
@@ -217,41 +246,43 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
             x_max[parity] = key;
         }
         cluster.sync();
-        key = 0;
+        key = lane < ctas ? *cluster.map_shared_rank(&x_max[parity], lane) : 0;
 #pragma unroll
-        for (int i = 0; i < kCluster; ++i) key = max(key, *cluster.map_shared_rank(&x_max[parity], i));
+        for (int d = 8; d > 0; d /= 2) key = max(key, static_cast<uint64_t>(__shfl_xor_sync(~0u, key, d)));
+        key = __shfl_sync(~0u, key, 0);
         parity ^= 1;
         r.top = unordered(static_cast<uint32_t>(key >> 32));
         r.best = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
         r.less = 0.0f;
 
-        // sum of the lane's weights (of the residual's once `rest`)
+        // sum of the lane's weights (of the residual's once `rest`): at most 2^11 logits a lane, so 32 bits a half
         auto sum = [&]() -> int64_t {
-            int64_t s = 0;
-#pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
-                const int i = lo + k * 128 + lane * 4;
-                if (i < hi) {
-                    float y[4];
-                    if (DRAFTS && rest) load4(q, i, hi, p.vec, y, 0.0f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float e = i + j < hi ? share(r, z[k][j], i + j) : 0.0f;
-                        s += weight(DRAFTS && rest && i + j < hi ? residual(r, e, y[j]) : e);
-                    }
-                }
-            }
-            for (int i = lo + kHeld * 128 + lane * 4; i < hi; i += 128) {
-                float x[4], y[4];
-                load4(l, i, hi, p.vec, x, -INFINITY);
-                if (DRAFTS && rest) load4(q, i, hi, p.vec, y, 0.0f);
+            uint32_t hi = 0, lo_bits = 0;
+            auto add = [&](const float (&x)[4], const float (&y)[4], int i) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = i + j < hi ? share(r, scaled(x[j], r.inv), i + j) : 0.0f;
-                    s += weight(DRAFTS && rest && i + j < hi ? residual(r, e, y[j]) : e);
+                    const float e = i + j < hi_end ? share(r, x[j], i + j) : 0.0f;
+                    const Weight w = split_weight(DRAFTS && rest && i + j < hi_end ? residual(r, e, y[j]) : e);
+                    hi += w.hi;
+                    lo_bits += w.lo;
                 }
+            };
+#pragma unroll 2
+            for (int i0 = lo; i0 < hi_end; i0 += 128) {
+                const int i = i0 + lane * 4;
+                float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (i0 < held_end) {
+                    const float4 v = mine[(i0 - lo) / 4];
+                    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+                } else {
+                    load4(l, i, hi_end, p.vec, x, -INFINITY);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
+                }
+                if (DRAFTS && rest) load4(q, i, hi_end, p.vec, y, 0.0f);
+                add(x, y, i);
             }
-            return s;
+            return (static_cast<int64_t>(hi) << 20) + lo_bits;
         };
         rest = false;
         total = exchange(sum());
@@ -337,15 +368,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
         // ---- the next token: the first whose prefix sum exceeds the target
         __syncthreads();
         total = 0;
-#pragma unroll
-        for (int i = 0; i < kCluster; ++i) total += cta_w[i];
+        for (int i = 0; i < ctas; ++i) total += cta_w[i];
         if (total == 0) {
             if (rank == 0 && tid == 0) p.next[b] = -1;
         } else {
             int64_t want = __double2ll_rz(static_cast<double>(uniforms[0]) * static_cast<double>(total));
             want = max(static_cast<int64_t>(0), min(want, total - 1));
             int owner = 0;
-            while (owner < kCluster - 1 && want >= cta_w[owner]) want -= cta_w[owner++];
+            while (owner < ctas - 1 && want >= cta_w[owner]) want -= cta_w[owner++];
             if (owner == rank) {
                 int ow = 0;
                 while (ow < kVerifyWarps - 1 && want >= warp_w[ow]) want -= warp_w[ow++];
@@ -353,12 +383,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
                     for (int i = lo + lane * 4;; i += 128) {  // ends: the warp's weights exceed `want`
                         float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         int64_t w[4];
-                        load4(l, i, hi, p.vec, x, -INFINITY);
-                        if (DRAFTS && rest) load4(q, i, hi, p.vec, y, 0.0f);
+                        load4(l, i, hi_end, p.vec, x, -INFINITY);
+                        if (DRAFTS && rest) load4(q, i, hi_end, p.vec, y, 0.0f);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float e = i + j < hi ? share(r, scaled(x[j], r.inv), i + j) : 0.0f;
-                            w[j] = weight(DRAFTS && rest && i + j < hi ? residual(r, e, y[j]) : e);
+                            const float e = i + j < hi_end ? share(r, scaled(x[j], r.inv), i + j) : 0.0f;
+                            w[j] = weight(DRAFTS && rest && i + j < hi_end ? residual(r, e, y[j]) : e);
                         }
                         if (!DRAFTS) {
                             // refused children have no weight
@@ -392,7 +422,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
                             break;
                         }
                         want -= __shfl_sync(~0u, upto, 31);
-                        if (i - lane * 4 + 128 >= hi) break;  // not reached: the sums are exact
+                        if (i - lane * 4 + 128 >= hi_end) break;  // not reached: the sums are exact
                     }
                 }
             }
@@ -405,12 +435,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerifyWarps 
 
 template <typename T>
 cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(p.requests) * kCluster;
-    if (p.draft)
-        q8kv_verify_kernel<T, true><<<grid, kVerifyWarps * 32, 0, stream>>>(p);
-    else
-        q8kv_verify_kernel<T, false><<<grid, kVerifyWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    auto *fn = p.draft ? q8kv_verify_kernel<T, true> : q8kv_verify_kernel<T, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.requests) * p.cluster);
+    cfg.blockDim = dim3(kVerifyWarps * 32);
+    cfg.dynamicSmemBytes = kVerifyWarps * kHeld * sizeof(float);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+// Clusters of 16 are beyond the size that every GPU takes: allowed per kernel, when a plan is made.
+template <typename T>
+cudaError_t allow_clusters() {
+    cudaError_t e = cudaFuncSetAttribute(q8kv_verify_kernel<T, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(q8kv_verify_kernel<T, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
 }
 
 }  // namespace
@@ -421,6 +467,7 @@ struct q8kv_verify_s {
     int device = 0;
     int max_requests = 0, vocab = 0;
     int64_t max_rows = 0;
+    int sms = 0;
 };
 
 extern "C" {
@@ -441,6 +488,14 @@ q8mv_status_t q8kv_verify_plan(q8kv_verify_plan_t *out, int32_t max_requests, in
     p->max_requests = max_requests;
     p->max_rows = max_rows;
     p->vocab = vocab;
+    cudaError_t e = cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device);
+    if (e == cudaSuccess) e = kv::allow_clusters<float>();
+    if (e == cudaSuccess) e = kv::allow_clusters<__half>();
+    if (e == cudaSuccess) e = kv::allow_clusters<__nv_bfloat16>();
+    if (e != cudaSuccess) {
+        delete p;
+        return q8i::cuda_status(e);
+    }
     *out = p;
     return Q8MV_OK;
 }
@@ -497,7 +552,9 @@ q8mv_status_t q8kv_verify(q8kv_verify_plan_t plan, const q8kv_verify_args_t *a, 
     p.rows = a->rows;
     p.requests = a->requests;
     p.vocab = a->vocab;
-    const int parts = kv::kCluster * kv::kVerifyWarps;
+    // 16 CTAs a request while four an SM hold them all, else 8
+    p.cluster = a->requests * 16 <= plan->sms * 4 ? 16 : 8;
+    const int parts = p.cluster * kv::kVerifyWarps;
     p.seg = static_cast<int>(kv::ceil_div(kv::ceil_div(a->vocab, parts), 4) * 4);
     p.vec = kv::aligned(a->logits, 4 * size) && a->logits_row % 4 == 0 && kv::aligned(a->draft_probs, 16) &&
             a->draft_row % 4 == 0;
