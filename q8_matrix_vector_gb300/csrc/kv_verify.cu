@@ -57,7 +57,7 @@ struct VerifyParams {
 struct Row {
     float inv;       // 1 / temperature
     float top;       // largest z
-    int best;        // its first index
+    int best;        // its first index, if greedy
     bool greedy;
     float per;       // f32(2^40 / W), drafts only
     float less;      // a
@@ -77,10 +77,11 @@ __device__ __forceinline__ float scaled(float l, float inv) {
     return z == z ? z : -INFINITY;
 }
 
+// e of logit i, for rows whose largest z is not -inf; no branches but the uniform one
 __device__ __forceinline__ float share(const Row &r, float z, int i) {
-    if (r.top == -INFINITY) return 0.0f;
     if (r.greedy) return i == r.best ? 1.0f : 0.0f;
-    return z == r.top ? 1.0f : expf(z - r.top);
+    const float e = expf(z - r.top);
+    return z == r.top ? 1.0f : e;  // inf - inf
 }
 
 // Whole-number weight trunc(2^40 e), 0 <= e <= 1, as 2^20 hi + lo.
@@ -133,9 +134,12 @@ template <typename T, bool DRAFTS>
 __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const VerifyParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ float4 held[];           // [warp][kHeld / 128][lane]
-    __shared__ uint64_t x_max[2];
-    __shared__ int64_t x_sum[2];
-    __shared__ uint64_t warp_max[kVerifyWarps];
+    // what the CTAs tell one another: each writes to its place in everybody's copy
+    __shared__ uint32_t x_max[2][kMaxCluster];
+    __shared__ int32_t x_best[2][kMaxCluster];
+    __shared__ int64_t x_sum[2][kMaxCluster];
+    __shared__ uint32_t warp_max[kVerifyWarps];
+    __shared__ int32_t warp_best[kVerifyWarps];
     __shared__ int64_t warp_w[kVerifyWarps];   // sums of the warps' weights as they stand
     __shared__ int64_t cta_w[kMaxCluster];     // and of all CTAs'
     __shared__ int32_t s_tokens[kNodes], s_parents[kNodes];
@@ -192,17 +196,17 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         mine = warp_sum(mine);
         if (lane == 0) warp_w[warp] = mine;
         __syncthreads();
-        if (tid == 0) {
+        if (tid < ctas) {
             int64_t s = 0;
 #pragma unroll
             for (int i = 0; i < kVerifyWarps; ++i) s += warp_w[i];
-            x_sum[parity] = s;
+            *cluster.map_shared_rank(&x_sum[parity][rank], tid) = s;
         }
         cluster.sync();
-        if (tid < ctas) cta_w[tid] = *cluster.map_shared_rank(&x_sum[parity], tid);
-        __syncthreads();
         int64_t s = 0;
-        for (int i = 0; i < ctas; ++i) s += cta_w[i];
+        for (int i = 0; i < ctas; ++i) s += x_sum[parity][i];
+        if (tid < ctas) cta_w[tid] = x_sum[parity][tid];
+        __syncthreads();
         parity ^= 1;
         return s;
     };
@@ -215,19 +219,13 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         const float *q = DRAFTS ? p.draft + (row0 + cur) * p.draft_row : nullptr;
         // ---- the row's maximum
         float top = -INFINITY;
-        int best = lo;
         float4 *mine = held + warp * (kHeld / 4) + lane;
         auto look = [&](int i) -> float4 {
             float x[4];
             load4(l, i, hi_end, p.vec, x, -INFINITY);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = scaled(x[j], r.inv);
-                if (x[j] > top) {
-                    top = x[j];
-                    best = i + j;
-                }
-            }
+            for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
+            top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
             return make_float4(x[0], x[1], x[2], x[3]);
         };
         const int held_end = min(hi_end, lo + kHeld);
@@ -235,39 +233,61 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
 #pragma unroll 4
         for (int i = lo + kHeld; i < hi_end; i += 128) look(i + lane * 4);
-        uint64_t key = static_cast<uint64_t>(ordered(top)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(best));
+        const uint32_t most = __reduce_max_sync(~0u, ordered(top));
+        if (lane == 0) warp_max[warp] = most;
+        if (r.greedy) {  // the first index of the warp's largest
+            int best = INT32_MAX;
+            for (int i = lo + lane * 4; i < hi_end && best == INT32_MAX; i += 128) {
+                float x[4];
+                load4(l, i, hi_end, p.vec, x, -INFINITY);
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) key = max(key, static_cast<uint64_t>(__shfl_xor_sync(~0u, key, d)));
-        if (lane == 0) warp_max[warp] = key;
+                for (int j = 3; j >= 0; --j)
+                    if (i + j < hi_end && ordered(scaled(x[j], r.inv)) == most) best = i + j;
+            }
+            best = __reduce_min_sync(~0u, best);
+            if (lane == 0) warp_best[warp] = best;
+        }
         __syncthreads();
-        if (tid == 0) {
+        if (tid < ctas) {
+            uint32_t m = warp_max[0];
+            int best = r.greedy ? warp_best[0] : 0;
 #pragma unroll
-            for (int i = 1; i < kVerifyWarps; ++i) key = max(key, warp_max[i]);
-            x_max[parity] = key;
+            for (int i = 1; i < kVerifyWarps; ++i) {
+                if (r.greedy && warp_max[i] > m) best = warp_best[i];
+                m = max(m, warp_max[i]);
+            }
+            *cluster.map_shared_rank(&x_max[parity][rank], tid) = m;
+            if (r.greedy) *cluster.map_shared_rank(&x_best[parity][rank], tid) = best;
         }
         cluster.sync();
-        key = lane < ctas ? *cluster.map_shared_rank(&x_max[parity], lane) : 0;
-#pragma unroll
-        for (int d = 8; d > 0; d /= 2) key = max(key, static_cast<uint64_t>(__shfl_xor_sync(~0u, key, d)));
-        key = __shfl_sync(~0u, key, 0);
+        {
+            uint32_t m = x_max[parity][0];
+            int best = r.greedy ? x_best[parity][0] : 0;
+            for (int i = 1; i < ctas; ++i) {
+                if (r.greedy && x_max[parity][i] > m) best = x_best[parity][i];
+                m = max(m, x_max[parity][i]);
+            }
+            r.top = unordered(m);
+            r.best = best;
+        }
         parity ^= 1;
-        r.top = unordered(static_cast<uint32_t>(key >> 32));
-        r.best = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
         r.less = 0.0f;
 
         // sum of the lane's weights (of the residual's once `rest`): at most 2^11 logits a lane, so 32 bits a half
         auto sum = [&]() -> int64_t {
+            if (r.top == -INFINITY) return 0;
             uint32_t hi = 0, lo_bits = 0;
             auto add = [&](const float (&x)[4], const float (&y)[4], int i) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = i + j < hi_end ? share(r, x[j], i + j) : 0.0f;
-                    const Weight w = split_weight(DRAFTS && rest && i + j < hi_end ? residual(r, e, y[j]) : e);
+                    // past the warp's end z is -inf and e 0; `best` may be there, in another warp's part
+                    const float e = share(r, x[j], i + j < hi_end ? i + j : -1);
+                    const Weight w = split_weight(DRAFTS && rest ? residual(r, e, y[j]) : e);
                     hi += w.hi;
                     lo_bits += w.lo;
                 }
             };
-#pragma unroll 2
+#pragma unroll 4
             for (int i0 = lo; i0 < hi_end; i0 += 128) {
                 const int i = i0 + lane * 4;
                 float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -297,35 +317,40 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             if (warp == 0) {
                 int said = 0, who = nodes;
                 for (int i0 = from; i0 < nodes && said == 0 && open && total > 0; i0 += 32) {
-                    const int mine = i0 + lane;
-                    const bool is_child = mine < nodes && parents[mine] == cur;
-                    uint32_t todo = __ballot_sync(~0u, is_child);
+                    // every lane looks up its node's token; then they are tested in order
+                    const int node = i0 + lane;
+                    const bool is_child = node < nodes && parents[node] == cur;
+                    const int tok = is_child ? tokens[node] : -1;
+                    const bool valid = tok >= 0 && tok < p.vocab;
+                    const float e = valid ? share(r, scaled(to_f32(l[tok]), r.inv), tok) : 0.0f;
+                    const float u = is_child ? uniforms[node] : 0.0f;
+                    const float qx = DRAFTS && valid ? q[tok] : 0.0f;
+                    int64_t wx = weight(e);
+                    if (!DRAFTS) {
+                        // a sibling before with the same token was refused when this one is tested: its weight is gone
+                        bool twin = (__match_any_sync(~0u, valid ? tok : -1 - lane) & ((1u << lane) - 1u)) != 0;
+                        for (int j = cur + 1; j < i0; ++j) twin |= parents[j] == cur && tokens[j] == tok;
+                        if (twin) wx = 0;
+                    }
+                    uint32_t todo = __ballot_sync(~0u, valid);  // an invalid token has no weight and was never drawn
                     while (todo != 0 && said == 0) {
-                        const int i = i0 + __ffs(todo) - 1;
+                        const int at = __ffs(todo) - 1;
                         todo &= todo - 1;
-                        const int x = tokens[i];
-                        const bool valid = x >= 0 && x < p.vocab;
-                        const float e = valid ? share(r, scaled(to_f32(l[x]), r.inv), x) : 0.0f;
+                        bool ok;
                         if constexpr (DRAFTS) {
-                            const float qx = valid ? q[x] : 0.0f;
-                            const float left = residual(r, e, qx);
-                            const bool ok = valid && __fmul_rn(__fmul_rn(uniforms[i], qx), norm) < left;
-                            who = i;
-                            said = ok ? 1 : valid ? 2 : 0;  // an invalid token was not drawn: nothing to take out
+                            ok = __fmul_rn(__fmul_rn(u, qx), norm) < residual(r, e, qx);
                         } else {
-                            // a sibling with the same token has been refused: its weight is gone
-                            bool twin = false;
-                            for (int j = cur + 1 + lane; j < i; j += 32) twin |= parents[j] == cur && tokens[j] == x;
-                            const int64_t wx = __any_sync(~0u, twin) ? 0 : weight(e);
-                            if (static_cast<double>(uniforms[i]) * static_cast<double>(total) < static_cast<double>(wx)) {
-                                who = i;
-                                said = 1;
-                            } else {
-                                total -= wx;
-                                if (valid && lane == 0) {
-                                    cta_w[x / chunk] -= wx;
-                                    if (x / chunk == rank) warp_w[x % chunk / seg] -= wx;
-                                }
+                            ok = static_cast<double>(u) * static_cast<double>(total) < static_cast<double>(wx);
+                        }
+                        ok = __shfl_sync(~0u, ok, at);
+                        if (ok || DRAFTS) {
+                            who = i0 + at;
+                            said = ok ? 1 : 2;
+                        } else {
+                            total -= __shfl_sync(~0u, wx, at);
+                            if (lane == at) {
+                                cta_w[tok / chunk] -= wx;
+                                if (tok / chunk == rank) warp_w[tok % chunk / seg] -= wx;
                             }
                         }
                     }
@@ -387,8 +412,8 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                         if (DRAFTS && rest) load4(q, i, hi_end, p.vec, y, 0.0f);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float e = i + j < hi_end ? share(r, scaled(x[j], r.inv), i + j) : 0.0f;
-                            w[j] = weight(DRAFTS && rest && i + j < hi_end ? residual(r, e, y[j]) : e);
+                            const float e = share(r, scaled(x[j], r.inv), i + j < hi_end ? i + j : -1);
+                            w[j] = weight(DRAFTS && rest ? residual(r, e, y[j]) : e);
                         }
                         if (!DRAFTS) {
                             // refused children have no weight
