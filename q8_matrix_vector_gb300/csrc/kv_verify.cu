@@ -77,11 +77,15 @@ __device__ __forceinline__ float scaled(float l, float inv) {
     return z == z ? z : -INFINITY;
 }
 
-// e of logit i, for rows whose largest z is not -inf; no branches but the uniform one
-__device__ __forceinline__ float share(const Row &r, float z, int i) {
-    if (r.greedy) return i == r.best ? 1.0f : 0.0f;
+// e of a logit, not greedy, of a row whose largest z is not -inf
+__device__ __forceinline__ float soft(const Row &r, float z) {
     const float e = expf(z - r.top);
     return z == r.top ? 1.0f : e;  // inf - inf
+}
+
+// the same for logit i of any such row
+__device__ __forceinline__ float share(const Row &r, float z, int i) {
+    return r.greedy ? (i == r.best ? 1.0f : 0.0f) : soft(r, z);
 }
 
 // Whole-number weight trunc(2^40 e), 0 <= e <= 1, as 2^20 hi + lo.
@@ -178,6 +182,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         parents = s_parents;
         uniforms = s_uniforms;
     }
+    __syncthreads();
     if (rank == 0)
         for (int i = tid; i < nodes; i += blockDim.x) path[i] = i == 0 ? 0 : -1;
 
@@ -203,12 +208,11 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             *cluster.map_shared_rank(&x_sum[parity][rank], tid) = s;
         }
         cluster.sync();
-        int64_t s = 0;
-        for (int i = 0; i < ctas; ++i) s += x_sum[parity][i];
-        if (tid < ctas) cta_w[tid] = x_sum[parity][tid];
+        const int64_t s = lane < ctas ? x_sum[parity][lane] : 0;
+        if (tid < ctas) cta_w[tid] = s;
         __syncthreads();
         parity ^= 1;
-        return s;
+        return warp_sum(s);
     };
 
     int cur = 0, count = 0;
@@ -217,6 +221,20 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
     for (;;) {
         const T *l = static_cast<const T *>(p.logits) + (row0 + cur) * p.logits_row;
         const float *q = DRAFTS ? p.draft + (row0 + cur) * p.draft_row : nullptr;
+        // warp 0 looks up the first nodes after this one: those that are children, and their tokens' logits
+        int child_tok = -1;
+        float child_l = 0.0f, child_q = 0.0f, child_u = 0.0f;
+        if (warp == 0) {
+            const int node = cur + 1 + lane;
+            const bool is_child = node < nodes && parents[node] == cur;
+            const int tok = is_child ? tokens[node] : -1;
+            if (tok >= 0 && tok < p.vocab) {
+                child_tok = tok;
+                child_l = to_f32(l[tok]);
+                child_u = uniforms[node];
+                if (DRAFTS) child_q = q[tok];
+            }
+        }
         // ---- the row's maximum
         float top = -INFINITY;
         float4 *mine = held + warp * (kHeld / 4) + lane;
@@ -233,6 +251,17 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
 #pragma unroll 4
         for (int i = lo + kHeld; i < hi_end; i += 128) look(i + lane * 4);
+        {
+            // L2 starts on the row of the first child, the likeliest to be next: on a path of n rows the others'
+            // loads then take an L2 round trip each
+            const int node = cur + 1 + lane;
+            const uint32_t kids = __ballot_sync(~0u, node < nodes && parents[node] == cur);
+            if (kids != 0) {
+                const T *next = static_cast<const T *>(p.logits) + (row0 + cur + __ffs(kids)) * p.logits_row;
+                for (int i = lo + lane * static_cast<int>(128 / sizeof(T)); i < held_end; i += 32 * static_cast<int>(128 / sizeof(T)))
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
+            }
+        }
         const uint32_t most = __reduce_max_sync(~0u, ordered(top));
         if (lane == 0) warp_max[warp] = most;
         if (r.greedy) {  // the first index of the warp's largest
@@ -261,14 +290,10 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         }
         cluster.sync();
         {
-            uint32_t m = x_max[parity][0];
-            int best = r.greedy ? x_best[parity][0] : 0;
-            for (int i = 1; i < ctas; ++i) {
-                if (r.greedy && x_max[parity][i] > m) best = x_best[parity][i];
-                m = max(m, x_max[parity][i]);
-            }
+            const uint32_t mine_max = lane < ctas ? x_max[parity][lane] : 0, m = __reduce_max_sync(~0u, mine_max);
             r.top = unordered(m);
-            r.best = best;
+            r.best = 0;
+            if (r.greedy) r.best = __reduce_min_sync(~0u, mine_max == m ? x_best[parity][lane & (kMaxCluster - 1)] : INT32_MAX);
         }
         parity ^= 1;
         r.less = 0.0f;
@@ -276,12 +301,15 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         // sum of the lane's weights (of the residual's once `rest`): at most 2^11 logits a lane, so 32 bits a half
         auto sum = [&]() -> int64_t {
             if (r.top == -INFINITY) return 0;
+            if (r.greedy) {  // one logit has all the weight
+                if (lane != 0 || r.best < lo || r.best >= hi_end) return 0;
+                return weight(DRAFTS && rest ? residual(r, 1.0f, q[r.best]) : 1.0f);
+            }
             uint32_t hi = 0, lo_bits = 0;
-            auto add = [&](const float (&x)[4], const float (&y)[4], int i) {
+            auto add = [&](const float (&x)[4], const float (&y)[4]) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    // past the warp's end z is -inf and e 0; `best` may be there, in another warp's part
-                    const float e = share(r, x[j], i + j < hi_end ? i + j : -1);
+                    const float e = soft(r, x[j]);  // 0 past the warp's end, where z is -inf
                     const Weight w = split_weight(DRAFTS && rest ? residual(r, e, y[j]) : e);
                     hi += w.hi;
                     lo_bits += w.lo;
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                     for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
                 }
                 if (DRAFTS && rest) load4(q, i, hi_end, p.vec, y, 0.0f);
-                add(x, y, i);
+                add(x, y);
             }
             return (static_cast<int64_t>(hi) << 20) + lo_bits;
         };
@@ -318,13 +346,18 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                 int said = 0, who = nodes;
                 for (int i0 = from; i0 < nodes && said == 0 && open && total > 0; i0 += 32) {
                     // every lane looks up its node's token; then they are tested in order
-                    const int node = i0 + lane;
-                    const bool is_child = node < nodes && parents[node] == cur;
-                    const int tok = is_child ? tokens[node] : -1;
-                    const bool valid = tok >= 0 && tok < p.vocab;
-                    const float e = valid ? share(r, scaled(to_f32(l[tok]), r.inv), tok) : 0.0f;
-                    const float u = is_child ? uniforms[node] : 0.0f;
-                    const float qx = DRAFTS && valid ? q[tok] : 0.0f;
+                    int tok = child_tok;
+                    float lx = child_l, qx = child_q, u = child_u;
+                    if (i0 != cur + 1) {
+                        const int node = i0 + lane;
+                        tok = node < nodes && parents[node] == cur ? tokens[node] : -1;
+                        if (tok < 0 || tok >= p.vocab) tok = -1;
+                        lx = tok >= 0 ? to_f32(l[tok]) : 0.0f;
+                        u = tok >= 0 ? uniforms[node] : 0.0f;
+                        qx = DRAFTS && tok >= 0 ? q[tok] : 0.0f;
+                    }
+                    const bool valid = tok >= 0;
+                    const float e = valid ? share(r, scaled(lx, r.inv), tok) : 0.0f;
                     int64_t wx = weight(e);
                     if (!DRAFTS) {
                         // a sibling before with the same token was refused when this one is tested: its weight is gone
