@@ -13,6 +13,12 @@ namespace kv {
 
 namespace {
 
+constexpr int kManyBlocks = 152 * 4;
+// Tokens a lane takes of a large call, for loads in flight.  8190 tokens of 32 heads x 128 bf16 written: 54.3,
+// 51.4, 73.6 us with 1, 2, 4 (the raw inputs of 4 leave too few warps); 32768 tokens of 8 heads read: 40.1, 39.3
+// with 1, 4.
+constexpr int kWriteTokens = 2, kReadTokens = 4;
+
 struct IoParams {
     Cache c;
     const void *in[2];   // k, v (write)
@@ -38,121 +44,174 @@ __device__ __forceinline__ bool place_of(const Cache &c, int64_t slot, int64_t *
     return true;
 }
 
+// 16 bytes of T as they are in memory
+template <typename T>
+union Piece {
+    uint4 v;
+    T t[16 / sizeof(T)];
+};
+
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_elems(const T *p, float (&x)[16 / sizeof(T)]) {
-    constexpr int E = 16 / sizeof(T);
+__device__ __forceinline__ uint4 load_piece(const T *p) {
+    Piece<T> x;
     if constexpr (VEC) {
-        union {
-            uint4 u;
-            T t[E];
-        } v;
-        v.u = __ldg(reinterpret_cast<const uint4 *>(p));
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = to_f32(v.t[i]);
+        x.v = __ldg(reinterpret_cast<const uint4 *>(p));
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = to_f32(p[i]);
+        for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) x.t[i] = p[i];
     }
+    return x.v;
 }
 
+// Four codes rint(x * id).  Usually x * id is within +-127.5 and the sum with
+// 1.5 * 2^23 leaves it, rounded to even, in the low byte; a conversion would run at
+// an eighth of that rate.
 __device__ __forceinline__ uint32_t pack4(const float *x, float id) {
-    uint32_t w = 0;
+    constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+    uint32_t c[4];
 #pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], id), kRound));
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
+}
+
+// The same for blocks with NaN (0), infinities or an overflowing 127 / amax.
+__device__ __noinline__ uint32_t pack4_any(float x0, float x1, float x2, float x3, float id) {
+    const float x[4] = {x0, x1, x2, x3};
+    uint32_t w = 0;
     for (int i = 0; i < 4; ++i) {
-        // NaN becomes 0; the clamp only acts where 127 / amax overflows (amax < 4e-37)
-        const int c = max(-127, min(127, __float2int_rn(__fmul_rn(x[i], id))));
+        const int c = max(-127, min(127, __float2int_rn(__fmul_rn(x[i], id))));  // NaN becomes 0
         w |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * i);
     }
     return w;
 }
 
 // d = amax / 127, c = rint(x * (127 / amax)): the recipe of q8mv_quantize_rows.
-template <typename T, bool VEC>
+// U tokens a lane: their loads, which do not wait for the slots, are all in flight.
+template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(256) q8kv_write_kernel(const IoParams p) {
     constexpr int E = 16 / sizeof(T), PER = 32 / E;  // elements a lane, lanes a block
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.y * U) + threadIdx.y;
     const int at = blockIdx.y * blockDim.x + threadIdx.x;
-    int64_t page = 0;
-    int place = 0;
     // whole groups of PER lanes share (token, head, block), so they leave together
-    if (i >= p.n || at >= p.lanes || !place_of(p.c, p.slots[i], &page, &place)) return;
+    if (at >= p.lanes) return;
     const unsigned group = ((1u << PER) - 1u) << ((threadIdx.y * blockDim.x + threadIdx.x) & 31 & ~(PER - 1));
     const int per_head = p.c.blocks * PER;
     const int h = at / per_head, in_row = at - h * per_head, e0 = in_row * E, b = in_row / PER;
     const bool live = e0 < p.c.dim;
-    const int64_t r = row_of(p.c, page, h, place);
-    float x[2][E];
+    uint4 raw[U][2];
+    int64_t slot[U];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const T *src = static_cast<const T *>(p.in[s]) + i * p.row[s] + h * p.head[s] + e0;
-        if (live) {
-            load_elems<T, VEC>(src, x[s]);
-        } else {
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * blockDim.y;
+        slot[u] = i < p.n ? __ldg(p.slots + i) : -1;
 #pragma unroll
-            for (int j = 0; j < E; ++j) x[s][j] = 0.0f;
+        for (int s = 0; s < 2; ++s) {
+            const T *src = static_cast<const T *>(p.in[s]) + i * p.row[s] + h * p.head[s] + e0;
+            raw[u][s] = live && i < p.n ? load_piece<T, VEC>(src) : make_uint4(0, 0, 0, 0);
         }
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        float amax = 0.0f;
+    for (int u = 0; u < U; ++u) {
+        int64_t page;
+        int place;
+        const bool there = place_of(p.c, slot[u], &page, &place);
+        const int64_t r = there ? row_of(p.c, page, h, place) : 0;
+        float x[2][E], amax[2];
+        bool nan[2];
 #pragma unroll
-        for (int j = 0; j < E; ++j) amax = fmaxf(amax, fabsf(x[s][j]));
+        for (int s = 0; s < 2; ++s) {
+            Piece<T> piece;
+            piece.v = raw[u][s];
+            amax[s] = 0.0f;
+            nan[s] = false;
 #pragma unroll
-        for (int d = 1; d < PER; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(group, amax, d));
-        const float id = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
-        int8_t *codes = (s == 0 ? p.c.k_codes : p.c.v_codes) + r * p.c.dim + e0;
-        float *scales = (s == 0 ? p.c.k_scales : p.c.v_scales) + r * p.c.blocks + b;
-        if (live) {
-            if constexpr (E == 8)
-                *reinterpret_cast<uint2 *>(codes) = make_uint2(pack4(x[s], id), pack4(x[s] + 4, id));
-            else
-                *reinterpret_cast<uint32_t *>(codes) = pack4(x[s], id);
+            for (int j = 0; j < E; ++j) {
+                x[s][j] = to_f32(piece.t[j]);
+                amax[s] = fmaxf(amax[s], fabsf(x[s][j]));
+                nan[s] |= x[s][j] != x[s][j];
+            }
+#pragma unroll
+            for (int d = 1; d < PER; d *= 2) amax[s] = fmaxf(amax[s], __shfl_xor_sync(group, amax[s], d));
         }
-        if ((in_row & (PER - 1)) == 0) *scales = __fdiv_rn(amax, 127.0f);
+        // the block's four divisions, one in each of its first four lanes: 127 / amax and amax / 127 of k, then of v
+        const int lane = threadIdx.x & 31, of = lane & (PER - 1), first_lane = lane - of;
+        const float a = of & 2 ? amax[1] : amax[0], num = of & 1 ? a : 127.0f, den = of & 1 ? 127.0f : a;
+        const float ratio = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
+        const float id[2] = {__shfl_sync(group, ratio, first_lane), __shfl_sync(group, ratio, first_lane + 2)};
+        if (there) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                int8_t *codes = (s == 0 ? p.c.k_codes : p.c.v_codes) + r * p.c.dim + e0;
+                if (live) {
+                    uint32_t w[E / 4];
+                    if (!nan[s] && amax[s] < INFINITY && id[s] < INFINITY) {
+#pragma unroll
+                        for (int j = 0; j < E / 4; ++j) w[j] = pack4(x[s] + 4 * j, id[s]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < E / 4; ++j)
+                            w[j] = pack4_any(x[s][4 * j], x[s][4 * j + 1], x[s][4 * j + 2], x[s][4 * j + 3], id[s]);
+                    }
+                    if constexpr (E == 8)
+                        *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(codes) = w[0];
+                }
+            }
+            if (of == 1) (p.c.k_scales + r * p.c.blocks)[b] = ratio;
+            if (of == 3) (p.c.v_scales + r * p.c.blocks)[b] = ratio;
+        }
     }
 }
 
-template <typename T>
+template <typename T, int U>
 __global__ void __launch_bounds__(256) q8kv_read_kernel(const IoParams p) {
     constexpr int E = 16 / sizeof(T);
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.y * U) + threadIdx.y;
     const int at = blockIdx.y * blockDim.x + threadIdx.x;
-    if (i >= p.n || at >= p.lanes) return;
+    if (at >= p.lanes) return;
     const int per_head = p.c.dim / E;
     const int h = at / per_head, e0 = (at - h * per_head) * E, b = e0 / 32;
-    int64_t page = 0;
-    int place = 0;
-    const bool live = place_of(p.c, p.slots[i], &page, &place);
-    uint32_t w[2][E / 4] = {};
-    float d[2] = {};
-    if (live) {
-        const int64_t r = row_of(p.c, page, h, place);
+    int64_t slot[U];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int8_t *codes = (s == 0 ? p.c.k_codes : p.c.v_codes) + r * p.c.dim + e0;
-            if constexpr (E == 8) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(codes);
-                w[s][0] = u.x;
-                w[s][1] = u.y;
-            } else {
-                w[s][0] = *reinterpret_cast<const uint32_t *>(codes);
+    for (int u = 0; u < U; ++u) slot[u] = first + u * blockDim.y < p.n ? __ldg(p.slots + first + u * blockDim.y) : -1;
+    uint32_t w[U][2][E / 4] = {};
+    float d[U][2] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        int64_t page;
+        int place;
+        if (place_of(p.c, slot[u], &page, &place)) {
+            const int64_t r = row_of(p.c, page, h, place);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int8_t *codes = (s == 0 ? p.c.k_codes : p.c.v_codes) + r * p.c.dim + e0;
+                if constexpr (E == 8) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(codes);
+                    w[u][s][0] = v.x;
+                    w[u][s][1] = v.y;
+                } else {
+                    w[u][s][0] = *reinterpret_cast<const uint32_t *>(codes);
+                }
+                d[u][s] = ((s == 0 ? p.c.k_scales : p.c.v_scales) + r * p.c.blocks)[b];
             }
-            d[s] = ((s == 0 ? p.c.k_scales : p.c.v_scales) + r * p.c.blocks)[b];
         }
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        union {
-            uint4 u;
-            T t[E];
-        } v;
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * blockDim.y;
+        if (i >= p.n) break;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int c = static_cast<int8_t>(w[s][j / 4] >> (8 * (j % 4)));
-            v.t[j] = from_f32<T>(__fmul_rn(static_cast<float>(c), d[s]));
+        for (int s = 0; s < 2; ++s) {
+            Piece<T> x;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int c = static_cast<int8_t>(w[u][s][j / 4] >> (8 * (j % 4)));
+                x.t[j] = from_f32<T>(__fmul_rn(static_cast<float>(c), d[u][s]));
+            }
+            T *out = static_cast<T *>(p.out[s]) + (i * p.c.heads + h) * p.c.dim + e0;
+            *reinterpret_cast<uint4 *>(out) = x.v;
         }
-        T *out = static_cast<T *>(p.out[s]) + (i * p.c.heads + h) * p.c.dim + e0;
-        *reinterpret_cast<uint4 *>(out) = v.u;
     }
 }
 
@@ -163,13 +222,16 @@ struct MoveParams {
     int lanes;  // lanes of one token: heads * (2 * dim / 16 + 2 * blocks)
 };
 
-constexpr int kMoveBatch = 8;
+constexpr int kMoveBatch = 8, kMovePairs = 32;
 
 // One lane owns one 16-byte piece of codes or one scale of every row that its
 // request moves, so the order of a request's pairs is the lane's own program
 // order and needs no barrier.  Eight pairs are loaded before any is stored,
-// unless one of them is read by a later one of the eight.
+// unless one of them is read by a later one of the eight.  The pairs' rows are
+// found once per block, 32 at a time.
 __global__ void __launch_bounds__(256) q8kv_move_kernel(const MoveParams p) {
+    __shared__ int64_t from[kMovePairs], to[kMovePairs];  // of head 0; -1: the pair is skipped
+    __shared__ int meets[kMovePairs / kMoveBatch];
     const int64_t *src = p.src + static_cast<int64_t>(blockIdx.y) * p.path;
     const int64_t *dst = p.dst + static_cast<int64_t>(blockIdx.y) * p.path;
     const int at = blockIdx.x * blockDim.x + threadIdx.x;
@@ -177,7 +239,7 @@ __global__ void __launch_bounds__(256) q8kv_move_kernel(const MoveParams p) {
     const bool mine = at < p.lanes;
     const int h = mine ? at / per_head : 0, in = mine ? at - h * per_head : 0;
     const bool wide = in < 2 * pieces;
-    // byte address of the lane's piece in row 0, and the bytes of one row of its array
+    // address of the lane's piece in row 0 of its head, and the bytes of one row of its array
     char *base;
     int64_t pitch;
     if (wide) {
@@ -188,74 +250,105 @@ __global__ void __launch_bounds__(256) q8kv_move_kernel(const MoveParams p) {
         base = reinterpret_cast<char *>(s < p.c.blocks ? p.c.k_scales + s : p.c.v_scales + s - p.c.blocks);
         pitch = 4LL * p.c.blocks;
     }
-    for (int i0 = 0; i0 < p.path; i0 += kMoveBatch) {
-        const int n = min(kMoveBatch, p.path - i0);
-        int64_t from[kMoveBatch], to[kMoveBatch];
-        bool meet = false;
-#pragma unroll
-        for (int i = 0; i < kMoveBatch; ++i) {
-            const int64_t s = i < n ? src[i0 + i] : -1, d = i < n ? dst[i0 + i] : -1;
-            int64_t page;
+    base += h * p.c.stride_head * pitch;
+    for (int i0 = 0; i0 < p.path; i0 += kMovePairs) {
+        const int n = min(kMovePairs, p.path - i0);
+        __syncthreads();
+        if (threadIdx.x < kMovePairs) {  // one warp
+            const int i = threadIdx.x;
+            int64_t page, f = -1, t = -1;
             int place;
-            const bool ok = place_of(p.c, d, &page, &place);
-            to[i] = ok ? row_of(p.c, page, h, place) : -1;
-            from[i] = ok && place_of(p.c, s, &page, &place) ? row_of(p.c, page, h, place) : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kMoveBatch; ++i)
-#pragma unroll
-            for (int j = i + 1; j < kMoveBatch; ++j) meet |= from[j] >= 0 && from[i] >= 0 && from[j] == to[i];
-        if (!mine) continue;
-        if (wide) {
-            if (!meet) {
-                uint4 v[kMoveBatch];
-#pragma unroll
-                for (int i = 0; i < kMoveBatch; ++i)
-                    if (from[i] >= 0) v[i] = *reinterpret_cast<const uint4 *>(base + from[i] * pitch);
-#pragma unroll
-                for (int i = 0; i < kMoveBatch; ++i)
-                    if (from[i] >= 0) *reinterpret_cast<uint4 *>(base + to[i] * pitch) = v[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < kMoveBatch; ++i)
-                    if (from[i] >= 0)
-                        *reinterpret_cast<uint4 *>(base + to[i] * pitch) =
-                            *reinterpret_cast<const uint4 *>(base + from[i] * pitch);
+            if (i < n && place_of(p.c, dst[i0 + i], &page, &place)) {
+                t = row_of(p.c, page, 0, place);
+                if (place_of(p.c, src[i0 + i], &page, &place)) f = row_of(p.c, page, 0, place);
             }
-        } else {
-            if (!meet) {
-                float v[kMoveBatch];
+            from[i] = f;
+            to[i] = f >= 0 ? t : -1;
+            __syncwarp();
+            bool meet = false;
+            for (int j = i & ~(kMoveBatch - 1); j < i; ++j) meet |= f >= 0 && f == to[j];
+            const unsigned any = __ballot_sync(~0u, meet);
+            if (i < kMovePairs / kMoveBatch) meets[i] = (any >> (i * kMoveBatch)) & ((1u << kMoveBatch) - 1u);
+        }
+        __syncthreads();
+        if (!mine) continue;
+        for (int g = 0; g < n; g += kMoveBatch) {
+            int64_t f[kMoveBatch], t[kMoveBatch];
 #pragma unroll
-                for (int i = 0; i < kMoveBatch; ++i)
-                    if (from[i] >= 0) v[i] = *reinterpret_cast<const float *>(base + from[i] * pitch);
+            for (int i = 0; i < kMoveBatch; ++i) {
+                f[i] = from[g + i];
+                t[i] = to[g + i];
+            }
+            const bool meet = meets[g / kMoveBatch] != 0;
+            if (wide) {
+                if (!meet) {
+                    uint4 v[kMoveBatch];
 #pragma unroll
-                for (int i = 0; i < kMoveBatch; ++i)
-                    if (from[i] >= 0) *reinterpret_cast<float *>(base + to[i] * pitch) = v[i];
+                    for (int i = 0; i < kMoveBatch; ++i)
+                        if (f[i] >= 0) v[i] = *reinterpret_cast<const uint4 *>(base + f[i] * pitch);
+#pragma unroll
+                    for (int i = 0; i < kMoveBatch; ++i)
+                        if (f[i] >= 0) *reinterpret_cast<uint4 *>(base + t[i] * pitch) = v[i];
+                } else {
+                    for (int i = 0; i < kMoveBatch; ++i)
+                        if (from[g + i] >= 0)
+                            *reinterpret_cast<uint4 *>(base + to[g + i] * pitch) =
+                                *reinterpret_cast<const uint4 *>(base + from[g + i] * pitch);
+                }
             } else {
+                if (!meet) {
+                    float v[kMoveBatch];
 #pragma unroll
-                for (int i = 0; i < kMoveBatch; ++i)
-                    if (from[i] >= 0)
-                        *reinterpret_cast<float *>(base + to[i] * pitch) =
-                            *reinterpret_cast<const float *>(base + from[i] * pitch);
+                    for (int i = 0; i < kMoveBatch; ++i)
+                        if (f[i] >= 0) v[i] = *reinterpret_cast<const float *>(base + f[i] * pitch);
+#pragma unroll
+                    for (int i = 0; i < kMoveBatch; ++i)
+                        if (f[i] >= 0) *reinterpret_cast<float *>(base + t[i] * pitch) = v[i];
+                } else {
+                    for (int i = 0; i < kMoveBatch; ++i)
+                        if (from[g + i] >= 0)
+                            *reinterpret_cast<float *>(base + to[g + i] * pitch) =
+                                *reinterpret_cast<const float *>(base + from[g + i] * pitch);
+                }
             }
         }
     }
 }
 
 // Threads of one token along x (a multiple of 32, at most 256), tokens along y.
-void shape(int lanes, int64_t n, dim3 *grid, dim3 *block) {
+// `tokens` tokens a thread once that leaves several blocks an SM, else one.
+struct Shape {
+    dim3 grid, block;
+    bool many;
+};
+
+Shape shape(int lanes, int64_t n, int tokens) {
     const unsigned x = lanes >= 256 ? 256u : static_cast<unsigned>((lanes + 31) / 32 * 32);
     const unsigned y = 256u / x;
-    *block = dim3(x, y);
-    *grid = dim3(static_cast<unsigned>(ceil_div(n, y)), static_cast<unsigned>(ceil_div(lanes, x)));
+    Shape s;
+    s.block = dim3(x, y);
+    const int64_t across = ceil_div(lanes, x);
+    s.many = ceil_div(n, tokens * y) * across >= kManyBlocks;
+    s.grid = dim3(static_cast<unsigned>(ceil_div(n, s.many ? tokens * y : y)), static_cast<unsigned>(across));
+    return s;
 }
 
 template <typename T>
-void launch_write(const IoParams &p, bool vec, dim3 grid, dim3 block, cudaStream_t stream) {
-    if (vec)
-        q8kv_write_kernel<T, true><<<grid, block, 0, stream>>>(p);
+void launch_write(const IoParams &p, bool vec, const Shape &s, cudaStream_t stream) {
+    if (!vec)
+        q8kv_write_kernel<T, false, 1><<<s.grid, s.block, 0, stream>>>(p);
+    else if (s.many)
+        q8kv_write_kernel<T, true, kWriteTokens><<<s.grid, s.block, 0, stream>>>(p);
     else
-        q8kv_write_kernel<T, false><<<grid, block, 0, stream>>>(p);
+        q8kv_write_kernel<T, true, 1><<<s.grid, s.block, 0, stream>>>(p);
+}
+
+template <typename T>
+void launch_read(const IoParams &p, const Shape &s, cudaStream_t stream) {
+    if (s.many)
+        q8kv_read_kernel<T, kReadTokens><<<s.grid, s.block, 0, stream>>>(p);
+    else
+        q8kv_read_kernel<T, 1><<<s.grid, s.block, 0, stream>>>(p);
 }
 
 bool valid_stride(int64_t s) { return s >= 0 && s < (1LL << 40); }
@@ -308,14 +401,17 @@ q8mv_status_t q8kv_cache_write(const q8kv_cache_t *cache, int64_t n, const void 
     const int64_t e = 16 / size;
     const bool vec = kv::aligned(k, 16) && kv::aligned(v, 16) &&
                      ((k_row | k_head | v_row | v_head) & (e - 1)) == 0;
-    dim3 grid, block;
-    kv::shape(p.lanes, n, &grid, &block);
+    kv::Shape s = kv::shape(p.lanes, n, kv::kWriteTokens);
+    if (!vec && s.many) {  // element-wise loads: one token a thread
+        s.many = false;
+        s.grid.x = static_cast<unsigned>(kv::ceil_div(n, s.block.y));
+    }
     if (type == Q8KV_F32)
-        kv::launch_write<float>(p, vec, grid, block, stream);
+        kv::launch_write<float>(p, vec, s, stream);
     else if (type == Q8KV_F16)
-        kv::launch_write<__half>(p, vec, grid, block, stream);
+        kv::launch_write<__half>(p, vec, s, stream);
     else
-        kv::launch_write<__nv_bfloat16>(p, vec, grid, block, stream);
+        kv::launch_write<__nv_bfloat16>(p, vec, s, stream);
     return q8i::cuda_status(cudaGetLastError());
 }
 
@@ -332,14 +428,13 @@ q8mv_status_t q8kv_cache_read(const q8kv_cache_t *cache, int64_t n, const int64_
     p.n = n;
     const int size = kv::type_size(type);
     p.lanes = p.c.heads * p.c.dim * size / 16;
-    dim3 grid, block;
-    kv::shape(p.lanes, n, &grid, &block);
+    const kv::Shape s = kv::shape(p.lanes, n, kv::kReadTokens);
     if (type == Q8KV_F32)
-        kv::q8kv_read_kernel<float><<<grid, block, 0, stream>>>(p);
+        kv::launch_read<float>(p, s, stream);
     else if (type == Q8KV_F16)
-        kv::q8kv_read_kernel<__half><<<grid, block, 0, stream>>>(p);
+        kv::launch_read<__half>(p, s, stream);
     else
-        kv::q8kv_read_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(p);
+        kv::launch_read<__nv_bfloat16>(p, s, stream);
     return q8i::cuda_status(cudaGetLastError());
 }
 
