@@ -81,24 +81,22 @@ def _fail(status: int, what: str):
     raise Q8mvError(status, what)
 
 
-def _stream(device: int) -> int:
-    """The raw handle of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device)
+# the raw handle of a device's current stream, and the current device: without the objects and the
+# initialisation checks of torch.cuda's own functions, several times their cost
+_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 
 
-def _call(fn, what: str, device: int, *args):
-    """fn(*args, current stream) with `device` current."""
-    if torch.cuda.current_device() == device:
-        status = fn(*args, _stream(device))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _stream(device))
-    if status != 0:
-        _fail(status, what)
+def _elsewhere(fn, device, *args):
+    """fn(*args, current stream) with another device than the current one."""
+    with torch.cuda.device(device):
+        return fn(*args, _stream(device))
 
 
 def _ints(t, dtype, numel, device, name):
-    """A contiguous device tensor of `numel` whole numbers (-1: any number)."""
+    """A contiguous device tensor of `numel` numbers of one type (-1: any number): its address."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and (numel < 0 or t.numel() == numel):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -107,27 +105,24 @@ def _ints(t, dtype, numel, device, name):
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel >= 0 and t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
 
 
 def _rows(t, tail, device, name):
-    """A floating [n, *tail] device tensor whose last axis is contiguous: (type code, strides)."""
+    """A floating [n, *tail] device tensor whose last axis is contiguous: (n, type code, strides)."""
+    code = _TYPES.get(t.dtype)
+    shape, stride = t.shape, t.stride()
+    if code is not None and t.get_device() == device and shape[1:] == tail and (stride[-1] == 1 or tail[-1] == 1):
+        return shape[0], code, stride
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    code = _TYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
-    shape = t.shape
-    if len(shape) != len(tail) + 1 or tuple(shape[1:]) != tail:
+    if tuple(shape[1:]) != tail:
         raise ValueError(f"{name} must have shape (n, {', '.join(map(str, tail))}), got {tuple(shape)}")
-    stride = t.stride()
-    if stride[-1] != 1 and tail[-1] != 1:
-        raise ValueError(f"{name}'s last axis must be contiguous")
-    return code, stride
+    raise ValueError(f"{name}'s last axis must be contiguous")
 
 
 class Cache:
@@ -195,7 +190,7 @@ class Cache:
             reach = s * (n - 1) + reach
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, dim
-        self.device = device
+        self.device, self._where = device, k_codes.device
         self._tail = (heads, dim)
         self._desc = CacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), pages,
                                page_size, heads, dim, 0, *strides)
@@ -206,44 +201,61 @@ class Cache:
     def write(self, k, v, slots) -> None:
         """Quantise keys and values [n, heads, head_dim] (f32, f16 or bf16) into slots [n] (int64, each once;
         slots outside the cache, as -1, are skipped)."""
-        code, ks = _rows(k, self._tail, self.device, "k")
-        code_v, vs = _rows(v, self._tail, self.device, "v")
-        n = len(k)
-        if code_v != code or len(v) != n:
+        device, tail = self.device, self._tail
+        n, code, ks = _rows(k, tail, device, "k")
+        n_v, code_v, vs = _rows(v, tail, device, "v")
+        if code_v != code or n_v != n:
             raise ValueError("k and v must have the same type and number of tokens")
-        _call(self._write, "q8kv_cache_write", self.device, self._ref, n, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1],
-              vs[0], vs[1], _ints(slots, torch.int64, n, self.device, "slots"))
+        at = _ints(slots, torch.int64, n, device, "slots")
+        if _current() == device:
+            status = self._write(self._ref, n, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1], vs[0], vs[1], at, _stream(device))
+        else:
+            status = _elsewhere(self._write, device, self._ref, n, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1], vs[0],
+                                vs[1], at)
+        if status:
+            _fail(status, "q8kv_cache_write")
 
     def read(self, slots, dtype=torch.float32, out=None):
         """(k, v) [n, heads, head_dim] of slots [n] (int64) in ``dtype``; zeros for slots outside the cache."""
-        at = _ints(slots, torch.int64, -1, self.device, "slots")
+        device = self.device
+        at = _ints(slots, torch.int64, -1, device, "slots")
         n = slots.numel()
         if out is None:
             code = _TYPES.get(dtype)
             if code is None:
                 raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
-            k = torch.empty((n, *self._tail), dtype=dtype, device=slots.device)
+            k = torch.empty((n, *self._tail), dtype=dtype, device=self._where)
             v = torch.empty_like(k)
         else:
             k, v = out
-            code, _ = _rows(k, self._tail, self.device, "out[0]")
-            code_v, _ = _rows(v, self._tail, self.device, "out[1]")
-            if code != code_v or len(k) != n or len(v) != n or not k.is_contiguous() or not v.is_contiguous():
+            n_k, code, _ = _rows(k, self._tail, device, "out[0]")
+            n_v, code_v, _ = _rows(v, self._tail, device, "out[1]")
+            if code != code_v or n_k != n or n_v != n or not k.is_contiguous() or not v.is_contiguous():
                 raise ValueError(f"out must be two contiguous tensors of one type with {n} tokens")
-        _call(self._read, "q8kv_cache_read", self.device, self._ref, n, at, k.data_ptr(), v.data_ptr(), code)
+        if _current() == device:
+            status = self._read(self._ref, n, at, k.data_ptr(), v.data_ptr(), code, _stream(device))
+        else:
+            status = _elsewhere(self._read, device, self._ref, n, at, k.data_ptr(), v.data_ptr(), code)
+        if status:
+            _fail(status, "q8kv_cache_read")
         return k, v
 
     def move(self, src, dst) -> None:
         """Slots dst[b, i] become copies of src[b, i] ([batch, path] int64), i in order within a request; pairs
         with a slot outside the cache are skipped, and slots of different requests must not meet."""
-        a = _ints(src, torch.int64, -1, self.device, "src")
+        device = self.device
+        a = _ints(src, torch.int64, -1, device, "src")
         shape = src.shape
-        if len(shape) == 1:
-            shape = (1, *shape)
-        if len(shape) != 2 or src.shape != dst.shape:
+        if shape != dst.shape or not 1 <= len(shape) <= 2:
             raise ValueError(f"src and dst must be [batch, path], got {tuple(src.shape)} and {tuple(dst.shape)}")
-        _call(self._move, "q8kv_cache_move", self.device, self._ref, shape[0], shape[1], a,
-              _ints(dst, torch.int64, -1, self.device, "dst"))
+        batch, path = shape if len(shape) == 2 else (1, shape[0])
+        b = _ints(dst, torch.int64, -1, device, "dst")
+        if _current() == device:
+            status = self._move(self._ref, batch, path, a, b, _stream(device))
+        else:
+            status = _elsewhere(self._move, device, self._ref, batch, path, a, b)
+        if status:
+            _fail(status, "q8kv_cache_move")
 
 
 class _Plan:
@@ -273,6 +285,7 @@ class _Plan:
         self._h = handle.value
         device = args[-1]
         self.device = device if device >= 0 else torch.cuda.current_device()
+        self._where = torch.device("cuda", self.device)
 
 
 class TreeAttention(_Plan):
@@ -283,7 +296,7 @@ class TreeAttention(_Plan):
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, max_requests: int, max_rows: int, device: int = -1):
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
-        self._tail = (heads, head_dim)
+        self._tail, self._packed = (heads, head_dim), (heads * head_dim, head_dim)
         self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 0.0
         self._make("q8kv_attend_plan", heads, kv_heads, head_dim, max_requests, max_rows, int(device))
         self._fn = _library().q8kv_attend
@@ -299,12 +312,13 @@ class TreeAttention(_Plan):
         (None: nodes up to itself).  ``scale`` defaults to 1 / sqrt(head_dim).
         """
         device = self.device
-        code, qs = _rows(q, self._tail, device, "q")
-        rows = len(q)
+        rows, code, qs = _rows(q, self._tail, device, "q")
         at_len = _ints(lengths, torch.int32, -1, device, "lengths")
         requests = lengths.numel()
-        if table.dim() != 2 or len(table) != requests:
-            raise ValueError(f"table must be [{requests}, columns], got {tuple(table.shape)}")
+        shape = table.shape
+        if len(shape) != 2 or shape[0] != requests:
+            raise ValueError(f"table must be [{requests}, columns], got {tuple(shape)}")
+        cols = shape[1]
         at_table = _ints(table, torch.int32, -1, device, "table")
         at_starts = _ints(starts, torch.int32, requests + 1, device, "starts") if starts is not None else 0
         if starts is None and (rows % requests if requests else rows):
@@ -319,20 +333,24 @@ class TreeAttention(_Plan):
                 # a mask without words lets no node see another: it is not the missing mask
                 at_mask, words = at_mask or at_len, 0
         if out is None:
-            out = torch.empty((rows, *self._tail), dtype=q.dtype, device=q.device)
-            os = (self.heads * self.head_dim, self.head_dim)
+            out = torch.empty((rows, *self._tail), dtype=q.dtype, device=self._where)
+            os = self._packed
         else:
-            code_out, os = _rows(out, self._tail, device, "out")
-            if code_out != code or len(out) != rows:
+            rows_out, code_out, os = _rows(out, self._tail, device, "out")
+            if code_out != code or rows_out != rows:
                 raise ValueError(f"out must have the type and rows of q, got {out.dtype} {tuple(out.shape)}")
         if cache.device != device:
             raise ValueError(f"the cache is on cuda:{cache.device}, the plan on cuda:{device}")
-        sums = torch.empty((rows, self.heads), dtype=torch.float32, device=q.device) if lse else None
-        cols = table.shape[1]
+        sums = torch.empty((rows, self.heads), dtype=torch.float32, device=self._where) if lse else None
         _ATTEND.pack_into(self._args, 0, q.data_ptr(), out.data_ptr(), sums.data_ptr() if lse else 0, code, requests, rows,
                           qs[0], qs[1], os[0], os[1], at_starts, at_len, at_table, cols, cols, words, at_mask, words,
                           self._scale if scale is None else scale)
-        _call(self._fn, "q8kv_attend", device, self._h, cache._ref, self._args)
+        if _current() == device:
+            status = self._fn(self._h, cache._ref, self._args, _stream(device))
+        else:
+            status = _elsewhere(self._fn, device, self._h, cache._ref, self._args)
+        if status:
+            _fail(status, "q8kv_attend")
         return (out, sums) if lse else out
 
 
@@ -361,8 +379,7 @@ class TreeVerify(_Plan):
         for each).  path holds each request's accepted nodes in order from 0, then -1; count how many drafts.
         """
         device = self.device
-        code, ls = _rows(logits, self._tail, device, "logits")
-        rows = len(logits)
+        rows, code, ls = _rows(logits, self._tail, device, "logits")
         if requests is None:
             requests = starts.numel() - 1 if starts is not None else temperature.numel() if temperature is not None else 1
         at_tokens = _ints(tokens, torch.int32, rows, device, "tokens")
@@ -374,15 +391,19 @@ class TreeVerify(_Plan):
             raise ValueError(f"{rows} rows do not divide over {requests} requests: pass starts")
         at_draft, draft_row = 0, 0
         if draft_probs is not None:
-            code_draft, ds = _rows(draft_probs, self._tail, device, "draft_probs")
-            if code_draft != 0 or len(draft_probs) != rows:
+            rows_draft, code_draft, ds = _rows(draft_probs, self._tail, device, "draft_probs")
+            if code_draft != 0 or rows_draft != rows:
                 raise ValueError(f"draft_probs must be float32 with {rows} rows, got {draft_probs.dtype} {tuple(draft_probs.shape)}")
             at_draft, draft_row = draft_probs.data_ptr(), ds[0]
-        path = torch.empty(rows, dtype=torch.int32, device=logits.device)
-        count = torch.empty(requests, dtype=torch.int32, device=logits.device)
-        token = torch.empty(requests, dtype=torch.int32, device=logits.device)
+        path, count, token = torch.empty(rows + 2 * requests, dtype=torch.int32, device=self._where).split(
+            (rows, requests, requests))
         _VERIFY.pack_into(self._args, 0, logits.data_ptr(), at_draft, at_tokens, at_parents, at_uniforms, at_temperature,
                           at_starts, path.data_ptr(), count.data_ptr(), token.data_ptr(), ls[0], draft_row, rows, requests,
                           self.vocab, code, 0)
-        _call(self._fn, "q8kv_verify", device, self._h, self._args)
+        if _current() == device:
+            status = self._fn(self._h, self._args, _stream(device))
+        else:
+            status = _elsewhere(self._fn, device, self._h, self._args)
+        if status:
+            _fail(status, "q8kv_verify")
         return path, count, token
