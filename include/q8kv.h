@@ -110,7 +110,10 @@ q8mv_status_t q8kv_cache_move(const q8kv_cache_t *cache, int64_t batch, int64_t 
  * row; products accumulate in f32, each block's scale is folded in f32, the
  * softmax runs in f32, and its weights times the values' scales enter the
  * second product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs,
- * whose own rounding is eight times coarser).  Sums are split over the GPU by
+ * whose own rounding is eight times coarser).  With more than 32 bf16 query rows
+ * a request and kv head (head_dim up to 128), keys enter the first product with
+ * 22 bits and values the second with f16's 11; a value that is not finite then makes all of
+ * a row that sees it NaN.  Sums are split over the GPU by
  * the lengths alone and joined in a fixed order: same inputs, same bits.
  */
 typedef struct q8kv_attend_s *q8kv_attend_plan_t;
@@ -140,6 +143,16 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
                                int32_t max_requests, int64_t max_rows, int device);
 q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, const q8kv_attend_args_t *args,
                           cudaStream_t stream);
+/*
+ * Calls with many bf16 query rows a request run on a kernel that waits on
+ * shared-memory barriers; every wait is bounded (about 2 s).  Synchronises the
+ * plan's device and reports in *device_error whether one ran out since the last
+ * check (1, else 0); the output of that call is undefined.  Clears the word and,
+ * if it was set, the plan's counters.
+ */
+q8mv_status_t q8kv_attend_check(q8kv_attend_plan_t plan, int32_t *device_error);
+/* For tests of the bounded waits only: the bound in nanoseconds (0 restores it). */
+q8mv_status_t q8kv_attend_set_wait(q8kv_attend_plan_t plan, uint64_t wait_ns);
 /* Synchronises the plan's device, then releases its workspace.  NULL is accepted. */
 q8mv_status_t q8kv_attend_destroy(q8kv_attend_plan_t plan);
 

@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 UNITS = [os.path.join(CSRC, name) for name in
          ("q8mv.cu", "batched.cu", "pair.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_f32.cu", "kv_attend_f16.cu",
-          "kv_attend_bf16.cu", "kv_verify.cu")]
+          "kv_attend_bf16.cu", "kv_attend_tc.cu", "kv_verify.cu")]
 SRC = UNITS[0]
 HDR = os.path.join(ROOT, "include", "q8mv.h")
 HDRS = [HDR, os.path.join(ROOT, "include", "q8kv.h")]

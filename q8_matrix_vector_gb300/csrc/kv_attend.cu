@@ -9,6 +9,7 @@ namespace kv {
 namespace {
 
 AttendVariant variant(int dim, int type, AttendShape shape) {
+    if (shape == kRows128) return type == Q8KV_BF16 ? attend_variant_tc(dim) : AttendVariant{};
     return type == Q8KV_F32   ? attend_variant_f32(dim, shape)
            : type == Q8KV_F16 ? attend_variant_f16(dim, shape)
                               : attend_variant_bf16(dim, shape);
@@ -17,6 +18,8 @@ AttendVariant variant(int dim, int type, AttendShape shape) {
 }  // namespace
 
 }  // namespace kv
+
+static constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 
 struct q8kv_attend_s {
     int device = 0;
@@ -28,6 +31,9 @@ struct q8kv_attend_s {
     int64_t max_items = 0;
     float *partial = nullptr;
     unsigned *tickets = nullptr;
+    int64_t tickets_n = 0;
+    int *err = nullptr;
+    uint64_t wait_ns = kDefaultWaitNs;
 };
 
 extern "C" {
@@ -58,7 +64,7 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
     p->max_rows = max_rows;
     p->max_items = items;
     int sms = 0;
-    int64_t slots = 0;  // rows of partial results
+    int64_t floats = 0;  // of partial results: two per CTA
     int64_t tickets = items;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device);
     for (int t = 0; t < 3; ++t)
@@ -68,21 +74,24 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
             if (k.fn == nullptr) continue;
             e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
             if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, k.fn, kv::kWarps * 32, k.smem);
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, k.fn, k.threads, k.smem);
             p->grid[t][v] = sms * std::max(1, ctas);
             tickets = std::max(tickets, items + 2 * kv::ceil_div(p->grid[t][v], kv::kJoinGroup));
-            const int rows = v == kv::kRows8 ? 8 : v == kv::kRows16 ? 16 : 32;
-            slots = std::max<int64_t>(slots, 2LL * p->grid[t][v] * rows);
+            floats = std::max<int64_t>(floats, 2LL * p->grid[t][v] * k.part);
         }
-    if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * slots * static_cast<size_t>(head_dim + kv::kPartExtra));
+    if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * static_cast<size_t>(floats));
     if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(tickets));
     if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(tickets));
-    // the tickets' zeros, before any stream may use them
+    p->tickets_n = tickets;
+    if (e == cudaSuccess) e = cudaMalloc(&p->err, sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(int));
+    // the zeros, before any stream may use them
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaGetLastError();
         if (p->partial) cudaFree(p->partial);
         if (p->tickets) cudaFree(p->tickets);
+        if (p->err) cudaFree(p->err);
         delete p;
         return q8i::cuda_status(e);
     }
@@ -143,6 +152,9 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.tickets = plan->tickets;
     p.tickets_n = static_cast<int>(plan->max_items);
     p.group_tickets = plan->tickets + plan->max_items;
+    p.err = plan->err;
+    p.wait_ns = plan->wait_ns;
+    p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;
     // 8, 16 or 32 query rows at a time, by the mean of a request's: the fewest that hold them.
     // With 8, and a token's heads side by side, each warp can take a head of its own, so that a CTA reads longer
     // stretches: DRAM gives 128-byte pieces of 1 KB rows slowly (1.2 GB of cache, f32: 318 us with one head a CTA,
@@ -152,12 +164,36 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     const double reach = static_cast<double>(a->requests) * a->table_cols * p.c.page_size * p.c.heads *
                          (2.0 * p.c.dim + 8.0 * p.c.blocks);
     const bool side_by_side = p.c.stride_head < p.c.stride_token && p.c.heads % kv::kWarps == 0 && reach >= 5e8;
+    const bool wide = mean > 32 && a->type == Q8KV_BF16 && p.c.dim <= 128;
     const kv::AttendShape v = mean <= 8                            ? side_by_side ? kv::kHeads4 : kv::kRows8
+                              : wide                               ? kv::kRows128
                               : mean <= 16 || p.c.dim > 128 ? kv::kRows16
                                                             : kv::kRows32;
     const kv::AttendVariant &k = plan->variant[a->type][v];
-    k.fn<<<plan->grid[a->type][v], kv::kWarps * 32, k.smem, stream>>>(p);
+    k.fn<<<plan->grid[a->type][v], k.threads, k.smem, stream>>>(p);
     return q8i::cuda_status(cudaGetLastError());
+}
+
+q8mv_status_t q8kv_attend_check(q8kv_attend_plan_t p, int32_t *device_error) {
+    if (p == nullptr || device_error == nullptr) return Q8MV_ERR_INVALID_ARG;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(p->device);
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    int word = 0;
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaMemcpy(&word, p->err, sizeof(int), cudaMemcpyDeviceToHost));
+    if (st == Q8MV_OK && word != 0) {
+        st = q8i::cuda_status(cudaMemset(p->err, 0, sizeof(int)));
+        if (st == Q8MV_OK) st = q8i::cuda_status(cudaMemset(p->tickets, 0, sizeof(unsigned) * p->tickets_n));
+        if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    }
+    *device_error = word;
+    return st;
+}
+
+q8mv_status_t q8kv_attend_set_wait(q8kv_attend_plan_t p, uint64_t wait_ns) {
+    if (p == nullptr || wait_ns > 10000000000ull) return Q8MV_ERR_INVALID_ARG;
+    p->wait_ns = wait_ns == 0 ? kDefaultWaitNs : wait_ns;
+    return Q8MV_OK;
 }
 
 q8mv_status_t q8kv_attend_destroy(q8kv_attend_plan_t p) {
@@ -167,6 +203,7 @@ q8mv_status_t q8kv_attend_destroy(q8kv_attend_plan_t p) {
     if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
     if (p->partial) cudaFree(p->partial);
     if (p->tickets) cudaFree(p->tickets);
+    if (p->err) cudaFree(p->err);
     delete p;
     return st;
 }

@@ -907,11 +907,17 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
 }
 
 // The variants of one type; 32 rows of a dim above 128 do not fit the registers.
+template <typename T, int DP, int QP, int PP, int NT, int HW>
+AttendVariant attend_variant_of(int dim) {
+    return {q8kv_attend_kernel<T, DP, NT, QP, PP, HW>, Smem<DP, NT, QP, HW>::kTotal, kWarps * 32,
+            8 * (HW == 1 ? NT : HW) * (dim + kPartExtra)};
+}
+
 template <typename T, int QP, int PP, int NT, int HW>
 AttendVariant attend_variant_of(int dim) {
-    if (dim <= 64) return {q8kv_attend_kernel<T, 64, NT, QP, PP, HW>, Smem<64, NT, QP, HW>::kTotal};
-    if (dim <= 128) return {q8kv_attend_kernel<T, 128, NT, QP, PP, HW>, Smem<128, NT, QP, HW>::kTotal};
-    if constexpr (NT <= 2) return {q8kv_attend_kernel<T, 256, NT, QP, PP, HW>, Smem<256, NT, QP, HW>::kTotal};
+    if (dim <= 64) return attend_variant_of<T, 64, QP, PP, NT, HW>(dim);
+    if (dim <= 128) return attend_variant_of<T, 128, QP, PP, NT, HW>(dim);
+    if constexpr (NT <= 2) return attend_variant_of<T, 256, QP, PP, NT, HW>(dim);
     return {};
 }
 
@@ -921,7 +927,8 @@ AttendVariant attend_variant_of(int dim, AttendShape shape) {
         case kRows8: return attend_variant_of<T, QP, PP, 1, 1>(dim);
         case kRows16: return attend_variant_of<T, QP, PP, 2, 1>(dim);
         case kRows32: return attend_variant_of<T, QP, PP, 4, 1>(dim);
-        default: return attend_variant_of<T, QP, PP, 1, kWarps>(dim);
+        case kHeads4: return attend_variant_of<T, QP, PP, 1, kWarps>(dim);
+        default: return {};
     }
 }
 

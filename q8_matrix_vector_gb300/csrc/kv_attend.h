@@ -35,21 +35,28 @@ struct AttendParams {
     unsigned *tickets;  // one per item
     int tickets_n;
     unsigned *group_tickets;  // two per kJoinGroup CTAs
+    int *err;           // the plan's error word, and the bound on waits (kRows128)
+    uint64_t wait_ns;
+    int out_vec;        // 16-byte stores of eight outputs are aligned (kRows128)
 };
 
 // What an item is: 8, 16 or 32 query rows (node, head of the group) of one kv head
-// whose keys the warps share, or 8 rows of four kv heads, one for each warp.
-enum AttendShape { kRows8 = 0, kRows16, kRows32, kHeads4, kAttendShapes };
+// whose keys the warps share, 8 rows of four kv heads, one for each warp, or 128
+// rows of one kv head on the tensor-memory path (kv_attend_tc.cuh).
+enum AttendShape { kRows8 = 0, kRows16, kRows32, kHeads4, kRows128, kAttendShapes };
 
 // One variant of the kernel: dim up to 64, 128 or 256, and a shape (kRows32: dim up
-// to 128).  The parts of q and of the weights go by the type (see q8kv.h), a
-// translation unit each.
+// to 128; kRows128: bf16 and dim up to 128).  The parts of q and of the weights go
+// by the type (see q8kv.h), a translation unit each.
 struct AttendVariant {
     void (*fn)(AttendParams) = nullptr;
     int smem = 0;
+    int threads = kWarps * 32;
+    int part = 0;  // floats of a partial result
 };
 AttendVariant attend_variant_f32(int dim, AttendShape shape);
 AttendVariant attend_variant_f16(int dim, AttendShape shape);
 AttendVariant attend_variant_bf16(int dim, AttendShape shape);
+AttendVariant attend_variant_tc(int dim);
 
 }  // namespace kv

@@ -1,0 +1,858 @@
+// Attention of wide draft trees over a Q8_0 cache on the 5th-generation tensor
+// cores (../../include/q8kv.h): up to 128 query rows (node, head of the group) of
+// one kv head at a time, bf16 queries and outputs.
+//
+//     S[r, j] = q[r] . K[j],   O[r] += P[r, j] V[j],   P = exp2(scale log2(e) S + E - M)
+//
+// Work is the line of units of kv_attend.cuh with 128-row items and tiles of 128
+// keys, one CTA per SM.  With 128 rows a code meets 128 multiplications on each
+// side, so the products belong to tcgen05.mma and the rest of the SM keeps it fed:
+//   * eight convert warps read the next tile's codes and scales into registers
+//     while they turn this one's into f16 operands in shared memory.  A key's row
+//     is normalised by a power of two (per 16 keys, or per key where some of them
+//     are drafted) that goes into the softmax, and code times scale is formed with
+//     the scale in two f16 parts.  K is kept in two f16 parts, 22 bits, since a
+//     score's error is a weight's relative one and lse is f32; V is rounded once to
+//     11 bits, as outputs are bf16.  (f32 and f16 outputs stay with kv_attend.cuh.)
+//     K and V tiles have the same layout, core matrices of 8 keys x 8 e: K is read
+//     K-major, V MN-major.
+//   * one thread issues the MMAs: S = Q K^T of tile g (lower part, then upper), then
+//     O += P V of tile g - 1.
+//   * two softmax warpgroups take alternate tiles, a thread a row, each with its own
+//     S, O (f32) and, in place of S, P (f16) in tensor memory: 2 x (128 + 128)
+//     columns, all of them.  While one exponentiates, the other's products run.
+//     P is 2^7 at the maximum, so that f16 holds weights down to 2^-31 of the largest,
+//     and the maximum only moves when P would pass 2^15: O is rarely rescaled.
+//   * at an item's end each warpgroup adds half of the columns of both O.
+// All hand-overs are mbarriers, every wait is bounded (2 s); one that runs out is
+// recorded in the plan's error word and the CTA leaves.
+#pragma once
+
+#include "kv_attend.cuh"
+
+namespace kv {
+
+constexpr int kTcRows = 128, kTcKeys = 128;
+constexpr int kTcSoftWarps = 8, kTcConvWarps = 8;
+constexpr int kTcMmaWarp = kTcSoftWarps + kTcConvWarps;
+constexpr int kTcThreads = (kTcMmaWarp + 1) * 32;
+constexpr int kTcChunk = kTcKeys * 16 + 16;     // bytes from 8 e to the next 8: 128 rows of 16, and 16 against bank conflicts
+constexpr uint64_t kTcWaitNs = 2000000000ull;
+constexpr int kTcErrWait = 1;
+constexpr float kTcTop = 7.0f;                  // log2 of P at the row's maximum when that is taken
+constexpr float kTcSlack = 15.0f;               // and how far P may grow before it is taken anew (f16 ends at 2^16)
+constexpr int kTcItemUnits = 3;
+
+template <int DP>
+struct TcSmem {
+    static constexpr int kTile = DP / 8 * kTcChunk;   // one operand of 128 rows
+    static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kLo = 5 * kTile, kMeta = 6 * kTile;
+    static constexpr int kMetaTile = kTcKeys * 16;    // per key: K's factor, E, 2^-E, flag
+    static constexpr int kTotal = kMeta + 4 * kMetaTile;
+    static constexpr int kPart = kTcRows * (DP + 2);  // floats of a partial result: O by 4 columns x 128 rows, m, l
+};
+
+__device__ __forceinline__ uint32_t tc_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void tc_bar_init(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(bar)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void tc_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(bar)) : "memory");
+}
+__device__ __forceinline__ bool tc_try(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(tc_smem(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ uint64_t tc_now() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// The phase of `parity`; false if the CTA is leaving or the time is up.
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, const volatile int *leave, uint64_t wait_ns) {
+    if (tc_try(bar, parity)) return true;
+    const uint64_t t0 = tc_now();
+    for (uint32_t i = 1;; ++i) {
+        if (tc_try(bar, parity)) return true;
+        if ((i & 31u) == 0) {
+            if (leave != nullptr && *leave) return false;
+            if (tc_now() - t0 > wait_ns) return false;
+        }
+    }
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory operand without swizzle: bytes between core matrices along K and along M or N.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t along_k, uint32_t along_mn) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(along_k >> 4) << 16) |
+           (static_cast<uint64_t>(along_mn >> 4) << 32) | (1ull << 46);
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc_smem(bar)) : "memory");
+}
+// 32 columns of the thread's lane
+__device__ __forceinline__ void tc_ld32(uint32_t at, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st32(uint32_t at, const float (&v)[32]) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// two f16 codes times a scale in two parts, rounded once, and what that leaves (exact but for c * lo's last bits)
+__device__ __forceinline__ uint32_t tc_scaled(uint32_t codes, uint32_t hi, uint32_t lo, uint32_t *rest) {
+    uint32_t t, y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(codes), "r"(lo));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(codes), "r"(hi), "r"(t));
+    if (rest != nullptr) {
+        uint32_t d;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(codes), "r"(hi), "r"(y ^ 0x80008000u));
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(*rest) : "r"(d), "r"(t));
+    }
+    return y;
+}
+
+// power of two with exponent e
+__device__ __forceinline__ float tc_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+template <int DP>
+__global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const AttendParams p) {
+    using T = __nv_bfloat16;
+    using S = TcSmem<DP>;
+    constexpr int PARTS = DP / 16, KPL = 32 / PARTS, NL = 16 / KPL;  // 16-byte pieces of a row, keys of a load, loads
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(8) uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2];
+    __shared__ __align__(8) uint64_t soft_bar;            // among the softmax warps
+    __shared__ __align__(8) uint64_t lo_free;             // K's lower part, which has one buffer
+    __shared__ uint32_t tmem_at;
+    __shared__ int leave, is_last;
+    __shared__ int64_t scan_units[kTcThreads / 32], scan_items[kTcThreads / 32];
+    __shared__ int64_t start_b, start_item, start_unit;
+    __shared__ float row_mul[4][kTcRows];                // by item
+    __shared__ float2 row_ml[2][kTcRows];                // a warpgroup's maximum and sum
+    __shared__ uint32_t there_bits[4][kTcConvWarps];     // by tile: the warp's keys that are there
+    __shared__ uint32_t plain_bits[4];                   // by tile: warps whose keys all rows see, one normaliser each
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const volatile int *leaving = &leave;
+
+    // ---- the CTA's share of the line of units (as in kv_attend.cuh)
+    Split split;
+    int64_t u, u_end;
+    Place w;
+    {
+        const int per = (p.requests + kTcThreads - 1) / kTcThreads;
+        const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
+        int64_t units = 0, items = 0;
+        auto units_in = [&](const Place &x) { return static_cast<int64_t>(p.c.heads) * x.tiles_r * (x.tiles_k + kTcItemUnits); };
+        for (int b = b0; b < b1; ++b) {
+            load_request<kTcRows, kTcKeys>(p, b, w);
+            units += units_in(w);
+            items += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+        }
+        int64_t iu = units, ii = items;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t a = __shfl_up_sync(~0u, iu, d), b = __shfl_up_sync(~0u, ii, d);
+            if (lane >= d) {
+                iu += a;
+                ii += b;
+            }
+        }
+        if (lane == 31) {
+            scan_units[warp] = iu;
+            scan_items[warp] = ii;
+        }
+        if (tid == 0) {
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(k_full + i, kTcConvWarps);
+                tc_bar_init(v_full + i, kTcConvWarps);
+                tc_bar_init(k_free + i, 1);
+                tc_bar_init(v_free + i, 1);
+                tc_bar_init(s_full + i, 1);
+                tc_bar_init(p_full + i, 4);
+            }
+            tc_bar_init(&soft_bar, kTcSoftWarps);
+            tc_bar_init(&lo_free, 1);
+            leave = 0;
+            for (int i = 0; i < 4; ++i) plain_bits[i] = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncthreads();
+        int64_t total = 0, before_u = 0, before_i = 0;
+        for (int i = 0; i < kTcThreads / 32; ++i) {
+            if (i < warp) {
+                before_u += scan_units[i];
+                before_i += scan_items[i];
+            }
+            total += scan_units[i];
+        }
+        if (total == 0) return;
+        split.units = total;
+        split.ctas = min(static_cast<int64_t>(gridDim.x), total);
+        if (blockIdx.x >= split.ctas) return;
+        u = split.begin(blockIdx.x);
+        u_end = split.begin(blockIdx.x + 1);
+        before_u += iu - units;
+        before_i += ii - items;
+        if (u >= before_u && u < before_u + units) {
+            int b = b0;
+            for (; b < b1; ++b) {
+                load_request<kTcRows, kTcKeys>(p, b, w);
+                const int64_t n = units_in(w);
+                if (u < before_u + n) break;
+                before_u += n;
+                before_i += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+            }
+            start_b = b;
+            start_unit = before_u;
+            start_item = before_i;
+        }
+        __syncthreads();
+        load_request<kTcRows, kTcKeys>(p, static_cast<int>(start_b), w);
+        const int64_t k = (u - start_unit) / (w.tiles_k + kTcItemUnits);
+        w.h = static_cast<int>(k / w.tiles_r);
+        w.rt = static_cast<int>(k - static_cast<int64_t>(w.h) * w.tiles_r);
+        w.item = start_item + k;
+        w.first = start_unit + k * (w.tiles_k + kTcItemUnits) + kTcItemUnits;
+    }
+    auto advance = [&](Place &x) {
+        x.first += x.tiles_k + kTcItemUnits;
+        ++x.item;
+        if (++x.rt == x.tiles_r) {
+            x.rt = 0;
+            if (++x.h == p.c.heads) {
+                x.h = 0;
+                do load_request<kTcRows, kTcKeys>(p, x.b + 1, x);
+                while (x.tiles_r == 0);
+            }
+        }
+    };
+    // the CTA's tiles of item x: kt0 .. kt1 - 1
+    auto tiles_of = [&](const Place &x, int64_t *kt0) -> int {
+        *kt0 = max(u, x.first) - x.first;
+        return static_cast<int>(max(min(u_end, x.first + x.tiles_k) - x.first, *kt0) - *kt0);
+    };
+    auto more = [&](const Place &x) { return x.first + x.tiles_k < u_end; };
+
+    if (warp == kTcMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&tmem_at)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_at;
+    const uint32_t base = tc_smem(smem);
+    bool bad = false;
+
+    if (warp == kTcMmaWarp) {
+        // ================ the MMAs
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(kTcKeys >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
+            constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(DP >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
+            int64_t g = 0;        // tile of the CTA
+            uint64_t *last_bar = nullptr;  // of the last commit
+            uint32_t last_ph = 0;
+            int last_first = 0;   // whether tile g - 1 was its warpgroup's first of an item
+            auto second = [&](int64_t t, bool first) -> bool {  // O += P V of tile t
+                const int x = static_cast<int>(t & 1);
+                const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
+                if (!tc_wait(p_full + x, ph, leaving, p.wait_ns) || !tc_wait(v_full + x, ph, leaving, p.wait_ns)) return false;
+                tc_after();
+                const uint32_t v = base + S::kV + x * S::kTile;
+#pragma unroll
+                for (int k = 0; k < kTcKeys / 16; ++k)
+                    tc_mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, tc_desc(v + k * 256, 128, kTcChunk), idesc_o,
+                              first && k == 0 ? 0u : 1u);
+                tc_commit(v_free + x);
+                last_bar = v_free + x;
+                last_ph = ph;
+                return true;
+            };
+            for (;;) {
+                int64_t kt0;
+                const int n = tiles_of(w, &kt0);
+                for (int i = 0; i < n && !bad; ++i, ++g) {
+                    const int x = static_cast<int>(g & 1);
+                    const uint32_t ph = static_cast<uint32_t>(g >> 1) & 1u;
+                    if (!tc_wait(k_full + x, ph, leaving, p.wait_ns)) {
+                        bad = true;
+                        break;
+                    }
+                    tc_after();
+                    const uint32_t q = base + S::kQ, k = base + S::kK + x * S::kTile, low = base + S::kLo;
+#pragma unroll
+                    for (int e = 0; e < DP / 16; ++e)
+                        tc_mma_ss(tmem + x * 128, tc_desc(q + 2 * e * kTcChunk, kTcChunk, 128),
+                                  tc_desc(low + 2 * e * kTcChunk, kTcChunk, 128), idesc_s, e == 0 ? 0u : 1u);
+                    tc_commit(&lo_free);
+#pragma unroll
+                    for (int e = 0; e < DP / 16; ++e)
+                        tc_mma_ss(tmem + x * 128, tc_desc(q + 2 * e * kTcChunk, kTcChunk, 128),
+                                  tc_desc(k + 2 * e * kTcChunk, kTcChunk, 128), idesc_s, 1u);
+                    tc_commit(k_free + x);
+                    tc_commit(s_full + x);
+                    last_bar = k_free + x;
+                    last_ph = ph;
+                    if (g > 0 && !second(g - 1, last_first != 0)) {
+                        bad = true;
+                        break;
+                    }
+                    last_first = i < 2;
+                }
+                if (bad || !more(w)) break;
+                advance(w);
+            }
+            if (!bad && g > 0 && !second(g - 1, last_first != 0)) bad = true;
+            if (bad) leave = 1;
+            // what was issued, before the tensor memory goes back
+            if (last_bar != nullptr && !tc_wait(last_bar, last_ph, nullptr, p.wait_ns)) bad = true;
+            if (bad) atomicOr(p.err, kTcErrWait);
+        }
+    } else if (warp >= kTcSoftWarps) {
+        // ================ convert
+        const int cw = warp - kTcSoftWarps, part = lane % PARTS, sub = lane / PARTS;
+        const bool live = part * 16 < p.c.dim;
+        const int ct = tid - kTcSoftWarps * 32;  // thread among the convert warps
+        int64_t g = 0;
+        int item_no = 0;
+        uint4 kr[NL], vr[NL];
+        float ksc[NL], vsc[NL];
+        uint32_t there = 0;
+        auto fetch = [&](const Place &x, int64_t tile) {
+            const int64_t pos = tile * kTcKeys + cw * 16 + (lane & 15);
+            const int64_t keys = min(static_cast<int64_t>(x.prefix) + x.nodes, static_cast<int64_t>(p.table_cols) * p.c.page_size);
+            uint32_t row = kNoRow;
+            if (pos < keys) {
+                const uint32_t at = static_cast<uint32_t>(pos), col = (__umulhi(at, p.page_mul) + at) >> p.page_shift;
+                const int page = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_row + col);
+                if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.c.pages))
+                    row = static_cast<uint32_t>(row_of(p.c, page, x.h, static_cast<int>(at - col * p.c.page_size)));
+            }
+            there = __ballot_sync(~0u, row != kNoRow) & 0xFFFFu;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const uint32_t r = __shfl_sync(~0u, row, i * KPL + sub);
+                kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+                ksc[i] = vsc[i] = 0.0f;
+                if (r != kNoRow && live) {
+                    const uint64_t at = static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim) + part * 16;
+                    kr[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.k_codes + at));
+                    vr[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.v_codes + at));
+                    const uint64_t sc = static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.blocks) + (part >> 1);
+                    ksc[i] = __ldg(p.c.k_scales + sc);
+                    vsc[i] = __ldg(p.c.v_scales + sc);
+                }
+            }
+        };
+        // exponent e with scales below 2^(e + 7): codes times scale / 2^e stay below 2^14
+        auto exponent = [](uint32_t bits) -> int { return max(min(static_cast<int>(bits >> 23) - 127 - 6, 120), -100); };
+        // 8 neighbouring e of a key to two places of a tile; half of a row's lanes store their upper 8 first: the
+        // eight lanes of a phase then meet 8 different banks
+        auto store = [&](uint32_t tile, int key, const uint32_t (&o)[8]) {
+            const bool up = part >= PARTS / 2;
+            const uint32_t at = tile + 2 * part * kTcChunk + key * 16;
+            const uint32_t first = at + (up ? kTcChunk : 0), then = at + (up ? 0 : kTcChunk);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(first), "r"(up ? o[4] : o[0]), "r"(up ? o[5] : o[1]), "r"(up ? o[6] : o[2]), "r"(up ? o[7] : o[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(then), "r"(up ? o[0] : o[4]), "r"(up ? o[1] : o[5]), "r"(up ? o[2] : o[6]), "r"(up ? o[3] : o[7]) : "memory");
+        };
+        // 16 codes times scale / 2^e to rows of the tile, and what that rounds off
+        auto convert = [&](uint32_t tile, int key, const uint4 &c, float scale, uint32_t (*rest)[8]) {
+            const __half hi = __float2half_rn(scale), lo = __float2half_rn(scale - __half2float(hi));
+            const uint32_t h2 = pack_half2(__half2float(hi), __half2float(hi)), l2 = pack_half2(__half2float(lo), __half2float(lo));
+            const uint32_t in[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = tc_scaled(unbias(__byte_perm(in[i / 2], 0x64646464u, i % 2 ? 0x4342u : 0x4140u)), h2, l2, rest ? &(*rest)[i] : nullptr);
+            store(tile, key, o);
+        };
+        int64_t kt0;
+        int n = tiles_of(w, &kt0);
+        if (n > 0) fetch(w, kt0);
+        for (;;) {
+            if (n > 0) {
+                // q, once the previous item's last S has been computed
+                if (g > 0 && !tc_wait(k_free + static_cast<int>((g - 1) & 1), static_cast<uint32_t>((g - 1) >> 1) & 1u, leaving, p.wait_ns)) bad = true;
+                if (__any_sync(~0u, bad)) {
+                    bad = true;
+                    break;
+                }
+                {
+                    const int r = ct >> 1, half = ct & 1;  // two threads a row
+                    const int rows = min(kTcRows, w.nodes * p.group - w.rt * kTcRows);
+                    const int idx = w.rt * kTcRows + r, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
+                    const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
+                    uint32_t top = 0;
+                    for (int e = half * (DP / 2); e < half * (DP / 2) + DP / 2; ++e)
+                        if (r < rows && e < p.c.dim) top = max(top, __float_as_uint(to_f32(src[e])) & 0x7FFFFFFFu);
+                    top = max(top, __shfl_xor_sync(~0u, top, 1));
+                    const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
+                    const float down = copysignf(tc_pow2(-ex), p.scale_log2);
+                    for (int c8 = half * (DP / 16); c8 < half * (DP / 16) + DP / 16; ++c8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = c8 * 8 + 2 * e;
+                            const bool in = r < rows && at < p.c.dim;
+                            o[e] = pack_half2(in ? to_f32(src[at]) * down : 0.0f, in ? to_f32(src[at + 1]) * down : 0.0f);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + c8 * kTcChunk + r * 16), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                    }
+                    if (half == 0) row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
+                }
+            }
+            for (int i = 0; i < n; ++i, ++g) {
+                const int x = static_cast<int>(g & 1), ring = static_cast<int>(g & 3);
+                const uint32_t ph = static_cast<uint32_t>(g >> 1) & 1u;
+                const int64_t tile = kt0 + i;
+                const bool drafts = tile * kTcKeys + cw * 16 + 16 > w.prefix;
+                const bool plain = !drafts && there == 0xFFFFu;
+                // ---- normalisers: of each key, and of the warp's keys if all rows see them
+                int ek[NL], ev[NL];
+                bool odd[NL];
+                uint32_t top_k = 0, top_v = 0;
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    uint32_t bk = __float_as_uint(ksc[j]) & 0x7FFFFFFFu, bv = __float_as_uint(vsc[j]) & 0x7FFFFFFFu;
+#pragma unroll
+                    for (int d = 1; d < PARTS; d *= 2) {
+                        bk = max(bk, __shfl_xor_sync(~0u, bk, d));
+                        bv = max(bv, __shfl_xor_sync(~0u, bv, d));
+                    }
+                    // a scale that is not finite: the key's rows are 0 here, and the softmax makes NaN of who sees it
+                    odd[j] = bk >= 0x7F800000u || bv >= 0x7F800000u;
+                    if (odd[j]) {
+                        ksc[j] = vsc[j] = 0.0f;
+                        bk = bv = 0;
+                    }
+                    ek[j] = exponent(bk);
+                    ev[j] = exponent(bv);
+                    top_k = max(top_k, bk);
+                    top_v = max(top_v, bv);
+                }
+                const bool any_odd = __any_sync(~0u, odd[0] || odd[NL - 1] || (NL > 2 && (odd[1] || odd[NL - 2])));
+                if (plain && !any_odd) {
+                    const int uk = exponent(__reduce_max_sync(~0u, top_k)), uv = exponent(__reduce_max_sync(~0u, top_v));
+#pragma unroll
+                    for (int j = 0; j < NL; ++j) {
+                        ek[j] = uk;
+                        ev[j] = uv;
+                    }
+                }
+                // ---- K
+                if (g >= 2 && !tc_wait(k_free + x, ph ^ 1u, leaving, p.wait_ns)) bad = true;
+                if (__any_sync(~0u, bad)) {
+                    bad = true;
+                    break;
+                }
+                float4 *meta = reinterpret_cast<float4 *>(smem + S::kMeta + ring * S::kMetaTile);
+                const uint32_t kb = base + S::kK + x * S::kTile, vb = base + S::kV + x * S::kTile;
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    const int key = cw * 16 + j * KPL + sub;
+                    uint32_t rest[8];
+                    convert(kb, key, kr[j], ksc[j] * tc_pow2(-ek[j]), &rest);
+                    if (j == 0 && g >= 1) {  // the tile before has used its lower part
+                        if (!tc_wait(&lo_free, static_cast<uint32_t>(g - 1) & 1u, leaving, p.wait_ns)) bad = true;
+                        if (__any_sync(~0u, bad)) bad = true;
+                    }
+                    store(base + S::kLo, key, rest);
+                    if (part == 0) meta[key] = make_float4(tc_pow2(ek[j]), static_cast<float>(ev[j]), tc_pow2(-ev[j]), odd[j] ? 1.0f : 0.0f);
+                }
+                if (bad) break;
+                if (lane == 0) {
+                    there_bits[ring][cw] = there;
+                    if (plain && !any_odd)
+                        atomicOr(&plain_bits[ring], 1u << cw);
+                    else
+                        atomicAnd(&plain_bits[ring], ~(1u << cw));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) tc_arrive(k_full + x);
+                // ---- V
+                if (g >= 2 && !tc_wait(v_free + x, ph ^ 1u, leaving, p.wait_ns)) bad = true;
+                if (__any_sync(~0u, bad)) {
+                    bad = true;
+                    break;
+                }
+#pragma unroll
+                for (int j = 0; j < NL; ++j) convert(vb, cw * 16 + j * KPL + sub, vr[j], vsc[j] * tc_pow2(-ev[j]), nullptr);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) tc_arrive(v_full + x);
+                if (i + 1 < n) fetch(w, tile + 1);
+            }
+            if (bad || !more(w)) break;
+            if (n > 0) ++item_no;
+            advance(w);
+            n = tiles_of(w, &kt0);
+            if (n > 0) fetch(w, kt0);
+        }
+        if (bad) {
+            leave = 1;
+            if (lane == 0) atomicOr(p.err, kTcErrWait);
+        }
+    } else {
+        // ================ softmax: warpgroup x takes tiles g = x mod 2
+        const int x = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+        const int64_t pitch = S::kPart;
+        int64_t g = 0;
+        int item_no = 0;
+        bool first_item = true;
+        uint32_t soft_phase = 0;
+        // all softmax warps; false (in whole warps) if the CTA is leaving
+        auto soft_sync = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) tc_arrive(&soft_bar);
+            const bool ok = tc_wait(&soft_bar, soft_phase, leaving, p.wait_ns);
+            soft_phase ^= 1u;
+            return __all_sync(~0u, ok);
+        };
+        for (;;) {
+            int64_t kt0;
+            const int n = tiles_of(w, &kt0);
+            if (n > 0) {
+                const int idx = w.rt * kTcRows + r;
+                const bool whole = n == w.tiles_k;
+                float m = -INFINITY, l = 0.0f;
+                bool have = false;  // O holds something
+                float mul = 0.0f;
+                for (int i = 0; i < n; ++i, ++g) {
+                    if (static_cast<int>(g & 1) != x) continue;
+                    const int ring = static_cast<int>(g & 3);
+                    if (!tc_wait(s_full + x, static_cast<uint32_t>(g >> 1) & 1u, leaving, p.wait_ns)) bad = true;
+                    if (__any_sync(~0u, bad)) {
+                        bad = true;
+                        break;
+                    }
+                    tc_after();
+                    if (!have) mul = row_mul[item_no & 3][r];
+                    const float4 *meta = reinterpret_cast<const float4 *>(smem + S::kMeta + ring * S::kMetaTile);
+                    const uint32_t plain = *const_cast<const volatile uint32_t *>(&plain_bits[ring]);
+                    const bool fast = plain == (1u << kTcConvWarps) - 1u;
+                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (!fast) {
+                        const int64_t j0 = (kt0 + i) * kTcKeys - w.prefix;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            see[q] = there_bits[ring][2 * q] | (there_bits[ring][2 * q + 1] << 16);
+                            if (j0 + 32 * q + 32 > 0)
+                                see[q] &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, static_cast<int>(j0 + 32 * q), idx);
+                        }
+                    }
+                    // ---- the row's maximum of s + E
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float v[32];
+                        tc_ld32(ts + 32 * q, v);
+                        if (fast) {
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh) {
+                                float t0 = fmaxf(v[16 * hh], v[16 * hh + 1]), t1 = fmaxf(v[16 * hh + 2], v[16 * hh + 3]);
+#pragma unroll
+                                for (int e = 4; e < 16; e += 4) {
+                                    t0 = fmaxf(t0, fmaxf(v[16 * hh + e], v[16 * hh + e + 1]));
+                                    t1 = fmaxf(t1, fmaxf(v[16 * hh + e + 2], v[16 * hh + e + 3]));
+                                }
+                                const float4 c = meta[32 * q + 16 * hh];
+                                top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * c.x, c.y));
+                            }
+                        } else {
+                            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float4 c = meta[32 * q + e];
+                                if ((bits >> e) & 1u) {
+                                    top = fmaxf(top, fmaf(v[e], mul * c.x, c.y));
+                                    if (c.w != 0.0f) l = NAN;
+                                }
+                            }
+                        }
+                    }
+                    // ---- move the maximum?
+                    float f = 1.0f;
+                    if (top > m + kTcSlack || m == -INFINITY) {
+                        f = m == -INFINITY ? 0.0f : ex2(m - (top - kTcTop));
+                        m = top - kTcTop;
+                    }
+                    const float z = m == -INFINITY ? 0.0f : m;
+                    l *= f;
+                    if (have && __any_sync(~0u, f != 1.0f)) {
+#pragma unroll 1
+                        for (int q = 0; q < DP / 32; ++q) {
+                            float v[32];
+                            tc_ld32(to + 32 * q, v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] *= f;
+                            tc_st32(to + 32 * q, v);
+                        }
+                    }
+                    have = true;
+                    // ---- P
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float v[32];
+                        uint32_t o[16];
+                        tc_ld32(ts + 32 * q, v);
+                        if (fast) {
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh) {
+                                const float4 c = meta[32 * q + 16 * hh];
+                                const float a = mul * c.x, d = c.y - z;
+                                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) {
+                                    const float p0 = ex2(fmaf(v[16 * hh + e], a, d)), p1 = ex2(fmaf(v[16 * hh + e + 1], a, d));
+                                    sum0 += p0;
+                                    sum1 += p1;
+                                    o[8 * hh + e / 2] = pack_half2(p0, p1);
+                                }
+                                l = fmaf(sum0 + sum1, c.z, l);
+                            }
+                        } else {
+                            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float4 c0 = meta[32 * q + e], c1 = meta[32 * q + e + 1];
+                                const float p0 = (bits >> e) & 1u ? ex2(fmaf(v[e], mul * c0.x, c0.y - z)) : 0.0f;
+                                const float p1 = (bits >> (e + 1)) & 1u ? ex2(fmaf(v[e + 1], mul * c1.x, c1.y - z)) : 0.0f;
+                                l = fmaf(p0, c0.z, l);
+                                l = fmaf(p1, c1.z, l);
+                                o[e / 2] = pack_half2(p0, p1);
+                            }
+                        }
+                        tc_st16(ts + 16 * q, o);
+                    }
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) tc_arrive(p_full + x);
+                }
+                if (bad) break;
+                // ---- the item's results: both O must be complete
+                row_ml[x][r] = make_float2(m, l);
+                for (int back = 1; back <= 2 && back <= n; ++back) {
+                    const int64_t t = g - back;
+                    if (!tc_wait(v_free + static_cast<int>(t & 1), static_cast<uint32_t>(t >> 1) & 1u, leaving, p.wait_ns)) bad = true;
+                }
+                if (__any_sync(~0u, bad)) {
+                    bad = true;
+                    break;
+                }
+                tc_after();
+                if (!soft_sync()) {
+                    bad = true;
+                    break;
+                }
+                const float2 ml0 = row_ml[0][r], ml1 = row_ml[1][r];
+                const bool has[2] = {n > 1 || static_cast<int>((g - 1) & 1) == 0, n > 1 || static_cast<int>((g - 1) & 1) == 1};
+                const float top = fmaxf(ml0.x, ml1.x), z = top == -INFINITY ? 0.0f : top;
+                const float f0 = ex2(ml0.x - z), f1 = ex2(ml1.x - z);
+                const float sum = fmaf(f0, ml0.y, f1 * ml1.y);
+                const int rows = min(kTcRows, w.nodes * p.group - w.rt * kTcRows);
+                const int node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
+                const int64_t row = static_cast<int64_t>(w.row0) + node;
+                T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
+                first_item = false;
+                auto finish = [&](int e0, const float (&v)[32], float total) {  // columns e0 .. e0 + 31
+                    const float inv = total > 0.0f ? __frcp_rn(total) : total == 0.0f ? 0.0f : total;
+                    if (r >= rows) return;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        if (e0 + e < p.c.dim) {
+                            union {
+                                uint4 u;
+                                T t[8];
+                            } y;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y.t[k] = from_f32<T>(v[e + k] * inv);
+                            if (p.out_vec) {
+                                *reinterpret_cast<uint4 *>(out + e0 + e) = y.u;
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) out[e0 + e + k] = y.t[k];
+                            }
+                        }
+                    }
+                };
+                auto finish_lse = [&](float mm, float total) {
+                    if (x == 0 && r < rows && p.lse) p.lse[row * p.heads_q + hq] = (mm + log2f(total)) * 0.693147180559945f;
+                };
+                // warpgroup x has the columns x * DP / 2 ..
+#pragma unroll 1
+                for (int q = 0; q < DP / 64; ++q) {
+                    const int e0 = x * (DP / 2) + 32 * q;
+                    float v[32], a[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        if (has[y]) {  // a warpgroup without a tile has nothing in its O
+                            tc_ld32(tmem + lanes + 256 + y * 128 + e0, a);
+                            const float f = y ? f1 : f0;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = fmaf(f, a[e], v[e]);
+                        }
+                    if (whole) {
+                        finish(e0, v, sum);
+                    } else {
+                        float4 *part = reinterpret_cast<float4 *>(p.partial + slot * pitch) + e0 / 4 * kTcRows + r;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) part[e * kTcRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
+                }
+                if (whole)
+                    finish_lse(z, sum);
+                else if (x == 0)
+                    reinterpret_cast<float2 *>(p.partial + slot * pitch + kTcRows * DP)[r] = make_float2(top, sum);
+                tc_before();
+                if (!soft_sync()) {  // both O are read: the next item's products may replace them
+                    bad = true;
+                    break;
+                }
+                tc_after();
+                if (!whole && w.item < p.tickets_n) {
+                    auto join = [&](int parts, int64_t head, int64_t at, int64_t step, bool last) {
+                        auto part_of = [&](int i) { return p.partial + (i == 0 ? head : at + i * step) * pitch; };
+                        float up = -INFINITY, total = 0.0f;
+                        for (int i = 0; i < parts; ++i) up = fmaxf(up, __ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r).x);
+                        const float zz = up == -INFINITY ? 0.0f : up;
+                        for (int i = 0; i < parts; ++i) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r);
+                            total = fmaf(ex2(ml.x - zz), ml.y, total);
+                        }
+#pragma unroll 1
+                        for (int q = 0; q < DP / 64; ++q) {
+                            const int e0 = x * (DP / 2) + 32 * q;
+                            float v[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                            for (int i = 0; i < parts; ++i) {
+                                const float f = ex2(__ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r).x - zz);
+                                const float4 *src = reinterpret_cast<const float4 *>(part_of(i)) + e0 / 4 * kTcRows + r;
+                                float4 y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + e * kTcRows);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    v[4 * e] = fmaf(f, y[e].x, v[4 * e]);
+                                    v[4 * e + 1] = fmaf(f, y[e].y, v[4 * e + 1]);
+                                    v[4 * e + 2] = fmaf(f, y[e].z, v[4 * e + 2]);
+                                    v[4 * e + 3] = fmaf(f, y[e].w, v[4 * e + 3]);
+                                }
+                            }
+                            if (last) {
+                                finish(e0, v, total);
+                            } else {
+                                float4 *to4 = reinterpret_cast<float4 *>(p.partial + head * pitch) + e0 / 4 * kTcRows + r;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) to4[e * kTcRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            }
+                        }
+                        if (last) {
+                            finish_lse(zz, total);
+                        } else {
+                            if (!soft_sync()) bad = true;  // everybody has read the first part's maximum
+                            if (x == 0) reinterpret_cast<float2 *>(p.partial + head * pitch + kTcRows * DP)[r] = make_float2(up, total);
+                        }
+                    };
+                    auto arrive = [&](unsigned *ticket, unsigned count) -> bool {
+                        __threadfence();
+                        if (!soft_sync()) bad = true;
+                        if (tid == 0 && !bad) {
+                            const unsigned t = atomicAdd(ticket, 1u);
+                            is_last = t == count - 1;
+                            if (is_last) *ticket = 0;
+                        }
+                        if (!soft_sync()) bad = true;
+                        const bool yes = *const_cast<volatile int *>(&is_last) != 0;
+                        if (!soft_sync()) bad = true;
+                        if (yes) __threadfence();
+                        return yes && !bad;
+                    };
+                    const int c0 = static_cast<int>(split.owner(w.first)), c1 = static_cast<int>(split.owner(w.first + w.tiles_k - 1));
+                    const int slot_c0 = split.begin(c0) >= w.first - kTcItemUnits ? 2 * c0 : 2 * c0 + 1;
+                    if (c1 - c0 < kJoinGroup) {
+                        if (arrive(p.tickets + w.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
+                    } else {
+                        const int grp = blockIdx.x / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
+                        const int lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
+                        if (arrive(p.group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1)) {
+                            join(hi - lo + 1, lo == c0 ? slot_c0 : 2 * lo, 2 * lo, 2, false);
+                            if (arrive(p.tickets + w.item, g1 - g0 + 1)) join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
+                        }
+                    }
+                }
+                ++item_no;
+            }
+            if (bad || !more(w)) break;
+            advance(w);
+        }
+        if (bad) {
+            leave = 1;
+            if (lane == 0) atomicOr(p.err, kTcErrWait);
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == kTcMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+}  // namespace kv

@@ -61,6 +61,8 @@ def bind(lib: ctypes.CDLL) -> None:
             ("q8kv_cache_move", [ref(CacheDesc), i64, i64, p, p, p]),
             ("q8kv_attend_plan", [ref(p), i32, i32, i32, i32, i64, ctypes.c_int]),
             ("q8kv_attend", [p, ref(CacheDesc), p, p]),
+            ("q8kv_attend_check", [p, ref(i32)]),
+            ("q8kv_attend_set_wait", [p, ctypes.c_uint64]),
             ("q8kv_attend_destroy", [p]),
             ("q8kv_verify_plan", [ref(p), i32, i64, i32, ctypes.c_int]),
             ("q8kv_verify", [p, p, p]),
@@ -352,6 +354,21 @@ class TreeAttention(_Plan):
         if status:
             _fail(status, "q8kv_attend")
         return (out, sums) if lse else out
+
+
+    def check(self) -> int:
+        """Synchronise and return (and clear) whether a bounded wait of the plan's kernels ran out (1, else 0)."""
+        word = ctypes.c_int32()
+        status = _library().q8kv_attend_check(self._h, ctypes.byref(word))
+        if status:
+            _fail(status, "q8kv_attend_check")
+        return word.value
+
+    def set_wait(self, wait_ns: int = 0) -> None:
+        """For tests of the bounded waits: their bound (0: the default)."""
+        status = _library().q8kv_attend_set_wait(self._h, int(wait_ns))
+        if status:
+            _fail(status, "q8kv_attend_set_wait")
 
 
 class TreeVerify(_Plan):

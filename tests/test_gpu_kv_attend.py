@@ -128,6 +128,140 @@ def test_heads_side_by_side_cut_between_ctas(q8mv):
          layout="token", cols=9000).check()
 
 
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 112, 128])
+@pytest.mark.parametrize("layout,page", [("head", 16), ("token", 7)])
+def test_wide_trees(q8mv, dim, layout, page):
+    """More than 32 bf16 query rows a request: the tensor-memory path."""
+    Case(q8mv, dim, [300, 0, 5, 1000], [40, 0, 33, 70], heads=2, group=2, dim=dim, page=page, dtype="bfloat16",
+         layout=layout).check()
+
+
+@pytest.mark.parametrize("length", [0, 1, 15, 16, 90, 112, 127, 128, 129, 255, 256, 257, 700])
+@pytest.mark.parametrize("tree", [True, False])
+def test_wide_trees_around_the_tiles(q8mv, length, tree):
+    for nodes in (34, 129, 150):
+        Case(q8mv, length, [length], [nodes], heads=1, group=1, dim=64, page=5, dtype="bfloat16", tree=tree).check()
+
+
+def test_wide_trees_cut_between_ctas(q8mv):
+    Case(q8mv, 1, [20001], [35], heads=1, group=2, dim=64, page=64, dtype="bfloat16").check()
+    Case(q8mv, 2, [9000, 20011, 1, 5, 13000], [40, 33, 50, 35, 41], heads=2, group=4, dim=128, page=32,
+         dtype="bfloat16").check()
+    Case(q8mv, 3, [90] * 60, [40] * 60, heads=3, group=1, dim=128, page=16, dtype="bfloat16").check()
+
+
+def test_wide_trees_the_same_bits_again(q8mv):
+    import torch
+
+    c = Case(q8mv, 4, [3000, 700, 0], [50, 90, 36], heads=4, group=1, dim=128, dtype="bfloat16")
+    a = c.run()
+    for _ in range(20):
+        for x, y in zip(a, c.run()):
+            assert torch.equal(x, y)
+    assert c.plan.check() == 0
+    c.check(a)
+
+
+def test_wide_trees_and_what_is_not_seen(q8mv):
+    """Rows that see nothing; NaN, infinities and huge scales in unseen nodes and unused places."""
+    import torch
+
+    c = Case(q8mv, 5, [33, 140, 0], [40, 45, 50], heads=2, group=1, dim=64, dtype="bfloat16")
+    for b in range(3):
+        c.seen[b][:, 2] = False
+        c.seen[b][:, 37] = False
+    c.seen[2][5] = False
+    mask = np.zeros((135, 2), np.uint32)
+    for b, t in enumerate(c.nodes):
+        for i, j in zip(*np.nonzero(c.seen[b])):
+            mask[c.starts[b] + i, j // 32] |= np.uint32(1 << (j % 32))
+    c.mask = torch.from_numpy(mask.view(np.int32)).cuda()
+    c.check()
+    used = np.zeros(c.host.kc.shape[0] * 16, bool)
+    for b, (p, t) in enumerate(zip(c.lengths, c.nodes)):
+        for j in [*range(p), *(p + i for i in range(t) if i not in (2, 37))]:
+            used[c.table[b, j // 16] * 16 + j % 16] = True
+    for bad in (np.nan, np.inf, -np.inf, 3e38, 1e30):
+        for a in (c.host.ks, c.host.vs):
+            flat = a.reshape(a.shape[0], a.shape[1], 16, -1)
+            for s in np.flatnonzero(~used):
+                flat[s // 16, :, s % 16] = bad
+        c.device()
+        c.check()
+    c.table[0, 1] = 10 ** 9
+    c.table[1, 0] = -5
+    c.device()
+    c.check()
+
+
+def test_wide_trees_and_seen_values_that_are_not_finite(q8mv):
+    import torch
+
+    c = Case(q8mv, 6, [20], [40], heads=1, group=1, dim=64, dtype="bfloat16", tree=False)
+    slot = c.table[0, 50 // 16] * 16 + 50 % 16  # node 30
+    c.host.vs[slot // 16, :, slot % 16] = np.nan
+    out, _ = c.run()
+    assert torch.isfinite(out[:30]).all() and torch.isnan(out[30:]).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1e12, 1e30])
+def test_wide_trees_with_scales_of_any_size(q8mv, size):
+    c = Case(q8mv, 7, [200], [40], dim=64, dtype="bfloat16")
+    c.host.vs *= np.float32(size)
+    c.check()
+    c = Case(q8mv, 8, [200], [40], dim=64, dtype="bfloat16")
+    c.host.ks *= np.float32(size)
+    c.q = (c.q * (1 / size)).to(c.q.dtype)
+    c.check()
+
+
+def test_wide_trees_strided_rows(q8mv):
+    import torch
+
+    c = Case(q8mv, 9, [300], [40], heads=2, group=2, dim=128, dtype="bfloat16")
+    want = c.run()
+    outs = torch.full((40, 4, 140), 7.0, device="cuda", dtype=torch.bfloat16)
+    got = c.run(out=outs[:, :, 5:133])
+    assert torch.equal(got[0], want[0])
+    assert bool((outs[:, :, :5] == 7).all()) and bool((outs[:, :, 133:] == 7).all())
+
+
+@pytest.mark.parametrize("scale", [30.0, -30.0])
+def test_wide_trees_large_scores(q8mv, scale):
+    """Scores hundreds apart: where one key has all of a row's weight (the next below e^-40), out is its value within
+    the two roundings of a value (f16 in the product, bf16 at the end), measured by the row's largest value."""
+    c = Case(q8mv, 12, [300], [40], heads=2, group=2, dim=128, dtype="bfloat16")
+    out, lse = (x.double().cpu().numpy() for x in c.run(scale=scale))
+    pos = np.arange(340)
+    keys, values = c.host.rows(c.table[0, pos // 16].astype(np.int64) * 16 + pos % 16)
+    q = c.q.double().cpu().numpy()
+    alone = 0
+    for i in range(40):
+        seen = np.array([j < 300 or c.sees(0, i, int(j) - 300) for j in pos])
+        for a in range(4):
+            s = np.where(seen, scale * (keys[:, a // 2] @ q[i, a]), -np.inf)
+            first, second = np.argsort(-s)[:2]
+            assert abs(lse[i, a] - s[first]) <= 1e-6 * abs(scale) * np.abs(keys[:, a // 2] * q[i, a]).sum(-1).max() + 1
+            if s[first] - s[second] > 40:
+                alone += 1
+                v = values[first, a // 2]
+                assert np.all(np.abs(out[i, a] - v) <= (2.0 ** -11 + 2.0 ** -8) * np.abs(v).max())
+    assert alone > 40
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_plan_goes_on(q8mv):
+    c = Case(q8mv, 10, [3000, 100], [40, 50], heads=2, group=2, dim=128, dtype="bfloat16")
+    c.check()
+    c.plan.set_wait(1)  # nanosecond: the first wait that has to wait runs out
+    c.run()
+    assert c.plan.check() == 1
+    c.plan.set_wait(0)
+    assert c.plan.check() == 0
+    c.check()
+    with pytest.raises(q8mv.Q8mvError):
+        c.plan.set_wait(11 * 10 ** 9)
+
+
 def test_items_cut_between_ctas(q8mv):
     """Few heads, long sequences: many CTAs share an item, and a CTA has two parts."""
     Case(q8mv, 1, [40001], [1], heads=1, group=2, dim=64, page=64, tree=False).check()

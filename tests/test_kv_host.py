@@ -36,7 +36,7 @@ def declared():
 def test_every_declared_entry_point_is_exported_and_no_other(q8):
     out = subprocess.run(["nm", "-D", "--defined-only", q8.LIB], check=True, capture_output=True, text=True).stdout
     ours = sorted(s for s in (line.split()[-1] for line in out.splitlines() if line.strip()) if s.startswith("q8kv_"))
-    assert ours == declared() and len(ours) == 9
+    assert ours == declared() and len(ours) == 11
 
 
 def test_structures_match_the_header(kv, tmp_path):
