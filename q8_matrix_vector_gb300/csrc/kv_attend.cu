@@ -154,6 +154,7 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.group_tickets = plan->tickets + plan->max_items;
     p.err = plan->err;
     p.wait_ns = plan->wait_ns;
+    p.q_vec = kv::aligned(a->q, 16) && ((a->q_row | a->q_head) & 7) == 0;
     p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;
     // 8, 16 or 32 query rows at a time, by the mean of a request's: the fewest that hold them.
     // With 8, and a token's heads side by side, each warp can take a head of its own, so that a CTA reads longer

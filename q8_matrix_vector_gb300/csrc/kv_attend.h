@@ -37,7 +37,7 @@ struct AttendParams {
     unsigned *group_tickets;  // two per kJoinGroup CTAs
     int *err;           // the plan's error word, and the bound on waits (kRows128)
     uint64_t wait_ns;
-    int out_vec;        // 16-byte stores of eight outputs are aligned (kRows128)
+    int q_vec, out_vec; // 16-byte loads of eight queries, stores of eight outputs are aligned (kRows128)
 };
 
 // What an item is: 8, 16 or 32 query rows (node, head of the group) of one kv head

@@ -7,15 +7,15 @@
 // Work is the line of units of kv_attend.cuh with 128-row items and tiles of 128
 // keys, one CTA per SM.  With 128 rows a code meets 128 multiplications on each
 // side, so the products belong to tcgen05.mma and the rest of the SM keeps it fed:
-//   * eight convert warps read the next tile's codes and scales into registers
-//     while they turn this one's into f16 operands in shared memory.  A key's row
-//     is normalised by a power of two (per 16 keys, or per key where some of them
-//     are drafted) that goes into the softmax, and code times scale is formed with
-//     the scale in two f16 parts.  K is kept in two f16 parts, 22 bits, since a
-//     score's error is a weight's relative one and lse is f32; V is rounded once to
-//     11 bits, as outputs are bf16.  (f32 and f16 outputs stay with kv_attend.cuh.)
-//     K and V tiles have the same layout, core matrices of 8 keys x 8 e: K is read
-//     K-major, V MN-major.
+//   * four convert warps take 32 keys of a tile each.  cp.async brings the next
+//     tile's codes and scales while they turn this one's into f16 operands in shared
+//     memory, K a tile ahead of V.  A key's row is normalised by a power of two (one
+//     for the warp's 32 keys, or one per key where some of them are drafted) that
+//     goes into the softmax, and code times scale is formed with the scale in two
+//     f16 parts.  K is kept in two f16 parts, 22 bits, since a score's error is a
+//     weight's relative one and lse is f32; V is rounded once to 11 bits, as outputs
+//     are bf16.  (f32 and f16 outputs stay with kv_attend.cuh.)  K and V tiles have
+//     the same layout, core matrices of 8 keys x 8 e: K is read K-major, V MN-major.
 //   * one thread issues the MMAs: S = Q K^T of tile g (lower part, then upper), then
 //     O += P V of tile g - 1.
 //   * two softmax warpgroups take alternate tiles, a thread a row, each with its own
@@ -33,7 +33,7 @@
 namespace kv {
 
 constexpr int kTcRows = 128, kTcKeys = 128;
-constexpr int kTcSoftWarps = 8, kTcConvWarps = 8;
+constexpr int kTcSoftWarps = 8, kTcConvWarps = 4;
 constexpr int kTcMmaWarp = kTcSoftWarps + kTcConvWarps;
 constexpr int kTcThreads = (kTcMmaWarp + 1) * 32;
 constexpr int kTcChunk = kTcKeys * 16 + 16;     // bytes from 8 e to the next 8: 128 rows of 16, and 16 against bank conflicts
@@ -46,9 +46,14 @@ constexpr int kTcItemUnits = 3;
 template <int DP>
 struct TcSmem {
     static constexpr int kTile = DP / 8 * kTcChunk;   // one operand of 128 rows
-    static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kLo = 5 * kTile, kMeta = 6 * kTile;
+    static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kLo = 4 * kTile, kMeta = 5 * kTile;
     static constexpr int kMetaTile = kTcKeys * 16;    // per key: K's factor, E, 2^-E, flag
-    static constexpr int kTotal = kMeta + 4 * kMetaTile;
+    // a convert warp's next 32 keys as they are in the cache: codes of K and V, scales of both
+    static constexpr int kRaw = kMeta + 4 * kMetaTile, kRawV = 32 * DP, kRawS = 64 * DP;
+    static constexpr int kRawWarp = 64 * DP + 2 * 32 * (DP / 32) * 4;
+    // its normalised scales, V's of two tiles and K's
+    static constexpr int kVs = kRaw + kTcConvWarps * kRawWarp, kVsWarp = 3 * 32 * (DP / 32) * 4;
+    static constexpr int kTotal = kVs + kTcConvWarps * kVsWarp;
     static constexpr int kPart = kTcRows * (DP + 2);  // floats of a partial result: O by 4 columns x 128 rows, m, l
 };
 
@@ -124,6 +129,16 @@ __device__ __forceinline__ void tc_ld32(uint32_t at, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// 16 columns of the thread's lane, not waited for
+__device__ __forceinline__ void tc_ld16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_st32(uint32_t at, const float (&v)[32]) {
     uint32_t r[32];
 #pragma unroll
@@ -137,13 +152,10 @@ __device__ __forceinline__ void tc_st32(uint32_t at, const float (&v)[32]) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(at),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+__device__ __forceinline__ void tc_st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // two f16 codes times a scale in two parts, rounded once, and what that leaves (exact but for c * lo's last bits)
@@ -162,13 +174,22 @@ __device__ __forceinline__ uint32_t tc_scaled(uint32_t codes, uint32_t hi, uint3
 // power of two with exponent e
 __device__ __forceinline__ float tc_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
+// A convert warp's place: an item, and which of its tiles here.
+struct TcTile {
+    Place w;
+    int64_t kt;
+    int n, i;  // the item's tiles of this CTA, and which of them
+    bool any;
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const AttendParams p) {
     using T = __nv_bfloat16;
     using S = TcSmem<DP>;
-    constexpr int PARTS = DP / 16, KPL = 32 / PARTS, NL = 16 / KPL;  // 16-byte pieces of a row, keys of a load, loads
+    constexpr int PARTS = DP / 16, KPL = 32 / PARTS, NL = 32 / KPL;  // 16-byte pieces of a row, keys of a load, loads
+    constexpr int NB = DP / 32;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2];
+    __shared__ __align__(8) uint64_t k_full[2], k_free[2], v_full, v_free[2], s_full[2], p_full[2];
     __shared__ __align__(8) uint64_t soft_bar;            // among the softmax warps
     __shared__ __align__(8) uint64_t lo_free;             // K's lower part, which has one buffer
     __shared__ uint32_t tmem_at;
@@ -177,8 +198,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
     __shared__ int64_t start_b, start_item, start_unit;
     __shared__ float row_mul[4][kTcRows];                // by item
     __shared__ float2 row_ml[2][kTcRows];                // a warpgroup's maximum and sum
-    __shared__ uint32_t there_bits[4][kTcConvWarps];     // by tile: the warp's keys that are there
-    __shared__ uint32_t plain_bits[4];                   // by tile: warps whose keys all rows see, one normaliser each
+    __shared__ TcTile tiles[kTcConvWarps][2];
+    __shared__ Place places[kTcSoftWarps];
+    __shared__ uint32_t there_bits[4][kTcConvWarps];     // by tile: the keys that are there
+    __shared__ uint32_t plain_keys[4][kTcConvWarps];     // by tile: whether all rows see a warp's keys, with one normaliser
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const volatile int *leaving = &leave;
@@ -213,7 +236,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         if (tid == 0) {
             for (int i = 0; i < 2; ++i) {
                 tc_bar_init(k_full + i, kTcConvWarps);
-                tc_bar_init(v_full + i, kTcConvWarps);
                 tc_bar_init(k_free + i, 1);
                 tc_bar_init(v_free + i, 1);
                 tc_bar_init(s_full + i, 1);
@@ -221,8 +243,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             }
             tc_bar_init(&soft_bar, kTcSoftWarps);
             tc_bar_init(&lo_free, 1);
+            tc_bar_init(&v_full, kTcConvWarps);
             leave = 0;
-            for (int i = 0; i < 4; ++i) plain_bits[i] = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
@@ -306,9 +328,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             auto second = [&](int64_t t, bool first) -> bool {  // O += P V of tile t
                 const int x = static_cast<int>(t & 1);
                 const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
-                if (!tc_wait(p_full + x, ph, leaving, p.wait_ns) || !tc_wait(v_full + x, ph, leaving, p.wait_ns)) return false;
+                if (!tc_wait(p_full + x, ph, leaving, p.wait_ns) ||
+                    !tc_wait(&v_full, static_cast<uint32_t>(t) & 1u, leaving, p.wait_ns))
+                    return false;
                 tc_after();
-                const uint32_t v = base + S::kV + x * S::kTile;
+                const uint32_t v = base + S::kV;
 #pragma unroll
                 for (int k = 0; k < kTcKeys / 16; ++k)
                     tc_mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, tc_desc(v + k * 256, 128, kTcChunk), idesc_o,
@@ -363,47 +387,100 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         const int cw = warp - kTcSoftWarps, part = lane % PARTS, sub = lane / PARTS;
         const bool live = part * 16 < p.c.dim;
         const int ct = tid - kTcSoftWarps * 32;  // thread among the convert warps
-        int64_t g = 0;
-        int item_no = 0;
-        uint4 kr[NL], vr[NL];
-        float ksc[NL], vsc[NL];
-        uint32_t there = 0;
-        auto fetch = [&](const Place &x, int64_t tile) {
-            const int64_t pos = tile * kTcKeys + cw * 16 + (lane & 15);
-            const int64_t keys = min(static_cast<int64_t>(x.prefix) + x.nodes, static_cast<int64_t>(p.table_cols) * p.c.page_size);
-            uint32_t row = kNoRow;
-            if (pos < keys) {
-                const uint32_t at = static_cast<uint32_t>(pos), col = (__umulhi(at, p.page_mul) + at) >> p.page_shift;
-                const int page = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_row + col);
-                if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.c.pages))
-                    row = static_cast<uint32_t>(row_of(p.c, page, x.h, static_cast<int>(at - col * p.c.page_size)));
+        unsigned char *raw = smem + S::kRaw + cw * S::kRawWarp;
+        float *raw_s = reinterpret_cast<float *>(raw + S::kRawS);  // K: [key][NB], then V
+        float *v_norm = reinterpret_cast<float *>(smem + S::kVs + cw * S::kVsWarp);  // [tile % 2][key][NB]
+        for (int i = lane; i < S::kRawWarp / 16; i += 32) reinterpret_cast<uint4 *>(raw)[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        // A tile of the CTA: its item and its number there.  The warp keeps two in shared memory, this one and the
+        // next but one: in registers they would push the codes out.
+        TcTile *const here = tiles[cw], *const ahead = tiles[cw] + 1;
+        auto settle = [&](TcTile &t) {  // to the first item with tiles, from t.w on
+            for (;;) {
+                t.n = tiles_of(t.w, &t.kt);
+                t.i = 0;
+                t.any = t.n > 0;
+                if (t.any || !more(t.w)) return;
+                advance(t.w);
             }
-            there = __ballot_sync(~0u, row != kNoRow) & 0xFFFFu;
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const uint32_t r = __shfl_sync(~0u, row, i * KPL + sub);
-                kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-                ksc[i] = vsc[i] = 0.0f;
-                if (r != kNoRow && live) {
-                    const uint64_t at = static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim) + part * 16;
-                    kr[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.k_codes + at));
-                    vr[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.v_codes + at));
-                    const uint64_t sc = static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.blocks) + (part >> 1);
-                    ksc[i] = __ldg(p.c.k_scales + sc);
-                    vsc[i] = __ldg(p.c.v_scales + sc);
+        };
+        auto step = [&](TcTile *at) {
+            __syncwarp();
+            if (lane == 0 && at->any) {
+                ++at->kt;
+                if (++at->i == at->n) {
+                    at->any = more(at->w);
+                    if (at->any) {
+                        TcTile t = *at;
+                        advance(t.w);
+                        settle(t);
+                        *at = t;
+                    }
                 }
             }
+            __syncwarp();
+        };
+        // row of the lane's key in a tile, or kNoRow
+        auto find = [&](const TcTile *t) -> uint32_t {
+            if (!t->any) return kNoRow;
+            const int64_t pos = t->kt * kTcKeys + cw * 32 + lane;
+            const int64_t keys = min(static_cast<int64_t>(t->w.prefix) + t->w.nodes, static_cast<int64_t>(p.table_cols) * p.c.page_size);
+            if (pos >= keys) return kNoRow;
+            const uint32_t at = static_cast<uint32_t>(pos), col = (__umulhi(at, p.page_mul) + at) >> p.page_shift;
+            const int page = __ldg(p.table + static_cast<int64_t>(t->w.b) * p.table_row + col);
+            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
+            return static_cast<uint32_t>(row_of(p.c, page, t->w.h, static_cast<int>(at - col * p.c.page_size)));
+        };
+        const bool wide_scales = NB == 4 && p.c.blocks == 4;
+        auto codes = [&](const int8_t *from, uint32_t to, uint32_t row) {  // the warp's rows of one array
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const uint32_t r = __shfl_sync(~0u, row, j * KPL + sub);
+                if (r != kNoRow && live)
+                    cp_async16(to + (j * KPL + sub) * DP + part * 16, from + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim) + part * 16);
+            }
+        };
+        auto issue_a = [&](uint32_t row) {  // codes of K, scales of both; an absent key's scales are 0
+            codes(p.c.k_codes, tc_smem(raw), row);
+            const uint32_t at = tc_smem(raw_s) + lane * (NB * 4);
+            if (row != kNoRow) {
+                const float *ks = p.c.k_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
+                const float *vs = p.c.v_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
+                if (wide_scales) {
+                    cp_async16(at, ks);
+                    cp_async16(at + 32 * NB * 4, vs);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        if (b < p.c.blocks) {
+                            cp_async4(at + 4 * b, ks + b);
+                            cp_async4(at + 32 * NB * 4 + 4 * b, vs + b);
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) raw_s[lane * NB + b] = raw_s[32 * NB + lane * NB + b] = 0.0f;
+            }
+            cp_commit();
+        };
+        auto issue_b = [&](uint32_t row) {  // codes of V
+            codes(p.c.v_codes, tc_smem(raw) + S::kRawV, row);
+            cp_commit();
         };
         // exponent e with scales below 2^(e + 7): codes times scale / 2^e stay below 2^14
         auto exponent = [](uint32_t bits) -> int { return max(min(static_cast<int>(bits >> 23) - 127 - 6, 120), -100); };
-        // 8 neighbouring e of a key to two places of a tile; half of a row's lanes store their upper 8 first: the
-        // eight lanes of a phase then meet 8 different banks
+        // A lane's two groups of 8 e go to two places of a tile.  Half of a row's lanes store their upper group first
+        // (their words are swapped when they are read): the eight lanes of a phase then meet 8 different banks.
+        const bool up = part >= PARTS / 2;
+        const uint32_t place = 2 * part * kTcChunk;
+        const uint32_t place0 = place + (up ? kTcChunk : 0), place1 = place + (up ? 0 : kTcChunk);
         auto store = [&](uint32_t tile, int key, const uint32_t (&o)[8]) {
-            const bool up = part >= PARTS / 2;
-            const uint32_t at = tile + 2 * part * kTcChunk + key * 16;
-            const uint32_t first = at + (up ? kTcChunk : 0), then = at + (up ? 0 : kTcChunk);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(first), "r"(up ? o[4] : o[0]), "r"(up ? o[5] : o[1]), "r"(up ? o[6] : o[2]), "r"(up ? o[7] : o[3]) : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(then), "r"(up ? o[0] : o[4]), "r"(up ? o[1] : o[5]), "r"(up ? o[2] : o[6]), "r"(up ? o[3] : o[7]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + place0 + key * 16), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + place1 + key * 16), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+        };
+        auto read = [&](const unsigned char *from, int j) -> uint4 {
+            const uint4 c = *reinterpret_cast<const uint4 *>(from + (j * KPL + sub) * DP + part * 16);
+            return up ? make_uint4(c.z, c.w, c.x, c.y) : c;
         };
         // 16 codes times scale / 2^e to rows of the tile, and what that rounds off
         auto convert = [&](uint32_t tile, int key, const uint4 &c, float scale, uint32_t (*rest)[8]) {
@@ -416,129 +493,180 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 o[i] = tc_scaled(unbias(__byte_perm(in[i / 2], 0x64646464u, i % 2 ? 0x4342u : 0x4140u)), h2, l2, rest ? &(*rest)[i] : nullptr);
             store(tile, key, o);
         };
-        int64_t kt0;
-        int n = tiles_of(w, &kt0);
-        if (n > 0) fetch(w, kt0);
-        for (;;) {
-            if (n > 0) {
+        auto waited = [&](uint64_t *bar, int64_t phase) -> bool {  // whole warps
+            if (!tc_wait(bar, static_cast<uint32_t>(phase) & 1u, leaving, p.wait_ns)) bad = true;
+            bad = __any_sync(~0u, bad);
+            return !bad;
+        };
+
+        int item_no = -1;
+        // q and K of tile g
+        auto do_k = [&](int64_t g, uint32_t row, uint32_t row_after) -> bool {
+            const TcTile &t = *here;
+            const bool all_before = t.kt * kTcKeys + cw * 32 + 32 <= t.w.prefix;
+            if (t.i == 0) {
                 // q, once the previous item's last S has been computed
-                if (g > 0 && !tc_wait(k_free + static_cast<int>((g - 1) & 1), static_cast<uint32_t>((g - 1) >> 1) & 1u, leaving, p.wait_ns)) bad = true;
-                if (__any_sync(~0u, bad)) {
-                    bad = true;
-                    break;
-                }
-                {
-                    const int r = ct >> 1, half = ct & 1;  // two threads a row
-                    const int rows = min(kTcRows, w.nodes * p.group - w.rt * kTcRows);
-                    const int idx = w.rt * kTcRows + r, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
-                    const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
-                    uint32_t top = 0;
-                    for (int e = half * (DP / 2); e < half * (DP / 2) + DP / 2; ++e)
-                        if (r < rows && e < p.c.dim) top = max(top, __float_as_uint(to_f32(src[e])) & 0x7FFFFFFFu);
-                    top = max(top, __shfl_xor_sync(~0u, top, 1));
-                    const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
-                    const float down = copysignf(tc_pow2(-ex), p.scale_log2);
-                    for (int c8 = half * (DP / 16); c8 < half * (DP / 16) + DP / 16; ++c8) {
-                        uint32_t o[4];
+                ++item_no;
+                if (g > 0 && !waited(k_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
+                const int r = ct;
+                const int rows = min(kTcRows, t.w.nodes * p.group - t.w.rt * kTcRows);
+                const int idx = t.w.rt * kTcRows + r, node = idx / p.group, hq = t.w.h * p.group + idx - node * p.group;
+                const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(t.w.row0) + node) * p.q_row + hq * p.q_head;
+                union Eight {
+                    uint4 u;
+                    T t[8];
+                };
+                constexpr int H = DP / 16;  // half a row's groups of 8
+                Eight x[H];
+                auto load = [&](int half) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int at = c8 * 8 + 2 * e;
-                            const bool in = r < rows && at < p.c.dim;
-                            o[e] = pack_half2(in ? to_f32(src[at]) * down : 0.0f, in ? to_f32(src[at + 1]) * down : 0.0f);
+                    for (int k = 0; k < H; ++k) {
+                        const int e = 8 * (half * H + k);
+                        x[k].u = make_uint4(0, 0, 0, 0);
+                        if (r < rows && e < p.c.dim) {
+                            if (p.q_vec) {
+                                x[k].u = __ldg(reinterpret_cast<const uint4 *>(src + e));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) x[k].t[j] = src[e + j];
+                            }
                         }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + c8 * kTcChunk + r * 16), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
                     }
-                    if (half == 0) row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
+                };
+                uint32_t top = 0;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    load(half);
+#pragma unroll
+                    for (int k = 0; k < H; ++k)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(x[k].t[j])) & 0x7FFFFFFFu);
+                }
+                const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
+                const float down = copysignf(tc_pow2(-ex), p.scale_log2);
+#pragma unroll 1
+                for (int half = 1; half >= 0; --half) {  // the second half is still here
+                    if (half == 0) load(0);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(to_f32(x[k].t[2 * e]) * down, to_f32(x[k].t[2 * e + 1]) * down);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + (half * H + k) * kTcChunk + r * 16), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                    }
+                }
+                row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
+            }
+            if (g <= 1)
+                cp_wait<0>();
+            else
+                cp_wait<1>();  // all but the V after it
+            __syncwarp();
+            const int x = static_cast<int>(g & 1), ring = static_cast<int>(g & 3);
+            // the buffer of tile g - 2; then the rings' entries of tile g - 4 are free too
+            if (g >= 2 && !waited(k_free + x, (g >> 1) - 1)) return false;
+            float4 *meta = reinterpret_cast<float4 *>(smem + S::kMeta + ring * S::kMetaTile) + cw * 32;
+            float *vn = v_norm + x * (32 * NB);
+            const uint32_t there = __ballot_sync(~0u, row != kNoRow);
+            bool plain = all_before && there == ~0u;
+            float *kn = v_norm + 2 * (32 * NB);
+            // ---- normalisers, a lane a key: of each key, and of all keys if every row sees them
+            {
+                float kk[NB], vv[NB];
+                uint32_t bk = 0, bv = 0;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    kk[b] = raw_s[lane * NB + b];
+                    vv[b] = raw_s[32 * NB + lane * NB + b];
+                    bk = max(bk, __float_as_uint(kk[b]) & 0x7FFFFFFFu);
+                    bv = max(bv, __float_as_uint(vv[b]) & 0x7FFFFFFFu);
+                }
+                // a scale that is not finite: the key's rows are 0 here, and the softmax makes NaN of who sees it
+                const bool odd = bk >= 0x7F800000u || bv >= 0x7F800000u;
+                plain = plain && !__any_sync(~0u, odd);
+                if (plain) {
+                    bk = __reduce_max_sync(~0u, bk);
+                    bv = __reduce_max_sync(~0u, bv);
+                }
+                const int ek = exponent(odd ? 0 : bk), ev = exponent(odd ? 0 : bv);
+                meta[lane] = make_float4(tc_pow2(ek), static_cast<float>(ev), tc_pow2(-ev), odd ? 1.0f : 0.0f);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    vn[lane * NB + b] = odd ? 0.0f : vv[b] * tc_pow2(-ev);
+                    kn[lane * NB + b] = odd ? 0.0f : kk[b] * tc_pow2(-ek);
                 }
             }
-            for (int i = 0; i < n; ++i, ++g) {
-                const int x = static_cast<int>(g & 1), ring = static_cast<int>(g & 3);
-                const uint32_t ph = static_cast<uint32_t>(g >> 1) & 1u;
-                const int64_t tile = kt0 + i;
-                const bool drafts = tile * kTcKeys + cw * 16 + 16 > w.prefix;
-                const bool plain = !drafts && there == 0xFFFFu;
-                // ---- normalisers: of each key, and of the warp's keys if all rows see them
-                int ek[NL], ev[NL];
-                bool odd[NL];
-                uint32_t top_k = 0, top_v = 0;
-#pragma unroll
-                for (int j = 0; j < NL; ++j) {
-                    uint32_t bk = __float_as_uint(ksc[j]) & 0x7FFFFFFFu, bv = __float_as_uint(vsc[j]) & 0x7FFFFFFFu;
-#pragma unroll
-                    for (int d = 1; d < PARTS; d *= 2) {
-                        bk = max(bk, __shfl_xor_sync(~0u, bk, d));
-                        bv = max(bv, __shfl_xor_sync(~0u, bv, d));
-                    }
-                    // a scale that is not finite: the key's rows are 0 here, and the softmax makes NaN of who sees it
-                    odd[j] = bk >= 0x7F800000u || bv >= 0x7F800000u;
-                    if (odd[j]) {
-                        ksc[j] = vsc[j] = 0.0f;
-                        bk = bv = 0;
-                    }
-                    ek[j] = exponent(bk);
-                    ev[j] = exponent(bv);
-                    top_k = max(top_k, bk);
-                    top_v = max(top_v, bv);
-                }
-                const bool any_odd = __any_sync(~0u, odd[0] || odd[NL - 1] || (NL > 2 && (odd[1] || odd[NL - 2])));
-                if (plain && !any_odd) {
-                    const int uk = exponent(__reduce_max_sync(~0u, top_k)), uv = exponent(__reduce_max_sync(~0u, top_v));
-#pragma unroll
-                    for (int j = 0; j < NL; ++j) {
-                        ek[j] = uk;
-                        ev[j] = uv;
-                    }
-                }
-                // ---- K
-                if (g >= 2 && !tc_wait(k_free + x, ph ^ 1u, leaving, p.wait_ns)) bad = true;
-                if (__any_sync(~0u, bad)) {
-                    bad = true;
-                    break;
-                }
-                float4 *meta = reinterpret_cast<float4 *>(smem + S::kMeta + ring * S::kMetaTile);
-                const uint32_t kb = base + S::kK + x * S::kTile, vb = base + S::kV + x * S::kTile;
-#pragma unroll
-                for (int j = 0; j < NL; ++j) {
-                    const int key = cw * 16 + j * KPL + sub;
-                    uint32_t rest[8];
-                    convert(kb, key, kr[j], ksc[j] * tc_pow2(-ek[j]), &rest);
-                    if (j == 0 && g >= 1) {  // the tile before has used its lower part
-                        if (!tc_wait(&lo_free, static_cast<uint32_t>(g - 1) & 1u, leaving, p.wait_ns)) bad = true;
-                        if (__any_sync(~0u, bad)) bad = true;
-                    }
-                    store(base + S::kLo, key, rest);
-                    if (part == 0) meta[key] = make_float4(tc_pow2(ek[j]), static_cast<float>(ev[j]), tc_pow2(-ev[j]), odd[j] ? 1.0f : 0.0f);
-                }
-                if (bad) break;
-                if (lane == 0) {
-                    there_bits[ring][cw] = there;
-                    if (plain && !any_odd)
-                        atomicOr(&plain_bits[ring], 1u << cw);
-                    else
-                        atomicAnd(&plain_bits[ring], ~(1u << cw));
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) tc_arrive(k_full + x);
-                // ---- V
-                if (g >= 2 && !tc_wait(v_free + x, ph ^ 1u, leaving, p.wait_ns)) bad = true;
-                if (__any_sync(~0u, bad)) {
-                    bad = true;
-                    break;
-                }
-#pragma unroll
-                for (int j = 0; j < NL; ++j) convert(vb, cw * 16 + j * KPL + sub, vr[j], vsc[j] * tc_pow2(-ev[j]), nullptr);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) tc_arrive(v_full + x);
-                if (i + 1 < n) fetch(w, tile + 1);
+            __syncwarp();
+            // ---- K
+            const uint32_t kb = base + S::kK + x * S::kTile;
+            if (g >= 1 && !waited(&lo_free, g - 1)) return false;  // the tile before has used its lower part
+#pragma unroll 2
+            for (int j = 0; j < NL; ++j) {
+                const int key = j * KPL + sub;
+                uint32_t rest[8];
+                convert(kb, cw * 32 + key, read(raw, j), live ? kn[key * NB + (part >> 1)] : 0.0f, &rest);
+                store(base + S::kLo, cw * 32 + key, rest);
             }
-            if (bad || !more(w)) break;
-            if (n > 0) ++item_no;
-            advance(w);
-            n = tiles_of(w, &kt0);
-            if (n > 0) fetch(w, kt0);
+            __syncwarp();
+            issue_a(row_after);
+            if (lane == 0) {
+                there_bits[ring][cw] = there;
+                plain_keys[ring][cw] = plain;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc_arrive(k_full + x);
+            return true;
+        };
+        // V of tile g
+        auto do_v = [&](int64_t g, uint32_t row_after) -> bool {
+            cp_wait<1>();  // all but the K after it
+            __syncwarp();
+            const float *vn = v_norm + (g & 1) * (32 * NB) + (part >> 1);
+            if (g >= 1 && !waited(v_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
+#pragma unroll 2
+            for (int j = 0; j < NL; ++j)
+                convert(base + S::kV, cw * 32 + j * KPL + sub, read(raw + S::kRawV, j), live ? vn[(j * KPL + sub) * NB] : 0.0f, nullptr);
+            __syncwarp();
+            issue_b(row_after);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc_arrive(&v_full);
+            return true;
+        };
+        if (lane == 0) {
+            TcTile t;
+            t.w = w;
+            settle(t);
+            *here = t;
+            *ahead = t;
         }
+        __syncwarp();
+        if (here->any) {
+            uint32_t row = find(here);
+            issue_a(row);
+            issue_b(row);
+            step(ahead);
+            uint32_t row1 = find(ahead);
+            bool ok = do_k(0, row, row1);
+            step(here);
+            step(ahead);
+            uint32_t row2 = find(ahead);
+            for (int64_t g = 0; ok; ++g) {  // K of tile g was converted; here is tile g + 1, ahead g + 2
+                const bool next = here->any;
+                if (next)
+                    ok = do_k(g + 1, row1, row2);
+                else
+                    cp_commit();  // in the place of K's group
+                if (ok) ok = do_v(g, row1);
+                if (!next) break;
+                step(here);
+                step(ahead);
+                row1 = row2;
+                row2 = find(ahead);
+            }
+        }
+        cp_wait<0>();
         if (bad) {
             leave = 1;
             if (lane == 0) atomicOr(p.err, kTcErrWait);
@@ -553,6 +681,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         int item_no = 0;
         bool first_item = true;
         uint32_t soft_phase = 0;
+        Place &pl = places[warp];  // the warp's copy
+        if (lane == 0) pl = w;
+        __syncwarp();
         // all softmax warps; false (in whole warps) if the CTA is leaving
         auto soft_sync = [&]() -> bool {
             __syncwarp();
@@ -563,10 +694,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         };
         for (;;) {
             int64_t kt0;
-            const int n = tiles_of(w, &kt0);
+            const int n = tiles_of(pl, &kt0);
             if (n > 0) {
-                const int idx = w.rt * kTcRows + r;
-                const bool whole = n == w.tiles_k;
+                const int idx = pl.rt * kTcRows + r;
+                const bool whole = n == pl.tiles_k;
                 float m = -INFINITY, l = 0.0f;
                 bool have = false;  // O holds something
                 float mul = 0.0f;
@@ -581,17 +712,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     tc_after();
                     if (!have) mul = row_mul[item_no & 3][r];
                     const float4 *meta = reinterpret_cast<const float4 *>(smem + S::kMeta + ring * S::kMetaTile);
-                    const uint32_t plain = *const_cast<const volatile uint32_t *>(&plain_bits[ring]);
-                    const bool fast = plain == (1u << kTcConvWarps) - 1u;
-                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (!fast) {
-                        const int64_t j0 = (kt0 + i) * kTcKeys - w.prefix;
+                    // per 32 keys: whether all rows see them, and which of them this row sees
+                    bool fast[4];
+                    uint32_t see[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            see[q] = there_bits[ring][2 * q] | (there_bits[ring][2 * q + 1] << 16);
-                            if (j0 + 32 * q + 32 > 0)
-                                see[q] &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, static_cast<int>(j0 + 32 * q), idx);
-                        }
+                    for (int q = 0; q < 4; ++q) {
+                        fast[q] = plain_keys[ring][q] != 0;
+                        see[q] = there_bits[ring][q];
+                        const int64_t j0 = (kt0 + i) * kTcKeys + 32 * q - pl.prefix;
+                        if (j0 + 32 > 0)
+                            see[q] &= sees(p.mask, p.mask_row, p.mask_words, p.group, pl.nodes, pl.row0, static_cast<int>(j0), idx);
                     }
                     // ---- the row's maximum of s + E
                     float top = -INFINITY;
@@ -599,22 +729,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     for (int q = 0; q < 4; ++q) {
                         float v[32];
                         tc_ld32(ts + 32 * q, v);
-                        if (fast) {
+                        if (q == 0 ? fast[0] : q == 1 ? fast[1] : q == 2 ? fast[2] : fast[3]) {
+                            float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
 #pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                float t0 = fmaxf(v[16 * hh], v[16 * hh + 1]), t1 = fmaxf(v[16 * hh + 2], v[16 * hh + 3]);
-#pragma unroll
-                                for (int e = 4; e < 16; e += 4) {
-                                    t0 = fmaxf(t0, fmaxf(v[16 * hh + e], v[16 * hh + e + 1]));
-                                    t1 = fmaxf(t1, fmaxf(v[16 * hh + e + 2], v[16 * hh + e + 3]));
-                                }
-                                const float4 c = meta[32 * q + 16 * hh];
-                                top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * c.x, c.y));
+                            for (int e = 4; e < 32; e += 4) {
+                                t0 = fmaxf(t0, v[e]);
+                                t1 = fmaxf(t1, v[e + 1]);
+                                t2 = fmaxf(t2, v[e + 2]);
+                                t3 = fmaxf(t3, v[e + 3]);
                             }
+                            const float4 c = meta[32 * q];
+                            top = fmaxf(top, fmaf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), mul * c.x, c.y));
                         } else {
                             const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
+                                if (e % 8 == 0) asm volatile("" ::: "memory");  // eight keys' factors at a time in registers
                                 const float4 c = meta[32 * q + e];
                                 if ((bits >> e) & 1u) {
                                     top = fmaxf(top, fmaf(v[e], mul * c.x, c.y));
@@ -642,40 +772,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                         }
                     }
                     have = true;
-                    // ---- P
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float v[32];
-                        uint32_t o[16];
-                        tc_ld32(ts + 32 * q, v);
-                        if (fast) {
+                    // ---- P, 16 keys at a time, the next 16 scores on their way
+                    auto weigh = [&](int c16, const uint32_t (&v)[16]) {
+                        uint32_t o[8];
+                        const int q = c16 >> 1;
+                        const float4 *mt = meta + 16 * c16;
+                        if (q == 0 ? fast[0] : q == 1 ? fast[1] : q == 2 ? fast[2] : fast[3]) {
+                            const float4 c = mt[0];
+                            const float a = mul * c.x, d = c.y - z;
+                            float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                const float4 c = meta[32 * q + 16 * hh];
-                                const float a = mul * c.x, d = c.y - z;
-                                float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-                                for (int e = 0; e < 16; e += 2) {
-                                    const float p0 = ex2(fmaf(v[16 * hh + e], a, d)), p1 = ex2(fmaf(v[16 * hh + e + 1], a, d));
-                                    sum0 += p0;
-                                    sum1 += p1;
-                                    o[8 * hh + e / 2] = pack_half2(p0, p1);
-                                }
-                                l = fmaf(sum0 + sum1, c.z, l);
+                            for (int e = 0; e < 16; e += 2) {
+                                const float p0 = ex2(fmaf(__uint_as_float(v[e]), a, d)), p1 = ex2(fmaf(__uint_as_float(v[e + 1]), a, d));
+                                sum0 += p0;
+                                sum1 += p1;
+                                o[e / 2] = pack_half2(p0, p1);
                             }
+                            l = fmaf(sum0 + sum1, c.z, l);
                         } else {
-                            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+                            const uint32_t bits = (q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3]) >> (16 * (c16 & 1));
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float4 c0 = meta[32 * q + e], c1 = meta[32 * q + e + 1];
-                                const float p0 = (bits >> e) & 1u ? ex2(fmaf(v[e], mul * c0.x, c0.y - z)) : 0.0f;
-                                const float p1 = (bits >> (e + 1)) & 1u ? ex2(fmaf(v[e + 1], mul * c1.x, c1.y - z)) : 0.0f;
+                            for (int e = 0; e < 16; e += 2) {
+                                const float4 c0 = mt[e], c1 = mt[e + 1];
+                                const float p0 = (bits >> e) & 1u ? ex2(fmaf(__uint_as_float(v[e]), mul * c0.x, c0.y - z)) : 0.0f;
+                                const float p1 = (bits >> (e + 1)) & 1u ? ex2(fmaf(__uint_as_float(v[e + 1]), mul * c1.x, c1.y - z)) : 0.0f;
                                 l = fmaf(p0, c0.z, l);
                                 l = fmaf(p1, c1.z, l);
                                 o[e / 2] = pack_half2(p0, p1);
                             }
                         }
-                        tc_st16(ts + 16 * q, o);
+                        tc_st8(ts + 8 * c16, o);
+                    };
+                    {
+                        uint32_t va[16], vb[16];
+                        tc_ld16(ts, va);
+                        tc_wait_ld();
+#pragma unroll 1
+                        for (int c16 = 0; c16 < 8; c16 += 2) {
+                            // (P's columns 8 c16 .. lie before the scores that are still to come)
+                            tc_ld16(ts + 16 * (c16 + 1), vb);
+                            weigh(c16, va);
+                            tc_wait_ld();
+                            if (c16 + 2 < 8) tc_ld16(ts + 16 * (c16 + 2), va);
+                            weigh(c16 + 1, vb);
+                            tc_wait_ld();
+                        }
                     }
                     tc_wait_st();
                     tc_before();
@@ -685,6 +826,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 if (bad) break;
                 // ---- the item's results: both O must be complete
                 row_ml[x][r] = make_float2(m, l);
+                // (a barrier each, by turns: one for all could be two phases behind here, which looks like none)
                 for (int back = 1; back <= 2 && back <= n; ++back) {
                     const int64_t t = g - back;
                     if (!tc_wait(v_free + static_cast<int>(t & 1), static_cast<uint32_t>(t >> 1) & 1u, leaving, p.wait_ns)) bad = true;
@@ -703,9 +845,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 const float top = fmaxf(ml0.x, ml1.x), z = top == -INFINITY ? 0.0f : top;
                 const float f0 = ex2(ml0.x - z), f1 = ex2(ml1.x - z);
                 const float sum = fmaf(f0, ml0.y, f1 * ml1.y);
-                const int rows = min(kTcRows, w.nodes * p.group - w.rt * kTcRows);
-                const int node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
-                const int64_t row = static_cast<int64_t>(w.row0) + node;
+                const int rows = min(kTcRows, pl.nodes * p.group - pl.rt * kTcRows);
+                const int node = idx / p.group, hq = pl.h * p.group + idx - node * p.group;
+                const int64_t row = static_cast<int64_t>(pl.row0) + node;
                 T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
                 const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
                 first_item = false;
@@ -766,7 +908,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     break;
                 }
                 tc_after();
-                if (!whole && w.item < p.tickets_n) {
+                if (!whole && pl.item < p.tickets_n) {
                     auto join = [&](int parts, int64_t head, int64_t at, int64_t step, bool last) {
                         auto part_of = [&](int i) { return p.partial + (i == 0 ? head : at + i * step) * pitch; };
                         float up = -INFINITY, total = 0.0f;
@@ -785,15 +927,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                             for (int i = 0; i < parts; ++i) {
                                 const float f = ex2(__ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r).x - zz);
                                 const float4 *src = reinterpret_cast<const float4 *>(part_of(i)) + e0 / 4 * kTcRows + r;
-                                float4 y[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + e * kTcRows);
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
-                                    v[4 * e] = fmaf(f, y[e].x, v[4 * e]);
-                                    v[4 * e + 1] = fmaf(f, y[e].y, v[4 * e + 1]);
-                                    v[4 * e + 2] = fmaf(f, y[e].z, v[4 * e + 2]);
-                                    v[4 * e + 3] = fmaf(f, y[e].w, v[4 * e + 3]);
+                                    if (e == 4) asm volatile("" ::: "memory");
+                                    const float4 y = __ldcg(src + e * kTcRows);
+                                    v[4 * e] = fmaf(f, y.x, v[4 * e]);
+                                    v[4 * e + 1] = fmaf(f, y.y, v[4 * e + 1]);
+                                    v[4 * e + 2] = fmaf(f, y.z, v[4 * e + 2]);
+                                    v[4 * e + 3] = fmaf(f, y.w, v[4 * e + 3]);
                                 }
                             }
                             if (last) {
@@ -825,23 +966,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                         if (yes) __threadfence();
                         return yes && !bad;
                     };
-                    const int c0 = static_cast<int>(split.owner(w.first)), c1 = static_cast<int>(split.owner(w.first + w.tiles_k - 1));
-                    const int slot_c0 = split.begin(c0) >= w.first - kTcItemUnits ? 2 * c0 : 2 * c0 + 1;
+                    const int c0 = static_cast<int>(split.owner(pl.first)), c1 = static_cast<int>(split.owner(pl.first + pl.tiles_k - 1));
+                    const int slot_c0 = split.begin(c0) >= pl.first - kTcItemUnits ? 2 * c0 : 2 * c0 + 1;
                     if (c1 - c0 < kJoinGroup) {
-                        if (arrive(p.tickets + w.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
+                        if (arrive(p.tickets + pl.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
                     } else {
                         const int grp = blockIdx.x / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
                         const int lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
                         if (arrive(p.group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1)) {
                             join(hi - lo + 1, lo == c0 ? slot_c0 : 2 * lo, 2 * lo, 2, false);
-                            if (arrive(p.tickets + w.item, g1 - g0 + 1)) join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
+                            if (arrive(p.tickets + pl.item, g1 - g0 + 1)) join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
                         }
                     }
                 }
                 ++item_no;
             }
-            if (bad || !more(w)) break;
-            advance(w);
+            if (bad || !more(pl)) break;
+            __syncwarp();
+            if (lane == 0) {
+                Place next = pl;
+                advance(next);
+                pl = next;
+            }
+            __syncwarp();
         }
         if (bad) {
             leave = 1;
