@@ -15,7 +15,8 @@
 //     f16 parts.  K is kept in two f16 parts, 22 bits, since a score's error is a
 //     weight's relative one and lse is f32; V is rounded once to 11 bits, as outputs
 //     are bf16.  (f32 and f16 outputs stay with kv_attend.cuh.)  K and V tiles have
-//     the same layout, core matrices of 8 keys x 8 e: K is read K-major, V MN-major.
+//     the same layout, 128-byte rows of a key's 64 e, swizzled: K is read K-major, V
+//     MN-major.
 //   * one thread issues the MMAs: S = Q K^T of tile g (lower part, then upper), then
 //     O += P V of tile g - 1.
 //   * two softmax warpgroups take alternate tiles, a thread a row, each with its own
@@ -33,10 +34,11 @@
 namespace kv {
 
 constexpr int kTcRows = 128, kTcKeys = 128;
-constexpr int kTcSoftWarps = 8, kTcConvWarps = 4;
+constexpr int kTcSoftWarps = 8, kTcConvWarps = 8;
+constexpr int kTcWarpKeys = 128 / kTcConvWarps;  // keys of a tile that a convert warp takes
 constexpr int kTcMmaWarp = kTcSoftWarps + kTcConvWarps;
 constexpr int kTcThreads = (kTcMmaWarp + 1) * 32;
-constexpr int kTcChunk = kTcKeys * 16 + 16;     // bytes from 8 e to the next 8: 128 rows of 16, and 16 against bank conflicts
+constexpr int kTcHalf = kTcKeys * 128;          // 128 rows of 64 f16
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 constexpr int kTcErrWait = 1;
 constexpr float kTcTop = 7.0f;                  // log2 of P at the row's maximum when that is taken
@@ -45,15 +47,16 @@ constexpr int kTcItemUnits = 3;
 
 template <int DP>
 struct TcSmem {
-    static constexpr int kTile = DP / 8 * kTcChunk;   // one operand of 128 rows
-    static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kLo = 4 * kTile, kMeta = 5 * kTile;
+    static constexpr int kTile = DP / 64 * kTcHalf;   // one operand of 128 rows: 64 e after 64 e
+    static constexpr int kQ = 0, kK = kTile, kLo = 2 * kTile, kV = 3 * kTile, kMeta = 4 * kTile;
     static constexpr int kMetaTile = kTcKeys * 16;    // per key: K's factor, E, 2^-E, flag
-    // a convert warp's next 32 keys as they are in the cache: codes of K and V, scales of both
-    static constexpr int kRaw = kMeta + 4 * kMetaTile, kRawV = 32 * DP, kRawS = 64 * DP;
-    static constexpr int kRawWarp = 64 * DP + 2 * 32 * (DP / 32) * 4;
-    // its normalised scales, V's of two tiles and K's
-    static constexpr int kVs = kRaw + kTcConvWarps * kRawWarp, kVsWarp = 3 * 32 * (DP / 32) * 4;
-    static constexpr int kTotal = kVs + kTcConvWarps * kVsWarp;
+    // a convert warp's keys of a tile as they are in the cache: codes of K and V, scales of both
+    // (a row's pitch is 16 mod 128 bytes: 8 lanes read 16 bytes of 8 rows)
+    static constexpr int kRaw = kMeta + 4 * kMetaTile, kRawPitch = DP + 16;
+    static constexpr int kRawV = kTcWarpKeys * kRawPitch, kRawS = 2 * kTcWarpKeys * kRawPitch;
+    static constexpr int kRawWarp = 2 * kTcWarpKeys * kRawPitch + 2 * kTcWarpKeys * (DP / 32) * 4;
+    static constexpr int kUsed = kRaw + 2 * kTcConvWarps * kRawWarp;  // of two tiles
+    static constexpr int kTotal = kUsed + 1024;  // the swizzled tiles begin on 1024 bytes
     static constexpr int kPart = kTcRows * (DP + 2);  // floats of a partial result: O by 4 columns x 128 rows, m, l
 };
 
@@ -90,13 +93,24 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, const vo
         }
     }
 }
+// one lane of a warp that is together
+__device__ __forceinline__ bool tc_elect() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Shared-memory operand without swizzle: bytes between core matrices along K and along M or N.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t along_k, uint32_t along_mn) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(along_k >> 4) << 16) |
-           (static_cast<uint64_t>(along_mn >> 4) << 32) | (1ull << 46);
+// Shared-memory operand of 128-byte rows, 128-byte swizzle (rows in eights 1024 bytes apart); `next`: bytes to the next
+// 64 elements along M or N, where a row runs along it.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t next) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(next >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// place of 16 bytes, the c-th of a row, in an operand's tile
+__device__ __forceinline__ uint32_t tc_place(int row, int c) {
+    return static_cast<uint32_t>((c >> 3) * kTcHalf + row * 128 + (((c ^ row) & 7) << 4));
 }
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
@@ -186,12 +200,12 @@ template <int DP>
 __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const AttendParams p) {
     using T = __nv_bfloat16;
     using S = TcSmem<DP>;
-    constexpr int PARTS = DP / 16, KPL = 32 / PARTS, NL = 32 / KPL;  // 16-byte pieces of a row, keys of a load, loads
-    constexpr int NB = DP / 32;
-    extern __shared__ __align__(1024) unsigned char smem[];
+    constexpr int PARTS = DP / 16, KPL = 32 / PARTS, NL = kTcWarpKeys / KPL;  // 16-byte pieces of a row, keys of a load, loads
+    constexpr int NB = DP / 32, WK = kTcWarpKeys;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *const smem = smem_raw + ((1024u - (tc_smem(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t k_full[2], k_free[2], v_full, v_free[2], s_full[2], p_full[2];
     __shared__ __align__(8) uint64_t soft_bar;            // among the softmax warps
-    __shared__ __align__(8) uint64_t lo_free;             // K's lower part, which has one buffer
     __shared__ uint32_t tmem_at;
     __shared__ int leave, is_last;
     __shared__ int64_t scan_units[kTcThreads / 32], scan_items[kTcThreads / 32];
@@ -242,7 +256,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 tc_bar_init(p_full + i, 4);
             }
             tc_bar_init(&soft_bar, kTcSoftWarps);
-            tc_bar_init(&lo_free, 1);
             tc_bar_init(&v_full, kTcConvWarps);
             leave = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -317,80 +330,86 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
     bool bad = false;
 
     if (warp == kTcMmaWarp) {
-        // ================ the MMAs
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(kTcKeys >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
-            constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(DP >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
-            int64_t g = 0;        // tile of the CTA
-            uint64_t *last_bar = nullptr;  // of the last commit
-            uint32_t last_ph = 0;
-            int last_first = 0;   // whether tile g - 1 was its warpgroup's first of an item
-            auto second = [&](int64_t t, bool first) -> bool {  // O += P V of tile t
-                const int x = static_cast<int>(t & 1);
-                const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
-                if (!tc_wait(p_full + x, ph, leaving, p.wait_ns) ||
-                    !tc_wait(&v_full, static_cast<uint32_t>(t) & 1u, leaving, p.wait_ns))
-                    return false;
-                tc_after();
-                const uint32_t v = base + S::kV;
+        // ================ the MMAs.  The warp stays together and one lane issues: the operands' descriptors are then
+        // uniform and need no moves between register files, which held the issue to 200 cycles an MMA.
+        constexpr uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(kTcKeys >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
+        constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(DP >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
+        const bool first_lane = tc_elect();
+        const uint64_t dq = tc_desc(base + S::kQ, 16), dk = tc_desc(base + S::kK, 16), dl = tc_desc(base + S::kLo, 16),
+                       dv = tc_desc(base + S::kV, kTcHalf);
+        // 64 e further, 16 e further, 16 keys further, as descriptors count
+        constexpr uint64_t kHalfStep = kTcHalf >> 4, kStep = 32 >> 4, kKeyStep = 2048 >> 4;
+        auto scores = [&](uint32_t d) {  // S = Q K^T, lower part first
 #pragma unroll
-                for (int k = 0; k < kTcKeys / 16; ++k)
-                    tc_mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, tc_desc(v + k * 256, 128, kTcChunk), idesc_o,
-                              first && k == 0 ? 0u : 1u);
+            for (int e = 0; e < DP / 16; ++e)
+                tc_mma_ss(d, dq + (e / 4) * kHalfStep + (e % 4) * kStep, dl + (e / 4) * kHalfStep + (e % 4) * kStep, idesc_s, e == 0 ? 0u : 1u);
+#pragma unroll
+            for (int e = 0; e < DP / 16; ++e)
+                tc_mma_ss(d, dq + (e / 4) * kHalfStep + (e % 4) * kStep, dk + (e / 4) * kHalfStep + (e % 4) * kStep, idesc_s, 1u);
+        };
+        auto products = [&](uint32_t d, uint32_t a, uint32_t add) {  // O += P V
+            tc_mma_ts(d, a, dv, idesc_o, add);
+#pragma unroll
+            for (int k = 1; k < kTcKeys / 16; ++k) tc_mma_ts(d, a + k * 8, dv + k * kKeyStep, idesc_o, 1u);
+        };
+        int64_t g = 0;                 // tile of the CTA
+        uint64_t *last_bar = nullptr;  // of the last commit
+        uint32_t last_ph = 0;
+        int last_first = 0;            // whether tile g - 1 was its warpgroup's first of an item
+        auto second = [&](int64_t t, bool first) -> bool {
+            const uint32_t x = static_cast<uint32_t>(t) & 1u, ph = static_cast<uint32_t>(t >> 1) & 1u;
+            bool ok = tc_wait(p_full + x, ph, leaving, p.wait_ns) && tc_wait(&v_full, static_cast<uint32_t>(t) & 1u, leaving, p.wait_ns);
+            ok = __all_sync(~0u, ok);
+            if (!ok) return false;
+            tc_after();
+            if (first_lane) {
+                products(tmem + 256 + x * 128, tmem + x * 128, first ? 0u : 1u);
                 tc_commit(v_free + x);
-                last_bar = v_free + x;
-                last_ph = ph;
-                return true;
-            };
-            for (;;) {
-                int64_t kt0;
-                const int n = tiles_of(w, &kt0);
-                for (int i = 0; i < n && !bad; ++i, ++g) {
-                    const int x = static_cast<int>(g & 1);
-                    const uint32_t ph = static_cast<uint32_t>(g >> 1) & 1u;
-                    if (!tc_wait(k_full + x, ph, leaving, p.wait_ns)) {
-                        bad = true;
-                        break;
-                    }
-                    tc_after();
-                    const uint32_t q = base + S::kQ, k = base + S::kK + x * S::kTile, low = base + S::kLo;
-#pragma unroll
-                    for (int e = 0; e < DP / 16; ++e)
-                        tc_mma_ss(tmem + x * 128, tc_desc(q + 2 * e * kTcChunk, kTcChunk, 128),
-                                  tc_desc(low + 2 * e * kTcChunk, kTcChunk, 128), idesc_s, e == 0 ? 0u : 1u);
-                    tc_commit(&lo_free);
-#pragma unroll
-                    for (int e = 0; e < DP / 16; ++e)
-                        tc_mma_ss(tmem + x * 128, tc_desc(q + 2 * e * kTcChunk, kTcChunk, 128),
-                                  tc_desc(k + 2 * e * kTcChunk, kTcChunk, 128), idesc_s, 1u);
+            }
+            __syncwarp();
+            last_bar = v_free + x;
+            last_ph = ph;
+            return true;
+        };
+        for (;;) {
+            int64_t kt0;
+            const int n = tiles_of(w, &kt0);
+            for (int i = 0; i < n && !bad; ++i, ++g) {
+                const uint32_t x = static_cast<uint32_t>(g) & 1u, ph = static_cast<uint32_t>(g >> 1) & 1u;
+                if (!__all_sync(~0u, tc_wait(k_full + x, ph, leaving, p.wait_ns))) {
+                    bad = true;
+                    break;
+                }
+                tc_after();
+                if (first_lane) {
+                    scores(tmem + x * 128);
                     tc_commit(k_free + x);
                     tc_commit(s_full + x);
-                    last_bar = k_free + x;
-                    last_ph = ph;
-                    if (g > 0 && !second(g - 1, last_first != 0)) {
-                        bad = true;
-                        break;
-                    }
-                    last_first = i < 2;
                 }
-                if (bad || !more(w)) break;
-                advance(w);
+                __syncwarp();
+                last_bar = k_free + x;
+                last_ph = ph;
+                if (g > 0 && !second(g - 1, last_first != 0)) {
+                    bad = true;
+                    break;
+                }
+                last_first = i < 2;
             }
-            if (!bad && g > 0 && !second(g - 1, last_first != 0)) bad = true;
-            if (bad) leave = 1;
-            // what was issued, before the tensor memory goes back
-            if (last_bar != nullptr && !tc_wait(last_bar, last_ph, nullptr, p.wait_ns)) bad = true;
-            if (bad) atomicOr(p.err, kTcErrWait);
+            if (bad || !more(w)) break;
+            advance(w);
         }
+        if (!bad && g > 0 && !second(g - 1, last_first != 0)) bad = true;
+        if (bad) leave = 1;
+        // what was issued, before the tensor memory goes back
+        if (last_bar != nullptr && !tc_wait(last_bar, last_ph, nullptr, p.wait_ns)) bad = true;
+        if (bad && lane == 0) atomicOr(p.err, kTcErrWait);
     } else if (warp >= kTcSoftWarps) {
         // ================ convert
         const int cw = warp - kTcSoftWarps, part = lane % PARTS, sub = lane / PARTS;
         const bool live = part * 16 < p.c.dim;
         const int ct = tid - kTcSoftWarps * 32;  // thread among the convert warps
-        unsigned char *raw = smem + S::kRaw + cw * S::kRawWarp;
-        float *raw_s = reinterpret_cast<float *>(raw + S::kRawS);  // K: [key][NB], then V
-        float *v_norm = reinterpret_cast<float *>(smem + S::kVs + cw * S::kVsWarp);  // [tile % 2][key][NB]
-        for (int i = lane; i < S::kRawWarp / 16; i += 32) reinterpret_cast<uint4 *>(raw)[i] = make_uint4(0, 0, 0, 0);
+        unsigned char *const raws = smem + S::kRaw + cw * (2 * S::kRawWarp);  // by tile % 2: K, V, scales of K [key][NB], of V
+        for (int i = lane; i < 2 * S::kRawWarp / 16; i += 32) reinterpret_cast<uint4 *>(raws)[i] = make_uint4(0, 0, 0, 0);
         __syncwarp();
         // A tile of the CTA: its item and its number there.  The warp keeps two in shared memory, this one and the
         // next but one: in registers they would push the codes out.
@@ -423,9 +442,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         // row of the lane's key in a tile, or kNoRow
         auto find = [&](const TcTile *t) -> uint32_t {
             if (!t->any) return kNoRow;
-            const int64_t pos = t->kt * kTcKeys + cw * 32 + lane;
+            const int64_t pos = t->kt * kTcKeys + cw * WK + lane;
             const int64_t keys = min(static_cast<int64_t>(t->w.prefix) + t->w.nodes, static_cast<int64_t>(p.table_cols) * p.c.page_size);
-            if (pos >= keys) return kNoRow;
+            if (lane >= WK || pos >= keys) return kNoRow;
             const uint32_t at = static_cast<uint32_t>(pos), col = (__umulhi(at, p.page_mul) + at) >> p.page_shift;
             const int page = __ldg(p.table + static_cast<int64_t>(t->w.b) * p.table_row + col);
             if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
@@ -437,10 +456,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             for (int j = 0; j < NL; ++j) {
                 const uint32_t r = __shfl_sync(~0u, row, j * KPL + sub);
                 if (r != kNoRow && live)
-                    cp_async16(to + (j * KPL + sub) * DP + part * 16, from + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim) + part * 16);
+                    cp_async16(to + (j * KPL + sub) * S::kRawPitch + part * 16, from + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim) + part * 16);
             }
         };
-        auto issue_a = [&](uint32_t row) {  // codes of K, scales of both; an absent key's scales are 0
+        auto issue_a = [&](uint32_t row, int64_t g) {  // codes of K, scales of both; an absent key's scales are 0
+            unsigned char *raw = raws + (g & 1) * S::kRawWarp;
+            float *raw_s = reinterpret_cast<float *>(raw + S::kRawS);
             codes(p.c.k_codes, tc_smem(raw), row);
             const uint32_t at = tc_smem(raw_s) + lane * (NB * 4);
             if (row != kNoRow) {
@@ -448,42 +469,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 const float *vs = p.c.v_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
                 if (wide_scales) {
                     cp_async16(at, ks);
-                    cp_async16(at + 32 * NB * 4, vs);
+                    cp_async16(at + WK * NB * 4, vs);
                 } else {
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
                         if (b < p.c.blocks) {
                             cp_async4(at + 4 * b, ks + b);
-                            cp_async4(at + 32 * NB * 4 + 4 * b, vs + b);
+                            cp_async4(at + WK * NB * 4 + 4 * b, vs + b);
                         }
                 }
-            } else {
+            } else if (lane < WK) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) raw_s[lane * NB + b] = raw_s[32 * NB + lane * NB + b] = 0.0f;
+                for (int b = 0; b < NB; ++b) raw_s[lane * NB + b] = raw_s[WK * NB + lane * NB + b] = 0.0f;
             }
             cp_commit();
         };
-        auto issue_b = [&](uint32_t row) {  // codes of V
-            codes(p.c.v_codes, tc_smem(raw) + S::kRawV, row);
+        auto issue_b = [&](uint32_t row, int64_t g) {  // codes of V
+            codes(p.c.v_codes, tc_smem(raws) + static_cast<uint32_t>(g & 1) * S::kRawWarp + S::kRawV, row);
             cp_commit();
         };
         // exponent e with scales below 2^(e + 7): codes times scale / 2^e stay below 2^14
         auto exponent = [](uint32_t bits) -> int { return max(min(static_cast<int>(bits >> 23) - 127 - 6, 120), -100); };
-        // A lane's two groups of 8 e go to two places of a tile.  Half of a row's lanes store their upper group first
-        // (their words are swapped when they are read): the eight lanes of a phase then meet 8 different banks.
-        const bool up = part >= PARTS / 2;
-        const uint32_t place = 2 * part * kTcChunk;
-        const uint32_t place0 = place + (up ? kTcChunk : 0), place1 = place + (up ? 0 : kTcChunk);
-        auto store = [&](uint32_t tile, int key, const uint32_t (&o)[8]) {
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + place0 + key * 16), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + place1 + key * 16), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+        // Converting, a lane has one key (lane % WK) and every second piece of its row: 8 lanes store 16 bytes of 8 keys,
+        // which the swizzle puts into 8 different banks' lines.
+        static_assert(WK == 16, "two lanes a key");
+        const int key = lane & 15, odd_piece = lane >> 4;
+        auto store = [&](uint32_t tile, int piece, const uint32_t (&o)[8]) {
+            const int r = cw * WK + key;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + tc_place(r, 2 * piece)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + tc_place(r, 2 * piece + 1)), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
         };
-        auto read = [&](const unsigned char *from, int j) -> uint4 {
-            const uint4 c = *reinterpret_cast<const uint4 *>(from + (j * KPL + sub) * DP + part * 16);
-            return up ? make_uint4(c.z, c.w, c.x, c.y) : c;
-        };
-        // 16 codes times scale / 2^e to rows of the tile, and what that rounds off
-        auto convert = [&](uint32_t tile, int key, const uint4 &c, float scale, uint32_t (*rest)[8]) {
+        // a piece of 16 codes times scale / 2^e to the tile, and what that rounds off
+        auto convert = [&](uint32_t tile, int piece, const unsigned char *from, float scale, uint32_t (*rest)[8]) {
+            const uint4 c = *reinterpret_cast<const uint4 *>(from + key * S::kRawPitch + piece * 16);
             const __half hi = __float2half_rn(scale), lo = __float2half_rn(scale - __half2float(hi));
             const uint32_t h2 = pack_half2(__half2float(hi), __half2float(hi)), l2 = pack_half2(__half2float(lo), __half2float(lo));
             const uint32_t in[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 o[i] = tc_scaled(unbias(__byte_perm(in[i / 2], 0x64646464u, i % 2 ? 0x4342u : 0x4140u)), h2, l2, rest ? &(*rest)[i] : nullptr);
-            store(tile, key, o);
+            store(tile, piece, o);
         };
         auto waited = [&](uint64_t *bar, int64_t phase) -> bool {  // whole warps
             if (!tc_wait(bar, static_cast<uint32_t>(phase) & 1u, leaving, p.wait_ns)) bad = true;
@@ -500,15 +518,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         };
 
         int item_no = -1;
+        float v_scale[NB];  // the lane's key's scales of V, normalised, of the tile whose K was converted last
         // q and K of tile g
         auto do_k = [&](int64_t g, uint32_t row, uint32_t row_after) -> bool {
             const TcTile &t = *here;
-            const bool all_before = t.kt * kTcKeys + cw * 32 + 32 <= t.w.prefix;
+            // the scores of the tile before, which end its use of q and K (and tile g - 4's of the rings' entries)
+            if (g > 0 && !waited(k_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
+            const bool all_before = t.kt * kTcKeys + (cw + 1) * WK <= t.w.prefix;
             if (t.i == 0) {
-                // q, once the previous item's last S has been computed
                 ++item_no;
-                if (g > 0 && !waited(k_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
-                const int r = ct;
+                constexpr int TPR = kTcConvWarps * 32 / kTcRows, H = DP / 8 / TPR;  // threads a row, a thread's groups of 8
+                const int r = ct / TPR, g0 = ct % TPR * H;
                 const int rows = min(kTcRows, t.w.nodes * p.group - t.w.rt * kTcRows);
                 const int idx = t.w.rt * kTcRows + r, node = idx / p.group, hq = t.w.h * p.group + idx - node * p.group;
                 const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(t.w.row0) + node) * p.q_row + hq * p.q_head;
@@ -516,70 +536,60 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     uint4 u;
                     T t[8];
                 };
-                constexpr int H = DP / 16;  // half a row's groups of 8
-                Eight x[H];
-                auto load = [&](int half) {
+                Eight q8[H];
+                uint32_t top = 0;
 #pragma unroll
-                    for (int k = 0; k < H; ++k) {
-                        const int e = 8 * (half * H + k);
-                        x[k].u = make_uint4(0, 0, 0, 0);
-                        if (r < rows && e < p.c.dim) {
-                            if (p.q_vec) {
-                                x[k].u = __ldg(reinterpret_cast<const uint4 *>(src + e));
-                            } else {
+                for (int k = 0; k < H; ++k) {
+                    const int e = 8 * (g0 + k);
+                    q8[k].u = make_uint4(0, 0, 0, 0);
+                    if (r < rows && e < p.c.dim) {
+                        if (p.q_vec) {
+                            q8[k].u = __ldg(reinterpret_cast<const uint4 *>(src + e));
+                        } else {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) x[k].t[j] = src[e + j];
-                            }
+                            for (int j = 0; j < 8; ++j) q8[k].t[j] = src[e + j];
                         }
                     }
-                };
-                uint32_t top = 0;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    load(half);
-#pragma unroll
-                    for (int k = 0; k < H; ++k)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(x[k].t[j])) & 0x7FFFFFFFu);
                 }
+#pragma unroll
+                for (int k = 0; k < H; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(q8[k].t[j])) & 0x7FFFFFFFu);
+#pragma unroll
+                for (int d = 1; d < TPR; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
                 const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
                 const float down = copysignf(tc_pow2(-ex), p.scale_log2);
-#pragma unroll 1
-                for (int half = 1; half >= 0; --half) {  // the second half is still here
-                    if (half == 0) load(0);
 #pragma unroll
-                    for (int k = 0; k < H; ++k) {
+                for (int k = 0; k < H; ++k) {
                     uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(to_f32(x[k].t[2 * e]) * down, to_f32(x[k].t[2 * e + 1]) * down);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + (half * H + k) * kTcChunk + r * 16), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
-                    }
+                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(to_f32(q8[k].t[2 * e]) * down, to_f32(q8[k].t[2 * e + 1]) * down);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + tc_place(r, g0 + k)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
                 }
-                row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
+                if (g0 == 0)
+                    row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
             }
-            if (g <= 1)
-                cp_wait<0>();
+            if (g <= 2)
+                cp_wait<2>();
             else
-                cp_wait<1>();  // all but the V after it
+                cp_wait<3>();  // V of g - 1, K of g + 1 and V of g may be on their way
             __syncwarp();
+            const unsigned char *raw = raws + (g & 1) * S::kRawWarp;
+            const float *raw_s = reinterpret_cast<const float *>(raw + S::kRawS);
             const int x = static_cast<int>(g & 1), ring = static_cast<int>(g & 3);
-            // the buffer of tile g - 2; then the rings' entries of tile g - 4 are free too
-            if (g >= 2 && !waited(k_free + x, (g >> 1) - 1)) return false;
-            float4 *meta = reinterpret_cast<float4 *>(smem + S::kMeta + ring * S::kMetaTile) + cw * 32;
-            float *vn = v_norm + x * (32 * NB);
+            float4 *meta = reinterpret_cast<float4 *>(smem + S::kMeta + ring * S::kMetaTile) + cw * WK;
             const uint32_t there = __ballot_sync(~0u, row != kNoRow);
-            bool plain = all_before && there == ~0u;
-            float *kn = v_norm + 2 * (32 * NB);
-            // ---- normalisers, a lane a key: of each key, and of all keys if every row sees them
+            bool plain = all_before && there == (WK == 32 ? ~0u : (1u << (WK & 31)) - 1u);
+            // ---- normalisers: of each key, and of all keys if every row sees them
+            float k_scale[NB];
             {
-                float kk[NB], vv[NB];
                 uint32_t bk = 0, bv = 0;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    kk[b] = raw_s[lane * NB + b];
-                    vv[b] = raw_s[32 * NB + lane * NB + b];
-                    bk = max(bk, __float_as_uint(kk[b]) & 0x7FFFFFFFu);
-                    bv = max(bv, __float_as_uint(vv[b]) & 0x7FFFFFFFu);
+                    k_scale[b] = raw_s[key * NB + b];
+                    v_scale[b] = raw_s[WK * NB + key * NB + b];
+                    bk = max(bk, __float_as_uint(k_scale[b]) & 0x7FFFFFFFu);
+                    bv = max(bv, __float_as_uint(v_scale[b]) & 0x7FFFFFFFu);
                 }
                 // a scale that is not finite: the key's rows are 0 here, and the softmax makes NaN of who sees it
                 const bool odd = bk >= 0x7F800000u || bv >= 0x7F800000u;
@@ -589,26 +599,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     bv = __reduce_max_sync(~0u, bv);
                 }
                 const int ek = exponent(odd ? 0 : bk), ev = exponent(odd ? 0 : bv);
-                meta[lane] = make_float4(tc_pow2(ek), static_cast<float>(ev), tc_pow2(-ev), odd ? 1.0f : 0.0f);
+                if (lane < WK) meta[key] = make_float4(tc_pow2(ek), static_cast<float>(ev), tc_pow2(-ev), odd ? 1.0f : 0.0f);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    vn[lane * NB + b] = odd ? 0.0f : vv[b] * tc_pow2(-ev);
-                    kn[lane * NB + b] = odd ? 0.0f : kk[b] * tc_pow2(-ek);
+                    v_scale[b] = odd ? 0.0f : v_scale[b] * tc_pow2(-ev);
+                    k_scale[b] = odd ? 0.0f : k_scale[b] * tc_pow2(-ek);
                 }
             }
-            __syncwarp();
             // ---- K
-            const uint32_t kb = base + S::kK + x * S::kTile;
-            if (g >= 1 && !waited(&lo_free, g - 1)) return false;  // the tile before has used its lower part
-#pragma unroll 2
-            for (int j = 0; j < NL; ++j) {
-                const int key = j * KPL + sub;
+            const uint32_t kb = base + S::kK;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
                 uint32_t rest[8];
-                convert(kb, cw * 32 + key, read(raw, j), live ? kn[key * NB + (part >> 1)] : 0.0f, &rest);
-                store(base + S::kLo, cw * 32 + key, rest);
+                convert(kb, 2 * b + odd_piece, raw, k_scale[b], &rest);
+                store(base + S::kLo, 2 * b + odd_piece, rest);
             }
-            __syncwarp();
-            issue_a(row_after);
             if (lane == 0) {
                 there_bits[ring][cw] = there;
                 plain_keys[ring][cw] = plain;
@@ -616,22 +621,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc_arrive(k_full + x);
+            // (after the fence, which would wait for these copies: 2000 cycles a tile)
+            issue_a(row_after, g + 2);
             return true;
         };
         // V of tile g
-        auto do_v = [&](int64_t g, uint32_t row_after) -> bool {
-            cp_wait<1>();  // all but the K after it
+        auto do_v = [&](int64_t g, const float (&scale)[NB], uint32_t row_after) -> bool {
+            cp_wait<3>();  // K of g + 1 .. g + 2 and V of g + 1 may be on their way
             __syncwarp();
-            const float *vn = v_norm + (g & 1) * (32 * NB) + (part >> 1);
             if (g >= 1 && !waited(v_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
-#pragma unroll 2
-            for (int j = 0; j < NL; ++j)
-                convert(base + S::kV, cw * 32 + j * KPL + sub, read(raw + S::kRawV, j), live ? vn[(j * KPL + sub) * NB] : 0.0f, nullptr);
-            __syncwarp();
-            issue_b(row_after);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) convert(base + S::kV, 2 * b + odd_piece, raws + (g & 1) * S::kRawWarp + S::kRawV, scale[b], nullptr);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc_arrive(&v_full);
+            issue_b(row_after, g + 2);
             return true;
         };
         if (lane == 0) {
@@ -643,27 +647,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         }
         __syncwarp();
         if (here->any) {
-            uint32_t row = find(here);
-            issue_a(row);
-            issue_b(row);
+            // r0, r1, r2: rows of the tiles g + 1, g + 2 and g + 3 of the loop below; `here` is tile g + 1, `ahead` g + 3
+            uint32_t r0 = find(here);
+            issue_a(r0, 0);
+            issue_b(r0, 0);
             step(ahead);
-            uint32_t row1 = find(ahead);
-            bool ok = do_k(0, row, row1);
+            uint32_t r1 = find(ahead);
+            issue_a(r1, 1);
+            issue_b(r1, 1);
+            step(ahead);
+            uint32_t r2 = find(ahead);
+            bool ok = do_k(0, r0, r2);
+            int64_t keys = 1;  // tiles whose K is converted
             step(here);
             step(ahead);
-            uint32_t row2 = find(ahead);
-            for (int64_t g = 0; ok; ++g) {  // K of tile g was converted; here is tile g + 1, ahead g + 2
-                const bool next = here->any;
-                if (next)
-                    ok = do_k(g + 1, row1, row2);
+            r0 = r1;
+            r1 = r2;
+            r2 = find(ahead);
+            for (int64_t g = 0; ok; ++g) {
+                float scale[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) scale[b] = v_scale[b];
+                if (here->any)
+                    ok = do_k(keys++, r0, r2);
                 else
                     cp_commit();  // in the place of K's group
-                if (ok) ok = do_v(g, row1);
-                if (!next) break;
+                if (ok) ok = do_v(g, scale, r1);
+                if (g + 1 == keys) break;
                 step(here);
                 step(ahead);
-                row1 = row2;
-                row2 = find(ahead);
+                r0 = r1;
+                r1 = r2;
+                r2 = find(ahead);
             }
         }
         cp_wait<0>();
@@ -712,45 +727,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     tc_after();
                     if (!have) mul = row_mul[item_no & 3][r];
                     const float4 *meta = reinterpret_cast<const float4 *>(smem + S::kMeta + ring * S::kMetaTile);
-                    // per 32 keys: whether all rows see them, and which of them this row sees
-                    bool fast[4];
-                    uint32_t see[4];
+                    // for each convert warp's keys, whether all rows see them; and which of 32 keys this row sees
+                    uint32_t fast = 0, see[4];
+#pragma unroll
+                    for (int q = 0; q < kTcConvWarps; ++q) fast |= plain_keys[ring][q] << q;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        fast[q] = plain_keys[ring][q] != 0;
-                        see[q] = there_bits[ring][q];
+                        see[q] = WK == 32 ? there_bits[ring][q] : there_bits[ring][2 * q] | there_bits[ring][2 * q + 1] << 16;
                         const int64_t j0 = (kt0 + i) * kTcKeys + 32 * q - pl.prefix;
                         if (j0 + 32 > 0)
                             see[q] &= sees(p.mask, p.mask_row, p.mask_words, p.group, pl.nodes, pl.row0, static_cast<int>(j0), idx);
                     }
                     // ---- the row's maximum of s + E
                     float top = -INFINITY;
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float v[32];
-                        tc_ld32(ts + 32 * q, v);
-                        if (q == 0 ? fast[0] : q == 1 ? fast[1] : q == 2 ? fast[2] : fast[3]) {
-                            float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+                    auto look = [&](int c16, const uint32_t (&v)[16]) {
+                        const float4 *mt = meta + 16 * c16;
+                        if ((fast >> (c16 * 16 / WK)) & 1u) {
+                            float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
 #pragma unroll
-                            for (int e = 4; e < 32; e += 4) {
-                                t0 = fmaxf(t0, v[e]);
-                                t1 = fmaxf(t1, v[e + 1]);
-                                t2 = fmaxf(t2, v[e + 2]);
-                                t3 = fmaxf(t3, v[e + 3]);
+                            for (int e = 2; e < 16; e += 2) {
+                                t0 = fmaxf(t0, __uint_as_float(v[e]));
+                                t1 = fmaxf(t1, __uint_as_float(v[e + 1]));
                             }
-                            const float4 c = meta[32 * q];
-                            top = fmaxf(top, fmaf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), mul * c.x, c.y));
+                            const float4 c = mt[0];
+                            top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * c.x, c.y));
                         } else {
-                            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+                            const int q = c16 >> 1;
+                            const uint32_t bits = (q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3]) >> (16 * (c16 & 1));
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (e % 8 == 0) asm volatile("" ::: "memory");  // eight keys' factors at a time in registers
-                                const float4 c = meta[32 * q + e];
+                            for (int e = 0; e < 16; ++e) {
+                                const float4 c = mt[e];
                                 if ((bits >> e) & 1u) {
-                                    top = fmaxf(top, fmaf(v[e], mul * c.x, c.y));
+                                    top = fmaxf(top, fmaf(__uint_as_float(v[e]), mul * c.x, c.y));
                                     if (c.w != 0.0f) l = NAN;
                                 }
                             }
+                        }
+                    };
+                    {
+                        uint32_t va[16], vb[16];
+                        tc_ld16(ts, va);
+                        tc_wait_ld();
+#pragma unroll 1
+                        for (int c16 = 0; c16 < 8; c16 += 2) {
+                            tc_ld16(ts + 16 * (c16 + 1), vb);
+                            look(c16, va);
+                            tc_wait_ld();
+                            if (c16 + 2 < 8) tc_ld16(ts + 16 * (c16 + 2), va);
+                            look(c16 + 1, vb);
+                            tc_wait_ld();
                         }
                     }
                     // ---- move the maximum?
@@ -777,7 +802,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                         uint32_t o[8];
                         const int q = c16 >> 1;
                         const float4 *mt = meta + 16 * c16;
-                        if (q == 0 ? fast[0] : q == 1 ? fast[1] : q == 2 ? fast[2] : fast[3]) {
+                        if ((fast >> (c16 * 16 / WK)) & 1u) {
                             const float4 c = mt[0];
                             const float a = mul * c.x, d = c.y - z;
                             float sum0 = 0.0f, sum1 = 0.0f;
