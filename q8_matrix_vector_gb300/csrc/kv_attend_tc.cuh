@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         };
 
         int item_no = -1;
-        float v_scale[NB];  // the lane's key's scales of V, normalised, of the tile whose K was converted last
+        float v_scale[NB] = {};  // the lane's key's scales of V, normalised, of the tile whose K was converted last
         // q and K of tile g
         auto do_k = [&](int64_t g, uint32_t row, uint32_t row_after) -> bool {
             const TcTile &t = *here;
@@ -536,34 +536,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     uint4 u;
                     T t[8];
                 };
-                Eight q8[H];
-                uint32_t top = 0;
-#pragma unroll
-                for (int k = 0; k < H; ++k) {
+                auto eight = [&](int k) -> Eight {  // the k-th of the thread's groups
                     const int e = 8 * (g0 + k);
-                    q8[k].u = make_uint4(0, 0, 0, 0);
+                    Eight y;
+                    y.u = make_uint4(0, 0, 0, 0);
                     if (r < rows && e < p.c.dim) {
                         if (p.q_vec) {
-                            q8[k].u = __ldg(reinterpret_cast<const uint4 *>(src + e));
+                            y.u = __ldg(reinterpret_cast<const uint4 *>(src + e));
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) q8[k].t[j] = src[e + j];
+                            for (int j = 0; j < 8; ++j) y.t[j] = src[e + j];
                         }
                     }
+                    return y;
+                };
+                uint32_t top = 0;
+#pragma unroll 4
+                for (int k = 0; k < H; ++k) {
+                    const Eight y = eight(k);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(y.t[j])) & 0x7FFFFFFFu);
                 }
-#pragma unroll
-                for (int k = 0; k < H; ++k)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(q8[k].t[j])) & 0x7FFFFFFFu);
 #pragma unroll
                 for (int d = 1; d < TPR; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
                 const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
                 const float down = copysignf(tc_pow2(-ex), p.scale_log2);
-#pragma unroll
+#pragma unroll 4
                 for (int k = 0; k < H; ++k) {
+                    const Eight y = eight(k);
                     uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(to_f32(q8[k].t[2 * e]) * down, to_f32(q8[k].t[2 * e + 1]) * down);
+                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(to_f32(y.t[2 * e]) * down, to_f32(y.t[2 * e + 1]) * down);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + tc_place(r, g0 + k)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
                 }
                 if (g0 == 0)
@@ -648,6 +651,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         __syncwarp();
         if (here->any) {
             // r0, r1, r2: rows of the tiles g + 1, g + 2 and g + 3 of the loop below; `here` is tile g + 1, `ahead` g + 3
+            // (g = -1: only the first tile's K)
             uint32_t r0 = find(here);
             issue_a(r0, 0);
             issue_b(r0, 0);
@@ -657,22 +661,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             issue_b(r1, 1);
             step(ahead);
             uint32_t r2 = find(ahead);
-            bool ok = do_k(0, r0, r2);
-            int64_t keys = 1;  // tiles whose K is converted
-            step(here);
-            step(ahead);
-            r0 = r1;
-            r1 = r2;
-            r2 = find(ahead);
-            for (int64_t g = 0; ok; ++g) {
+            int64_t keys = 0;  // tiles whose K is converted
+            for (int64_t g = -1;; ++g) {
                 float scale[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) scale[b] = v_scale[b];
-                if (here->any)
-                    ok = do_k(keys++, r0, r2);
-                else
+                if (here->any) {
+                    if (!do_k(keys++, r0, r2)) break;
+                } else {
                     cp_commit();  // in the place of K's group
-                if (ok) ok = do_v(g, scale, r1);
+                }
+                if (g >= 0 && !do_v(g, scale, r1)) break;
                 if (g + 1 == keys) break;
                 step(here);
                 step(ahead);
