@@ -111,10 +111,14 @@ q8mv_status_t q8kv_cache_move(const q8kv_cache_t *cache, int64_t batch, int64_t 
  * softmax runs in f32, and its weights times the values' scales enter the
  * second product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs,
  * whose own rounding is eight times coarser).  With more than 32 bf16 query rows
- * a request and kv head (head_dim up to 128), keys enter the first product with
- * 22 bits and values the second with f16's 11; a value that is not finite then makes all of
- * a row that sees it NaN.  Sums are split over the GPU by
- * the lengths alone and joined in a fixed order: same inputs, same bits.
+ * a request and kv head (head_dim up to 128), and page tables long enough, keys
+ * may enter the first product with 22 bits and values the second with f16's 11;
+ * a value that is not finite then makes all of a row that sees it NaN.  Sums are
+ * split over the GPU by the call's shape and the lengths alone and joined in a
+ * fixed order: same inputs, same bits.
+ * Limits here: rows of the cache, (pages - 1) * stride_page + (heads - 1) *
+ * stride_head + (page_size - 1) * stride_token, below 2^32 - 1, and positions,
+ * table_cols * page_size, below 2^31 - 512.
  */
 typedef struct q8kv_attend_s *q8kv_attend_plan_t;
 

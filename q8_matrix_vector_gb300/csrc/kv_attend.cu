@@ -156,20 +156,27 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.wait_ns = plan->wait_ns;
     p.q_vec = kv::aligned(a->q, 16) && ((a->q_row | a->q_head) & 7) == 0;
     p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;
-    // 8, 16 or 32 query rows at a time, by the mean of a request's: the fewest that hold them.
+    // By the mean rows of a request, the fewest at a time that hold them: 8 or 16 (16 requests of 700 .. 4000 tokens, 8
+    // heads of 128, bf16: 12 rows 47.9 us by 8, 39.2 by 16; 8 rows 32.0 and 37.8).  32 at a time do not fit the
+    // registers (32 rows 60 us by 16, 90 by 32), nor do 16 of a head_dim above 128 (as fast as by 8, with spills).
+    const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
     // With 8, and a token's heads side by side, each warp can take a head of its own, so that a CTA reads longer
     // stretches: DRAM gives 128-byte pieces of 1 KB rows slowly (1.2 GB of cache, f32: 318 us with one head a CTA,
     // 240 us with four; 0.59 GB: 143 and 119 us).  But four heads' partial results are to be joined instead of one's
     // (0.28 GB of two requests: 68 and 81 us; 5 MB: 11.6 and 16.3 us), so only where the tables reach 0.5 GB.
-    const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
-    const double reach = static_cast<double>(a->requests) * a->table_cols * p.c.page_size * p.c.heads *
-                         (2.0 * p.c.dim + 8.0 * p.c.blocks);
-    const bool side_by_side = p.c.stride_head < p.c.stride_token && p.c.heads % kv::kWarps == 0 && reach >= 5e8;
-    const bool wide = mean > 32 && a->type == Q8KV_BF16 && p.c.dim <= 128;
-    const kv::AttendShape v = mean <= 8                            ? side_by_side ? kv::kHeads4 : kv::kRows8
-                              : wide                               ? kv::kRows128
-                              : mean <= 16 || p.c.dim > 128 ? kv::kRows16
-                                                            : kv::kRows32;
+    const int64_t reach = static_cast<int64_t>(a->table_cols) * p.c.page_size;
+    const double bytes = static_cast<double>(reach) * a->requests * p.c.heads * (2.0 * p.c.dim + 8.0 * p.c.blocks);
+    const bool side_by_side = p.c.stride_head < p.c.stride_token && p.c.heads % kv::kWarps == 0 && bytes >= 5e8;
+    // 128 bf16 rows at a time where there are more than 32 (36 rows of the 16 requests above: 75 us, by 16 rows 83;
+    // 128 rows: 86 and 189; but 32 rows: 75 and 60), and enough to do: its tiles of 128 keys take longer to fill and to
+    // join.  In tiles of 16 rows x 128 keys of the tables' reach, one request of 124 rows: 2048 tiles 45 us, by 16
+    // rows 31; four of 64 rows: 4096 tiles 50 and 49; four of 124 rows: 8192 tiles 53 and 82.
+    const double tiles = static_cast<double>(kv::ceil_div(mean, 16) * kv::ceil_div(reach, 128)) * a->requests * p.c.heads;
+    const bool wide = a->type == Q8KV_BF16 && p.c.dim <= 128 && mean > 32 && tiles >= 4096;
+    const kv::AttendShape v = wide                         ? kv::kRows128
+                              : mean <= 8 && side_by_side  ? kv::kHeads4
+                              : mean <= 8 || p.c.dim > 128 ? kv::kRows8
+                                                           : kv::kRows16;
     const kv::AttendVariant &k = plan->variant[a->type][v];
     k.fn<<<plan->grid[a->type][v], k.threads, k.smem, stream>>>(p);
     return q8i::cuda_status(cudaGetLastError());

@@ -305,57 +305,57 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
     for (int i = lane; i < S::kStage * kStages / 16; i += 32) reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
     auto issue = [&](bool any, int slot, uint32_t row) {
-            if (any) {
-                unsigned char *st = ring + slot * S::kStage;
-                const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(st));
-                const uint32_t sv = sk + kStepKeys * S::kKPitch;
-                const uint32_t ss = sv + kStepKeys * S::kVPitch;
-                constexpr int CPR = DP / 16;         // 16-byte pieces of a row
-                constexpr int KPI = 32 / CPR;        // keys of one load of the warp
-                const int part = lane % CPR, k0 = lane / CPR;
-                const bool live = part * 16 < p.c.dim;
-                const int8_t *kc = p.c.k_codes + part * 16, *vc = p.c.v_codes + part * 16;
-                const uint32_t dk0 = sk + k0 * S::kKPitch + part * 16, dv0 = sv + k0 * S::kVPitch + part * 16;
+        if (any) {
+            unsigned char *st = ring + slot * S::kStage;
+            const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(st));
+            const uint32_t sv = sk + kStepKeys * S::kKPitch;
+            const uint32_t ss = sv + kStepKeys * S::kVPitch;
+            constexpr int CPR = DP / 16;         // 16-byte pieces of a row
+            constexpr int KPI = 32 / CPR;        // keys of one load of the warp
+            const int part = lane % CPR, k0 = lane / CPR;
+            const bool live = part * 16 < p.c.dim;
+            const int8_t *kc = p.c.k_codes + part * 16, *vc = p.c.v_codes + part * 16;
+            const uint32_t dk0 = sk + k0 * S::kKPitch + part * 16, dv0 = sv + k0 * S::kVPitch + part * 16;
 #pragma unroll
-                for (int j = 0; j < CPR; ++j) {
-                    const uint32_t r = __shfl_sync(~0u, row, k0 + j * KPI);
-                    if (r != kNoRow && live) {
-                        cp_async16(dk0 + j * KPI * S::kKPitch, kc + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim));
-                        cp_async16(dv0 + j * KPI * S::kVPitch, vc + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim));
-                    }
+            for (int j = 0; j < CPR; ++j) {
+                const uint32_t r = __shfl_sync(~0u, row, k0 + j * KPI);
+                if (r != kNoRow && live) {
+                    cp_async16(dk0 + j * KPI * S::kKPitch, kc + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim));
+                    cp_async16(dv0 + j * KPI * S::kVPitch, vc + static_cast<uint64_t>(r) * static_cast<uint32_t>(p.c.dim));
                 }
-                const uint32_t dk = ss + lane * (NB * 4), dv = dk + S::kScaleBytes;
-                if (row != kNoRow) {
-                    const float *ks = p.c.k_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
-                    const float *vs = p.c.v_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
-                    if (wide_scales) {
+            }
+            const uint32_t dk = ss + lane * (NB * 4), dv = dk + S::kScaleBytes;
+            if (row != kNoRow) {
+                const float *ks = p.c.k_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
+                const float *vs = p.c.v_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
+                if (wide_scales) {
 #pragma unroll
-                        for (int b = 0; b < (NB + 3) / 4; ++b) {
-                            if (b * 4 < p.c.blocks) {
-                                cp_async16(dk + b * 16, ks + b * 4);
-                                cp_async16(dv + b * 16, vs + b * 4);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            if (b < p.c.blocks) {
-                                cp_async4(dk + b * 4, ks + b);
-                                cp_async4(dv + b * 4, vs + b);
-                            }
+                    for (int b = 0; b < (NB + 3) / 4; ++b) {
+                        if (b * 4 < p.c.blocks) {
+                            cp_async16(dk + b * 16, ks + b * 4);
+                            cp_async16(dv + b * 16, vs + b * 4);
                         }
                     }
                 } else {
-                    // an absent key has scales of 0: whatever codes the ring holds, it adds nothing
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        *reinterpret_cast<float *>(st + (dk - sk) + 4 * b) = 0.0f;
-                        *reinterpret_cast<float *>(st + (dv - sk) + 4 * b) = 0.0f;
+                        if (b < p.c.blocks) {
+                            cp_async4(dk + b * 4, ks + b);
+                            cp_async4(dv + b * 4, vs + b);
+                        }
                     }
                 }
+            } else {
+                // an absent key has scales of 0: whatever codes the ring holds, it adds nothing
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    *reinterpret_cast<float *>(st + (dk - sk) + 4 * b) = 0.0f;
+                    *reinterpret_cast<float *>(st + (dv - sk) + 4 * b) = 0.0f;
+                }
             }
-            cp_commit();
-        };
+        }
+        cp_commit();
+    };
 
     // What a CTA does of one item: key tiles kt0 .. kt1 - 1, one step of the warp in each.
     struct Work {
@@ -402,109 +402,108 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
     for (;;) {
         const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
         if (k.n_steps > 0) {
-        // ---- q rows to shared memory: a power of two per row, then f16 parts
-        for (int rr = tid >> 3; rr < HW * ROWS; rr += kWarps * 4) {
-            const int l8 = tid & 7, hw = rr / ROWS, r = rr % ROWS;
-            const int idx = w.rt * ROWS + r, node = idx / p.group, hq = (w.h + hw) * p.group + idx - node * p.group;
-            const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
-            float x[DP / 8];
-            float top = 0.0f;
+            // ---- q rows to shared memory: a power of two per row, then f16 parts
+            for (int rr = tid >> 3; rr < HW * ROWS; rr += kWarps * 4) {
+                const int l8 = tid & 7, hw = rr / ROWS, r = rr % ROWS;
+                const int idx = w.rt * ROWS + r, node = idx / p.group, hq = (w.h + hw) * p.group + idx - node * p.group;
+                const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
+                float x[DP / 8];
+                float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-                const int e = l8 + 8 * i;
-                x[i] = r < rows && e < p.c.dim ? to_f32(src[e]) : 0.0f;
-                top = fmaxf(top, fabsf(x[i]));
-            }
-#pragma unroll
-            for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13, -100), 100);
-            // 2^-ex, and the sign of the scale, so that the rows' factors are positive
-            const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - ex) << 23), p.scale_log2);
-            float sum[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) sum[b] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-                const float y = x[i] * down;
-                const __half hi = __float2half_rn(y);
-                __half *dst = reinterpret_cast<__half *>(q_sm + hw * S::kQHead + r * S::kQPitch) + l8 + 8 * i;
-                *dst = hi;
-                float used = __half2float(hi);
-                if constexpr (QP == 2) {
-                    const __half lo = __float2half_rn(y - used);
-                    dst[ROWS * S::kQPitch / 2] = lo;
-                    used += __half2float(lo);
+                for (int i = 0; i < DP / 8; ++i) {
+                    const int e = l8 + 8 * i;
+                    x[i] = r < rows && e < p.c.dim ? to_f32(src[e]) : 0.0f;
+                    top = fmaxf(top, fabsf(x[i]));
                 }
-                sum[i / 4] += used;
+#pragma unroll
+                for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13, -100), 100);
+                // 2^-ex, and the sign of the scale, so that the rows' factors are positive
+                const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - ex) << 23), p.scale_log2);
+                float sum[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) sum[b] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) {
+                    const float y = x[i] * down;
+                    const __half hi = __float2half_rn(y);
+                    __half *dst = reinterpret_cast<__half *>(q_sm + hw * S::kQHead + r * S::kQPitch) + l8 + 8 * i;
+                    *dst = hi;
+                    float used = __half2float(hi);
+                    if constexpr (QP == 2) {
+                        const __half lo = __float2half_rn(y - used);
+                        dst[ROWS * S::kQPitch / 2] = lo;
+                        used += __half2float(lo);
+                    }
+                    sum[i / 4] += used;
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int d = 1; d < 8; d *= 2) sum[b] += __shfl_xor_sync(~0u, sum[b], d);
+                    if (l8 == 0) bias_sm[hw * (ROWS * NB) + ((r >> 1) * NB + b) * 2 + (r & 1)] = -128.0f / 16777216.0f * sum[b];
+                }
+                // not 0: a score of -inf has to stay that
+                if (l8 == 0)
+                    row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex + 24) << 23) * fabsf(p.scale_log2), 1e-37f);
             }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int d = 1; d < 8; d *= 2) sum[b] += __shfl_xor_sync(~0u, sum[b], d);
-                if (l8 == 0) bias_sm[hw * (ROWS * NB) + ((r >> 1) * NB + b) * 2 + (r & 1)] = -128.0f / 16777216.0f * sum[b];
-            }
-            // not 0: a score of -inf has to stay that
-            if (l8 == 0)
-                row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex + 24) << 23) * fabsf(p.scale_log2), 1e-37f);
-        }
-        __syncthreads();
+            __syncthreads();
 
-        float o[NT][NB * 2][4];
+            float o[NT][NB * 2][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < NB * 2; ++i)
+                for (int i = 0; i < NB * 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[t][i][j] = 0.0f;
-        // of rows 8 t + 2c and 8 t + 2c + 1; m: running maximum (log2) plus E
-        float m[NT][2], l[NT][2], mul[NT][2];
+                    for (int j = 0; j < 4; ++j) o[t][i][j] = 0.0f;
+            // of rows 8 t + 2c and 8 t + 2c + 1; m: running maximum (log2) plus E
+            float m[NT][2], l[NT][2], mul[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                m[t][r] = -INFINITY;
-                l[t][r] = 0.0f;
-                mul[t][r] = row_mul[(HW == 1 ? 0 : warp * ROWS) + 8 * t + 2 * c + r];
-            }
+                for (int r = 0; r < 2; ++r) {
+                    m[t][r] = -INFINITY;
+                    l[t][r] = 0.0f;
+                    mul[t][r] = row_mul[(HW == 1 ? 0 : warp * ROWS) + 8 * t + 2 * c + r];
+                }
 
-        const unsigned char *my_q = q_sm + (HW == 1 ? 0 : warp * S::kQHead);
-        const float *my_bias = bias_sm + (HW == 1 ? 0 : warp * (ROWS * NB));
-        int slot = slot0;
-        for (int i = 0; i < k.n_steps; ++i) {
-            // row_cur[0] is step i's; the next free stage takes step i + kStages - 1
-            row_cur[kStages - 1] = row_next;
-            issue(i + kStages - 1 < k.n_steps, slot == 0 ? kStages - 1 : slot - 1, row_next);
-            row_next = find(k, i + kStages);
-            cp_wait<kStages - 1>();
-            __syncwarp();
-            const unsigned char *sk = ring + slot * S::kStage, *sv = sk + kStepKeys * S::kKPitch;
-            const float *ks = reinterpret_cast<const float *>(sv + kStepKeys * S::kVPitch);
-            const float *vs = ks + kStepKeys * NB;
-            const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow);
-            const int base = k.base0 + i * KEYS;
-            if (there != 0) {
-                // 2^(E + 14) is above the scales of the lane's key, and of all keys
-                uint32_t top_bits = 0;
+            const unsigned char *my_q = q_sm + (HW == 1 ? 0 : warp * S::kQHead);
+            const float *my_bias = bias_sm + (HW == 1 ? 0 : warp * (ROWS * NB));
+            int slot = slot0;
+            for (int i = 0; i < k.n_steps; ++i) {
+                // row_cur[0] is step i's; the next free stage takes step i + kStages - 1
+                row_cur[kStages - 1] = row_next;
+                issue(i + kStages - 1 < k.n_steps, slot == 0 ? kStages - 1 : slot - 1, row_next);
+                row_next = find(k, i + kStages);
+                cp_wait<kStages - 1>();
+                __syncwarp();
+                const unsigned char *sk = ring + slot * S::kStage, *sv = sk + kStepKeys * S::kKPitch;
+                const float *ks = reinterpret_cast<const float *>(sv + kStepKeys * S::kVPitch);
+                const float *vs = ks + kStepKeys * NB;
+                const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow);
+                const int base = k.base0 + i * KEYS;
+                if (there != 0) {
+                    // 2^(E + 14) is above the scales of the lane's key, and of all keys
+                    uint32_t top_bits = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) top_bits = max(top_bits, __float_as_uint(vs[lane * NB + b]) & 0x7FFFFFFFu);
-                const float e_key = static_cast<float>(max(min(static_cast<int>(top_bits >> 23) - 127 + 1 - 14, 114), -100));
-                const float e_all = static_cast<float>(
-                    max(min(static_cast<int>(__reduce_max_sync(~0u, top_bits) >> 23) - 127 + 1 - 14, 114), -100));
+                    for (int b = 0; b < NB; ++b) top_bits = max(top_bits, __float_as_uint(vs[lane * NB + b]) & 0x7FFFFFFFu);
+                    const float e_key = static_cast<float>(max(min(static_cast<int>(top_bits >> 23) - 127 + 1 - 14, 114), -100));
+                    const float e_all = static_cast<float>(
+                        max(min(static_cast<int>(__reduce_max_sync(~0u, top_bits) >> 23) - 127 + 1 - 14, 114), -100));
 
-                // ---- scores: s[t][2 j + k][r] of key 16 j + 8 k + g and row 8 t + 2c + r
-                float s[NT][4][2];
+                    // ---- scores: s[t][2 j + k][r] of key 16 j + 8 k + g and row 8 t + 2c + r
+                    float s[NT][4][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float d0[NB], d1[NB];  // scales of keys 16 j + g and 16 j + 8 + g
-                    load_scales<NB>(ks + (16 * j + g) * NB, d0);
-                    load_scales<NB>(ks + (16 * j + 8 + g) * NB, d1);
+                    for (int j = 0; j < 2; ++j) {
+                        float d0[NB], d1[NB];  // scales of keys 16 j + g and 16 j + 8 + g
+                        load_scales<NB>(ks + (16 * j + g) * NB, d0);
+                        load_scales<NB>(ks + (16 * j + 8 + g) * NB, d1);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) s[t][2 * j][r] = s[t][2 * j + 1][r] = 0.0f;
+                            for (int r = 0; r < 2; ++r) s[t][2 * j][r] = s[t][2 * j + 1][r] = 0.0f;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        {
+                        for (int b = 0; b < NB; ++b) {
                             const uint2 x = *reinterpret_cast<const uint2 *>(sk + (16 * j + g) * S::kKPitch + b * 32 + c * 8);
                             const uint2 y = *reinterpret_cast<const uint2 *>(sk + (16 * j + 8 + g) * S::kKPitch + b * 32 + c * 8);
                             const uint32_t x0 = x.x ^ 0x80808080u, x1 = x.y ^ 0x80808080u;
@@ -532,82 +531,80 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
                             }
                         }
                     }
-                }
-                // ---- softmax
-                const bool drafts = base + kStepKeys > w.prefix;
-                const bool partial = drafts || there != ~0u;
-                bool moved = false;
-                float z[NT][2];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float top[2];
-                    if (partial) {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            uint32_t see = there;
-                            if (drafts)
-                                see &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
-                                            w.rt * ROWS + 8 * t + 2 * c + r);
-                            top[r] = -INFINITY;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int key = 8 * k + g;
-                                if (((see >> key) & 1u) == 0) s[t][k][r] = -INFINITY;
-                                // a row's E comes from keys that it sees, so that no other's scale matters
-                                top[r] = fmaxf(top[r], fmaf(s[t][k][r], mul[t][r], __shfl_sync(~0u, e_key, key)));
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r)
-                            top[r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-                        for (int d = 4; d < 32; d *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
-                        const float n = fmaxf(m[t][r], top[r]);
-                        moved |= n != m[t][r];
-                        z[t][r] = n;
-                    }
-                }
-                if (__any_sync(~0u, moved)) {
+                    // ---- softmax
+                    const bool drafts = base + kStepKeys > w.prefix;
+                    const bool partial = drafts || there != ~0u;
+                    bool moved = false;
+                    float z[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        float f[2];
+                        float top[2];
+                        if (partial) {
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                uint32_t see = there;
+                                if (drafts)
+                                    see &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
+                                                w.rt * ROWS + 8 * t + 2 * c + r);
+                                top[r] = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int key = 8 * k + g;
+                                    if (((see >> key) & 1u) == 0) s[t][k][r] = -INFINITY;
+                                    // a row's E comes from keys that it sees, so that no other's scale matters
+                                    top[r] = fmaxf(top[r], fmaf(s[t][k][r], mul[t][r], __shfl_sync(~0u, e_key, key)));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                top[r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
+                        }
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            f[r] = ex2(m[t][r] - (z[t][r] == -INFINITY ? 0.0f : z[t][r]));
-                            m[t][r] = z[t][r];
-                            l[t][r] *= f[r];
-                        }
 #pragma unroll
-                        for (int k = 0; k < NB * 2; ++k) {
-                            o[t][k][0] *= f[0];
-                            o[t][k][1] *= f[1];
-                            o[t][k][2] *= f[0];
-                            o[t][k][3] *= f[1];
+                            for (int d = 4; d < 32; d *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
+                            const float n = fmaxf(m[t][r], top[r]);
+                            moved |= n != m[t][r];
+                            z[t][r] = n;
                         }
                     }
-                }
+                    if (__any_sync(~0u, moved)) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                        for (int t = 0; t < NT; ++t) {
+                            float f[2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float n = z[t][r] == -INFINITY ? 0.0f : -z[t][r];
+                            for (int r = 0; r < 2; ++r) {
+                                f[r] = ex2(m[t][r] - (z[t][r] == -INFINITY ? 0.0f : z[t][r]));
+                                m[t][r] = z[t][r];
+                                l[t][r] *= f[r];
+                            }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            s[t][k][r] = ex2(fmaf(s[t][k][r], mul[t][r], n));
-                            l[t][r] += s[t][k][r];
+                            for (int k = 0; k < NB * 2; ++k) {
+                                o[t][k][0] *= f[0];
+                                o[t][k][1] *= f[1];
+                                o[t][k][2] *= f[0];
+                                o[t][k][3] *= f[1];
+                            }
                         }
                     }
-                // ---- O^T += V^T (P dV)^T, block by block, 16 keys at a time
-                float dv[4][NB];  // scales of keys 8 k + g
 #pragma unroll
-                for (int k = 0; k < 4; ++k) load_scales<NB>(vs + (8 * k + g) * NB, dv[k]);
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    {
+                        for (int r = 0; r < 2; ++r) {
+                            const float n = z[t][r] == -INFINITY ? 0.0f : -z[t][r];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                s[t][k][r] = ex2(fmaf(s[t][k][r], mul[t][r], n));
+                                l[t][r] += s[t][k][r];
+                            }
+                        }
+                    // ---- O^T += V^T (P dV)^T, block by block, 16 keys at a time
+                    float dv[4][NB];  // scales of keys 8 k + g
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) load_scales<NB>(vs + (8 * k + g) * NB, dv[k]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
                         // The tensor cores cut their f32 sums toward zero.  Over thousands of keys that bias is
                         // 1e-5 of the sum: with f32 or f16 outputs a step's 32 keys are summed apart, and added
                         // with rounding.
@@ -672,229 +669,228 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
                         }
                     }
                 }
+                __syncwarp();
+                slot = slot + 1 == kStages ? 0 : slot + 1;
+#pragma unroll
+                for (int j = 0; j + 1 < kStages; ++j) row_cur[j] = row_cur[j + 1];
             }
-            __syncwarp();
-            slot = slot + 1 == kStages ? 0 : slot + 1;
+            slot0 = slot;
+            // ---- the next item's first keys are on their way while the warps of this one are joined
+            const Place done = w;
+            const Work did = k;
+            const bool more = w.first + w.tiles_k < u_end;
+            if (more) {
+                advance(w);
+                k = work_of(w);
+                begin(k);
+            }
+            const bool whole = did.kt0 == 0 && did.kt1 == done.tiles_k;
+            const int pitch = p.c.dim + kPartExtra;
+            const int64_t slot_p = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
+            first_item = false;
+            // tile t, row r8 of the item's results: its output row and query head
+            auto place_row = [&](int t, int r8, int64_t *row, int *hq) -> bool {
+                const int r = HW == 1 ? 8 * t + r8 : r8;
+                const int idx = done.rt * ROWS + r, node = idx / p.group;
+                *row = static_cast<int64_t>(done.row0) + node;
+                *hq = (done.h + (HW == 1 ? 0 : t)) * p.group + idx - node * p.group;
+                return r < rows;
+            };
+            if constexpr (HW > 1) {
+                // each warp has whole results of its head
 #pragma unroll
-            for (int j = 0; j + 1 < kStages; ++j) row_cur[j] = row_cur[j + 1];
-        }
-        slot0 = slot;
-        // ---- the next item's first keys are on their way while the warps of this one are joined
-        const Place done = w;
-        const Work did = k;
-        const bool more = w.first + w.tiles_k < u_end;
-        if (more) {
-            advance(w);
-            k = work_of(w);
-            begin(k);
-        }
-        const bool whole = did.kt0 == 0 && did.kt1 == done.tiles_k;
-        const int pitch = p.c.dim + kPartExtra;
-        const int64_t slot_p = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
-        first_item = false;
-        // tile t, row r8 of the item's results: its output row and query head
-        auto place_row = [&](int t, int r8, int64_t *row, int *hq) -> bool {
-            const int r = HW == 1 ? 8 * t + r8 : r8;
-            const int idx = done.rt * ROWS + r, node = idx / p.group;
-            *row = static_cast<int64_t>(done.row0) + node;
-            *hq = (done.h + (HW == 1 ? 0 : t)) * p.group + idx - node * p.group;
-            return r < rows;
-        };
-        if constexpr (HW > 1) {
-            // each warp has whole results of its head
+                for (int r = 0; r < 2; ++r) {
+                    const int r8 = 2 * c + r;
+                    int64_t row;
+                    int hq;
+                    const bool live = place_row(warp, r8, &row, &hq);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int r8 = 2 * c + r;
+                    for (int d = 4; d < 32; d *= 2) l[0][r] += __shfl_xor_sync(~0u, l[0][r], d);
+                    if (live) {
+                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                        float *part = p.partial + (slot_p * (8 * TILES) + warp * 8 + r8) * pitch;
+                        const float sum = l[0][r], inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const int e = 32 * b + 4 * g;
+                            const float4 x = make_float4(o[0][2 * b][r], o[0][2 * b][2 + r], o[0][2 * b + 1][r], o[0][2 * b + 1][2 + r]);
+                            if (e < p.c.dim) {
+                                if (whole) {
+                                    out[e] = from_f32<T>(x.x * inv);
+                                    out[e + 1] = from_f32<T>(x.y * inv);
+                                    out[e + 2] = from_f32<T>(x.z * inv);
+                                    out[e + 3] = from_f32<T>(x.w * inv);
+                                } else {
+                                    *reinterpret_cast<float4 *>(part + e) = x;
+                                }
+                            }
+                        }
+                        if (g == 0) {
+                            if (!whole) {
+                                part[p.c.dim] = m[0][r];
+                                part[p.c.dim + 1] = sum;
+                            } else if (p.lse) {
+                                p.lse[row * p.heads_q + hq] = ((m[0][r] == -INFINITY ? 0.0f : m[0][r]) + log2f(sum)) * 0.693147180559945f;
+                            }
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t > 0) __syncthreads();
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float *at = jo + (warp * 8 + 2 * c + r) * S::kJoinPitch;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            *reinterpret_cast<float4 *>(at + 32 * b + 4 * g) =
+                                make_float4(o[t][2 * b][r], o[t][2 * b][2 + r], o[t][2 * b + 1][r], o[t][2 * b + 1][2 + r]);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) l[t][r] += __shfl_xor_sync(~0u, l[t][r], d);
+                        if (g == 0) {
+                            at[DP] = m[t][r];
+                            at[DP + 1] = l[t][r];
+                        }
+                    }
+                    __syncthreads();
+                    // kWarps * 4 threads a row
+                    constexpr int TPR = kWarps * 4;
+                    const int r8 = tid / TPR, lr = tid % TPR;
+                    float f[kWarps], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < kWarps; ++q) top = fmaxf(top, jo[(q * 8 + r8) * S::kJoinPitch + DP]);
+                    const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                    for (int q = 0; q < kWarps; ++q) {
+                        const float *x = jo + (q * 8 + r8) * S::kJoinPitch;
+                        f[q] = ex2(x[DP] - z);
+                        sum = fmaf(f[q], x[DP + 1], sum);
+                    }
+                    int64_t row;
+                    int hq;
+                    if (place_row(t, r8, &row, &hq)) {
+                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                        float *part = p.partial + (slot_p * (8 * TILES) + 8 * t + r8) * pitch;
+                        const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
+#pragma unroll
+                        for (int q = 0; q < DP / TPR; ++q) {
+                            const int e = lr + TPR * q;
+                            if (e < p.c.dim) {
+                                float x = 0.0f;
+#pragma unroll
+                                for (int v = 0; v < kWarps; ++v) x = fmaf(f[v], jo[(v * 8 + r8) * S::kJoinPitch + e], x);
+                                if (whole)
+                                    out[e] = from_f32<T>(x * inv);
+                                else
+                                    part[e] = x;
+                            }
+                        }
+                        if (lr == 0) {
+                            if (!whole) {
+                                part[p.c.dim] = top;
+                                part[p.c.dim + 1] = sum;
+                            } else if (p.lse) {
+                                p.lse[row * p.heads_q + hq] = (z + log2f(sum)) * 0.693147180559945f;
+                            }
+                        }
+                    }
+                }
+            }
+            // (an item past the tickets exists only if `starts` is not ascending: it has no output)
+            if (!whole && done.item < p.tickets_n) {
+                constexpr int PR = 8 * TILES, TPR = kWarps * 32 / PR, V = DP / 4 / TPR;  // rows, threads a row, float4 a thread
+                const int pr = tid / TPR, lr = tid % TPR;
                 int64_t row;
                 int hq;
-                const bool live = place_row(warp, r8, &row, &hq);
+                const bool live = place_row(pr / 8, pr % 8, &row, &hq);
+                // Adds n parts, the first at slot `head`, the i-th at slot `at + i * step`: to the output, or to the
+                // first part's place.
+                auto join = [&](int n, int64_t head, int64_t at, int64_t step, bool last) {
+                    const float *from = p.partial + (at * PR + pr) * pitch, *from0 = p.partial + (head * PR + pr) * pitch;
+                    step *= PR * pitch;
+                    float top = -INFINITY, sum = 0.0f, x[V][4];
 #pragma unroll
-                for (int d = 4; d < 32; d *= 2) l[0][r] += __shfl_xor_sync(~0u, l[0][r], d);
-                if (live) {
-                    T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
-                    float *part = p.partial + (slot_p * (8 * TILES) + warp * 8 + r8) * pitch;
-                    const float sum = l[0][r], inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+                    for (int q = 0; q < V; ++q)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const int e = 32 * b + 4 * g;
-                        const float4 x = make_float4(o[0][2 * b][r], o[0][2 * b][2 + r], o[0][2 * b + 1][r], o[0][2 * b + 1][2 + r]);
-                        if (e < p.c.dim) {
-                            if (whole) {
-                                out[e] = from_f32<T>(x.x * inv);
-                                out[e + 1] = from_f32<T>(x.y * inv);
-                                out[e + 2] = from_f32<T>(x.z * inv);
-                                out[e + 3] = from_f32<T>(x.w * inv);
-                            } else {
-                                *reinterpret_cast<float4 *>(part + e) = x;
-                            }
-                        }
-                    }
-                    if (g == 0) {
-                        if (!whole) {
-                            part[p.c.dim] = m[0][r];
-                            part[p.c.dim + 1] = sum;
-                        } else if (p.lse) {
-                            p.lse[row * p.heads_q + hq] = ((m[0][r] == -INFINITY ? 0.0f : m[0][r]) + log2f(sum)) * 0.693147180559945f;
-                        }
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (t > 0) __syncthreads();
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float *at = jo + (warp * 8 + 2 * c + r) * S::kJoinPitch;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    *reinterpret_cast<float4 *>(at + 32 * b + 4 * g) =
-                        make_float4(o[t][2 * b][r], o[t][2 * b][2 + r], o[t][2 * b + 1][r], o[t][2 * b + 1][2 + r]);
-#pragma unroll
-                for (int d = 4; d < 32; d *= 2) l[t][r] += __shfl_xor_sync(~0u, l[t][r], d);
-                if (g == 0) {
-                    at[DP] = m[t][r];
-                    at[DP + 1] = l[t][r];
-                }
-            }
-            __syncthreads();
-            // kWarps * 4 threads a row
-            constexpr int TPR = kWarps * 4;
-            const int r8 = tid / TPR, lr = tid % TPR;
-            float f[kWarps], top = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) top = fmaxf(top, jo[(q * 8 + r8) * S::kJoinPitch + DP]);
-            const float z = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) {
-                const float *x = jo + (q * 8 + r8) * S::kJoinPitch;
-                f[q] = ex2(x[DP] - z);
-                sum = fmaf(f[q], x[DP + 1], sum);
-            }
-            int64_t row;
-            int hq;
-            if (place_row(t, r8, &row, &hq)) {
-                T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
-                float *part = p.partial + (slot_p * (8 * TILES) + 8 * t + r8) * pitch;
-                const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
-#pragma unroll
-                for (int q = 0; q < DP / TPR; ++q) {
-                    const int e = lr + TPR * q;
-                    if (e < p.c.dim) {
-                        float x = 0.0f;
-#pragma unroll
-                        for (int v = 0; v < kWarps; ++v) x = fmaf(f[v], jo[(v * 8 + r8) * S::kJoinPitch + e], x);
-                        if (whole)
-                            out[e] = from_f32<T>(x * inv);
-                        else
-                            part[e] = x;
-                    }
-                }
-                if (lr == 0) {
-                    if (!whole) {
-                        part[p.c.dim] = top;
-                        part[p.c.dim + 1] = sum;
-                    } else if (p.lse) {
-                        p.lse[row * p.heads_q + hq] = (z + log2f(sum)) * 0.693147180559945f;
-                    }
-                }
-            }
-        }
-        }
-        // (an item past the tickets exists only if `starts` is not ascending: it has no output)
-        if (!whole && done.item < p.tickets_n) {
-            constexpr int PR = 8 * TILES, TPR = kWarps * 32 / PR, V = DP / 4 / TPR;  // rows, threads a row, float4 a thread
-            const int pr = tid / TPR, lr = tid % TPR;
-            int64_t row;
-            int hq;
-            const bool live = place_row(pr / 8, pr % 8, &row, &hq);
-            // Adds n parts, the first at slot `head`, the i-th at slot `at + i * step`: to the output, or to the
-            // first part's place.
-            auto join = [&](int n, int64_t head, int64_t at, int64_t step, bool last) {
-                const float *from = p.partial + (at * PR + pr) * pitch, *from0 = p.partial + (head * PR + pr) * pitch;
-                step *= PR * pitch;
-                float top = -INFINITY, sum = 0.0f, x[V][4];
-#pragma unroll
-                for (int q = 0; q < V; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[q][e] = 0.0f;
-                if (live) {
-                    for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg((i == 0 ? from0 : from + i * step) + p.c.dim));
-                    const float z = top == -INFINITY ? 0.0f : top;
+                        for (int e = 0; e < 4; ++e) x[q][e] = 0.0f;
+                    if (live) {
+                        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg((i == 0 ? from0 : from + i * step) + p.c.dim));
+                        const float z = top == -INFINITY ? 0.0f : top;
 #pragma unroll (V <= 2 ? 8 : 4)
-                    for (int i = 0; i < n; ++i) {
-                        const float *part = i == 0 ? from0 : from + i * step;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + p.c.dim));
-                        const float f = ex2(ml.x - z);
-                        sum = fmaf(f, ml.y, sum);
+                        for (int i = 0; i < n; ++i) {
+                            const float *part = i == 0 ? from0 : from + i * step;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + p.c.dim));
+                            const float f = ex2(ml.x - z);
+                            sum = fmaf(f, ml.y, sum);
 #pragma unroll
-                        for (int q = 0; q < V; ++q) {
-                            const int e0 = 4 * (lr + TPR * q);
-                            if (e0 < p.c.dim) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + e0));
-                                x[q][0] = fmaf(f, y.x, x[q][0]);
-                                x[q][1] = fmaf(f, y.y, x[q][1]);
-                                x[q][2] = fmaf(f, y.z, x[q][2]);
-                                x[q][3] = fmaf(f, y.w, x[q][3]);
+                            for (int q = 0; q < V; ++q) {
+                                const int e0 = 4 * (lr + TPR * q);
+                                if (e0 < p.c.dim) {
+                                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + e0));
+                                    x[q][0] = fmaf(f, y.x, x[q][0]);
+                                    x[q][1] = fmaf(f, y.y, x[q][1]);
+                                    x[q][2] = fmaf(f, y.z, x[q][2]);
+                                    x[q][3] = fmaf(f, y.w, x[q][3]);
+                                }
                             }
                         }
                     }
-                }
-                __syncwarp();  // a row's threads have read the first part
-                if (live && last) {
-                    const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
-                    T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                    __syncwarp();  // a row's threads have read the first part
+                    if (live && last) {
+                        const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
 #pragma unroll
-                    for (int q = 0; q < V; ++q)
+                        for (int q = 0; q < V; ++q)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (4 * (lr + TPR * q) < p.c.dim) out[4 * (lr + TPR * q) + e] = from_f32<T>(x[q][e] * inv);
-                    if (lr == 0 && p.lse)
-                        p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
-                } else if (live) {
-                    float *to = p.partial + (head * PR + pr) * pitch;
+                            for (int e = 0; e < 4; ++e)
+                                if (4 * (lr + TPR * q) < p.c.dim) out[4 * (lr + TPR * q) + e] = from_f32<T>(x[q][e] * inv);
+                        if (lr == 0 && p.lse)
+                            p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
+                    } else if (live) {
+                        float *to = p.partial + (head * PR + pr) * pitch;
 #pragma unroll
-                    for (int q = 0; q < V; ++q)
-                        if (4 * (lr + TPR * q) < p.c.dim)
-                            *reinterpret_cast<float4 *>(to + 4 * (lr + TPR * q)) = make_float4(x[q][0], x[q][1], x[q][2], x[q][3]);
-                    if (lr == 0) {
-                        to[p.c.dim] = top;
-                        to[p.c.dim + 1] = sum;
+                        for (int q = 0; q < V; ++q)
+                            if (4 * (lr + TPR * q) < p.c.dim)
+                                *reinterpret_cast<float4 *>(to + 4 * (lr + TPR * q)) = make_float4(x[q][0], x[q][1], x[q][2], x[q][3]);
+                        if (lr == 0) {
+                            to[p.c.dim] = top;
+                            to[p.c.dim + 1] = sum;
+                        }
+                    }
+                };
+                // true in the CTA that is the last of n to come
+                auto arrive = [&](unsigned *ticket, unsigned n) -> bool {
+                    __threadfence();
+                    __syncthreads();
+                    if (tid == 0) {
+                        const unsigned t = atomicAdd(ticket, 1u);
+                        is_last = t == n - 1;
+                        if (is_last) *ticket = 0;
+                    }
+                    __syncthreads();
+                    const bool yes = is_last;
+                    if (yes) __threadfence();
+                    return yes;
+                };
+                // Parts c0 .. c1.  Up to kJoinGroup of them are joined at once; more are joined in groups of CTAs
+                // whose numbers agree but for the last bits, by each group's last, and then the groups.
+                const int c0 = static_cast<int>(split.owner(done.first)), c1 = static_cast<int>(split.owner(done.first + done.tiles_k - 1));
+                const int slot_c0 = split.begin(c0) >= done.first - kItemUnits ? 2 * c0 : 2 * c0 + 1;
+                if (c1 - c0 < kJoinGroup) {
+                    if (arrive(p.tickets + done.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
+                } else {
+                    const int grp = blockIdx.x / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
+                    const int lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
+                    // one item may come into a group from its left, and one may begin in it and leave it
+                    if (arrive(p.group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1)) {
+                        join(hi - lo + 1, lo == c0 ? slot_c0 : 2 * lo, 2 * lo, 2, false);
+                        if (arrive(p.tickets + done.item, g1 - g0 + 1))
+                            join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
                     }
                 }
-            };
-            // true in the CTA that is the last of n to come
-            auto arrive = [&](unsigned *ticket, unsigned n) -> bool {
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) {
-                    const unsigned t = atomicAdd(ticket, 1u);
-                    is_last = t == n - 1;
-                    if (is_last) *ticket = 0;
-                }
-                __syncthreads();
-                const bool yes = is_last;
-                if (yes) __threadfence();
-                return yes;
-            };
-            // Parts c0 .. c1.  Up to kJoinGroup of them are joined at once; more are joined in groups of CTAs
-            // whose numbers agree but for the last bits, by each group's last, and then the groups.
-            const int c0 = static_cast<int>(split.owner(done.first)), c1 = static_cast<int>(split.owner(done.first + done.tiles_k - 1));
-            const int slot_c0 = split.begin(c0) >= done.first - kItemUnits ? 2 * c0 : 2 * c0 + 1;
-            if (c1 - c0 < kJoinGroup) {
-                if (arrive(p.tickets + done.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
-            } else {
-                const int grp = blockIdx.x / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
-                const int lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
-                // one item may come into a group from its left, and one may begin in it and leave it
-                if (arrive(p.group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1)) {
-                    join(hi - lo + 1, lo == c0 ? slot_c0 : 2 * lo, 2 * lo, 2, false);
-                    if (arrive(p.tickets + done.item, g1 - g0 + 1))
-                        join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
-                }
             }
-        }
-        if (!more) break;
+            if (!more) break;
         } else {
             // only units of the item's fixed cost are here
             if (w.first + w.tiles_k >= u_end) break;
@@ -906,7 +902,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
     }
 }
 
-// The variants of one type; 32 rows of a dim above 128 do not fit the registers.
+// The variants of one type.
 template <typename T, int DP, int QP, int PP, int NT, int HW>
 AttendVariant attend_variant_of(int dim) {
     return {q8kv_attend_kernel<T, DP, NT, QP, PP, HW>, Smem<DP, NT, QP, HW>::kTotal, kWarps * 32,
@@ -917,7 +913,7 @@ template <typename T, int QP, int PP, int NT, int HW>
 AttendVariant attend_variant_of(int dim) {
     if (dim <= 64) return attend_variant_of<T, 64, QP, PP, NT, HW>(dim);
     if (dim <= 128) return attend_variant_of<T, 128, QP, PP, NT, HW>(dim);
-    if constexpr (NT <= 2) return attend_variant_of<T, 256, QP, PP, NT, HW>(dim);
+    if constexpr (NT == 1) return attend_variant_of<T, 256, QP, PP, NT, HW>(dim);
     return {};
 }
 
@@ -926,7 +922,6 @@ AttendVariant attend_variant_of(int dim, AttendShape shape) {
     switch (shape) {
         case kRows8: return attend_variant_of<T, QP, PP, 1, 1>(dim);
         case kRows16: return attend_variant_of<T, QP, PP, 2, 1>(dim);
-        case kRows32: return attend_variant_of<T, QP, PP, 4, 1>(dim);
         case kHeads4: return attend_variant_of<T, QP, PP, 1, kWarps>(dim);
         default: return {};
     }

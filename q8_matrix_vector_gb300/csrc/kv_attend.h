@@ -40,13 +40,13 @@ struct AttendParams {
     int q_vec, out_vec; // 16-byte loads of eight queries, stores of eight outputs are aligned (kRows128)
 };
 
-// What an item is: 8, 16 or 32 query rows (node, head of the group) of one kv head
+// What an item is: 8 or 16 query rows (node, head of the group) of one kv head
 // whose keys the warps share, 8 rows of four kv heads, one for each warp, or 128
 // rows of one kv head on the tensor-memory path (kv_attend_tc.cuh).
-enum AttendShape { kRows8 = 0, kRows16, kRows32, kHeads4, kRows128, kAttendShapes };
+enum AttendShape { kRows8 = 0, kRows16, kHeads4, kRows128, kAttendShapes };
 
-// One variant of the kernel: dim up to 64, 128 or 256, and a shape (kRows32: dim up
-// to 128; kRows128: bf16 and dim up to 128).  The parts of q and of the weights go
+// One variant of the kernel: dim up to 64, 128 or 256, and a shape (kRows16 and
+// kRows128: dim up to 128; kRows128: bf16).  The parts of q and of the weights go
 // by the type (see q8kv.h), a translation unit each.
 struct AttendVariant {
     void (*fn)(AttendParams) = nullptr;

@@ -67,12 +67,13 @@ __device__ __forceinline__ void tc_bar_init(uint64_t *bar, uint32_t n) {
 __device__ __forceinline__ void tc_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(bar)) : "memory");
 }
-__device__ __forceinline__ bool tc_try(uint64_t *bar, uint32_t parity) {
+// whether the phase of `parity` is over, after at most about `ns` (the hardware may give up earlier)
+__device__ __forceinline__ bool tc_try(uint64_t *bar, uint32_t parity, uint32_t ns) {
     uint32_t done;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
-        : "r"(tc_smem(bar)), "r"(parity)
+        : "r"(tc_smem(bar)), "r"(parity), "r"(ns)
         : "memory");
     return done != 0;
 }
@@ -81,16 +82,16 @@ __device__ __forceinline__ uint64_t tc_now() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// The phase of `parity`; false if the CTA is leaving or the time is up.
+// The phase of `parity`; false if the CTA is leaving or the time is up.  A warp sleeps up to 1 ms at a time, so the
+// clock is hardly ever read.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, const volatile int *leave, uint64_t wait_ns) {
-    if (tc_try(bar, parity)) return true;
+    if (tc_try(bar, parity, 0)) return true;
+    const uint32_t nap = static_cast<uint32_t>(wait_ns < 1000000 ? wait_ns : 1000000);
     const uint64_t t0 = tc_now();
-    for (uint32_t i = 1;; ++i) {
-        if (tc_try(bar, parity)) return true;
-        if ((i & 31u) == 0) {
-            if (leave != nullptr && *leave) return false;
-            if (tc_now() - t0 > wait_ns) return false;
-        }
+    for (;;) {
+        if (tc_try(bar, parity, nap)) return true;
+        if (leave != nullptr && *leave) return false;
+        if (tc_now() - t0 > wait_ns) return false;
     }
 }
 // one lane of a warp that is together

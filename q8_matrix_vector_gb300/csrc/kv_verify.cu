@@ -5,7 +5,7 @@
 // one prefix search.  Everything that is summed is a 64-bit whole number, so the
 // split over threads and CTAs cannot change a result.
 //
-// One cluster of up to 16 CTAs walks one request and only reads the rows that the
+// One cluster of 16 CTAs walks one request and only reads the rows that the
 // walk visits: a tree of many nodes costs its accepted path, not its size.  What
 // bounds it is the longest path of the batch, a chain of rows each with a load, two
 // exchanges and the tests; so a row is spread over 128 warps, and the CTAs are small
@@ -35,7 +35,7 @@ namespace kv {
 
 namespace {
 
-constexpr int kMaxCluster = 16;
+constexpr int kCluster = 16;                // CTAs of a request
 constexpr int kNodes = 256;                // of a request, that fit the shared copy
 constexpr int kVerifyWarps = 8;
 constexpr int kHeld = 1024;                // logits of a warp's part that are kept
@@ -49,7 +49,6 @@ struct VerifyParams {
     int32_t *path, *count, *next;
     int64_t logits_row, draft_row, rows;
     int requests, vocab, seg;  // seg: tokens of a warp, a multiple of 4
-    int cluster;               // CTAs of a request
     int vec;                   // four logits (and draft probabilities) may be loaded at once
 };
 
@@ -139,20 +138,21 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ float4 held[];           // [warp][kHeld / 128][lane]
     // what the CTAs tell one another: each writes to its place in everybody's copy
-    __shared__ uint32_t x_max[2][kMaxCluster];
-    __shared__ int32_t x_best[2][kMaxCluster];
-    __shared__ int64_t x_sum[2][kMaxCluster];
+    __shared__ uint32_t x_max[2][kCluster];
+    __shared__ int32_t x_best[2][kCluster];
+    __shared__ int64_t x_sum[2][kCluster];
     __shared__ uint32_t warp_max[kVerifyWarps];
     __shared__ int32_t warp_best[kVerifyWarps];
     __shared__ int64_t warp_w[kVerifyWarps];   // sums of the warps' weights as they stand
-    __shared__ int64_t cta_w[kMaxCluster];     // and of all CTAs'
+    __shared__ int64_t cta_w[kCluster];     // and of all CTAs'
     __shared__ int32_t s_tokens[kNodes], s_parents[kNodes];
     __shared__ float s_uniforms[kNodes];
     __shared__ int verdict, child;             // of the last test
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster.block_rank());
-    const int ctas = p.cluster, b = blockIdx.x / ctas;
+    constexpr int ctas = kCluster;
+    const int b = blockIdx.x / ctas;
     int64_t row0, row1;
     if (p.starts) {
         row0 = min(max(static_cast<int64_t>(p.starts[b]), static_cast<int64_t>(0)), p.rows);
@@ -293,12 +293,12 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             const uint32_t mine_max = lane < ctas ? x_max[parity][lane] : 0, m = __reduce_max_sync(~0u, mine_max);
             r.top = unordered(m);
             r.best = 0;
-            if (r.greedy) r.best = __reduce_min_sync(~0u, mine_max == m ? x_best[parity][lane & (kMaxCluster - 1)] : INT32_MAX);
+            if (r.greedy) r.best = __reduce_min_sync(~0u, mine_max == m ? x_best[parity][lane & (kCluster - 1)] : INT32_MAX);
         }
         parity ^= 1;
         r.less = 0.0f;
 
-        // sum of the lane's weights (of the residual's once `rest`): at most 2^11 logits a lane, so 32 bits a half
+        // sum of the lane's weights (of the residual's once `rest`): at most 2^10 logits a lane, so 32 bits a half
         auto sum = [&]() -> int64_t {
             if (r.top == -INFINITY) return 0;
             if (r.greedy) {  // one logit has all the weight
@@ -495,13 +495,13 @@ template <typename T>
 cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
     auto *fn = p.draft ? q8kv_verify_kernel<T, true> : q8kv_verify_kernel<T, false>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.requests) * p.cluster);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.requests) * kCluster);
     cfg.blockDim = dim3(kVerifyWarps * 32);
     cfg.dynamicSmemBytes = kVerifyWarps * kHeld * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[0].val.clusterDim.x = kCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -525,7 +525,6 @@ struct q8kv_verify_s {
     int device = 0;
     int max_requests = 0, vocab = 0;
     int64_t max_rows = 0;
-    int sms = 0;
 };
 
 extern "C" {
@@ -546,8 +545,7 @@ q8mv_status_t q8kv_verify_plan(q8kv_verify_plan_t *out, int32_t max_requests, in
     p->max_requests = max_requests;
     p->max_rows = max_rows;
     p->vocab = vocab;
-    cudaError_t e = cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device);
-    if (e == cudaSuccess) e = kv::allow_clusters<float>();
+    cudaError_t e = kv::allow_clusters<float>();
     if (e == cudaSuccess) e = kv::allow_clusters<__half>();
     if (e == cudaSuccess) e = kv::allow_clusters<__nv_bfloat16>();
     if (e != cudaSuccess) {
@@ -610,9 +608,7 @@ q8mv_status_t q8kv_verify(q8kv_verify_plan_t plan, const q8kv_verify_args_t *a, 
     p.rows = a->rows;
     p.requests = a->requests;
     p.vocab = a->vocab;
-    // 16 CTAs a request while four an SM hold them all, else 8
-    p.cluster = a->requests * 16 <= plan->sms * 4 ? 16 : 8;
-    const int parts = p.cluster * kv::kVerifyWarps;
+    constexpr int parts = kv::kCluster * kv::kVerifyWarps;
     p.seg = static_cast<int>(kv::ceil_div(kv::ceil_div(a->vocab, parts), 4) * 4);
     p.vec = kv::aligned(a->logits, 4 * size) && a->logits_row % 4 == 0 && kv::aligned(a->draft_probs, 16) &&
             a->draft_row % 4 == 0;

@@ -78,6 +78,13 @@ class Case:
         assert not out[none].any()
 
 
+def wide(q8mv, seed, lengths, nodes, heads=2, group=2, page=16, **more):
+    """A case whose tables reach far enough, in columns without pages, for the tensor-memory path."""
+    tiles = heads * len(nodes) * -(-(-(-sum(nodes) // len(nodes)) * group) // 16)  # of 16 rows, for 128 keys of reach
+    cols = max(-(-4096 // tiles) * 128 // page + 1, *(-(-(max(n, 0) + t) // page) for n, t in zip(lengths, nodes)), 1)
+    return Case(q8mv, seed, lengths, nodes, heads=heads, group=group, page=page, cols=cols, **more)
+
+
 @pytest.mark.parametrize("dtype", ref.TYPES)
 @pytest.mark.parametrize("dim", [16, 64, 80, 96, 128, 192, 256])
 @pytest.mark.parametrize("layout,page", [("head", 16), ("token", 7)])
@@ -131,8 +138,8 @@ def test_heads_side_by_side_cut_between_ctas(q8mv):
 @pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 112, 128])
 @pytest.mark.parametrize("layout,page", [("head", 16), ("token", 7)])
 def test_wide_trees(q8mv, dim, layout, page):
-    """More than 32 bf16 query rows a request: the tensor-memory path."""
-    Case(q8mv, dim, [300, 0, 5, 1000], [40, 0, 33, 70], heads=2, group=2, dim=dim, page=page, dtype="bfloat16",
+    """More than 32 bf16 query rows a request, and tables that reach far: the tensor-memory path."""
+    wide(q8mv, dim, [300, 0, 5, 1000], [40, 0, 33, 70], heads=2, group=2, dim=dim, page=page, dtype="bfloat16",
          layout=layout).check()
 
 
@@ -140,20 +147,20 @@ def test_wide_trees(q8mv, dim, layout, page):
 @pytest.mark.parametrize("tree", [True, False])
 def test_wide_trees_around_the_tiles(q8mv, length, tree):
     for nodes in (34, 129, 150):
-        Case(q8mv, length, [length], [nodes], heads=1, group=1, dim=64, page=5, dtype="bfloat16", tree=tree).check()
+        wide(q8mv, length, [length], [nodes], heads=1, group=1, dim=64, page=5, dtype="bfloat16", tree=tree).check()
 
 
 def test_wide_trees_cut_between_ctas(q8mv):
-    Case(q8mv, 1, [20001], [35], heads=1, group=2, dim=64, page=64, dtype="bfloat16").check()
-    Case(q8mv, 2, [9000, 20011, 1, 5, 13000], [40, 33, 50, 35, 41], heads=2, group=4, dim=128, page=32,
+    wide(q8mv, 1, [20001], [35], heads=1, group=2, dim=64, page=64, dtype="bfloat16").check()
+    wide(q8mv, 2, [9000, 20011, 1, 5, 13000], [40, 33, 50, 35, 41], heads=2, group=4, dim=128, page=32,
          dtype="bfloat16").check()
-    Case(q8mv, 3, [90] * 60, [40] * 60, heads=3, group=1, dim=128, page=16, dtype="bfloat16").check()
+    wide(q8mv, 3, [90] * 60, [40] * 60, heads=3, group=1, dim=128, page=16, dtype="bfloat16").check()
 
 
 def test_wide_trees_the_same_bits_again(q8mv):
     import torch
 
-    c = Case(q8mv, 4, [3000, 700, 0], [50, 90, 36], heads=4, group=1, dim=128, dtype="bfloat16")
+    c = wide(q8mv, 4, [3000, 700, 0], [50, 90, 36], heads=4, group=1, dim=128, dtype="bfloat16")
     a = c.run()
     for _ in range(20):
         for x, y in zip(a, c.run()):
@@ -166,7 +173,7 @@ def test_wide_trees_and_what_is_not_seen(q8mv):
     """Rows that see nothing; NaN, infinities and huge scales in unseen nodes and unused places."""
     import torch
 
-    c = Case(q8mv, 5, [33, 140, 0], [40, 45, 50], heads=2, group=1, dim=64, dtype="bfloat16")
+    c = wide(q8mv, 5, [33, 140, 0], [40, 45, 50], heads=2, group=1, dim=64, dtype="bfloat16")
     for b in range(3):
         c.seen[b][:, 2] = False
         c.seen[b][:, 37] = False
@@ -197,7 +204,7 @@ def test_wide_trees_and_what_is_not_seen(q8mv):
 def test_wide_trees_and_seen_values_that_are_not_finite(q8mv):
     import torch
 
-    c = Case(q8mv, 6, [20], [40], heads=1, group=1, dim=64, dtype="bfloat16", tree=False)
+    c = wide(q8mv, 6, [20], [40], heads=1, group=1, dim=64, dtype="bfloat16", tree=False)
     slot = c.table[0, 50 // 16] * 16 + 50 % 16  # node 30
     c.host.vs[slot // 16, :, slot % 16] = np.nan
     out, _ = c.run()
@@ -206,10 +213,10 @@ def test_wide_trees_and_seen_values_that_are_not_finite(q8mv):
 
 @pytest.mark.parametrize("size", [1e-30, 1e-12, 1e12, 1e30])
 def test_wide_trees_with_scales_of_any_size(q8mv, size):
-    c = Case(q8mv, 7, [200], [40], dim=64, dtype="bfloat16")
+    c = wide(q8mv, 7, [200], [40], dim=64, dtype="bfloat16")
     c.host.vs *= np.float32(size)
     c.check()
-    c = Case(q8mv, 8, [200], [40], dim=64, dtype="bfloat16")
+    c = wide(q8mv, 8, [200], [40], dim=64, dtype="bfloat16")
     c.host.ks *= np.float32(size)
     c.q = (c.q * (1 / size)).to(c.q.dtype)
     c.check()
@@ -218,7 +225,7 @@ def test_wide_trees_with_scales_of_any_size(q8mv, size):
 def test_wide_trees_strided_rows(q8mv):
     import torch
 
-    c = Case(q8mv, 9, [300], [40], heads=2, group=2, dim=128, dtype="bfloat16")
+    c = wide(q8mv, 9, [300], [40], heads=2, group=2, dim=128, dtype="bfloat16")
     want = c.run()
     outs = torch.full((40, 4, 140), 7.0, device="cuda", dtype=torch.bfloat16)
     got = c.run(out=outs[:, :, 5:133])
@@ -230,7 +237,7 @@ def test_wide_trees_strided_rows(q8mv):
 def test_wide_trees_large_scores(q8mv, scale):
     """Scores hundreds apart: where one key has all of a row's weight (the next below e^-40), out is its value within
     the two roundings of a value (f16 in the product, bf16 at the end), measured by the row's largest value."""
-    c = Case(q8mv, 12, [300], [40], heads=2, group=2, dim=128, dtype="bfloat16")
+    c = wide(q8mv, 12, [300], [40], heads=2, group=2, dim=128, dtype="bfloat16")
     out, lse = (x.double().cpu().numpy() for x in c.run(scale=scale))
     pos = np.arange(340)
     keys, values = c.host.rows(c.table[0, pos // 16].astype(np.int64) * 16 + pos % 16)
@@ -250,7 +257,7 @@ def test_wide_trees_large_scores(q8mv, scale):
 
 
 def test_a_wait_that_runs_out_is_reported_and_the_plan_goes_on(q8mv):
-    c = Case(q8mv, 10, [3000, 100], [40, 50], heads=2, group=2, dim=128, dtype="bfloat16")
+    c = wide(q8mv, 10, [3000, 100], [40, 50], heads=2, group=2, dim=128, dtype="bfloat16")
     c.check()
     c.plan.set_wait(1)  # nanosecond: the first wait that has to wait runs out
     c.run()
