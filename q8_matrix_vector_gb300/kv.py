@@ -355,7 +355,6 @@ class TreeAttention(_Plan):
             _fail(status, "q8kv_attend")
         return (out, sums) if lse else out
 
-
     def check(self) -> int:
         """Synchronise and return (and clear) whether a bounded wait of the plan's kernels ran out (1, else 0)."""
         word = ctypes.c_int32()
