@@ -78,8 +78,7 @@ __device__ __forceinline__ float scaled(float l, float inv) {
 
 // e of a logit, not greedy, of a row whose largest z is not -inf
 __device__ __forceinline__ float soft(const Row &r, float z) {
-    const float e = expf(z - r.top);
-    return z == r.top ? 1.0f : e;  // inf - inf
+    return fminf(expf(z - r.top), 1.0f);  // 1 for inf - inf
 }
 
 // the same for logit i of any such row
@@ -89,38 +88,52 @@ __device__ __forceinline__ float share(const Row &r, float z, int i) {
 
 // Whole-number weight trunc(2^40 e), 0 <= e <= 1, as 2^20 hi + lo.
 struct Weight {
-    uint32_t hi, lo;
+    uint32_t hi, lo;  // plus kWeightBias each, so that a sum can take that off once
 };
+constexpr uint32_t kWeightBias = 0x4B000000u;  // the bits of 2^23
 __device__ __forceinline__ Weight split_weight(float e) {
     const float y = __fmaf_rz(e, 1048576.0f, 8388608.0f);
     const float r = __fmaf_rn(e, 1048576.0f, 8388608.0f - y);  // exact, in [0, 1)
     const float x = __fmaf_rz(r, 1048576.0f, 8388608.0f);
-    return {__float_as_uint(y) - 0x4B000000u, __float_as_uint(x) - 0x4B000000u};
+    return {__float_as_uint(y), __float_as_uint(x)};
 }
 __device__ __forceinline__ int64_t weight(float e) {
     const Weight w = split_weight(e);
-    return (static_cast<int64_t>(w.hi) << 20) + w.lo;
+    return (static_cast<int64_t>(w.hi - kWeightBias) << 20) + (w.lo - kWeightBias);
 }
 
 __device__ __forceinline__ float residual(const Row &r, float e, float q) {
     return fmaxf(__fsub_rn(__fmul_rn(e, r.per), __fmul_rn(r.less, q)), 0.0f);
 }
 
+// four logits as they are in memory
+template <typename T>
+struct Four {
+    using type = uint2;
+};
+template <>
+struct Four<float> {
+    using type = float4;
+};
+template <typename T>
+__device__ __forceinline__ void unpack4(const typename Four<T>::type &v, float (&x)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+        union {
+            uint2 u;
+            T t[4];
+        } y;
+        y.u = v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = to_f32(y.t[k]);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void load4(const T *p, int i, int n, bool vec, float (&x)[4], float fill) {
     if (vec && i + 4 <= n) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
-            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-        } else {
-            union {
-                uint2 u;
-                T t[4];
-            } v;
-            v.u = __ldg(reinterpret_cast<const uint2 *>(p + i));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = to_f32(v.t[k]);
-        }
+        unpack4<T>(__ldg(reinterpret_cast<const typename Four<T>::type *>(p + i)), x);
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = i + k < n ? to_f32(p[i + k]) : fill;
@@ -247,8 +260,29 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             return make_float4(x[0], x[1], x[2], x[3]);
         };
         const int held_end = min(hi_end, lo + kHeld);
-#pragma unroll 8
-        for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
+        if (p.vec && ((held_end - lo) & 3) == 0) {
+            // all of the lane's loads at once: with a test for the row's end at each they would follow one another
+            using V = typename Four<T>::type;
+            V v[kHeld / 128];
+#pragma unroll
+            for (int k = 0; k < kHeld / 128; ++k) {
+                const int i = lo + 128 * k + 4 * lane;
+                if (i < held_end) v[k] = __ldg(reinterpret_cast<const V *>(l + i));
+            }
+#pragma unroll
+            for (int k = 0; k < kHeld / 128; ++k) {
+                if (lo + 128 * k >= held_end) break;
+                float x[4];
+                unpack4<T>(v[k], x);
+                const bool in = lo + 128 * k + 4 * lane < held_end;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = in ? scaled(x[j], r.inv) : -INFINITY;
+                top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+                mine[32 * k] = make_float4(x[0], x[1], x[2], x[3]);
+            }
+        } else {
+            for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
+        }
 #pragma unroll 4
         for (int i = lo + kHeld; i < hi_end; i += 128) look(i + lane * 4);
         {
@@ -305,8 +339,12 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                 if (lane != 0 || r.best < lo || r.best >= hi_end) return 0;
                 return weight(DRAFTS && rest ? residual(r, 1.0f, q[r.best]) : 1.0f);
             }
-            uint32_t hi = 0, lo_bits = 0;
-            auto add = [&](const float (&x)[4], const float (&y)[4]) {
+            const uint32_t n = 4 * static_cast<uint32_t>((hi_end - lo + 127) / 128);  // weights that the lane adds
+            uint32_t hi = 0 - n * kWeightBias, lo_bits = hi;
+            auto add = [&](const float4 &v, int i) {
+                const float x[4] = {v.x, v.y, v.z, v.w};
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (DRAFTS && rest) load4(q, i + lane * 4, hi_end, p.vec, y, 0.0f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float e = soft(r, x[j]);  // 0 past the warp's end, where z is -inf
@@ -316,19 +354,11 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                 }
             };
 #pragma unroll 4
-            for (int i0 = lo; i0 < hi_end; i0 += 128) {
-                const int i = i0 + lane * 4;
-                float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (i0 < held_end) {
-                    const float4 v = mine[(i0 - lo) / 4];
-                    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-                } else {
-                    load4(l, i, hi_end, p.vec, x, -INFINITY);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
-                }
-                if (DRAFTS && rest) load4(q, i, hi_end, p.vec, y, 0.0f);
-                add(x, y);
+            for (int i = lo; i < held_end; i += 128) add(mine[(i - lo) / 4], i);
+            for (int i = lo + kHeld; i < hi_end; i += 128) {
+                float x[4];
+                load4(l, i + lane * 4, hi_end, p.vec, x, -INFINITY);
+                add(make_float4(scaled(x[0], r.inv), scaled(x[1], r.inv), scaled(x[2], r.inv), scaled(x[3], r.inv)), i);
             }
             return (static_cast<int64_t>(hi) << 20) + lo_bits;
         };
