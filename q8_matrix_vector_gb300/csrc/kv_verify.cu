@@ -5,18 +5,26 @@
 // one prefix search.  Everything that is summed is a 64-bit whole number, so the
 // split over threads and CTAs cannot change a result.
 //
-// One cluster of 16 CTAs walks one request and only reads the rows that the
-// walk visits: a tree of many nodes costs its accepted path, not its size.  What
-// bounds it is the longest path of the batch, a chain of rows each with a load, two
-// exchanges and the tests; so a row is spread over 128 warps, and the CTAs are small
-// (256 threads, 32 KB) so that the clusters of 30 and more requests are resident
-// together and those that go on get the SMs of those that have ended.  A CTA owns a
-// contiguous part of the vocabulary and each of its 8 warps a contiguous part of
-// that, so the search at the end goes cluster -> CTA -> warp -> 128 tokens.  A lane
-// keeps the row's first logits in shared memory between the maximum and the sum
-// (all of a 131072-token vocabulary), so a row is read once.  Maxima and sums cross
-// the cluster through distributed shared memory; every CTA runs the children's
-// tests itself, on the same numbers, and reaches the same verdict.
+// One cluster of 16 CTAs walks one request and only reads the rows that the walk
+// visits, and the first child's of each: a tree of many nodes costs its accepted
+// path, not its size.  What bounds it is the longest path of the batch, a chain of
+// rows each with a load, a sum, exchanges over the cluster and the tests; so a row is
+// spread over 128 warps, and the CTAs are small (256 threads, 32 KB) so that the
+// clusters of 30 and more requests are resident together and those that go on get the
+// SMs of those that have ended.  (8 CTAs a request are slower at every size: 57.7 us
+// to 32.6 for one tree, 233 to 206 for 128.)  A CTA owns a contiguous part of the
+// vocabulary and each of its 8 warps a contiguous part of that, so the search at the
+// end goes cluster -> CTA -> warp -> 128 tokens.  A lane keeps the row's first logits
+// in shared memory between the maximum and the sum (all of a 131072-token
+// vocabulary), so a row is read once, all of a lane's loads in flight.  While a row is
+// summed the first child's takes its place, and that row's maximum is told with this
+// row's sum: on a path along first children a step takes 8400 cycles instead of 10600.
+// Maxima and sums cross the cluster through distributed shared memory; every CTA runs
+// the children's tests itself, on the same numbers, and reaches the same verdict.
+//
+// Vocabulary 128256, f32: 32 trees of 24 nodes, paths up to 9 rows, 56 us (70 MB
+// read: 19 % of the copy rate, 4.2 us a row of the longest path and the start); 2
+// chains of 6 with draft probabilities 23 us.
 //
 // A 64-bit conversion per logit runs at the few-per-cycle rate of the FP64 pipe
 // (4 us for an eighth of a 128256-token row).  The weight is split by two f32
@@ -39,6 +47,7 @@ constexpr int kCluster = 16;                // CTAs of a request
 constexpr int kNodes = 256;                // of a request, that fit the shared copy
 constexpr int kVerifyWarps = 8;
 constexpr int kHeld = 1024;                // logits of a warp's part that are kept
+constexpr int kVerifySmem = kVerifyWarps * kHeld * 4;
 
 struct VerifyParams {
     const void *logits;
@@ -50,6 +59,7 @@ struct VerifyParams {
     int64_t logits_row, draft_row, rows;
     int requests, vocab, seg;  // seg: tokens of a warp, a multiple of 4
     int vec;                   // four logits (and draft probabilities) may be loaded at once
+    int ahead;                 // rows are whole in shared memory, in fours: the likeliest next one is brought early
 };
 
 // The row that the walk stands on: what its weights are made of.
@@ -130,6 +140,24 @@ __device__ __forceinline__ void unpack4(const typename Four<T>::type &v, float (
     }
 }
 
+// z of four logits, all -inf unless `in`; top becomes the largest
+template <typename T>
+__device__ __forceinline__ float4 scaled4(const typename Four<T>::type &v, bool in, float inv, float &top) {
+    float x[4];
+    unpack4<T>(v, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = in ? scaled(x[j], inv) : -INFINITY;
+    top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// copies into the place that `old` was read from, after that has arrived
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t to, const void *from, const float4 &old) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES), "f"(old.x), "f"(old.y), "f"(old.z), "f"(old.w) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <typename T>
 __device__ __forceinline__ void load4(const T *p, int i, int n, bool vec, float (&x)[4], float fill) {
     if (vec && i + 4 <= n) {
@@ -202,6 +230,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
     Row r;
     const float t = p.temperature ? p.temperature[b] : 1.0f;
     r.greedy = !(t > 0.0f);
+    r.best = 0;
     r.inv = r.greedy ? 1.0f : __frcp_rn(t);
     const int seg = p.seg, chunk = seg * kVerifyWarps;
     const int64_t lo64 = static_cast<int64_t>(rank) * chunk + static_cast<int64_t>(warp) * seg;
@@ -209,28 +238,56 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
     const int hi_end = static_cast<int>(min(lo64 + seg, static_cast<int64_t>(p.vocab)));
 
     int parity = 0;
-    // sums the lanes' numbers: warp_w, cta_w, and the total
-    auto exchange = [&](int64_t mine) -> int64_t {
-        mine = warp_sum(mine);
-        if (lane == 0) warp_w[warp] = mine;
+    // What a step of the walk tells the cluster: the lanes' sums (then in warp_w, cta_w and the result), the warps'
+    // warp_max and warp_best of a row (then in top and best), or both.
+    uint32_t top_bits = 0;
+    int best = 0;
+    auto exchange = [&](bool sums, bool tops, int64_t mine) -> int64_t {
+        if (sums) {
+            mine = warp_sum(mine);
+            if (lane == 0) warp_w[warp] = mine;
+        }
         __syncthreads();
         if (tid < ctas) {
-            int64_t s = 0;
+            if (sums) {
+                int64_t s = 0;
 #pragma unroll
-            for (int i = 0; i < kVerifyWarps; ++i) s += warp_w[i];
-            *cluster.map_shared_rank(&x_sum[parity][rank], tid) = s;
+                for (int i = 0; i < kVerifyWarps; ++i) s += warp_w[i];
+                *cluster.map_shared_rank(&x_sum[parity][rank], tid) = s;
+            }
+            if (tops) {
+                uint32_t m = warp_max[0];
+                int first = r.greedy ? warp_best[0] : 0;
+#pragma unroll
+                for (int i = 1; i < kVerifyWarps; ++i) {
+                    if (r.greedy && warp_max[i] > m) first = warp_best[i];
+                    m = max(m, warp_max[i]);
+                }
+                *cluster.map_shared_rank(&x_max[parity][rank], tid) = m;
+                if (r.greedy) *cluster.map_shared_rank(&x_best[parity][rank], tid) = first;
+            }
         }
         cluster.sync();
-        const int64_t s = lane < ctas ? x_sum[parity][lane] : 0;
-        if (tid < ctas) cta_w[tid] = s;
-        __syncthreads();
+        if (tops) {
+            const uint32_t m = lane < ctas ? x_max[parity][lane] : 0;
+            top_bits = __reduce_max_sync(~0u, m);
+            if (r.greedy) best = __reduce_min_sync(~0u, m == top_bits ? x_best[parity][lane & (kCluster - 1)] : INT32_MAX);
+        }
+        int64_t s = 0;
+        if (sums) {
+            s = lane < ctas ? x_sum[parity][lane] : 0;
+            if (tid < ctas) cta_w[tid] = s;
+            __syncthreads();
+            s = warp_sum(s);
+        }
         parity ^= 1;
-        return warp_sum(s);
+        return s;
     };
 
     int cur = 0, count = 0;
     int64_t total = 0;
     bool rest = false;  // drafts: the weights are the residual's
+    bool ready = false; // the row is in shared memory and its maximum known
     for (;;) {
         const T *l = static_cast<const T *>(p.logits) + (row0 + cur) * p.logits_row;
         const float *q = DRAFTS ? p.draft + (row0 + cur) * p.draft_row : nullptr;
@@ -248,95 +305,89 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                 if (DRAFTS) child_q = q[tok];
             }
         }
-        // ---- the row's maximum
-        float top = -INFINITY;
         float4 *mine = held + warp * (kHeld / 4) + lane;
-        auto look = [&](int i) -> float4 {
-            float x[4];
-            load4(l, i, hi_end, p.vec, x, -INFINITY);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
-            top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-            return make_float4(x[0], x[1], x[2], x[3]);
-        };
         const int held_end = min(hi_end, lo + kHeld);
-        if (p.vec && ((held_end - lo) & 3) == 0) {
-            // all of the lane's loads at once: with a test for the row's end at each they would follow one another
-            using V = typename Four<T>::type;
-            V v[kHeld / 128];
+        // the warp's largest of a row whose lanes have `top`: and, if greedy, the first index that has it
+        auto peak = [&](float top, const T *row) {
+            const uint32_t most = __reduce_max_sync(~0u, ordered(top));
+            if (lane == 0) warp_max[warp] = most;
+            if (r.greedy) {
+                int first = INT32_MAX;
+                for (int i = lo; i < hi_end && first == INT32_MAX; i += 128) {
+                    float x[4];
+                    if (i < held_end) {
+                        const float4 v = mine[(i - lo) / 4];
+                        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+                    } else {
+                        load4(row, i + lane * 4, hi_end, p.vec, x, -INFINITY);
 #pragma unroll
-            for (int k = 0; k < kHeld / 128; ++k) {
-                const int i = lo + 128 * k + 4 * lane;
-                if (i < held_end) v[k] = __ldg(reinterpret_cast<const V *>(l + i));
-            }
+                        for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
+                    }
 #pragma unroll
-            for (int k = 0; k < kHeld / 128; ++k) {
-                if (lo + 128 * k >= held_end) break;
-                float x[4];
-                unpack4<T>(v[k], x);
-                const bool in = lo + 128 * k + 4 * lane < held_end;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = in ? scaled(x[j], r.inv) : -INFINITY;
-                top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-                mine[32 * k] = make_float4(x[0], x[1], x[2], x[3]);
+                    for (int j = 3; j >= 0; --j)
+                        if (i + lane * 4 + j < hi_end && ordered(x[j]) == most) first = i + lane * 4 + j;
+                }
+                first = __reduce_min_sync(~0u, first);
+                if (lane == 0) warp_best[warp] = first;
             }
-        } else {
-            for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
-        }
-#pragma unroll 4
-        for (int i = lo + kHeld; i < hi_end; i += 128) look(i + lane * 4);
-        {
-            // L2 starts on the row of the first child, the likeliest to be next: on a path of n rows the others'
-            // loads then take an L2 round trip each
-            const int node = cur + 1 + lane;
-            const uint32_t kids = __ballot_sync(~0u, node < nodes && parents[node] == cur);
-            if (kids != 0) {
-                const T *next = static_cast<const T *>(p.logits) + (row0 + cur + __ffs(kids)) * p.logits_row;
-                for (int i = lo + lane * static_cast<int>(128 / sizeof(T)); i < held_end; i += 32 * static_cast<int>(128 / sizeof(T)))
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
-            }
-        }
-        const uint32_t most = __reduce_max_sync(~0u, ordered(top));
-        if (lane == 0) warp_max[warp] = most;
-        if (r.greedy) {  // the first index of the warp's largest
-            int best = INT32_MAX;
-            for (int i = lo + lane * 4; i < hi_end && best == INT32_MAX; i += 128) {
+        };
+        if (!ready) {  // ---- the row's maximum
+            float top = -INFINITY;
+            auto look = [&](int i) -> float4 {
                 float x[4];
                 load4(l, i, hi_end, p.vec, x, -INFINITY);
 #pragma unroll
-                for (int j = 3; j >= 0; --j)
-                    if (i + j < hi_end && ordered(scaled(x[j], r.inv)) == most) best = i + j;
-            }
-            best = __reduce_min_sync(~0u, best);
-            if (lane == 0) warp_best[warp] = best;
-        }
-        __syncthreads();
-        if (tid < ctas) {
-            uint32_t m = warp_max[0];
-            int best = r.greedy ? warp_best[0] : 0;
+                for (int j = 0; j < 4; ++j) x[j] = scaled(x[j], r.inv);
+                top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+                return make_float4(x[0], x[1], x[2], x[3]);
+            };
+            if (p.vec && ((held_end - lo) & 3) == 0) {
+                // all of the lane's loads at once: with a test for the row's end at each they would follow one another
+                using V = typename Four<T>::type;
+                V v[kHeld / 128];
 #pragma unroll
-            for (int i = 1; i < kVerifyWarps; ++i) {
-                if (r.greedy && warp_max[i] > m) best = warp_best[i];
-                m = max(m, warp_max[i]);
+                for (int k = 0; k < kHeld / 128; ++k) {
+                    const int i = lo + 128 * k + 4 * lane;
+                    if (i < held_end) v[k] = __ldg(reinterpret_cast<const V *>(l + i));
+                }
+#pragma unroll
+                for (int k = 0; k < kHeld / 128; ++k) {
+                    if (lo + 128 * k >= held_end) break;
+                    mine[32 * k] = scaled4<T>(v[k], lo + 128 * k + 4 * lane < held_end, r.inv, top);
+                }
+            } else {
+                for (int i = lo; i < held_end; i += 128) mine[(i - lo) / 4] = look(i + lane * 4);
             }
-            *cluster.map_shared_rank(&x_max[parity][rank], tid) = m;
-            if (r.greedy) *cluster.map_shared_rank(&x_best[parity][rank], tid) = best;
+#pragma unroll 4
+            for (int i = lo + kHeld; i < hi_end; i += 128) look(i + lane * 4);
+            peak(top, l);
+            exchange(false, true, 0);
+            r.top = unordered(top_bits);
+            r.best = best;
         }
-        cluster.sync();
-        {
-            const uint32_t mine_max = lane < ctas ? x_max[parity][lane] : 0, m = __reduce_max_sync(~0u, mine_max);
-            r.top = unordered(m);
-            r.best = 0;
-            if (r.greedy) r.best = __reduce_min_sync(~0u, mine_max == m ? x_best[parity][lane & (kCluster - 1)] : INT32_MAX);
+        // ---- the row of the first child, the likeliest to be next, takes this row's place as that is summed, and its
+        // maximum is found and told along with the sum: on a path along first children a step has one exchange and
+        // waits for no row.  L2 starts on it now.
+        const uint32_t kids = __ballot_sync(~0u, cur + 1 + lane < nodes && parents[cur + 1 + lane] == cur);
+        const int next = p.ahead && kids != 0 ? cur + __ffs(kids) : -1;
+        const T *next_l = static_cast<const T *>(p.logits) + (row0 + cur + __ffs(kids)) * p.logits_row;
+        if (kids != 0) {
+            constexpr int kLine = 128 / sizeof(T);
+            for (int i = lo + lane * kLine; i < held_end; i += 32 * kLine) asm volatile("prefetch.global.L2 [%0];" ::"l"(next_l + i));
         }
-        parity ^= 1;
         r.less = 0.0f;
 
         // sum of the lane's weights (of the residual's once `rest`): at most 2^10 logits a lane, so 32 bits a half
-        auto sum = [&]() -> int64_t {
-            if (r.top == -INFINITY) return 0;
-            if (r.greedy) {  // one logit has all the weight
-                if (lane != 0 || r.best < lo || r.best >= hi_end) return 0;
+        // `fresh`: of a row that is in shared memory, and leaves it for the next one
+        auto sum = [&](bool fresh) -> int64_t {
+            const bool leaves = fresh && next >= 0;
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+            if (r.greedy || r.top == -INFINITY) {
+                if (leaves)
+                    for (int i = lo; i < hi_end; i += 128)
+                        if (i + 4 * lane < hi_end) cp_async<4 * sizeof(T)>(to + 4 * (i - lo), next_l + i + 4 * lane, mine[(i - lo) / 4]);
+                // one logit has all the weight
+                if (r.top == -INFINITY || lane != 0 || r.best < lo || r.best >= hi_end) return 0;
                 return weight(DRAFTS && rest ? residual(r, 1.0f, q[r.best]) : 1.0f);
             }
             const uint32_t n = 4 * static_cast<uint32_t>((hi_end - lo + 127) / 128);  // weights that the lane adds
@@ -353,9 +404,15 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                     lo_bits += w.lo;
                 }
             };
+            if (fresh) {
 #pragma unroll 4
-            for (int i = lo; i < held_end; i += 128) add(mine[(i - lo) / 4], i);
-            for (int i = lo + kHeld; i < hi_end; i += 128) {
+                for (int i = lo; i < held_end; i += 128) {
+                    const float4 v = mine[(i - lo) / 4];
+                    add(v, i);
+                    if (leaves && i + 4 * lane < hi_end) cp_async<4 * sizeof(T)>(to + 4 * (i - lo), next_l + i + 4 * lane, v);
+                }
+            }
+            for (int i = fresh ? lo + kHeld : lo; i < hi_end; i += 128) {
                 float x[4];
                 load4(l, i + lane * 4, hi_end, p.vec, x, -INFINITY);
                 add(make_float4(scaled(x[0], r.inv), scaled(x[1], r.inv), scaled(x[2], r.inv), scaled(x[3], r.inv)), i);
@@ -363,7 +420,21 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             return (static_cast<int64_t>(hi) << 20) + lo_bits;
         };
         rest = false;
-        total = exchange(sum());
+        {
+            const int64_t w = sum(true);
+            if (next >= 0) {
+                cp_async_wait();  // the lane's own
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kHeld / 128; ++k) {
+                    if (lo + 128 * k >= hi_end) break;
+                    mine[32 * k] = scaled4<T>(*reinterpret_cast<const typename Four<T>::type *>(mine + 32 * k),
+                                               lo + 128 * k + 4 * lane < hi_end, r.inv, top);
+                }
+                peak(top, next_l);
+            }
+            total = exchange(true, next >= 0, w);
+        }
         if (DRAFTS) r.per = static_cast<float>(1099511627776.0 / static_cast<double>(total));
 
         // ---- the children, in index order.  Warp 0 tests until one is accepted (verdict 1), none is
@@ -429,6 +500,11 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             if (!DRAFTS || said != 2) {
                 if (said == 1) {
                     cur = who;
+                    ready = who == next;
+                    if (ready) {
+                        r.top = unordered(top_bits);
+                        r.best = best;
+                    }
                     ++count;
                     if (rank == 0 && tid == 0) path[count] = who;
                 }
@@ -438,13 +514,13 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             // refused: take the draft's share out, once more
             r.less = __fadd_rn(r.less, norm);
             rest = true;
-            const int64_t left = exchange(sum());
+            const int64_t left = exchange(true, false, sum(false));
             from = who + 1;
             if (left == 0) {
                 // nothing is left: the target's own weights, and no other child
                 rest = false;
                 r.less = 0.0f;
-                total = exchange(sum());
+                total = exchange(true, false, sum(false));
                 open = false;
             } else {
                 total = left;
@@ -527,7 +603,7 @@ cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.requests) * kCluster);
     cfg.blockDim = dim3(kVerifyWarps * 32);
-    cfg.dynamicSmemBytes = kVerifyWarps * kHeld * sizeof(float);
+    cfg.dynamicSmemBytes = kVerifySmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -541,9 +617,11 @@ cudaError_t launch(const VerifyParams &p, cudaStream_t stream) {
 // Clusters of 16 are beyond the size that every GPU takes: allowed per kernel, when a plan is made.
 template <typename T>
 cudaError_t allow_clusters() {
-    cudaError_t e = cudaFuncSetAttribute(q8kv_verify_kernel<T, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(q8kv_verify_kernel<T, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaSuccess;
+    for (auto *fn : {q8kv_verify_kernel<T, true>, q8kv_verify_kernel<T, false>}) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kVerifySmem);
+    }
     return e;
 }
 
@@ -642,6 +720,7 @@ q8mv_status_t q8kv_verify(q8kv_verify_plan_t plan, const q8kv_verify_args_t *a, 
     p.seg = static_cast<int>(kv::ceil_div(kv::ceil_div(a->vocab, parts), 4) * 4);
     p.vec = kv::aligned(a->logits, 4 * size) && a->logits_row % 4 == 0 && kv::aligned(a->draft_probs, 16) &&
             a->draft_row % 4 == 0;
+    p.ahead = p.vec && p.seg <= kv::kHeld && a->vocab % 4 == 0;
     cudaError_t e;
     if (a->type == Q8KV_F32)
         e = kv::launch<float>(p, stream);
