@@ -85,81 +85,124 @@ __device__ __noinline__ uint32_t pack4_any(float x0, float x1, float x2, float x
     return w;
 }
 
+// max(a, b), NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// The largest |x| of a lane's elements, NaN if one is: 16-bit types in pairs.
+__device__ __forceinline__ float amax_of(const Piece<float> &x) {
+    return max_nan(max_nan(fabsf(x.t[0]), fabsf(x.t[1])), max_nan(fabsf(x.t[2]), fabsf(x.t[3])));
+}
+template <typename T2, typename P>
+__device__ __forceinline__ float amax_of_pairs(const P &x) {
+    const T2 *p = reinterpret_cast<const T2 *>(x.t);
+    const T2 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+    return max_nan(to_f32(m.x), to_f32(m.y));
+}
+__device__ __forceinline__ float amax_of(const Piece<__half> &x) { return amax_of_pairs<__half2>(x); }
+__device__ __forceinline__ float amax_of(const Piece<__nv_bfloat16> &x) { return amax_of_pairs<__nv_bfloat162>(x); }
+
+// Row of head 0 for each of the block's tokens, -1 if there is none: one thread a token does the divisions.
+template <int U>
+__device__ __forceinline__ void find_rows(const IoParams &p, int64_t (&rows)[8 * U]) {
+    const int t = threadIdx.y * blockDim.x + threadIdx.x;
+    if (t < static_cast<int>(blockDim.y) * U) {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.y * U) + t;
+        int64_t page;
+        int place;
+        rows[t] = i < p.n && place_of(p.c, __ldg(p.slots + i), &page, &place) ? row_of(p.c, page, 0, place) : -1;
+    }
+}
+
 // d = amax / 127, c = rint(x * (127 / amax)): the recipe of q8mv_quantize_rows.
 // U tokens a lane: their loads, which do not wait for the slots, are all in flight.
+// For many rows the issue slots bound it, next to HBM: a warp stays together
+// (shuffles of all lanes, one vote for blocks that are not ordinary), 16-bit
+// elements are compared in pairs and a NaN shows in the maximum.
 template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(256) q8kv_write_kernel(const IoParams p) {
     constexpr int E = 16 / sizeof(T), PER = 32 / E;  // elements a lane, lanes a block
+    __shared__ int64_t rows[8 * U];
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.y * U) + threadIdx.y;
     const int at = blockIdx.y * blockDim.x + threadIdx.x;
-    // whole groups of PER lanes share (token, head, block), so they leave together
-    if (at >= p.lanes) return;
-    const unsigned group = ((1u << PER) - 1u) << ((threadIdx.y * blockDim.x + threadIdx.x) & 31 & ~(PER - 1));
     const int per_head = p.c.blocks * PER;
     const int h = at / per_head, in_row = at - h * per_head, e0 = in_row * E, b = in_row / PER;
-    const bool live = e0 < p.c.dim;
-    uint4 raw[U][2];
-    int64_t slot[U];
+    const bool live = at < p.lanes && e0 < p.c.dim;
+    Piece<T> raw[U][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t i = first + u * blockDim.y;
-        slot[u] = i < p.n ? __ldg(p.slots + i) : -1;
+    for (int s = 0; s < 2; ++s) {
+        const T *src = static_cast<const T *>(p.in[s]) + first * p.row[s] + h * p.head[s] + e0;
+        const int64_t step = static_cast<int64_t>(blockDim.y) * p.row[s];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const T *src = static_cast<const T *>(p.in[s]) + i * p.row[s] + h * p.head[s] + e0;
-            raw[u][s] = live && i < p.n ? load_piece<T, VEC>(src) : make_uint4(0, 0, 0, 0);
-        }
+        for (int u = 0; u < U; ++u)
+            raw[u][s].v = live && first + u * blockDim.y < p.n ? load_piece<T, VEC>(src + u * step) : make_uint4(0, 0, 0, 0);
     }
+    find_rows<U>(p, rows);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, of = lane & (PER - 1), first_lane = lane - of;  // (blockDim.x: whole warps)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        int64_t page;
-        int place;
-        const bool there = place_of(p.c, slot[u], &page, &place);
-        const int64_t r = there ? row_of(p.c, page, h, place) : 0;
-        float x[2][E], amax[2];
-        bool nan[2];
+        const int64_t r0 = rows[u * blockDim.y + threadIdx.y];
+        const int64_t r = r0 + h * p.c.stride_head;
+        const bool there = live && r0 >= 0;
+        float amax[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            Piece<T> piece;
-            piece.v = raw[u][s];
-            amax[s] = 0.0f;
-            nan[s] = false;
+            amax[s] = amax_of(raw[u][s]);
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                x[s][j] = to_f32(piece.t[j]);
-                amax[s] = fmaxf(amax[s], fabsf(x[s][j]));
-                nan[s] |= x[s][j] != x[s][j];
-            }
-#pragma unroll
-            for (int d = 1; d < PER; d *= 2) amax[s] = fmaxf(amax[s], __shfl_xor_sync(group, amax[s], d));
+            for (int d = 1; d < PER; d *= 2) amax[s] = max_nan(amax[s], __shfl_xor_sync(~0u, amax[s], d));
         }
-        // the block's four divisions, one in each of its first four lanes: 127 / amax and amax / 127 of k, then of v
-        const int lane = threadIdx.x & 31, of = lane & (PER - 1), first_lane = lane - of;
-        const float a = of & 2 ? amax[1] : amax[0], num = of & 1 ? a : 127.0f, den = of & 1 ? 127.0f : a;
-        const float ratio = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
-        const float id[2] = {__shfl_sync(group, ratio, first_lane), __shfl_sync(group, ratio, first_lane + 2)};
-        if (there) {
+        const bool nan = amax[0] != amax[0] || amax[1] != amax[1];
+        if (__any_sync(~0u, nan)) {  // the largest of those that are numbers
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                int8_t *codes = (s == 0 ? p.c.k_codes : p.c.v_codes) + r * p.c.dim + e0;
-                if (live) {
-                    uint32_t w[E / 4];
-                    if (!nan[s] && amax[s] < INFINITY && id[s] < INFINITY) {
+                amax[s] = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < E / 4; ++j) w[j] = pack4(x[s] + 4 * j, id[s]);
-                    } else {
+                for (int j = 0; j < E; ++j) amax[s] = fmaxf(amax[s], fabsf(to_f32(raw[u][s].t[j])));
 #pragma unroll
-                        for (int j = 0; j < E / 4; ++j)
-                            w[j] = pack4_any(x[s][4 * j], x[s][4 * j + 1], x[s][4 * j + 2], x[s][4 * j + 3], id[s]);
-                    }
-                    if constexpr (E == 8)
-                        *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
-                    else
-                        *reinterpret_cast<uint32_t *>(codes) = w[0];
-                }
+                for (int d = 1; d < PER; d *= 2) amax[s] = fmaxf(amax[s], __shfl_xor_sync(~0u, amax[s], d));
             }
-            if (of == 1) (p.c.k_scales + r * p.c.blocks)[b] = ratio;
-            if (of == 3) (p.c.v_scales + r * p.c.blocks)[b] = ratio;
+        }
+        // the block's four divisions, one in each of its first four lanes: 127 / amax and amax / 127 of k, then of v
+        const float a = of & 2 ? amax[1] : amax[0], num = of & 1 ? a : 127.0f, den = of & 1 ? 127.0f : a;
+        const float ratio = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
+        const float id[2] = {__shfl_sync(~0u, ratio, first_lane), __shfl_sync(~0u, ratio, first_lane + 2)};
+        const bool usual = !nan && amax[0] < INFINITY && amax[1] < INFINITY && id[0] < INFINITY && id[1] < INFINITY;
+        uint32_t w[2][E / 4];
+        if (__all_sync(~0u, usual)) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < E / 4; ++j) {
+                    const T *t = raw[u][s].t + 4 * j;
+                    const float x[4] = {to_f32(t[0]), to_f32(t[1]), to_f32(t[2]), to_f32(t[3])};
+                    w[s][j] = pack4(x, id[s]);
+                }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < E / 4; ++j) {
+                    const T *t = raw[u][s].t + 4 * j;
+                    w[s][j] = pack4_any(to_f32(t[0]), to_f32(t[1]), to_f32(t[2]), to_f32(t[3]), id[s]);
+                }
+        }
+        if (there) {
+            const int64_t at_code = r * p.c.dim + e0;
+            if constexpr (E == 8) {
+                *reinterpret_cast<uint2 *>(p.c.k_codes + at_code) = make_uint2(w[0][0], w[0][1]);
+                *reinterpret_cast<uint2 *>(p.c.v_codes + at_code) = make_uint2(w[1][0], w[1][1]);
+            } else {
+                *reinterpret_cast<uint32_t *>(p.c.k_codes + at_code) = w[0][0];
+                *reinterpret_cast<uint32_t *>(p.c.v_codes + at_code) = w[1][0];
+            }
+        }
+        if (r0 >= 0 && at < p.lanes && (of & 1)) {
+            if (of == 1) p.c.k_scales[r * p.c.blocks + b] = ratio;
+            if (of == 3) p.c.v_scales[r * p.c.blocks + b] = ratio;
         }
     }
 }
@@ -167,22 +210,21 @@ __global__ void __launch_bounds__(256) q8kv_write_kernel(const IoParams p) {
 template <typename T, int U>
 __global__ void __launch_bounds__(256) q8kv_read_kernel(const IoParams p) {
     constexpr int E = 16 / sizeof(T);
+    __shared__ int64_t rows[8 * U];
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.y * U) + threadIdx.y;
     const int at = blockIdx.y * blockDim.x + threadIdx.x;
+    find_rows<U>(p, rows);
+    __syncthreads();
     if (at >= p.lanes) return;
     const int per_head = p.c.dim / E;
     const int h = at / per_head, e0 = (at - h * per_head) * E, b = e0 / 32;
-    int64_t slot[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) slot[u] = first + u * blockDim.y < p.n ? __ldg(p.slots + first + u * blockDim.y) : -1;
     uint32_t w[U][2][E / 4] = {};
     float d[U][2] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        int64_t page;
-        int place;
-        if (place_of(p.c, slot[u], &page, &place)) {
-            const int64_t r = row_of(p.c, page, h, place);
+        const int64_t r0 = rows[u * blockDim.y + threadIdx.y];
+        if (r0 >= 0) {
+            const int64_t r = r0 + h * p.c.stride_head;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int8_t *codes = (s == 0 ? p.c.k_codes : p.c.v_codes) + r * p.c.dim + e0;

@@ -22,8 +22,8 @@
 // Maxima and sums cross the cluster through distributed shared memory; every CTA runs
 // the children's tests itself, on the same numbers, and reaches the same verdict.
 //
-// Vocabulary 128256, f32: 32 trees of 24 nodes, paths up to 9 rows, 56 us (70 MB
-// read: 19 % of the copy rate, 4.2 us a row of the longest path and the start); 2
+// Vocabulary 128256, f32: 32 trees of 24 nodes, paths up to 9 rows, 56 us (49 MB
+// of visited rows, 13 % of the copy rate; 4.5 us a row of the longest path and the start); 2
 // chains of 6 with draft probabilities 23 us.
 //
 // A 64-bit conversion per logit runs at the few-per-cycle rate of the FP64 pipe
