@@ -6,18 +6,27 @@
 // elements or 4 f32), so its loads or stores are one full vector and a warp's
 // are contiguous; a 32-element block is then 4 or 8 neighbouring lanes and its
 // amax takes 2 or 3 shuffles.  Keys and values of the same place are handled by
-// the same lane, which keeps two independent loads in flight.
+// the same lane, which keeps two independent loads in flight.  A large write has
+// to be short of instructions too (a kernel with 20 an element took 50 us where
+// this one takes 38).
+//
+// 8190 tokens of 32 heads x 128, bf16: written in 37.7 us, read in 34.2 us (5.6 and
+// 6.1 TB/s, 82 and 90 % of the copy rate).  32768 tokens of 8 heads read: 35.0 us (5.9
+// TB/s).  64 requests' 9 rows of 256 heads moved: 29 us (85 MB, 2.9 TB/s: rows of
+// 128 and 16 bytes, 2 KB apart, of which DRAM moves 64 at a time; neither more blocks an
+// SM nor more rows in flight change it).  A few rows: 2.1, 2.5 and 3.5 us.
 #include "kv_common.cuh"
 
 namespace kv {
 
 namespace {
 
+// Tokens a lane takes of a large call, for loads in flight.  8190 tokens of 32 heads x 128 bf16 written: 44.7, 39.3,
+// 37.7 us with 1, 2, 4; read: 39.6, 34.2, 34.6, 34.8 with 1, 2, 4, 8; 32768 tokens of 8 heads read: 41.6, 35.0, 35.5,
+// 35.8.  A call that leaves less than four blocks an SM with that takes one a lane: 8 tokens of 8 heads, written and
+// read, 4.1 us, and 6.0 with several.
 constexpr int kManyBlocks = 152 * 4;
-// Tokens a lane takes of a large call, for loads in flight.  8190 tokens of 32 heads x 128 bf16 written: 54.3,
-// 51.4, 73.6 us with 1, 2, 4 (the raw inputs of 4 leave too few warps); 32768 tokens of 8 heads read: 40.1, 39.3
-// with 1, 4.
-constexpr int kWriteTokens = 2, kReadTokens = 4;
+constexpr int kWriteTokens = 4, kReadTokens = 2;
 
 struct IoParams {
     Cache c;
@@ -261,35 +270,54 @@ struct MoveParams {
     Cache c;
     const int64_t *src, *dst;
     int path;
-    int lanes;  // lanes of one token: heads * (2 * dim / 16 + 2 * blocks)
+    int scale_pieces;  // of one row and array: blocks / 4 of 16 bytes, or `blocks` of 4
+    int lanes;         // of one token: heads * 2 * (dim / 16 + scale_pieces)
 };
 
 constexpr int kMoveBatch = 8, kMovePairs = 32;
 
-// One lane owns one 16-byte piece of codes or one scale of every row that its
-// request moves, so the order of a request's pairs is the lane's own program
+// V bytes of every row of a request, pairs g .. g + kMoveBatch - 1: all loaded before any is stored, unless one of them
+// is read by a later one.
+template <typename V>
+__device__ __forceinline__ void move_batch(char *base, int64_t pitch, const int64_t *from, const int64_t *to, bool meet) {
+    if (!meet) {
+        V v[kMoveBatch];
+#pragma unroll
+        for (int i = 0; i < kMoveBatch; ++i)
+            if (from[i] >= 0) v[i] = *reinterpret_cast<const V *>(base + from[i] * pitch);
+#pragma unroll
+        for (int i = 0; i < kMoveBatch; ++i)
+            if (from[i] >= 0) *reinterpret_cast<V *>(base + to[i] * pitch) = v[i];
+    } else {
+        for (int i = 0; i < kMoveBatch; ++i)
+            if (from[i] >= 0) *reinterpret_cast<V *>(base + to[i] * pitch) = *reinterpret_cast<const V *>(base + from[i] * pitch);
+    }
+}
+
+// One lane owns one 16-byte piece of codes or of scales (one scale, where a row's
+// are not whole pieces) of every row that its request moves, so the order of a request's pairs is the lane's own program
 // order and needs no barrier.  Eight pairs are loaded before any is stored,
 // unless one of them is read by a later one of the eight.  The pairs' rows are
 // found once per block, 32 at a time.
-__global__ void __launch_bounds__(256) q8kv_move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(256, 3) q8kv_move_kernel(const MoveParams p) {
     __shared__ int64_t from[kMovePairs], to[kMovePairs];  // of head 0; -1: the pair is skipped
     __shared__ int meets[kMovePairs / kMoveBatch];
     const int64_t *src = p.src + static_cast<int64_t>(blockIdx.y) * p.path;
     const int64_t *dst = p.dst + static_cast<int64_t>(blockIdx.y) * p.path;
     const int at = blockIdx.x * blockDim.x + threadIdx.x;
-    const int pieces = p.c.dim / 16, per_head = 2 * pieces + 2 * p.c.blocks;
+    const int pieces = p.c.dim / 16, scales = p.scale_pieces, per_head = 2 * (pieces + scales);
     const bool mine = at < p.lanes;
     const int h = mine ? at / per_head : 0, in = mine ? at - h * per_head : 0;
-    const bool wide = in < 2 * pieces;
+    const bool wide = in < 2 * pieces || scales < p.c.blocks;
     // address of the lane's piece in row 0 of its head, and the bytes of one row of its array
     char *base;
     int64_t pitch;
-    if (wide) {
+    if (in < 2 * pieces) {
         base = reinterpret_cast<char *>(in < pieces ? p.c.k_codes : p.c.v_codes) + (in < pieces ? in : in - pieces) * 16;
         pitch = p.c.dim;
     } else {
         const int s = in - 2 * pieces;
-        base = reinterpret_cast<char *>(s < p.c.blocks ? p.c.k_scales + s : p.c.v_scales + s - p.c.blocks);
+        base = reinterpret_cast<char *>(s < scales ? p.c.k_scales : p.c.v_scales) + (s < scales ? s : s - scales) * (wide ? 16 : 4);
         pitch = 4LL * p.c.blocks;
     }
     base += h * p.c.stride_head * pitch;
@@ -315,44 +343,11 @@ __global__ void __launch_bounds__(256) q8kv_move_kernel(const MoveParams p) {
         __syncthreads();
         if (!mine) continue;
         for (int g = 0; g < n; g += kMoveBatch) {
-            int64_t f[kMoveBatch], t[kMoveBatch];
-#pragma unroll
-            for (int i = 0; i < kMoveBatch; ++i) {
-                f[i] = from[g + i];
-                t[i] = to[g + i];
-            }
             const bool meet = meets[g / kMoveBatch] != 0;
-            if (wide) {
-                if (!meet) {
-                    uint4 v[kMoveBatch];
-#pragma unroll
-                    for (int i = 0; i < kMoveBatch; ++i)
-                        if (f[i] >= 0) v[i] = *reinterpret_cast<const uint4 *>(base + f[i] * pitch);
-#pragma unroll
-                    for (int i = 0; i < kMoveBatch; ++i)
-                        if (f[i] >= 0) *reinterpret_cast<uint4 *>(base + t[i] * pitch) = v[i];
-                } else {
-                    for (int i = 0; i < kMoveBatch; ++i)
-                        if (from[g + i] >= 0)
-                            *reinterpret_cast<uint4 *>(base + to[g + i] * pitch) =
-                                *reinterpret_cast<const uint4 *>(base + from[g + i] * pitch);
-                }
-            } else {
-                if (!meet) {
-                    float v[kMoveBatch];
-#pragma unroll
-                    for (int i = 0; i < kMoveBatch; ++i)
-                        if (f[i] >= 0) v[i] = *reinterpret_cast<const float *>(base + f[i] * pitch);
-#pragma unroll
-                    for (int i = 0; i < kMoveBatch; ++i)
-                        if (f[i] >= 0) *reinterpret_cast<float *>(base + t[i] * pitch) = v[i];
-                } else {
-                    for (int i = 0; i < kMoveBatch; ++i)
-                        if (from[g + i] >= 0)
-                            *reinterpret_cast<float *>(base + to[g + i] * pitch) =
-                                *reinterpret_cast<const float *>(base + from[g + i] * pitch);
-                }
-            }
+            if (wide)
+                move_batch<uint4>(base, pitch, from + g, to + g, meet);
+            else
+                move_batch<float>(base, pitch, from + g, to + g, meet);
         }
     }
 }
@@ -490,7 +485,8 @@ q8mv_status_t q8kv_cache_move(const q8kv_cache_t *cache, int64_t batch, int64_t 
     p.src = src;
     p.dst = dst;
     p.path = static_cast<int>(path);
-    p.lanes = p.c.heads * (2 * (p.c.dim / 16) + 2 * p.c.blocks);
+    p.scale_pieces = p.c.blocks % 4 == 0 ? p.c.blocks / 4 : p.c.blocks;
+    p.lanes = p.c.heads * 2 * (p.c.dim / 16 + p.scale_pieces);
     const int threads = p.lanes >= 256 ? 256 : (p.lanes + 31) / 32 * 32;
     kv::q8kv_move_kernel<<<dim3(static_cast<unsigned>(kv::ceil_div(p.lanes, threads)), static_cast<unsigned>(batch)),
                            threads, 0, stream>>>(p);
