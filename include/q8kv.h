@@ -57,11 +57,12 @@ typedef struct {
  * from k + i * k_row + h * k_head and v + i * v_row + h * v_head (strides in
  * elements, >= 0; the last axis is contiguous; any alignment of the type), and
  * written to slots[i].  Per 32-element block of a row (the last may be
- * shorter), in IEEE f32 arithmetic on the inputs' f32 values, as
- * q8mv_quantize_rows:
- *     amax = max |x|,  d = amax / 127,  c = rint(x * (127 / amax))
- * (ties to even; c = 0 when amax = 0; +-127 where 127 / amax overflows).  NaN elements do not count in amax and
- * get code 0 unless amax is infinite; a block with an infinity has d = inf and
+ * shorter), in IEEE f32 arithmetic on the inputs' f32 values, every step rounded:
+ *     amax = max |x|,  d = amax / 127,  c = rint(x * (127 * (1 / amax)))
+ * (ties to even; c = 0 when amax = 0; +-127 where the factor overflows), as
+ * q8mv_quantize_rows but for the factor, which that rounds once: a code may be one
+ * apart where x is halfway between two.  NaN elements do not count in amax and get
+ * code 0 unless amax is infinite; a block with an infinity has d = inf and
  * codes 0, and reads back as NaN.  Slots outside the cache are skipped; the
  * slots of one call must differ.  n >= 0.
  */

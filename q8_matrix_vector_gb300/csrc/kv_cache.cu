@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t pack4(const float *x, float id) {
     return __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
 }
 
-// The same for blocks with NaN (0), infinities or an overflowing 127 / amax.
+// The same for blocks with NaN (0), infinities or an overflowing 127 (1 / amax).
 __device__ __noinline__ uint32_t pack4_any(float x0, float x1, float x2, float x3, float id) {
     const float x[4] = {x0, x1, x2, x3};
     uint32_t w = 0;
@@ -126,7 +126,7 @@ __device__ __forceinline__ void find_rows(const IoParams &p, int64_t (&rows)[8 *
     }
 }
 
-// d = amax / 127, c = rint(x * (127 / amax)): the recipe of q8mv_quantize_rows.
+// d = amax / 127, c = rint(x * (127 * (1 / amax))), every step rounded.
 // U tokens a lane: their loads, which do not wait for the slots, are all in flight.
 // For many rows the issue slots bound it, next to HBM: a warp stays together
 // (shuffles of all lanes, one vote for blocks that are not ordinary), 16-bit
@@ -175,9 +175,10 @@ __global__ void __launch_bounds__(256) q8kv_write_kernel(const IoParams p) {
                 for (int d = 1; d < PER; d *= 2) amax[s] = fmaxf(amax[s], __shfl_xor_sync(~0u, amax[s], d));
             }
         }
-        // the block's four divisions, one in each of its first four lanes: 127 / amax and amax / 127 of k, then of v
-        const float a = of & 2 ? amax[1] : amax[0], num = of & 1 ? a : 127.0f, den = of & 1 ? 127.0f : a;
-        const float ratio = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
+        // the block's four divisions, one in each of its first four lanes: 1 / amax and amax / 127 of k, then of v
+        const float a = of & 2 ? amax[1] : amax[0], num = of & 1 ? a : 1.0f, den = of & 1 ? 127.0f : a;
+        float ratio = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
+        if (!(of & 1)) ratio = __fmul_rn(127.0f, ratio);
         const float id[2] = {__shfl_sync(~0u, ratio, first_lane), __shfl_sync(~0u, ratio, first_lane + 2)};
         const bool usual = !nan && amax[0] < INFINITY && amax[1] < INFINITY && id[0] < INFINITY && id[1] < INFINITY;
         uint32_t w[2][E / 4];

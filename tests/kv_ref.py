@@ -19,7 +19,7 @@ def quantise(x):
             mag = np.abs(part)
             amax = np.where(np.isnan(mag), np.float32(0), mag).max(-1)
             scales[..., b] = amax / np.float32(127)
-            inv = np.where(amax > 0, np.float32(127) / amax, np.float32(0))[..., None]
+            inv = np.where(amax > 0, np.float32(127) * (np.float32(1) / amax), np.float32(0))[..., None]
             y = part * inv
             codes[..., 32 * b:32 * b + 32] = np.clip(np.rint(np.where(np.isnan(y), np.float32(0), y)), -127, 127)
     return codes, scales
