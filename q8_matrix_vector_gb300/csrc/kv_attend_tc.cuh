@@ -7,18 +7,18 @@
 // Work is the line of units of kv_attend.cuh with 128-row items and tiles of 128
 // keys, one CTA per SM.  With 128 rows a code meets 128 multiplications on each
 // side, so the products belong to tcgen05.mma and the rest of the SM keeps it fed:
-//   * four convert warps take 32 keys of a tile each.  cp.async brings the next
-//     tile's codes and scales while they turn this one's into f16 operands in shared
-//     memory, K a tile ahead of V.  A key's row is normalised by a power of two (one
-//     for the warp's 32 keys, or one per key where some of them are drafted) that
+//   * eight convert warps take 16 keys of a tile each.  cp.async brings the codes
+//     and scales of two tiles to come while they turn this one's into f16 operands in
+//     shared memory, K a tile ahead of V.  A key's row is normalised by a power of two
+//     (one for the warp's 16 keys, or one per key where some of them are drafted) that
 //     goes into the softmax, and code times scale is formed with the scale in two
 //     f16 parts.  K is kept in two f16 parts, 22 bits, since a score's error is a
 //     weight's relative one and lse is f32; V is rounded once to 11 bits, as outputs
 //     are bf16.  (f32 and f16 outputs stay with kv_attend.cuh.)  K and V tiles have
 //     the same layout, 128-byte rows of a key's 64 e, swizzled: K is read K-major, V
 //     MN-major.
-//   * one thread issues the MMAs: S = Q K^T of tile g (lower part, then upper), then
-//     O += P V of tile g - 1.
+//   * one lane of a warp that stays together issues the MMAs: S = Q K^T of tile g
+//     (lower part, then upper), then O += P V of tile g - 1.
 //   * two softmax warpgroups take alternate tiles, a thread a row, each with its own
 //     S, O (f32) and, in place of S, P (f16) in tensor memory: 2 x (128 + 128)
 //     columns, all of them.  While one exponentiates, the other's products run.
@@ -27,6 +27,11 @@
 //   * at an item's end each warpgroup adds half of the columns of both O.
 // All hand-overs are mbarriers, every wait is bounded (2 s); one that runs out is
 // recorded in the plan's error word and the CTA leaves.
+//
+// 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 86.6 us,
+// 241 TFLOP/s of the two products, 1.2 TB/s of cache.  A tile takes 5600 cycles, of
+// which the MMAs run 1400; turning its codes into operands bounds it, then 8 us until a
+// CTA's first scores are there and 10 us of joining cut items at the end.
 #pragma once
 
 #include "kv_attend.cuh"
@@ -39,11 +44,12 @@ constexpr int kTcWarpKeys = 128 / kTcConvWarps;  // keys of a tile that a conver
 constexpr int kTcMmaWarp = kTcSoftWarps + kTcConvWarps;
 constexpr int kTcThreads = (kTcMmaWarp + 1) * 32;
 constexpr int kTcHalf = kTcKeys * 128;          // 128 rows of 64 f16
-constexpr uint64_t kTcWaitNs = 2000000000ull;
 constexpr int kTcErrWait = 1;
 constexpr float kTcTop = 7.0f;                  // log2 of P at the row's maximum when that is taken
 constexpr float kTcSlack = 15.0f;               // and how far P may grow before it is taken anew (f16 ends at 2^16)
-constexpr int kTcItemUnits = 3;
+constexpr int kTcItemUnits = 4;                 // an item's fixed cost in tiles (16 requests of 700 .. 5000 tokens, 124 rows:
+                                                // 149, 114, 88.4, 86.5, 86.0, 89.6 us with 1 .. 6; 24 of 300 .. 3000, 68 rows: 83.1 with 4,
+                                                // 83.6 with 5)
 
 template <int DP>
 struct TcSmem {
