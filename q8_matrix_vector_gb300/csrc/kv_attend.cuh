@@ -3,8 +3,8 @@
 //     s[r, j] = scale * sum_b dK[j, b] * ( sum_{e in b} q[r, e] * cK[j, e] )
 //     out[r, e] = sum_j P[r, j] * dV[j, b(e)] * cV[j, e] / sum_j P[r, j],   P = exp(s - max)
 //
-// Work.  An item is (request, kv head, 16 query rows); its query rows are the
-// (node, head of the group) pairs that share the kv head, so a grouped head's
+// Work.  An item is (request, kv head, 8 or 16 query rows); its query rows are
+// the (node, head of the group) pairs that share the kv head, so a grouped head's
 // cache is read once for all of them.  Items times tiles of 128 keys form one
 // line of units, and CTA c takes units [c U / G, (c+1) U / G): every CTA has the
 // same share whatever the lengths are, an item is cut only where a share ends,
@@ -32,6 +32,15 @@
 //     scales of a step's keys and the running maximum taken over s + E (log2),
 //     P dV stays below 2^14 and is exact enough down to 2^-28 of that; the factor
 //     cancels in the quotient.
+//
+// One token a request, groups of 8, 8 kv heads of 128.  bf16: 32 requests of 180 ..
+// 8100 tokens 66.7 us (288 MB, 4.3 TB/s, 64 % of the copy rate), of 8000 tokens each
+// 108 us (82 %).  f32, two of 200001 .. 262143: 242 us (1.2 GB, 5.0 TB/s, 73 %; heads
+// apart in memory 80 %).  32 heads of one request of 511 tokens: 11.3 us.  Where the
+// cache is long, HBM and the issue of 940 instructions for a warp's 32 keys bound it
+// together: shared memory for two steps of keys leaves two CTAs, 8 warps, an SM, and
+// the tensor cores, that make the products, are idle most of the time.  Where it is
+// short, the chain lengths -> page -> keys -> join does, 8 us with no key at all.
 #pragma once
 
 #include "kv_attend.h"
@@ -200,7 +209,8 @@ static __device__ __noinline__ uint32_t sees(const uint32_t *mask, int64_t mask_
     return (word(0) << -j0) | ((1u << -j0) - 1u);  // keys below -j0 are prefix
 }
 
-template <typename T, int DP, int NT, int QP, int PP, int HW>
+// LIVE of the DP / 32 blocks are computed with: the rest lies past the head.
+template <typename T, int DP, int NT, int QP, int PP, int HW, int LIVE>
 __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv_attend_kernel(const AttendParams p) {
     using S = Smem<DP, NT, QP, HW>;
     static_assert(HW == 1 || (HW == kWarps && NT == 1), "one head for all warps, or one each with 8 rows");
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
 #pragma unroll
                             for (int r = 0; r < 2; ++r) s[t][2 * j][r] = s[t][2 * j + 1][r] = 0.0f;
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
+                        for (int b = 0; b < LIVE; ++b) {
                             const uint2 x = *reinterpret_cast<const uint2 *>(sk + (16 * j + g) * S::kKPitch + b * 32 + c * 8);
                             const uint2 y = *reinterpret_cast<const uint2 *>(sk + (16 * j + 8 + g) * S::kKPitch + b * 32 + c * 8);
                             const uint32_t x0 = x.x ^ 0x80808080u, x1 = x.y ^ 0x80808080u;
@@ -580,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
                                 l[t][r] *= f[r];
                             }
 #pragma unroll
-                            for (int k = 0; k < NB * 2; ++k) {
+                            for (int k = 0; k < LIVE * 2; ++k) {
                                 o[t][k][0] *= f[0];
                                 o[t][k][1] *= f[1];
                                 o[t][k][2] *= f[0];
@@ -604,7 +614,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
 #pragma unroll
                     for (int k = 0; k < 4; ++k) load_scales<NB>(vs + (8 * k + g) * NB, dv[k]);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
+                    for (int b = 0; b < LIVE; ++b) {
                         // The tensor cores cut their f32 sums toward zero.  Over thousands of keys that bias is
                         // 1e-5 of the sum: with f32 or f16 outputs a step's 32 keys are summed apart, and added
                         // with rounding.
@@ -902,18 +912,24 @@ __global__ void __launch_bounds__(kWarps * 32, DP == 64 && NT == 1 ? 3 : 2) q8kv
     }
 }
 
-// The variants of one type.
-template <typename T, int DP, int QP, int PP, int NT, int HW>
+// The variants of one type: dim up to 64, 96, 128, 192 or 256, the second and fourth in the layout of the next with
+// fewer blocks (4 requests of 67756 tokens, dim 80, f32: 126 us with all of
+// them, 111 so; one of 58636, dim 192, f16: 87 and 70).  A test of each block at run time cost full heads 2 to 6 %.
+template <typename T, int DP, int QP, int PP, int NT, int HW, int LIVE = DP / 32>
 AttendVariant attend_variant_of(int dim) {
-    return {q8kv_attend_kernel<T, DP, NT, QP, PP, HW>, Smem<DP, NT, QP, HW>::kTotal, kWarps * 32,
+    return {q8kv_attend_kernel<T, DP, NT, QP, PP, HW, LIVE>, Smem<DP, NT, QP, HW>::kTotal, kWarps * 32,
             8 * (HW == 1 ? NT : HW) * (dim + kPartExtra)};
 }
 
 template <typename T, int QP, int PP, int NT, int HW>
 AttendVariant attend_variant_of(int dim) {
     if (dim <= 64) return attend_variant_of<T, 64, QP, PP, NT, HW>(dim);
+    if (dim <= 96) return attend_variant_of<T, 128, QP, PP, NT, HW, 3>(dim);
     if (dim <= 128) return attend_variant_of<T, 128, QP, PP, NT, HW>(dim);
-    if constexpr (NT == 1) return attend_variant_of<T, 256, QP, PP, NT, HW>(dim);
+    if constexpr (NT == 1) {
+        if (dim <= 192) return attend_variant_of<T, 256, QP, PP, NT, HW, 6>(dim);
+        return attend_variant_of<T, 256, QP, PP, NT, HW>(dim);
+    }
     return {};
 }
 
