@@ -129,6 +129,15 @@ def test_heads_side_by_side_in_a_long_table(q8mv):
         c.check()
 
 
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("dim", [80, 96, 160, 192, 224])
+def test_heads_that_end_before_their_layout(q8mv, dtype, dim):
+    """Heads of fewer blocks than the layout that they share: by heads side by side, 8 rows and 16."""
+    Case(q8mv, dim, [0, 35, 64, 900], [1, 3, 0, 2], heads=4, group=2, dim=dim, dtype=dtype, layout="token", page=9, cols=80000).check()
+    Case(q8mv, dim, [7, 3000], [2, 1], heads=3, group=2, dim=dim, dtype=dtype).check()
+    Case(q8mv, dim, [7, 500], [5, 9], heads=3, group=2, dim=dim, dtype=dtype).check()
+
+
 def test_heads_side_by_side_cut_between_ctas(q8mv):
     Case(q8mv, 7, [20001], [1], heads=4, group=2, dim=64, page=64, tree=False, layout="token").check()
     Case(q8mv, 8, [9000, 20011, 1, 5, 3000], [2, 1, 1, 2, 1], heads=8, group=4, dim=128, page=32, dtype="bfloat16",

@@ -112,6 +112,27 @@ def test_with_draft_probabilities(q8mv, dtype, vocab, chain):
     run_and_check(q8mv, logits, tokens, parents, np.full_like(uniforms, 0.999999), starts, None, draft)
 
 
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("vocab", [4, 128, 5000, 33000])
+@pytest.mark.parametrize("chain", [True, False])
+def test_rows_that_are_brought_while_their_parents_are_summed(q8mv, dtype, vocab, chain):
+    """Vocabularies in whole fours, paths along first children and beside them, with draft probabilities and without."""
+    import torch
+
+    rng = np.random.default_rng(vocab + 1)
+    sizes = [9, 0, 14, 2]
+    logits, tokens, parents, uniforms, starts = inputs(rng, sizes, vocab, dtype, chain)
+    for u in (uniforms, np.full_like(uniforms, 1e-6), np.full_like(uniforms, 0.999999)):
+        run_and_check(q8mv, logits, tokens, parents, u, starts, np.array([0.7, 1.0, 0.0, 1.2], np.float32))
+    draft = torch.softmax(logits.float() + 0.3 * torch.randn(logits.shape, generator=torch.Generator("cuda").manual_seed(vocab), device="cuda"), -1)
+    for u in (uniforms, np.full_like(uniforms, 1e-6), np.full_like(uniforms, 0.999999)):
+        run_and_check(q8mv, logits, tokens, parents, u, starts, np.array([0.7, 1.0, 0.9, 1.2], np.float32), draft)
+    # the same rows where four cannot be loaded at once
+    other = torch.zeros(logits.shape[0], vocab + 3, device="cuda", dtype=logits.dtype)[:, 1:vocab + 1]
+    other.copy_(logits)
+    run_and_check(q8mv, other, tokens, parents, uniforms, starts)
+
+
 def test_a_large_vocabulary(q8mv):
     """More logits than a lane holds in registers."""
     rng = np.random.default_rng(4)
