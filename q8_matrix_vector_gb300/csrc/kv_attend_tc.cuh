@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             const int x = static_cast<int>(g & 1), ring = static_cast<int>(g & 3);
             float4 *meta = reinterpret_cast<float4 *>(smem + S::kMeta + ring * S::kMetaTile) + cw * WK;
             const uint32_t there = __ballot_sync(~0u, row != kNoRow);
-            bool plain = all_before && there == (WK == 32 ? ~0u : (1u << (WK & 31)) - 1u);
+            bool plain = all_before && there == (1u << WK) - 1u;
             // ---- normalisers: of each key, and of all keys if every row sees them
             float k_scale[NB];
             {
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     for (int q = 0; q < kTcConvWarps; ++q) fast |= plain_keys[ring][q] << q;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        see[q] = WK == 32 ? there_bits[ring][q] : there_bits[ring][2 * q] | there_bits[ring][2 * q + 1] << 16;
+                        see[q] = there_bits[ring][2 * q] | there_bits[ring][2 * q + 1] << 16;
                         const int64_t j0 = (kt0 + i) * kTcKeys + 32 * q - pl.prefix;
                         if (j0 + 32 > 0)
                             see[q] &= sees(p.mask, p.mask_row, p.mask_words, p.group, pl.nodes, pl.row0, static_cast<int>(j0), idx);
