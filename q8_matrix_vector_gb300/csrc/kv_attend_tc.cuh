@@ -26,7 +26,7 @@
 //     and the maximum only moves when P would pass 2^15: O is rarely rescaled.
 //   * at an item's end each warpgroup adds half of the columns of both O.
 // All hand-overs are mbarriers, every wait is bounded (2 s); one that runs out is
-// recorded in the plan's error word and the CTA leaves.
+// recorded in the plan's error word and the CTA leaves, once its MMAs have ended.
 //
 // 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 86.6 us,
 // 241 TFLOP/s of the two products, 1.2 TB/s of cache.  A tile takes 5600 cycles, of
@@ -45,6 +45,7 @@ constexpr int kTcMmaWarp = kTcSoftWarps + kTcConvWarps;
 constexpr int kTcThreads = (kTcMmaWarp + 1) * 32;
 constexpr int kTcHalf = kTcKeys * 128;          // 128 rows of 64 f16
 constexpr int kTcErrWait = 1;
+constexpr uint64_t kTcDrainNs = 2000000000ull;  // for MMAs that were issued: they end by themselves, whatever a plan's waits are
 constexpr float kTcTop = 7.0f;                  // log2 of P at the row's maximum when that is taken
 constexpr float kTcSlack = 15.0f;               // and how far P may grow before it is taken anew (f16 ends at 2^16)
 constexpr int kTcItemUnits = 4;                 // an item's fixed cost in tiles (16 requests of 700 .. 5000 tokens, 124 rows:
@@ -359,10 +360,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
 #pragma unroll
             for (int k = 1; k < kTcKeys / 16; ++k) tc_mma_ts(d, a + k * 8, dv + k * kKeyStep, idesc_o, 1u);
         };
-        int64_t g = 0;                 // tile of the CTA
-        uint64_t *last_bar = nullptr;  // of the last commit
-        uint32_t last_ph = 0;
-        int last_first = 0;            // whether tile g - 1 was its warpgroup's first of an item
+        int64_t g = 0;                    // tile of the CTA
+        int64_t scored = -1, summed = -1; // the last tiles whose scores and whose O += P V were issued
+        int last_first = 0;               // whether tile g - 1 was its warpgroup's first of an item
         auto second = [&](int64_t t, bool first) -> bool {
             const uint32_t x = static_cast<uint32_t>(t) & 1u, ph = static_cast<uint32_t>(t >> 1) & 1u;
             bool ok = tc_wait(p_full + x, ph, leaving, p.wait_ns) && tc_wait(&v_full, static_cast<uint32_t>(t) & 1u, leaving, p.wait_ns);
@@ -374,8 +374,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 tc_commit(v_free + x);
             }
             __syncwarp();
-            last_bar = v_free + x;
-            last_ph = ph;
+            summed = t;
             return true;
         };
         for (;;) {
@@ -394,8 +393,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     tc_commit(s_full + x);
                 }
                 __syncwarp();
-                last_bar = k_free + x;
-                last_ph = ph;
+                scored = g;
                 if (g > 0 && !second(g - 1, last_first != 0)) {
                     bad = true;
                     break;
@@ -407,8 +405,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         }
         if (!bad && g > 0 && !second(g - 1, last_first != 0)) bad = true;
         if (bad) leave = 1;
-        // what was issued, before the tensor memory goes back
-        if (last_bar != nullptr && !tc_wait(last_bar, last_ph, nullptr, p.wait_ns)) bad = true;
+        // What was issued has to end, and its last arrivals to be there, before the tensor memory, the operands and the
+        // barriers go back: also of a CTA that leaves because a wait ran out, so not with that wait's bound.
+        auto drain = [&](uint64_t *bars, int64_t t) {
+            if (t >= 0 && !tc_wait(bars + (t & 1), static_cast<uint32_t>(t >> 1) & 1u, nullptr, kTcDrainNs)) bad = true;
+        };
+        drain(k_free, scored);
+        drain(s_full, scored);
+        drain(v_free, summed);
         if (bad && lane == 0) atomicOr(p.err, kTcErrWait);
     } else if (warp >= kTcSoftWarps) {
         // ================ convert
