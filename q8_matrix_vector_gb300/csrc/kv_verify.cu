@@ -19,7 +19,8 @@
 // vocabulary), so a row is read once, all of a lane's loads in flight.  While a row is
 // summed the first child's takes its place, and that row's maximum is told with this
 // row's sum: on a path along first children a step takes 8400 cycles instead of 10600.
-// Maxima and sums cross the cluster through distributed shared memory; every CTA runs
+// Maxima and sums cross the cluster through distributed shared memory, the first time
+// once all of its CTAs are known to run; every CTA runs
 // the children's tests itself, on the same numbers, and reaches the same verdict.
 //
 // Vocabulary 128256, f32: 32 trees of 24 nodes, paths up to 9 rows, 56 us (49 MB
@@ -168,6 +169,10 @@ __device__ __forceinline__ void load4(const T *p, int i, int n, bool vec, float 
     }
 }
 
+// the cluster's barrier in two halves, for the order of execution alone
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(~0u, x, d);
@@ -210,6 +215,10 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
         }
         return;
     }
+    // Another CTA's shared memory may be written once that CTA runs: waited for before the first exchange, behind the
+    // first row's loads.
+    cluster_arrive();
+    bool started = false;
     const int32_t *tokens = p.tokens + row0, *parents = p.parents + row0;
     const float *uniforms = p.uniforms + row0;
     int32_t *path = p.path + row0;
@@ -248,6 +257,8 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
             if (lane == 0) warp_w[warp] = mine;
         }
         __syncthreads();
+        if (!started) cluster_wait();
+        started = true;
         if (tid < ctas) {
             if (sums) {
                 int64_t s = 0;

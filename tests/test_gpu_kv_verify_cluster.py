@@ -1,0 +1,23 @@
+"""The verification's exchanges over a cluster: requests that reach the first one at once, many of them at a time."""
+import numpy as np
+import pytest
+
+import kv_ref as ref
+from test_gpu_kv_verify import inputs, q8mv, run_and_check  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ref.TYPES)
+@pytest.mark.parametrize("vocab", [1, 3, 200])
+def test_rows_that_take_no_time(q8mv, dtype, vocab):  # noqa: F811
+    """More requests than fit the GPU, rows of a few logits, some CTAs without any: CTAs start while others exchange."""
+    rng = np.random.default_rng(vocab)
+    sizes = rng.integers(0, 4, 300).tolist()
+    logits, tokens, parents, uniforms, starts = inputs(rng, sizes, vocab, dtype)
+    temperature = rng.uniform(0.3, 1.5, len(sizes)).astype(np.float32)
+    temperature[::5] = 0
+    first = run_and_check(q8mv, logits, tokens, parents, uniforms, starts, temperature)
+    for _ in range(3):
+        for a, b in zip(first, run_and_check(q8mv, logits, tokens, parents, uniforms, starts, temperature)):
+            assert np.array_equal(a, b)
