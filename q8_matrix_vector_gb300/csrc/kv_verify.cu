@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32, 4) q8kv_verify_kernel(const
                                 cta_w[tok / chunk] -= wx;
                                 if (tok / chunk == rank) warp_w[tok % chunk / seg] -= wx;
                             }
+                            __syncwarp();  // the next one's lane may change the same words
                         }
                     }
                 }

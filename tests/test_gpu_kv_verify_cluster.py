@@ -21,3 +21,20 @@ def test_rows_that_take_no_time(q8mv, dtype, vocab):  # noqa: F811
     for _ in range(3):
         for a, b in zip(first, run_and_check(q8mv, logits, tokens, parents, uniforms, starts, temperature)):
             assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("vocab", [40, 5000])
+def test_children_refused_in_turn_from_the_same_words(q8mv, vocab):  # noqa: F811
+    """Up to 31 siblings whose tokens lie side by side: their weights leave the same sums one after another."""
+    import torch
+
+    rng = np.random.default_rng(vocab + 3)
+    nodes, batch = 32, 64
+    logits = torch.from_numpy(rng.standard_normal((nodes * batch, vocab)).astype(np.float32)).cuda()
+    tokens = np.concatenate([np.concatenate([[0], rng.permutation(31)]) for _ in range(batch)]).astype(np.int32)
+    parents = np.tile(np.array([-1] + [0] * (nodes - 1), np.int32), batch)
+    starts = (np.arange(batch + 1) * nodes).astype(np.int32)
+    uniforms = rng.random(nodes * batch).astype(np.float32)
+    uniforms.reshape(batch, nodes)[:, 1:] = 0.999999  # refused
+    for _ in range(3):
+        run_and_check(q8mv, logits, tokens, parents, uniforms, starts)
