@@ -178,8 +178,10 @@ class Cache:
             stride = t.stride()
             if (width > 1 and stride[3] != 1) or any(s % width for n, s in zip(t.shape, stride[:3]) if n > 1):
                 raise ValueError(f"{name}'s rows must be contiguous and whole rows apart")
+            if any(s < width for n, s in zip(t.shape, stride[:3]) if n > 1):
+                raise ValueError(f"{name} is expanded: its rows overlap")
             # the stride of an axis of one element says nothing
-            mine = tuple(max(1, s // width) if n > 1 else 1 for n, s in zip(t.shape, stride[:3]))
+            mine = tuple(s // width if n > 1 else 1 for n, s in zip(t.shape, stride[:3]))
             if strides is not None and mine != strides:
                 raise ValueError(f"{name} must have the strides of k_codes, counted in rows")
             strides = mine
