@@ -512,7 +512,6 @@ def __getattr__(name):
     if name in _KV:
         from . import kv
 
-        kv.bind(_lib)
         for n in _KV:
             globals()[n] = getattr(kv, n)
         return globals()[name]

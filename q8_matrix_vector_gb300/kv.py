@@ -52,8 +52,8 @@ _VERIFY = struct.Struct("=10Q3qiiii")
 assert _ATTEND.size == ctypes.sizeof(AttendArgs) and _VERIFY.size == ctypes.sizeof(VerifyArgs)
 
 
-def bind(lib: ctypes.CDLL) -> None:
-    """Declare the q8kv entry points of the loaded library."""
+def _bind(lib: ctypes.CDLL) -> None:
+    """Declare the q8kv entry points of the loaded library: undeclared, ctypes would cut pointers to 32 bits."""
     i32, i64, p, ref = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.POINTER
     for name, args in (
             ("q8kv_cache_write", [ref(CacheDesc), i64, p, p, i32, i64, i64, i64, i64, p, p]),
@@ -75,6 +75,9 @@ def _library():
     from . import _lib
 
     return _lib
+
+
+_bind(_library())
 
 
 def _fail(status: int, what: str):
