@@ -55,11 +55,11 @@ inline bool make_cache(const q8kv_cache_t *c, Cache *out) {
     if (c->heads < 1 || c->heads > 65535 || c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16 != 0)
         return false;
     if (c->stride_page < 1 || c->stride_head < 1 || c->stride_token < 1) return false;
-    // the last row's offset stays far inside 63 bits
-    const int64_t most = 1LL << 48;
-    if (c->stride_page > most || c->stride_head > most || c->stride_token > most) return false;
     if (c->pages > 0) {
-        if (c->stride_page > (1LL << 52) / c->pages) return false;
+        // each axis reaches 2^52 rows at most, so that the last row's offset in bytes (256 a row) fits 63 bits
+        const int64_t most = 1LL << 52;
+        if (c->stride_page > most / c->pages || c->stride_head > most / c->heads || c->stride_token > most / c->page_size)
+            return false;
         if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return false;
         if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) ||
             !aligned(c->v_scales, 16))
