@@ -150,10 +150,10 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
                           cudaStream_t stream);
 /*
  * Calls with many bf16 query rows a request run on a kernel that waits on
- * shared-memory barriers; every wait is bounded (about 2 s).  Synchronises the
- * plan's device and reports in *device_error whether one ran out since the last
- * check (1, else 0); the output of that call is undefined.  Clears the word and,
- * if it was set, the plan's counters.
+ * shared-memory barriers; every wait is bounded (about 2 s).  A call in which one
+ * runs out ends with an undefined output; the plan's other calls, checked or not,
+ * are as without it.  Synchronises the plan's device, reports in *device_error
+ * whether one ran out since the last check (1, else 0) and clears the word.
  */
 q8mv_status_t q8kv_attend_check(q8kv_attend_plan_t plan, int32_t *device_error);
 /* For tests of the bounded waits only: the bound in nanoseconds (0 restores it). */

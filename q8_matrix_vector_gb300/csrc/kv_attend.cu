@@ -31,7 +31,6 @@ struct q8kv_attend_s {
     int64_t max_items = 0;
     float *partial = nullptr;
     unsigned *tickets = nullptr;
-    int64_t tickets_n = 0;
     int *err = nullptr;
     uint64_t wait_ns = kDefaultWaitNs;
 };
@@ -82,7 +81,6 @@ q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t
     if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * static_cast<size_t>(floats));
     if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(tickets));
     if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(tickets));
-    p->tickets_n = tickets;
     if (e == cudaSuccess) e = cudaMalloc(&p->err, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(int));
     // the zeros, before any stream may use them
@@ -191,7 +189,6 @@ q8mv_status_t q8kv_attend_check(q8kv_attend_plan_t p, int32_t *device_error) {
     if (st == Q8MV_OK) st = q8i::cuda_status(cudaMemcpy(&word, p->err, sizeof(int), cudaMemcpyDeviceToHost));
     if (st == Q8MV_OK && word != 0) {
         st = q8i::cuda_status(cudaMemset(p->err, 0, sizeof(int)));
-        if (st == Q8MV_OK) st = q8i::cuda_status(cudaMemset(p->tickets, 0, sizeof(unsigned) * p->tickets_n));
         if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
     }
     *device_error = word;

@@ -26,7 +26,8 @@
 //     and the maximum only moves when P would pass 2^15: O is rarely rescaled.
 //   * at an item's end each warpgroup adds half of the columns of both O.
 // All hand-overs are mbarriers, every wait is bounded (2 s); one that runs out is
-// recorded in the plan's error word and the CTA leaves, once its MMAs have ended.
+// recorded in the plan's error word and the CTA leaves, once its MMAs have ended and
+// its parts of cut items are counted: the tickets are whole after every call.
 //
 // 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 86.6 us,
 // 241 TFLOP/s of the two products, 1.2 TB/s of cache.  A tile takes 5600 cycles, of
@@ -195,6 +196,24 @@ __device__ __forceinline__ uint32_t tc_scaled(uint32_t codes, uint32_t hi, uint3
 
 // power of two with exponent e
 __device__ __forceinline__ float tc_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Counts a part of a cut item, tiles first .. first + tiles_k - 1 of the line, that its CTA will not write: as the joins
+// of the kernel count it, so that the item's tickets are 0 again when all of its CTAs have come.
+static __device__ __noinline__ void tc_count(const Split split, unsigned *ticket, unsigned *group_tickets, int64_t first, int64_t tiles_k) {
+    auto arrive = [](unsigned *at, unsigned count) -> bool {
+        const bool last = atomicAdd(at, 1u) == count - 1;
+        if (last) *at = 0;
+        return last;
+    };
+    const int c0 = static_cast<int>(split.owner(first)), c1 = static_cast<int>(split.owner(first + tiles_k - 1));
+    if (c1 - c0 < kJoinGroup) {
+        arrive(ticket, c1 - c0 + 1);
+    } else {
+        const int grp = blockIdx.x / kJoinGroup, lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
+        if (arrive(group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1))
+            arrive(ticket, c1 / kJoinGroup - c0 / kJoinGroup + 1);
+    }
+}
 
 // A convert warp's place: an item, and which of its tiles here.
 struct TcTile {
@@ -706,6 +725,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         int item_no = 0;
         bool first_item = true;
         uint32_t soft_phase = 0;
+        bool counted = false;  // the item's part, if it is one
         Place &pl = places[warp];  // the warp's copy
         if (lane == 0) pl = w;
         __syncwarp();
@@ -715,6 +735,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             if (lane == 0) tc_arrive(&soft_bar);
             const bool ok = tc_wait(&soft_bar, soft_phase, leaving, p.wait_ns);
             soft_phase ^= 1u;
+            if (!ok) leave = 1;  // at once: a warp that leaves may come here a few times more
             return __all_sync(~0u, ok);
         };
         for (;;) {
@@ -945,6 +966,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 tc_after();
                 if (!whole && pl.item < p.tickets_n) {
                     auto join = [&](int parts, int64_t head, int64_t at, int64_t step, bool last) {
+                        if (bad) return;
                         auto part_of = [&](int i) { return p.partial + (i == 0 ? head : at + i * step) * pitch; };
                         float up = -INFINITY, total = 0.0f;
                         for (int i = 0; i < parts; ++i) up = fmaxf(up, __ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r).x);
@@ -990,16 +1012,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     auto arrive = [&](unsigned *ticket, unsigned count) -> bool {
                         __threadfence();
                         if (!soft_sync()) bad = true;
-                        if (tid == 0 && !bad) {
+                        if (tid == 0) {  // (also if the CTA is leaving: its output is undefined, but the tickets are not)
                             const unsigned t = atomicAdd(ticket, 1u);
                             is_last = t == count - 1;
                             if (is_last) *ticket = 0;
                         }
+                        __syncwarp();
                         if (!soft_sync()) bad = true;
                         const bool yes = *const_cast<volatile int *>(&is_last) != 0;
                         if (!soft_sync()) bad = true;
                         if (yes) __threadfence();
-                        return yes && !bad;
+                        return yes;
                     };
                     const int c0 = static_cast<int>(split.owner(pl.first)), c1 = static_cast<int>(split.owner(pl.first + pl.tiles_k - 1));
                     const int slot_c0 = split.begin(c0) >= pl.first - kTcItemUnits ? 2 * c0 : 2 * c0 + 1;
@@ -1016,7 +1039,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 }
                 ++item_no;
             }
+            counted = true;
             if (bad || !more(pl)) break;
+            counted = false;
             __syncwarp();
             if (lane == 0) {
                 Place next = pl;
@@ -1028,6 +1053,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         if (bad) {
             leave = 1;
             if (lane == 0) atomicOr(p.err, kTcErrWait);
+            // what the first thread has not counted yet
+            if (tid == 0) {
+                Place y = pl;
+                for (;;) {
+                    int64_t kt0;
+                    const int n = tiles_of(y, &kt0);
+                    if (!counted && n > 0 && n != y.tiles_k && y.item < p.tickets_n)
+                        tc_count(split, p.tickets + y.item, p.group_tickets, y.first, y.tiles_k);
+                    if (!more(y)) break;
+                    advance(y);
+                    counted = false;
+                }
+            }
         }
     }
     tc_before();
