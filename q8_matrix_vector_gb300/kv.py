@@ -382,7 +382,7 @@ class TreeVerify(_Plan):
     _destroy = "q8kv_verify_destroy"
 
     def __init__(self, max_requests: int, max_rows: int, vocab: int, device: int = -1):
-        self.vocab = vocab
+        self.vocab, self.max_requests = vocab, max_requests
         self._make("q8kv_verify_plan", max_requests, max_rows, vocab, int(device))
         self._fn = _library().q8kv_verify
         self._args = ctypes.create_string_buffer(_VERIFY.size)
@@ -397,12 +397,20 @@ class TreeVerify(_Plan):
         their own).  uniforms [rows] f32 in [0, 1): node 0's draws the next token, the others' test their node.
         temperature [requests] f32 (0: greedy).  draft_probs [rows, vocab] f32: row i is what node i's children were
         drawn from (None: they were not drawn).  starts [requests + 1] int32: requests' first nodes (None: as many
-        for each).  path holds each request's accepted nodes in order from 0, then -1; count how many drafts.
+        for each of ``requests``, which is taken from temperature if not given; a plan for one request has one).
+        path holds each request's accepted nodes in order from 0, then -1; count how many drafts.
         """
         device = self.device
         rows, code, ls = _rows(logits, self._tail, device, "logits")
         if requests is None:
-            requests = starts.numel() - 1 if starts is not None else temperature.numel() if temperature is not None else 1
+            if starts is not None:
+                requests = starts.numel() - 1
+            elif temperature is not None:
+                requests = temperature.numel()
+            elif self.max_requests == 1:
+                requests = 1
+            else:
+                raise ValueError(f"how many requests the {rows} rows are: pass starts, temperature or requests")
         at_tokens = _ints(tokens, torch.int32, rows, device, "tokens")
         at_parents = _ints(parents, torch.int32, rows, device, "parents")
         at_uniforms = _ints(uniforms, torch.float32, rows, device, "uniforms")

@@ -38,3 +38,22 @@ def test_children_refused_in_turn_from_the_same_words(q8mv, vocab):  # noqa: F81
     uniforms.reshape(batch, nodes)[:, 1:] = 0.999999  # refused
     for _ in range(3):
         run_and_check(q8mv, logits, tokens, parents, uniforms, starts)
+
+
+def test_how_many_requests_there_are_has_to_be_known(q8mv):  # noqa: F811
+    """Rows of several requests are not taken for one request's: its walk would be a wrong one without an error."""
+    import torch
+
+    rng = np.random.default_rng(16)
+    logits, tokens, parents, uniforms, starts = inputs(rng, [4, 4], 100, "float32")
+    t, p, u, s = (torch.from_numpy(a).cuda() for a in (tokens, parents, uniforms, starts))
+    plan = q8mv.TreeVerify(2, 8, 100)
+    with pytest.raises(ValueError):
+        plan(logits, t, p, u)
+    want = plan(logits, t, p, u, starts=s)
+    for how in (dict(requests=2), dict(temperature=torch.ones(2, device="cuda"))):
+        assert all(torch.equal(a, b) for a, b in zip(plan(logits, t, p, u, **how), want))
+    # a plan for one request needs nothing said
+    one = q8mv.TreeVerify(1, 4, 100)
+    for a, b in zip(one(logits[:4], t[:4], p[:4], u[:4]), (want[0][:4], want[1][:1], want[2][:1])):
+        assert torch.equal(a, b)
