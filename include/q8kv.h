@@ -64,7 +64,7 @@ typedef struct {
  * apart where x is halfway between two.  NaN elements do not count in amax and get
  * code 0 unless amax is infinite; a block with an infinity has d = inf and
  * codes 0, and reads back as NaN.  Slots outside the cache are skipped; the
- * slots of one call must differ.  n >= 0.
+ * slots of one call must differ.  0 <= n < 2^31, here and in q8kv_cache_read.
  */
 q8mv_status_t q8kv_cache_write(const q8kv_cache_t *cache, int64_t n, const void *k, const void *v, int32_t type,
                                int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
@@ -85,6 +85,7 @@ q8mv_status_t q8kv_cache_read(const q8kv_cache_t *cache, int64_t n, const int64_
  * outside the cache is skipped.  A later pair of the same request may read
  * what an earlier one wrote, as with the accepted nodes of a draft tree that
  * move up to follow their prefix; slots of different requests must not meet.
+ * batch <= 65535, path < 2^31.
  */
 q8mv_status_t q8kv_cache_move(const q8kv_cache_t *cache, int64_t batch, int64_t path, const int64_t *src,
                               const int64_t *dst, cudaStream_t stream);
@@ -142,7 +143,7 @@ typedef struct {
     float scale;
 } q8kv_attend_args_t;
 
-/* heads_q a multiple of heads_kv, at most max_requests requests and max_rows
+/* out and lse must not overlap the inputs or one another.  heads_q a multiple of heads_kv, at most max_requests requests and max_rows
  * rows in a call (max_requests <= 65536, max_rows <= 2^20).  device -1 = current. */
 q8mv_status_t q8kv_attend_plan(q8kv_attend_plan_t *out, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
                                int32_t max_requests, int64_t max_rows, int device);

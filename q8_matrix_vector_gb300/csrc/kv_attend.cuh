@@ -37,10 +37,13 @@
 // 8100 tokens 66.7 us (288 MB, 4.3 TB/s, 64 % of the copy rate), of 8000 tokens each
 // 108 us (82 %).  f32, two of 200001 .. 262143: 242 us (1.2 GB, 5.0 TB/s, 73 %; heads
 // apart in memory 80 %).  32 heads of one request of 511 tokens: 11.3 us.  Where the
-// cache is long, HBM and the issue of 940 instructions for a warp's 32 keys bound it
-// together: shared memory for two steps of keys leaves two CTAs, 8 warps, an SM, and
-// the tensor cores, that make the products, are idle most of the time.  Where it is
-// short, the chain lengths -> page -> keys -> join does, 8 us with no key at all.
+// cache is long, HBM and the latencies of 940 instructions for a warp's 32 keys bound
+// it together: shared memory for two steps of keys leaves two CTAs, 8 warps, an SM,
+// which issue in 0.44 of the cycles, and the tensor cores, that make the products, are
+// idle most of the time.  16 rows at a time are the same: 12 rows of 16 requests of 700
+// .. 4000 tokens 37 us (0.40, the tensor cores 13 %), 128 f32 rows 221 us (0.54, 32 %).
+// Where the cache is short, the chain lengths -> page -> keys -> join does, 8 us with no
+// key at all, and shares of one unit: the 511 tokens' 32 items are cut into 224 of them.
 #pragma once
 
 #include "kv_attend.h"

@@ -29,8 +29,8 @@
 // recorded in the plan's error word and the CTA leaves, once its MMAs have ended and
 // its parts of cut items are counted: the tickets are whole after every call.
 //
-// 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 86.6 us,
-// 241 TFLOP/s of the two products, 1.2 TB/s of cache.  A tile takes 5600 cycles, of
+// 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 87.3 us,
+// 239 TFLOP/s of the two products, 1.2 TB/s of cache.  A tile takes 5600 cycles, of
 // which the MMAs run 1400; turning its codes into operands bounds it, then 8 us until a
 // CTA's first scores are there and 10 us of joining cut items at the end.
 #pragma once

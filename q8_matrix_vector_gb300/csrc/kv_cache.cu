@@ -11,10 +11,13 @@
 // this one takes 38).
 //
 // 8190 tokens of 32 heads x 128, bf16: written in 37.7 us, read in 34.2 us (5.6 and
-// 6.1 TB/s, 82 and 90 % of the copy rate).  32768 tokens of 8 heads read: 35.0 us (5.9
-// TB/s).  64 requests' 9 rows of 256 heads moved: 29 us (85 MB, 2.9 TB/s: rows of
-// 128 and 16 bytes, 2 KB apart, of which DRAM moves 64 at a time; neither more blocks an
-// SM nor more rows in flight change it).  A few rows: 2.1, 2.5 and 3.5 us.
+// 6.1 TB/s, 82 and 90 % of the copy rate; a write issues in 0.73 of the cycles, 15
+// instructions an element).  32768 tokens of 8 heads read: 35.0 us (5.9 TB/s).  64
+// requests' 9 rows of 256 heads moved from anywhere to anywhere: 29 us (85 MB, 2.9 TB/s:
+// rows of 128 and 16 bytes, 2 KB apart, of which DRAM moves 64 at a time, which is 20
+// us; neither more blocks an SM nor more rows in flight change the rest, the loads'
+// latency), up a path as a verification leaves them 15 us.  A few rows: 2.1, 2.5 and 3.5
+// us.
 #include "kv_common.cuh"
 
 namespace kv {

@@ -23,9 +23,11 @@
 // once all of its CTAs are known to run; every CTA runs
 // the children's tests itself, on the same numbers, and reaches the same verdict.
 //
-// Vocabulary 128256, f32: 32 trees of 24 nodes, paths up to 9 rows, 56 us (49 MB
+// Vocabulary 128256, f32: 32 trees of 24 nodes, paths up to 9 rows, 57 us (49 MB
 // of visited rows, 13 % of the copy rate; 4.5 us a row of the longest path and the start); 2
-// chains of 6 with draft probabilities 23 us.
+// chains of 6 with draft probabilities 24 us, 8 trees of 24 with them 40 us.  Beyond 131072
+// tokens rows do not fit shared memory, none is brought early and part of each is read
+// twice: 32 trees at 151936 83 us, at 262144 112 us.
 //
 // A 64-bit conversion per logit runs at the few-per-cycle rate of the FP64 pipe
 // (4 us for an eighth of a 128256-token row).  The weight is split by two f32
