@@ -504,15 +504,18 @@ def version() -> int:
     return _lib.q8mv_version()
 
 
-# the Q8_0 key/value cache and its operators: torch is imported here, where they are first asked for
-_KV = ("Cache", "TreeAttention", "TreeVerify")
+# the key/value caches and their operators: torch is imported here, where they are first asked for
+_KV = {"kv": ("Cache", "TreeAttention", "TreeVerify"), "kv4": ("Cache4", "TreeAttention4"), "rotary": ("Rotary",),
+       "pages": ("Pages",)}
 
 
 def __getattr__(name):
-    if name in _KV:
-        from . import kv
+    for module, names in _KV.items():
+        if name in names:
+            from importlib import import_module
 
-        for n in _KV:
-            globals()[n] = getattr(kv, n)
-        return globals()[name]
+            found = import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -2,7 +2,8 @@
 
 Compiles the translation units under ``csrc/`` (``q8mv.cu``: the single-row
 kernels and the C ABI; ``batched.cu``: the batched kernel; ``pair.cu``: the
-feed-forward pair kernel; ``kv_*.cu``: the Q8_0 cache and its operators) in
+feed-forward pair kernel; ``kv_*.cu``: the Q8_0 cache, its operators and the pages
+of a cache; ``kv4_*.cu``: the Q4_0 cache; ``kvrope*.cu``: rotary positions) in
 parallel with nvcc and links them into ``libq8mv.so`` inside the package directory.  Run
 ``python -m q8_matrix_vector_gb300._build`` or call ``build_library()``;
 nothing here needs a GPU.
@@ -19,10 +20,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 UNITS = [os.path.join(CSRC, name) for name in
          ("q8mv.cu", "batched.cu", "pair.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_f32.cu", "kv_attend_f16.cu",
-          "kv_attend_bf16.cu", "kv_attend_tc.cu", "kv_verify.cu")]
+          "kv_attend_bf16.cu", "kv_attend_tc.cu", "kv_verify.cu", "kv4_cache.cu", "kv4_attend.cu", "kv4_attend_f32.cu",
+          "kv4_attend_f16.cu", "kv4_attend_bf16.cu", "kvrope.cu", "kvrope_4.cu", "kvrope_8.cu", "kv_pages.cu")]
 SRC = UNITS[0]
 HDR = os.path.join(ROOT, "include", "q8mv.h")
-HDRS = [HDR, os.path.join(ROOT, "include", "q8kv.h")]
+HDRS = [HDR] + [os.path.join(ROOT, "include", name) for name in ("q8kv.h", "q4kv.h", "kvrope.h", "kvpage.h")]
 LIB = os.path.join(PKG, "libq8mv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

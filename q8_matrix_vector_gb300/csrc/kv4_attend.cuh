@@ -1,0 +1,805 @@
+// Attention of draft trees over a paged Q4_0 cache (../../include/q4kv.h).
+//
+//     s[r, j] = scale * sum_b dK[j, b] * ( sum_{e in b} q[r, e] * (cK[j, e] - 8) )
+//     out[r, e] = sum_j P[r, j] * dV[j, b(e)] * (cV[j, e] - 8) / sum_j P[r, j],   P = exp(s - max)
+//
+// Work is cut and joined as in kv_attend.cuh: (request, kv head, 8 or 16 query rows)
+// items on one line of units, equal shares of it a CTA, parts joined by the last to
+// come.  A warp takes 32 keys of a tile of 128, keeps its own maximum, sum and
+// accumulators, and fills its own ring with cp.async.  The cache is the first operand
+// of mma.sync m16n8k16, 8 rows the second.  What four bits change:
+//   * A nibble where it lies in a half word is, as an f16's bits, c 2^-24 or 16 c 2^-24,
+//     exactly: `and` alone makes operands of two.  Nibbles 0 and 4, 1 and 5 of a word
+//     are pairs, and 2 and 6, 3 and 7 after one shift by 8: five instructions for eight
+//     elements.  The 16 of every second pair is taken off q's f16 beforehand, or in the
+//     output at the end; 2^-24 with the rows' factors.
+//   * The order of a row's bytes (q4kv.h) puts what a lane needs of all blocks in one
+//     load: of a key 4 NB bytes (8 elements of each block), of a value 2 NB (4 of each).
+//     Values of two keys are paired by one byte permute a word.
+//   * The 8 is not subtracted from codes.  Of the scores it is the accumulators' initial
+//     value, -8 times the block's sum of q.  Of the values it is a product of its own, a
+//     matrix of -8 (-128 where the codes carry 16) with the same weights, whose result is
+//     the accumulator that the codes' products start from: one more mma a block in place
+//     of eight subtractions.  A step's 32 keys are summed in it and added to the output in
+//     f32 with rounding, so that neither the 8s nor the tensor cores' cut sums pile up.
+// The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents.
+#pragma once
+
+#include "kv4_attend.h"
+#include "kv_attend.cuh"
+
+namespace kv {
+
+constexpr int kStages4 = 2;
+
+// Shared memory of one variant: NB stored blocks, NT tiles of 8 query rows, QP parts of q.
+template <int NB, int NT, int QP>
+struct Smem4 {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kCodes = 16 * NB;                       // of a row
+    static constexpr int kKPitch = NB == 8 ? kCodes + 16 : kCodes;  // 8: rows two apart would share banks
+    static constexpr int kScales = NB == 2 ? 4 : NB <= 4 ? 8 : 16;  // bytes of a row's scales
+    static constexpr int kStage = kStepKeys * (kKPitch + kCodes + 2 * kScales);
+    static constexpr int kRing = kStage * kStages4 * kWarps;
+    static constexpr int kJoinPitch = 32 * NB + 4;
+    static constexpr int kJoin = kWarps * 8 * kJoinPitch * 4;
+    static constexpr int kQPitch = 64 * NB + ((64 * NB) % 128 == 64 ? 0 : 64);
+    static constexpr int kQ = QP * kRows * kQPitch;
+    static constexpr int kBias = kRows * NB * 4;
+    static constexpr int kTotal = kRing + kJoin + kQ + kBias;
+    // where the 16-byte piece `c` of value row r is: spread so that the lanes of a load meet no bank twice
+    static __host__ __device__ constexpr int v_piece(int r, int c) {
+        return NB == 4 ? c ^ (r & 2) : NB == 8 ? c ^ ((r & 3) << 1) : c;
+    }
+};
+
+// 4 NB bytes of a key, or 2 NB of a value, of this lane
+template <int NB>
+__device__ __forceinline__ void load_key(const unsigned char *at, uint32_t (&w)[NB]) {
+    if constexpr (NB % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NB; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(at + 4 * i);
+            w[i] = x.x;
+            w[i + 1] = x.y;
+            w[i + 2] = x.z;
+            w[i + 3] = x.w;
+        }
+    } else if constexpr (NB % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < NB; i += 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(at + 4 * i);
+            w[i] = x.x;
+            w[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) w[i] = *reinterpret_cast<const uint32_t *>(at + 4 * i);
+    }
+}
+template <int NB>
+__device__ __forceinline__ void load_value(const unsigned char *at, uint32_t (&w)[(NB + 1) / 2]) {
+    if constexpr (NB == 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
+    } else if constexpr (NB == 4) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+    } else if constexpr (NB % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) w[i] = *reinterpret_cast<const uint32_t *>(at + 4 * i);
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(at);
+#pragma unroll
+        for (int i = 0; i < (NB + 1) / 2; ++i)
+            w[i] = h[2 * i] | (2 * i + 1 < NB ? static_cast<uint32_t>(h[2 * i + 1]) << 16 : 0u);
+    }
+}
+
+// scales of one key, two a word
+template <int NB>
+__device__ __forceinline__ void load_scales4(const unsigned char *at, uint32_t (&w)[(NB + 1) / 2]) {
+    if constexpr (NB > 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        if constexpr (NB == 8) w[3] = x.w;
+    } else if constexpr (NB > 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(at);
+    }
+}
+__device__ __forceinline__ float scale_of(uint32_t w, int b) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    return b & 1 ? __high2float(h) : __low2float(h);
+}
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Exponent E for scales whose greatest magnitude is the f16 of these 15 bits: 2^(E + 14) is above it.  (A subnormal
+// counts as 2^-14; an infinity or NaN as any: what sees it is NaN.)
+__device__ __forceinline__ float exponent_of(uint32_t bits) {
+    return static_cast<float>(max(static_cast<int>(bits >> 10), 1) - 15 + 1 - 14);
+}
+
+template <typename T, int NB, int NT, int QP, int PP>
+__global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 ? 3 : 2)
+    q4kv_attend_kernel(const Attend4Params pp) {
+    using S = Smem4<NB, NT, QP>;
+    constexpr int ROWS = S::kRows, KEYS = kStepKeys * kWarps, W = (NB + 1) / 2;
+    const AttendParams &p = pp.a;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int64_t scan_units[kWarps], scan_items[kWarps];
+    __shared__ int64_t start_b, start_item, start_unit;
+    __shared__ float row_mul[ROWS];
+    __shared__ int is_last;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, c = lane & 3;
+    float *jo = reinterpret_cast<float *>(smem + S::kRing);  // [warp][8 rows][kJoinPitch]
+    unsigned char *q_sm = smem + S::kRing + S::kJoin;
+    float *bias_sm = reinterpret_cast<float *>(q_sm + S::kQ);  // [row / 2][block][row % 2]
+
+    // ---- the CTA's share of the line of units (kv_attend.cuh)
+    Split split;
+    int64_t u, u_end;
+    Place w;
+    {
+        const int per = (p.requests + kWarps * 32 - 1) / (kWarps * 32);
+        const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
+        int64_t units = 0, items = 0;
+        for (int b = b0; b < b1; ++b) {
+            load_request<ROWS, KEYS>(p, b, w);
+            units += units_of<1>(p, w);
+            items += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+        }
+        int64_t iu = units, ii = items;  // inclusive over the warp
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t a = __shfl_up_sync(~0u, iu, d), b = __shfl_up_sync(~0u, ii, d);
+            if (lane >= d) {
+                iu += a;
+                ii += b;
+            }
+        }
+        if (lane == 31) {
+            scan_units[warp] = iu;
+            scan_items[warp] = ii;
+        }
+        __syncthreads();
+        int64_t total = 0, before_u = 0, before_i = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) {
+                before_u += scan_units[i];
+                before_i += scan_items[i];
+            }
+            total += scan_units[i];
+        }
+        if (total == 0) return;
+        split.units = total;
+        split.ctas = min(static_cast<int64_t>(gridDim.x), total);
+        if (blockIdx.x >= split.ctas) return;
+        u = split.begin(blockIdx.x);
+        u_end = split.begin(blockIdx.x + 1);
+        before_u += iu - units;
+        before_i += ii - items;
+        if (u >= before_u && u < before_u + units) {  // exactly one thread
+            int b = b0;
+            for (; b < b1; ++b) {
+                load_request<ROWS, KEYS>(p, b, w);
+                const int64_t n = units_of<1>(p, w);
+                if (u < before_u + n) break;
+                before_u += n;
+                before_i += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+            }
+            start_b = b;
+            start_unit = before_u;
+            start_item = before_i;
+        }
+        __syncthreads();
+        load_request<ROWS, KEYS>(p, static_cast<int>(start_b), w);
+        const int64_t k = (u - start_unit) / (w.tiles_k + kItemUnits);  // item within the request
+        w.h = static_cast<int>(k / w.tiles_r);
+        w.rt = static_cast<int>(k - static_cast<int64_t>(w.h) * w.tiles_r);
+        w.item = start_item + k;
+        w.first = start_unit + k * (w.tiles_k + kItemUnits) + kItemUnits;
+    }
+    auto advance = [&](Place &x) {
+        x.first += x.tiles_k + kItemUnits;
+        ++x.item;
+        if (++x.rt == x.tiles_r) {
+            x.rt = 0;
+            if (++x.h == p.c.heads) {
+                x.h = 0;
+                do load_request<ROWS, KEYS>(p, x.b + 1, x);
+                while (x.tiles_r == 0);
+            }
+        }
+    };
+
+    // ---- the warp's ring: a stage takes 32 keys, K codes, V codes, K scales, V scales
+    unsigned char *ring = smem + warp * (S::kStage * kStages4);
+    for (int i = lane; i < S::kStage * kStages4 / 16; i += 32) reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    auto issue = [&](bool any, int slot, uint32_t row) {
+        if (any) {
+            unsigned char *st = ring + slot * S::kStage;
+            const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(st));
+            const uint32_t sv = sk + kStepKeys * S::kKPitch;
+            const uint32_t ss = sv + kStepKeys * S::kCodes;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                // 32 pieces of 16 bytes at a time, NB a key
+                const int i = lane + 32 * j, key = i / NB, piece = i % NB;
+                const uint32_t r = __shfl_sync(~0u, row, key);
+                if (r != kNoRow) {
+                    const uint64_t from = static_cast<uint64_t>(r) * S::kCodes + piece * 16;
+                    cp_async16(sk + key * S::kKPitch + piece * 16, p.c.k_codes + from);
+                    cp_async16(sv + key * S::kCodes + S::v_piece(key, piece) * 16, p.c.v_codes + from);
+                }
+            }
+            const uint32_t dk = ss + lane * S::kScales, dv = dk + kStepKeys * S::kScales;
+            if (row != kNoRow) {
+                const char *ks = reinterpret_cast<const char *>(p.c.k_scales) + static_cast<uint64_t>(row) * S::kScales;
+                const char *vs = reinterpret_cast<const char *>(p.c.v_scales) + static_cast<uint64_t>(row) * S::kScales;
+                if constexpr (S::kScales == 16) {
+                    cp_async16(dk, ks);
+                    cp_async16(dv, vs);
+                } else if constexpr (S::kScales == 8) {
+                    cp_async8(dk, ks);
+                    cp_async8(dv, vs);
+                } else {
+                    cp_async4(dk, ks);
+                    cp_async4(dv, vs);
+                }
+            } else {
+                // an absent key has scales of 0: whatever codes the ring holds, it adds nothing
+#pragma unroll
+                for (int i = 0; i < S::kScales; i += 4) {
+                    *reinterpret_cast<uint32_t *>(st + (dk - sk) + i) = 0u;
+                    *reinterpret_cast<uint32_t *>(st + (dv - sk) + i) = 0u;
+                }
+            }
+        }
+        cp_commit();
+    };
+
+    // What a CTA does of one item: key tiles kt0 .. kt1 - 1, one step of the warp in each.
+    struct Work {
+        int64_t kt0, kt1;
+        int base0, n_steps, keys, h;
+        const int32_t *table;
+    };
+    auto work_of = [&](const Place &x) -> Work {
+        Work k;
+        k.kt0 = max(u, x.first) - x.first;
+        k.kt1 = max(min(u_end, x.first + x.tiles_k) - x.first, k.kt0);
+        k.base0 = static_cast<int>(k.kt0) * KEYS + warp * kStepKeys;
+        k.n_steps = static_cast<int>(k.kt1 - k.kt0);
+        k.keys = static_cast<int>(min(static_cast<int64_t>(x.prefix) + x.nodes,
+                                      static_cast<int64_t>(p.table_cols) * p.c.page_size));
+        k.h = x.h;
+        k.table = p.table + static_cast<int64_t>(x.b) * p.table_row;
+        return k;
+    };
+    // row number of the lane's key of step i, or kNoRow
+    auto find = [&](const Work &k, int i) -> uint32_t {
+        const int pos = k.base0 + i * KEYS + lane;
+        if (i >= k.n_steps || pos >= k.keys) return kNoRow;
+        const uint32_t col = (__umulhi(pos, p.page_mul) + pos) >> p.page_shift;  // pos / page_size
+        const int page = __ldg(k.table + col);
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
+        return static_cast<uint32_t>(row_of(p.c, page, k.h, pos - static_cast<int>(col) * p.c.page_size));
+    };
+    uint32_t row_cur[kStages4];  // rows of the steps in the ring: their lanes' keys are there
+    uint32_t row_next;
+    int slot0 = 0;  // stage of the item's first step
+    auto begin = [&](const Work &k) {
+#pragma unroll
+        for (int i = 0; i < kStages4 - 1; ++i) {
+            row_cur[i] = find(k, i);
+            issue(i < k.n_steps, (slot0 + i) % kStages4, row_cur[i]);
+        }
+        row_next = find(k, kStages4 - 1);
+    };
+    // Row g of an octet of the operands is place (g & 1) * 4 + g / 2 of eight keys, so that the four keys 2c, 2c + 1 of a
+    // lane's values, over c, are neighbours in shared memory.
+    const int place = (g & 1) * 4 + (g >> 1);
+
+    Work k = work_of(w);
+    begin(k);
+    bool first_item = true;  // that has tiles here
+    for (;;) {
+        const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
+        if (k.n_steps > 0) {
+            // ---- q rows to shared memory: a power of two per row, then f16 parts.  16 threads a row: a thread's elements
+            // are pairs e, e + 4 of one word, as the operands have them
+            for (int rr = tid >> 3; rr < ROWS; rr += kWarps * 4) {
+                const int l8 = tid & 7;
+                const int idx = w.rt * ROWS + rr, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
+                const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
+                float x[4 * NB];
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i) {
+                    const int e = l8 + 8 * i;
+                    x[i] = rr < rows && e < pp.dim ? to_f32(src[e]) : 0.0f;
+                    top = fmaxf(top, fabsf(x[i]));
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13, -100), 100);
+                // 2^-ex, and the sign of the scale, so that the rows' factors are positive
+                const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - ex) << 23), p.scale_log2);
+                // element l8 of each word of 8: its nibble is pair l8 % 4, half l8 / 4; odd pairs carry 16
+                const float part16 = l8 & 1 ? 0.0625f : 1.0f, times16 = l8 & 1 ? 16.0f : 1.0f;
+                float sum[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) sum[b] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i) {
+                    const float y = x[i] * down * part16;
+                    const __half hi = __float2half_rn(y);
+                    __half *dst = reinterpret_cast<__half *>(q_sm + rr * S::kQPitch) + 8 * i + 2 * (l8 & 3) + (l8 >> 2);
+                    *dst = hi;
+                    float used = __half2float(hi);
+                    if constexpr (QP == 2) {
+                        const __half lo = __float2half_rn(y - used);
+                        dst[ROWS * S::kQPitch / 2] = lo;
+                        used += __half2float(lo);
+                    }
+                    sum[i / 4] += used * times16;
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int d = 1; d < 8; d *= 2) sum[b] += __shfl_xor_sync(~0u, sum[b], d);
+                    if (l8 == 0) bias_sm[((rr >> 1) * NB + b) * 2 + (rr & 1)] = -8.0f / 16777216.0f * sum[b];
+                }
+                // not 0: a score of -inf has to stay that
+                if (l8 == 0)
+                    row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex + 24) << 23) * fabsf(p.scale_log2), 1e-37f);
+            }
+            __syncthreads();
+
+            float o[NT][NB * 2][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < NB * 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[t][i][j] = 0.0f;
+            // of rows 8 t + 2c and 8 t + 2c + 1; m: running maximum (log2) plus E
+            float m[NT][2], l[NT][2], mul[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    m[t][r] = -INFINITY;
+                    l[t][r] = 0.0f;
+                    mul[t][r] = row_mul[8 * t + 2 * c + r];
+                }
+
+            int slot = slot0;
+            for (int i = 0; i < k.n_steps; ++i) {
+                // row_cur[0] is step i's; the next free stage takes step i + kStages4 - 1
+                row_cur[kStages4 - 1] = row_next;
+                issue(i + kStages4 - 1 < k.n_steps, slot == 0 ? kStages4 - 1 : slot - 1, row_next);
+                row_next = find(k, i + kStages4);
+                cp_wait<kStages4 - 1>();
+                __syncwarp();
+                const unsigned char *sk = ring + slot * S::kStage, *sv = sk + kStepKeys * S::kKPitch;
+                const unsigned char *ks = sv + kStepKeys * S::kCodes, *vs = ks + kStepKeys * S::kScales;
+                const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow);
+                const int base = k.base0 + i * KEYS;
+                if (there != 0) {
+                    // 2^(E + 14) is above the scales of the lane's key, and of all keys
+                    uint32_t top_bits = 0;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        top_bits = max(top_bits, reinterpret_cast<const uint16_t *>(vs + lane * S::kScales)[b] & 0x7FFFu);
+                    const float e_key = exponent_of(top_bits), e_all = exponent_of(__reduce_max_sync(~0u, top_bits));
+
+                    // ---- scores: s[t][2 j + k][r] of key 16 j + 8 k + place and row 8 t + 2c + r
+                    float s[NT][4][2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t d0[W], d1[W];
+                        load_scales4<NB>(ks + (16 * j + place) * S::kScales, d0);
+                        load_scales4<NB>(ks + (16 * j + 8 + place) * S::kScales, d1);
+                        uint32_t x[NB], y[NB];
+                        load_key<NB>(sk + (16 * j + place) * S::kKPitch + c * (4 * NB), x);
+                        load_key<NB>(sk + (16 * j + 8 + place) * S::kKPitch + c * (4 * NB), y);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) s[t][2 * j][r] = s[t][2 * j + 1][r] = 0.0f;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const uint32_t xs = x[b] >> 8, ys = y[b] >> 8;
+                            const uint32_t a0[4] = {x[b] & 0x000F000Fu, y[b] & 0x000F000Fu, x[b] & 0x00F000F0u, y[b] & 0x00F000F0u};
+                            const uint32_t a1[4] = {xs & 0x000F000Fu, ys & 0x000F000Fu, xs & 0x00F000F0u, ys & 0x00F000F0u};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const float2 z = *reinterpret_cast<const float2 *>(bias_sm + ((4 * t + c) * NB + b) * 2);
+                                float part[4] = {z.x, z.y, z.x, z.y};
+#pragma unroll
+                                for (int q = 0; q < QP; ++q) {
+                                    const uint4 qq = *reinterpret_cast<const uint4 *>(
+                                        q_sm + (q * ROWS + 8 * t + g) * S::kQPitch + b * 64 + c * 16);
+                                    mma_f16(part, a0, qq.x, qq.y, part);
+                                    mma_f16(part, a1, qq.z, qq.w, part);
+                                }
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    s[t][2 * j][r] = fmaf(part[r], scale_of(d0[b / 2], b), s[t][2 * j][r]);
+                                    s[t][2 * j + 1][r] = fmaf(part[2 + r], scale_of(d1[b / 2], b), s[t][2 * j + 1][r]);
+                                }
+                            }
+                        }
+                    }
+                    // ---- softmax
+                    const bool drafts = base + kStepKeys > w.prefix;
+                    const bool partial = drafts || there != ~0u;
+                    bool moved = false;
+                    float z[NT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float top[2];
+                        if (partial) {
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                uint32_t see = there;
+                                if (drafts)
+                                    see &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
+                                                w.rt * ROWS + 8 * t + 2 * c + r);
+                                top[r] = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int key = 8 * k + place;
+                                    if (((see >> key) & 1u) == 0) s[t][k][r] = -INFINITY;
+                                    // a row's E comes from keys that it sees, so that no other's scale matters
+                                    top[r] = fmaxf(top[r], fmaf(s[t][k][r], mul[t][r], __shfl_sync(~0u, e_key, key)));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                top[r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
+                            const float n = fmaxf(m[t][r], top[r]);
+                            moved |= n != m[t][r];
+                            z[t][r] = n;
+                        }
+                    }
+                    if (__any_sync(~0u, moved)) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            float f[2];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                f[r] = ex2(m[t][r] - (z[t][r] == -INFINITY ? 0.0f : z[t][r]));
+                                m[t][r] = z[t][r];
+                                l[t][r] *= f[r];
+                            }
+#pragma unroll
+                            for (int k = 0; k < NB * 2; ++k) {
+                                o[t][k][0] *= f[0];
+                                o[t][k][1] *= f[1];
+                                o[t][k][2] *= f[0];
+                                o[t][k][3] *= f[1];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float n = z[t][r] == -INFINITY ? 0.0f : -z[t][r];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                s[t][k][r] = ex2(fmaf(s[t][k][r], mul[t][r], n));
+                                l[t][r] += s[t][k][r];
+                            }
+                        }
+                    // ---- O^T += V^T (P dV)^T, two blocks at a time (a word's halves), 16 keys at a time
+                    uint32_t dv[4][W];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) load_scales4<NB>(vs + (8 * k + place) * S::kScales, dv[k]);
+                    // the lane's keys 16 j + {2c, 2c + 1, 8 + 2c, 8 + 2c + 1}: places c, 4 + c, 8 + c, 12 + c
+                    uint32_t v[2][4][W];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const int r = 16 * j + 4 * n + c;
+                            load_value<NB>(sv + r * S::kCodes + S::v_piece(r, g * NB / 8) * 16 + g * (2 * NB) % 16, v[j][n]);
+                        }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        uint32_t wgt[2][NT][PP][2];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float d = scale_of(dv[k][b / 2], b);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const float(&pr)[2] = s[t][k];
+                                float x0 = pr[0] * d, x1 = pr[1] * d;
+                                if (partial) {
+                                    // a key that the row does not see keeps weight 0 whatever its scale is
+                                    x0 = pr[0] == 0.0f ? 0.0f : x0;
+                                    x1 = pr[1] == 0.0f ? 0.0f : x1;
+                                }
+                                const uint32_t h = pack_half2(x0, x1);
+                                wgt[k >> 1][t][0][k & 1] = transpose8(h);
+                                if constexpr (PP == 2) {
+                                    const float2 back = unpack_half2(h);
+                                    wgt[k >> 1][t][PP - 1][k & 1] = transpose8(pack_half2(x0 - back.x, x1 - back.y));
+                                }
+                            }
+                        }
+                        // -8 2^-24 and -128 2^-24 times the weights, then the codes
+                        float acc[NT][2][4];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const uint32_t eight[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
+                            float off[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int q = 0; q < PP; ++q) mma_f16(off, eight, wgt[j][t][q][0], wgt[j][t][q][1], off);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) acc[t][0][k] = acc[t][1][k] = off[k];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
+                            const uint32_t x = __byte_perm(v[j][0][b / 2], v[j][1][b / 2], sel);
+                            const uint32_t y = __byte_perm(v[j][2][b / 2], v[j][3][b / 2], sel);
+                            const uint32_t xs = x >> 8, ys = y >> 8;
+                            const uint32_t a0[4] = {x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u};
+                            const uint32_t a1[4] = {xs & 0x000F000Fu, xs & 0x00F000F0u, ys & 0x000F000Fu, ys & 0x00F000F0u};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int q = 0; q < PP; ++q) {
+                                    mma_f16(acc[t][0], a0, wgt[j][t][q][0], wgt[j][t][q][1], acc[t][0]);
+                                    mma_f16(acc[t][1], a1, wgt[j][t][q][0], wgt[j][t][q][1], acc[t][1]);
+                                }
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) o[t][2 * b + e][k] += acc[t][e][k];
+                    }
+                }
+                __syncwarp();
+                slot = slot + 1 == kStages4 ? 0 : slot + 1;
+#pragma unroll
+                for (int j = 0; j + 1 < kStages4; ++j) row_cur[j] = row_cur[j + 1];
+            }
+            slot0 = slot;
+            // ---- the next item's first keys are on their way while the warps of this one are joined
+            const Place done = w;
+            const Work did = k;
+            const bool more = w.first + w.tiles_k < u_end;
+            if (more) {
+                advance(w);
+                k = work_of(w);
+                begin(k);
+            }
+            const bool whole = did.kt0 == 0 && did.kt1 == done.tiles_k;
+            const int pitch = pp.dim + kPartExtra;
+            const int64_t slot_p = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
+            first_item = false;
+            // tile t, row r8 of the item's results: its output row and query head
+            auto place_row = [&](int t, int r8, int64_t *row, int *hq) -> bool {
+                const int r = 8 * t + r8;
+                const int idx = done.rt * ROWS + r, node = idx / p.group;
+                *row = static_cast<int64_t>(done.row0) + node;
+                *hq = done.h * p.group + idx - node * p.group;
+                return r < rows;
+            };
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t > 0) __syncthreads();
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float *at = jo + (warp * 8 + 2 * c + r) * S::kJoinPitch;
+                    // elements 4 g + {0 .. 3} of each block, in units of 2^-24, 16 in the odd ones
+                    constexpr float one = 16777216.0f, sixteen = 1048576.0f;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        *reinterpret_cast<float4 *>(at + 32 * b + 4 * g) =
+                            make_float4(o[t][2 * b][r] * one, o[t][2 * b][2 + r] * sixteen, o[t][2 * b + 1][r] * one,
+                                        o[t][2 * b + 1][2 + r] * sixteen);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) l[t][r] += __shfl_xor_sync(~0u, l[t][r], d);
+                    if (g == 0) {
+                        at[32 * NB] = m[t][r];
+                        at[32 * NB + 1] = l[t][r];
+                    }
+                }
+                __syncthreads();
+                // kWarps * 4 threads a row
+                constexpr int TPR = kWarps * 4;
+                const int r8 = tid / TPR, lr = tid % TPR;
+                float f[kWarps], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) top = fmaxf(top, jo[(q * 8 + r8) * S::kJoinPitch + 32 * NB]);
+                const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) {
+                    const float *x = jo + (q * 8 + r8) * S::kJoinPitch;
+                    f[q] = ex2(x[32 * NB] - z);
+                    sum = fmaf(f[q], x[32 * NB + 1], sum);
+                }
+                int64_t row;
+                int hq;
+                if (place_row(t, r8, &row, &hq)) {
+                    T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                    float *part = p.partial + (slot_p * ROWS + 8 * t + r8) * pitch;
+                    const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
+#pragma unroll
+                    for (int q = 0; q < 32 * NB / TPR; ++q) {
+                        const int e = lr + TPR * q;
+                        if (e < pp.dim) {
+                            float x = 0.0f;
+#pragma unroll
+                            for (int v = 0; v < kWarps; ++v) x = fmaf(f[v], jo[(v * 8 + r8) * S::kJoinPitch + e], x);
+                            if (whole)
+                                out[e] = from_f32<T>(x * inv);
+                            else
+                                part[e] = x;
+                        }
+                    }
+                    if (lr == 0) {
+                        if (!whole) {
+                            part[pp.dim] = top;
+                            part[pp.dim + 1] = sum;
+                        } else if (p.lse) {
+                            p.lse[row * p.heads_q + hq] = (z + log2f(sum)) * 0.693147180559945f;
+                        }
+                    }
+                }
+            }
+            // (an item past the tickets exists only if `starts` is not ascending: it has no output)
+            if (!whole && done.item < p.tickets_n) {
+                constexpr int TPR = kWarps * 32 / ROWS, V = (8 * NB + TPR - 1) / TPR;  // threads a row, float4 a thread
+                const int pr = tid / TPR, lr = tid % TPR;
+                int64_t row;
+                int hq;
+                const bool live = place_row(pr / 8, pr % 8, &row, &hq);
+                // Adds n parts, the first at slot `head`, the i-th at slot `at + i * step`: to the output, or to the
+                // first part's place.
+                auto join = [&](int n, int64_t head, int64_t at, int64_t step, bool last) {
+                    const float *from = p.partial + (at * ROWS + pr) * pitch, *from0 = p.partial + (head * ROWS + pr) * pitch;
+                    step *= ROWS * pitch;
+                    float top = -INFINITY, sum = 0.0f, x[V][4];
+#pragma unroll
+                    for (int q = 0; q < V; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[q][e] = 0.0f;
+                    if (live) {
+                        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg((i == 0 ? from0 : from + i * step) + pp.dim));
+                        const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll (V <= 2 ? 8 : 4)
+                        for (int i = 0; i < n; ++i) {
+                            const float *part = i == 0 ? from0 : from + i * step;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + pp.dim));
+                            const float f = ex2(ml.x - z);
+                            sum = fmaf(f, ml.y, sum);
+#pragma unroll
+                            for (int q = 0; q < V; ++q) {
+                                const int e0 = 4 * (lr + TPR * q);
+                                if (e0 < pp.dim) {
+                                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + e0));
+                                    x[q][0] = fmaf(f, y.x, x[q][0]);
+                                    x[q][1] = fmaf(f, y.y, x[q][1]);
+                                    x[q][2] = fmaf(f, y.z, x[q][2]);
+                                    x[q][3] = fmaf(f, y.w, x[q][3]);
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();  // a row's threads have read the first part
+                    if (live && last) {
+                        const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+#pragma unroll
+                        for (int q = 0; q < V; ++q)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (4 * (lr + TPR * q) < pp.dim) out[4 * (lr + TPR * q) + e] = from_f32<T>(x[q][e] * inv);
+                        if (lr == 0 && p.lse)
+                            p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
+                    } else if (live) {
+                        float *to = p.partial + (head * ROWS + pr) * pitch;
+#pragma unroll
+                        for (int q = 0; q < V; ++q)
+                            if (4 * (lr + TPR * q) < pp.dim)
+                                *reinterpret_cast<float4 *>(to + 4 * (lr + TPR * q)) = make_float4(x[q][0], x[q][1], x[q][2], x[q][3]);
+                        if (lr == 0) {
+                            to[pp.dim] = top;
+                            to[pp.dim + 1] = sum;
+                        }
+                    }
+                };
+                // true in the CTA that is the last of n to come
+                auto arrive = [&](unsigned *ticket, unsigned n) -> bool {
+                    __threadfence();
+                    __syncthreads();
+                    if (tid == 0) {
+                        const unsigned t = atomicAdd(ticket, 1u);
+                        is_last = t == n - 1;
+                        if (is_last) *ticket = 0;
+                    }
+                    __syncthreads();
+                    const bool yes = is_last;
+                    if (yes) __threadfence();
+                    return yes;
+                };
+                // Parts c0 .. c1, up to kJoinGroup at once, more in two levels (kv_attend.cuh)
+                const int c0 = static_cast<int>(split.owner(done.first)), c1 = static_cast<int>(split.owner(done.first + done.tiles_k - 1));
+                const int slot_c0 = split.begin(c0) >= done.first - kItemUnits ? 2 * c0 : 2 * c0 + 1;
+                if (c1 - c0 < kJoinGroup) {
+                    if (arrive(p.tickets + done.item, c1 - c0 + 1)) join(c1 - c0 + 1, slot_c0, 2 * c0, 2, true);
+                } else {
+                    const int grp = blockIdx.x / kJoinGroup, g0 = c0 / kJoinGroup, g1 = c1 / kJoinGroup;
+                    const int lo = max(c0, grp * kJoinGroup), hi = min(c1, grp * kJoinGroup + kJoinGroup - 1);
+                    // one item may come into a group from its left, and one may begin in it and leave it
+                    if (arrive(p.group_tickets + 2 * grp + (c0 < grp * kJoinGroup ? 0 : 1), hi - lo + 1)) {
+                        join(hi - lo + 1, lo == c0 ? slot_c0 : 2 * lo, 2 * lo, 2, false);
+                        if (arrive(p.tickets + done.item, g1 - g0 + 1))
+                            join(g1 - g0 + 1, slot_c0, 2 * kJoinGroup * g0, 2 * kJoinGroup, true);
+                    }
+                }
+            }
+            if (!more) break;
+        } else {
+            // only units of the item's fixed cost are here
+            if (w.first + w.tiles_k >= u_end) break;
+            advance(w);
+            k = work_of(w);
+            begin(k);
+        }
+        __syncthreads();  // the join's reads, before the next item's q
+    }
+}
+
+template <typename T, int NB, int NT, int QP, int PP>
+Attend4Variant attend4_variant_of() {
+    return {q4kv_attend_kernel<T, NB, NT, QP, PP>, Smem4<NB, NT, QP>::kTotal, 8 * NT};
+}
+
+template <typename T, int QP, int PP>
+Attend4Variant attend4_variant_of(int blocks, Attend4Shape shape) {
+    const bool wide = shape == k4Rows16;
+    switch (blocks) {
+        case 2: return wide ? attend4_variant_of<T, 2, 2, QP, PP>() : attend4_variant_of<T, 2, 1, QP, PP>();
+        case 3: return wide ? attend4_variant_of<T, 3, 2, QP, PP>() : attend4_variant_of<T, 3, 1, QP, PP>();
+        case 4: return wide ? attend4_variant_of<T, 4, 2, QP, PP>() : attend4_variant_of<T, 4, 1, QP, PP>();
+        case 6: return wide ? Attend4Variant{} : attend4_variant_of<T, 6, 1, QP, PP>();
+        case 8: return wide ? Attend4Variant{} : attend4_variant_of<T, 8, 1, QP, PP>();
+        default: return {};
+    }
+}
+
+}  // namespace kv

@@ -18,6 +18,7 @@
 // us; neither more blocks an SM nor more rows in flight change the rest, the loads'
 // latency), up a path as a verification leaves them 15 us.  A few rows: 2.1, 2.5 and 3.5
 // us.
+#include "kv4.h"
 #include "kv_common.cuh"
 
 namespace kv {
@@ -356,24 +357,6 @@ __global__ void __launch_bounds__(256, 3) q8kv_move_kernel(const MoveParams p) {
     }
 }
 
-// Threads of one token along x (a multiple of 32, at most 256), tokens along y.
-// `tokens` tokens a thread once that leaves several blocks an SM, else one.
-struct Shape {
-    dim3 grid, block;
-    bool many;
-};
-
-Shape shape(int lanes, int64_t n, int tokens) {
-    const unsigned x = lanes >= 256 ? 256u : static_cast<unsigned>((lanes + 31) / 32 * 32);
-    const unsigned y = 256u / x;
-    Shape s;
-    s.block = dim3(x, y);
-    const int64_t across = ceil_div(lanes, x);
-    s.many = ceil_div(n, tokens * y) * across >= kManyBlocks;
-    s.grid = dim3(static_cast<unsigned>(ceil_div(n, s.many ? tokens * y : y)), static_cast<unsigned>(across));
-    return s;
-}
-
 template <typename T>
 void launch_write(const IoParams &p, bool vec, const Shape &s, cudaStream_t stream) {
     if (!vec)
@@ -392,9 +375,39 @@ void launch_read(const IoParams &p, const Shape &s, cudaStream_t stream) {
         q8kv_read_kernel<T, 1><<<s.grid, s.block, 0, stream>>>(p);
 }
 
+}  // namespace
+
 bool valid_stride(int64_t s) { return s >= 0 && s < (1LL << 40); }
 
-}  // namespace
+Shape shape(int lanes, int64_t n, int tokens) {
+    const unsigned x = lanes >= 256 ? 256u : static_cast<unsigned>((lanes + 31) / 32 * 32);
+    const unsigned y = 256u / x;
+    Shape s;
+    s.block = dim3(x, y);
+    const int64_t across = ceil_div(lanes, x);
+    s.many = ceil_div(n, tokens * y) * across >= kManyBlocks;
+    s.grid = dim3(static_cast<unsigned>(ceil_div(n, s.many ? tokens * y : y)), static_cast<unsigned>(across));
+    return s;
+}
+
+q8mv_status_t cache_move(const Cache &c, int64_t batch, int64_t path, const int64_t *src, const int64_t *dst,
+                         cudaStream_t stream) {
+    if (batch < 0 || batch > 65535 || path < 0 || path >= (1LL << 31)) return Q8MV_ERR_INVALID_ARG;
+    if (batch == 0 || path == 0 || c.slots == 0) return Q8MV_OK;
+    if (!src || !dst || !aligned(src, 8) || !aligned(dst, 8)) return Q8MV_ERR_INVALID_ARG;
+    MoveParams p = {};
+    p.c = c;
+    p.src = src;
+    p.dst = dst;
+    p.path = static_cast<int>(path);
+    p.scale_pieces = c.blocks % 4 == 0 ? c.blocks / 4 : c.blocks;
+    p.lanes = c.heads * 2 * (c.dim / 16 + p.scale_pieces);
+    const int threads = p.lanes >= 256 ? 256 : (p.lanes + 31) / 32 * 32;
+    q8kv_move_kernel<<<dim3(static_cast<unsigned>(ceil_div(p.lanes, threads)), static_cast<unsigned>(batch)), threads, 0,
+                       stream>>>(p);
+    return q8i::cuda_status(cudaGetLastError());
+}
+
 
 q8mv_status_t DeviceScope::enter(int device) {
     q8mv_status_t st = q8i::cuda_status(cudaGetDevice(&prev_));
@@ -481,20 +494,9 @@ q8mv_status_t q8kv_cache_read(const q8kv_cache_t *cache, int64_t n, const int64_
 
 q8mv_status_t q8kv_cache_move(const q8kv_cache_t *cache, int64_t batch, int64_t path, const int64_t *src,
                               const int64_t *dst, cudaStream_t stream) {
-    kv::MoveParams p = {};
-    if (!kv::make_cache(cache, &p.c) || batch < 0 || batch > 65535 || path < 0 || path >= (1LL << 31))
-        return Q8MV_ERR_INVALID_ARG;
-    if (batch == 0 || path == 0 || p.c.slots == 0) return Q8MV_OK;
-    if (!src || !dst || !kv::aligned(src, 8) || !kv::aligned(dst, 8)) return Q8MV_ERR_INVALID_ARG;
-    p.src = src;
-    p.dst = dst;
-    p.path = static_cast<int>(path);
-    p.scale_pieces = p.c.blocks % 4 == 0 ? p.c.blocks / 4 : p.c.blocks;
-    p.lanes = p.c.heads * 2 * (p.c.dim / 16 + p.scale_pieces);
-    const int threads = p.lanes >= 256 ? 256 : (p.lanes + 31) / 32 * 32;
-    kv::q8kv_move_kernel<<<dim3(static_cast<unsigned>(kv::ceil_div(p.lanes, threads)), static_cast<unsigned>(batch)),
-                           threads, 0, stream>>>(p);
-    return q8i::cuda_status(cudaGetLastError());
+    kv::Cache c;
+    if (!kv::make_cache(cache, &c)) return Q8MV_ERR_INVALID_ARG;
+    return kv::cache_move(c, batch, path, src, dst, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,469 @@
+// Storing keys and values in the Q4_0 cache, and rotating q and k with it: one
+// kernel for q4kv_cache_write, kvrope_apply and kvrope_write_q8 / _q4
+// (../../include/q4kv.h, kvrope.h).
+//
+// As q8kv_write_kernel (kv_cache.cu): a lane takes 16 bytes of the wide side, a
+// 32-element block is 4 or 8 neighbouring lanes, keys and values of the same place
+// are the same lane's, and a block's maximum takes 2 or 3 shuffles.  HBM bounds a
+// prompt, next to the issue slots; one round trip a few rows.
+//   * 4 bits.  The largest of x and of -x, the signed extreme is the greater one;
+//     16-bit types are compared in pairs.  x / d + 8 is left, rounded to even, in the
+//     low bits of its sum with 1.5 * 2^23 + 8; eight codes are put together by
+//     multiply-adds of those words, whose exponents' sum is a constant to take off.
+//   * Rotation.  The cosines and sines of a block's tokens are worked out once, by all
+//     its threads, into shared memory, for all heads.  p * turns modulo 2^64 is the
+//     angle to the last bit at any position.  Its top 8 bits pick one of 256 points of
+//     the circle, kept as two f32 each; the rest, below pi / 256, is a two-term f32 number,
+//     and sin r = r - r^3/6 + r^5/120, cos r - 1 = -r^2/2 + r^4/24 have terms so small
+//     that f32 is enough; the angles' sum adds up to 2^-35.  The rounding to f32 is then
+//     as good as always that of the exact value, so that rotated keys get the codes that
+//     a program in 64 bits gives them.
+//     For q a lane takes both halves of its pairs, so that q may be rotated in place;
+//     k's other half is read by the lane that needs it (it is in L1).
+#pragma once
+
+#include "kv4.h"
+#include "kv_common.cuh"
+
+namespace kv {
+
+struct StoreParams {
+    Cache c;            // BITS = 4: Cache4::rows
+    int dim, blocks;    // elements of a head, stored blocks of a row
+    const void *in[2];  // k, v; strides in elements
+    int64_t row[2], head[2];
+    const int64_t *slots;
+    int64_t n;
+    int lanes;  // of one token's k and v: heads * blocks * (32 / E)
+    int kv_y;   // blocks along y that store; those behind rotate q
+    // rotation
+    const void *q;
+    void *out;
+    int64_t q_row, q_head, out_row, out_head;
+    int q_lanes, q_items;  // of one token, and of one of its heads
+    const int64_t *positions;
+    const uint64_t *turns;
+    const float4 *circle;  // cos and sin of k / 256 of a turn, then what they lack
+    float factor;
+    int half;  // pairs of a head
+    int interleaved, back;
+};
+
+namespace store {
+
+template <typename T>
+union Piece {
+    uint4 v;
+    T t[16 / sizeof(T)];
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// cos and sin of t / 2^64 turns, rounded to f32 once
+__device__ __forceinline__ void turn(uint64_t t, const float4 *circle, float *c, float *s) {
+    const uint32_t k = static_cast<uint32_t>((t + (1ull << 55)) >> 56);  // the nearest point
+    const int64_t r = static_cast<int64_t>(t - (static_cast<uint64_t>(k) << 56));  // within +-2^55
+    const float4 z = __ldg(circle + (k & 255u));
+    const int hi = static_cast<int>(r >> 25);  // within +-2^30
+    const float h = __int2float_rn(hi);
+    // what h lacks, in units of 2^25
+    const float l = __fadd_rn(__int2float_rn(hi - static_cast<int>(h)),
+                              __fmul_rn(__uint2float_rn(static_cast<uint32_t>(r) & 0x1FFFFFFu), 0x1p-25f));
+    // 2 pi / 2^39 in two parts
+    constexpr float k1 = 0x1.921fb6p-37f, k2 = -0x1.777a5cp-62f;
+    const float x = __fmul_rn(h, k1);
+    const float x2 = __fmul_rn(x, x);
+    const float low = __fadd_rn(__fmaf_rn(h, k1, -x), __fmaf_rn(l, k1, __fmul_rn(h, k2)));
+    const float sl = __fmaf_rn(__fmul_rn(x2, x), __fmaf_rn(x2, 1.0f / 120.0f, -1.0f / 6.0f), low);  // sin = x + sl
+    const float cm = __fmaf_rn(-x, low, __fmul_rn(x2, __fmaf_rn(x2, 1.0f / 24.0f, -0.5f)));         // cos = 1 + cm
+    // C cos - S sin, S cos + C sin: the great terms with their roundings' errors
+    const float p = __fmul_rn(z.y, x), q = __fmul_rn(z.x, x);
+    const float pe = __fmaf_rn(z.y, x, -p), qe = __fmaf_rn(z.x, x, -q);
+    const float a = __fsub_rn(z.x, p), b = __fadd_rn(z.y, q);
+    // (|C| is above |S x| or 0, and so the other way about: the difference of a sum is exact)
+    const float ae = __fsub_rn(__fsub_rn(z.x, a), p), be = __fadd_rn(__fsub_rn(z.y, b), q);
+    const float ar = __fmaf_rn(z.x, cm, __fmaf_rn(-z.y, sl, __fmaf_rn(-z.w, x, __fsub_rn(z.z, pe))));
+    const float br = __fmaf_rn(z.y, cm, __fmaf_rn(z.x, sl, __fmaf_rn(z.z, x, __fadd_rn(z.w, qe))));
+    *c = __fadd_rn(a, __fadd_rn(ae, ar));
+    *s = __fadd_rn(b, __fadd_rn(be, br));
+}
+
+// The largest x and the largest -x (and 0) of a lane's elements, NaN if one is.
+template <int E>
+__device__ __forceinline__ float2 extremes(const float (&y)[E]) {
+    float2 m = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        m.x = max_nan(m.x, y[j]);
+        m.y = max_nan(m.y, -y[j]);
+    }
+    return m;
+}
+__device__ __forceinline__ __half2 pair2(__half a, __half b) { return __halves2half2(a, b); }
+__device__ __forceinline__ __nv_bfloat162 pair2(__nv_bfloat16 a, __nv_bfloat16 b) { return __halves2bfloat162(a, b); }
+template <typename T2>
+__device__ __forceinline__ T2 extremes_of_pairs(const uint4 &v) {
+    const T2 *p = reinterpret_cast<const T2 *>(&v);
+    const T2 a = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+    const T2 b = __hmax2_nan(__hmax2_nan(__hneg2(p[0]), __hneg2(p[1])), __hmax2_nan(__hneg2(p[2]), __hneg2(p[3])));
+    return __hmax2_nan(pair2(a.x, b.x), pair2(a.y, b.y));
+}
+// over the PER lanes of a block
+template <int PER>
+__device__ __forceinline__ float2 over_block(float2 m) {
+#pragma unroll
+    for (int d = 1; d < PER; d *= 2) {
+        m.x = max_nan(m.x, __shfl_xor_sync(~0u, m.x, d));
+        m.y = max_nan(m.y, __shfl_xor_sync(~0u, m.y, d));
+    }
+    return m;
+}
+
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+
+// E codes of 4 bits.  `low`: x / d may be below -8.5 (d is subnormal).
+template <int E>
+__device__ __forceinline__ uint32_t pack_4(const float (&y)[E], float inv, bool low) {
+    uint32_t w = 0, bias = 0;
+#pragma unroll
+    for (int j = E - 1; j >= 0; --j) {
+        float z = fminf(__fadd_rn(__fmul_rn(y[j], inv), kRound + 8.0f), kRound + 15.0f);
+        if (low) z = fmaxf(z, kRound);
+        w = w * 16u + __float_as_uint(z);
+        bias = bias * 16u + 0x4B400000u;
+    }
+    return w - bias;
+}
+
+// Four codes of 8 bits, for any block: NaN becomes 0 (as kv_cache.cu)
+__device__ __forceinline__ uint32_t pack_8(const float *y, float inv) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = max(-127, min(127, __float2int_rn(__fmul_rn(y[i], inv))));
+        w |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * i);
+    }
+    return w;
+}
+__device__ __forceinline__ uint32_t pack_8_usual(const float *y, float inv) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__fadd_rn(__fmul_rn(y[i], inv), kRound));
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load(const T *p) {
+    Piece<T> x;
+    if constexpr (VEC) {
+        x.v = *reinterpret_cast<const uint4 *>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) x.t[i] = p[i];
+    }
+    return x.v;
+}
+
+// Element e of a head: its pair, and whether its sine counts negative (the first of the pair).
+__device__ __forceinline__ int pair_of(const StoreParams &p, int e, int *other, bool *first) {
+    if (p.interleaved) {
+        *other = e ^ 1;
+        *first = (e & 1) == 0;
+        return e >> 1;
+    }
+    *first = e < p.half;
+    *other = *first ? e + p.half : e - p.half;
+    return *first ? e : e - p.half;
+}
+
+template <typename T>
+__device__ __forceinline__ void rotate_pair(T &a, T &b, float c, float s) {
+    const float x = to_f32(a), y = to_f32(b);
+    a = from_f32<T>(__fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s)));
+    b = from_f32<T>(__fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s)));
+}
+
+}  // namespace store
+
+// One lane's item of one head of q.
+template <typename T, bool VEC>
+__device__ __forceinline__ void rotate_item(const StoreParams &p, const T *src, T *dst, int item, const float *cs, const float *sn) {
+    constexpr int E = 16 / sizeof(T);
+    using namespace store;
+    if constexpr (VEC) {
+        if (p.interleaved) {
+            const int e0 = item * E;
+            Piece<T> x;
+            x.v = load<T, true>(src + e0);
+            if (e0 < 2 * p.half)
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) rotate_pair(x.t[2 * j], x.t[2 * j + 1], cs[e0 / 2 + j], sn[e0 / 2 + j]);
+            *reinterpret_cast<uint4 *>(dst + e0) = x.v;
+        } else if (item * E < p.half) {
+            const int e0 = item * E;
+            Piece<T> x, y;
+            x.v = load<T, true>(src + e0);
+            y.v = load<T, true>(src + e0 + p.half);
+#pragma unroll
+            for (int j = 0; j < E; ++j) rotate_pair(x.t[j], y.t[j], cs[e0 + j], sn[e0 + j]);
+            *reinterpret_cast<uint4 *>(dst + e0) = x.v;
+            *reinterpret_cast<uint4 *>(dst + e0 + p.half) = y.v;
+        } else {
+            const int e0 = item * E + p.half;
+            *reinterpret_cast<uint4 *>(dst + e0) = load<T, true>(src + e0);
+        }
+    } else if (item < p.half) {
+        const int a = p.interleaved ? 2 * item : item, b = p.interleaved ? a + 1 : a + p.half;
+        T x = src[a], y = src[b];
+        rotate_pair(x, y, cs[item], sn[item]);
+        dst[a] = x;
+        dst[b] = y;
+    } else {
+        dst[item + p.half] = src[item + p.half];
+    }
+}
+
+// U tokens a lane.
+template <typename T, int BITS, bool ROT, bool VEC, int U>
+__global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
+    using namespace store;
+    constexpr int E = 16 / sizeof(T), PER = 32 / E;  // elements a lane, lanes a block
+    extern __shared__ float angles[];                // ROT: cos, then sin, [token of the block][pair]
+    __shared__ int64_t rows[8 * U];
+    const int tokens = blockDim.y * U, tid = threadIdx.y * blockDim.x + threadIdx.x;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
+    const bool stores = static_cast<int>(blockIdx.y) < p.kv_y;
+    const int at = (stores ? blockIdx.y : blockIdx.y - p.kv_y) * blockDim.x + threadIdx.x;
+
+    if constexpr (ROT) {
+        const int pairs = static_cast<int>(min(static_cast<int64_t>(tokens), p.n - first)) * p.half;
+        for (int i = tid; i < pairs; i += blockDim.x * blockDim.y) {
+            const int t = i / p.half, k = i - t * p.half;
+            float c, s;
+            turn(static_cast<uint64_t>(__ldg(p.positions + first + t)) * __ldg(p.turns + k), p.circle, &c, &s);
+            angles[i] = __fmul_rn(c, p.factor);
+            s = __fmul_rn(s, p.factor);
+            angles[tokens * p.half + i] = p.back ? -s : s;
+        }
+        if (!stores) {
+            __syncthreads();
+            if (at >= p.q_lanes) return;
+            const int h = at / p.q_items, item = at - h * p.q_items;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = u * blockDim.y + threadIdx.y;
+                const int64_t i = first + t;
+                if (i >= p.n) break;
+                const T *src = static_cast<const T *>(p.q) + i * p.q_row + h * p.q_head;
+                T *dst = static_cast<T *>(p.out) + i * p.out_row + h * p.out_head;
+                rotate_item<T, VEC>(p, src, dst, item, angles + t * p.half, angles + (tokens + t) * p.half);
+            }
+            return;
+        }
+    }
+    // ---- keys and values
+    const int per_head = p.blocks * PER;
+    const int h = at / per_head, in_row = at - h * per_head, e0 = in_row * E, b = in_row / PER;
+    const bool live = at < p.lanes && e0 < p.dim;
+    // a whole piece of the other halves of k's pairs (VEC, not interleaved)
+    const bool turns_piece = ROT && e0 < 2 * p.half;
+    const bool apart = ROT && VEC && turns_piece && !p.interleaved;
+    const int other0 = e0 < p.half ? e0 + p.half : e0 - p.half;
+    Piece<T> raw[U][2], oth[ROT && VEC ? U : 1];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const T *src = static_cast<const T *>(p.in[s]) + (first + threadIdx.y) * p.row[s] + h * p.head[s];
+        const int64_t step = static_cast<int64_t>(blockDim.y) * p.row[s];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool there = live && first + threadIdx.y + u * blockDim.y < p.n;
+            raw[u][s].v = there ? load<T, VEC>(src + e0 + u * step) : make_uint4(0, 0, 0, 0);
+            if constexpr (ROT && VEC)
+                if (s == 0) oth[u].v = there && apart ? load<T, true>(src + other0 + u * step) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (tid < tokens) {  // row of head 0 of each token, -1 if there is none
+        int64_t r = -1;
+        const int64_t slot = first + tid < p.n ? __ldg(p.slots + first + tid) : -1;
+        if (slot >= 0 && slot < p.c.slots) {
+            int64_t page;
+            int place;
+            if ((slot >> 32) == 0) {
+                const uint32_t s32 = static_cast<uint32_t>(slot), pg = s32 / static_cast<uint32_t>(p.c.page_size);
+                page = pg;
+                place = static_cast<int>(s32 - pg * static_cast<uint32_t>(p.c.page_size));
+            } else {
+                page = slot / p.c.page_size;
+                place = static_cast<int>(slot - page * p.c.page_size);
+            }
+            r = row_of(p.c, page, 0, place);
+        }
+        rows[tid] = r;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31, of = lane & (PER - 1), first_lane = lane - of;  // (blockDim.x: whole warps)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int t = u * blockDim.y + threadIdx.y;
+        const int64_t r0 = rows[t];
+        const int64_t r = r0 + h * p.c.stride_head;
+        float y[2][E];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < E; ++j) y[s][j] = to_f32(raw[u][s].t[j]);
+        if constexpr (ROT) {
+            if (live && turns_piece && first + t < p.n) {
+                const float *cs = angles + t * p.half, *sn = angles + (tokens + t) * p.half;
+                if (VEC && !p.interleaved) {
+                    const int i0 = e0 < p.half ? e0 : e0 - p.half;
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        const float s = e0 < p.half ? -sn[i0 + j] : sn[i0 + j];
+                        y[0][j] = __fadd_rn(__fmul_rn(y[0][j], cs[i0 + j]), __fmul_rn(to_f32(oth[VEC ? u : 0].t[j]), s));
+                    }
+                } else if (VEC) {
+#pragma unroll
+                    for (int j = 0; j < E; j += 2) {
+                        const float c = cs[(e0 + j) / 2], s = sn[(e0 + j) / 2], a = y[0][j], z = y[0][j + 1];
+                        y[0][j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(z, s));
+                        y[0][j + 1] = __fadd_rn(__fmul_rn(z, c), __fmul_rn(a, s));
+                    }
+                } else {
+                    const T *src = static_cast<const T *>(p.in[0]) + (first + t) * p.row[0] + h * p.head[0];
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        if (e0 + j < 2 * p.half) {
+                            int other;
+                            bool low;
+                            const int i = pair_of(p, e0 + j, &other, &low);
+                            const float s = low ? -sn[i] : sn[i];
+                            y[0][j] = __fadd_rn(__fmul_rn(y[0][j], cs[i]), __fmul_rn(to_f32(src[other]), s));
+                        }
+                }
+            }
+        }
+        float2 m[2];
+        if constexpr (sizeof(T) == 2 && !ROT) {
+            using T2 = decltype(pair2(raw[0][0].t[0], raw[0][0].t[0]));
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                T2 x = extremes_of_pairs<T2>(raw[u][s].v);
+#pragma unroll
+                for (int d = 1; d < PER; d *= 2) x = __hmax2_nan(x, __shfl_xor_sync(~0u, x, d));
+                m[s] = make_float2(to_f32(x.x), to_f32(x.y));
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) m[s] = over_block<PER>(extremes(y[s]));
+        }
+        const bool nan = m[0].x != m[0].x || m[1].x != m[1].x || m[0].y != m[0].y || m[1].y != m[1].y;
+        if (__any_sync(~0u, nan)) {  // of those that are numbers
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                m[s] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    m[s].x = fmaxf(m[s].x, y[s][j]);
+                    m[s].y = fmaxf(m[s].y, -y[s][j]);
+                }
+                m[s] = over_block<PER>(m[s]);
+            }
+        }
+        if constexpr (BITS == 4) {
+            // the block's two divisions: k's in its first lane, v's in its second
+            const float2 mine = of & 1 ? m[1] : m[0];
+            const float top = mine.y > mine.x ? -mine.y : mine.x;
+            const __half d = __float2half_rn(__fmul_rn(top, -0.125f));
+            const float f = __half2float(d);
+            const float ratio = f != 0.0f ? __fdiv_rn(1.0f, f) : 0.0f;
+            const float inv[2] = {__shfl_sync(~0u, ratio, first_lane), __shfl_sync(~0u, ratio, first_lane + 1)};
+            // 1 / d of an ordinary d is 2^14 at most; an infinite one leaves 0
+            const bool usual = !nan && fabsf(ratio) <= 16384.0f && fabsf(f) < INFINITY;
+            uint32_t w[2];
+            if (__all_sync(~0u, usual)) {
+                w[0] = pack_4(y[0], inv[0], false);
+                w[1] = pack_4(y[1], inv[1], false);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        const float z = __fmul_rn(y[s][j], inv[s]);
+                        if (!(fabsf(z) < INFINITY)) y[s][j] = 0.0f;  // NaN, or what an infinite d makes of it
+                        if (inv[s] == 0.0f) y[s][j] = 0.0f;
+                    }
+                w[0] = pack_4(y[0], inv[0], true);
+                w[1] = pack_4(y[1], inv[1], true);
+            }
+            if (r0 >= 0 && at < p.lanes) {
+                const int nb = p.blocks;
+                unsigned char *kc = reinterpret_cast<unsigned char *>(p.c.k_codes) + r * p.c.dim;
+                unsigned char *vc = reinterpret_cast<unsigned char *>(p.c.v_codes) + r * p.c.dim;
+                if constexpr (E == 8) {
+                    *reinterpret_cast<uint32_t *>(kc + 4 * (of * nb + b)) = w[0];
+                    *reinterpret_cast<uint16_t *>(vc + 2 * (2 * of * nb + b)) = static_cast<uint16_t>(w[1]);
+                    *reinterpret_cast<uint16_t *>(vc + 2 * ((2 * of + 1) * nb + b)) = static_cast<uint16_t>(w[1] >> 16);
+                } else {
+                    *reinterpret_cast<uint16_t *>(kc + 4 * ((of >> 1) * nb + b) + 2 * (of & 1)) = static_cast<uint16_t>(w[0]);
+                    *reinterpret_cast<uint16_t *>(vc + 2 * (of * nb + b)) = static_cast<uint16_t>(w[1]);
+                }
+                __half *sc = reinterpret_cast<__half *>(of & 1 ? p.c.v_scales : p.c.k_scales) + r * (2 * p.c.blocks);
+                if (of < 2) sc[b] = d;
+            }
+        } else {
+            const float amax[2] = {fmaxf(m[0].x, m[0].y), fmaxf(m[1].x, m[1].y)};
+            // as q8kv_write_kernel: 1 / amax and amax / 127 of k, then of v, a division a lane
+            const float a = of & 2 ? amax[1] : amax[0], num = of & 1 ? a : 1.0f, den = of & 1 ? 127.0f : a;
+            float ratio = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
+            if (!(of & 1)) ratio = __fmul_rn(127.0f, ratio);
+            const float inv[2] = {__shfl_sync(~0u, ratio, first_lane), __shfl_sync(~0u, ratio, first_lane + 2)};
+            const bool usual = !nan && amax[0] < INFINITY && amax[1] < INFINITY && inv[0] < INFINITY && inv[1] < INFINITY;
+            uint32_t w[2][E / 4];
+            if (__all_sync(~0u, usual)) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < E / 4; ++j) w[s][j] = pack_8_usual(y[s] + 4 * j, inv[s]);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < E / 4; ++j) w[s][j] = pack_8(y[s] + 4 * j, inv[s]);
+            }
+            if (live && r0 >= 0) {
+                const int64_t at_code = r * p.c.dim + e0;
+                if constexpr (E == 8) {
+                    *reinterpret_cast<uint2 *>(p.c.k_codes + at_code) = make_uint2(w[0][0], w[0][1]);
+                    *reinterpret_cast<uint2 *>(p.c.v_codes + at_code) = make_uint2(w[1][0], w[1][1]);
+                } else {
+                    *reinterpret_cast<uint32_t *>(p.c.k_codes + at_code) = w[0][0];
+                    *reinterpret_cast<uint32_t *>(p.c.v_codes + at_code) = w[1][0];
+                }
+            }
+            if (r0 >= 0 && at < p.lanes && (of & 1)) {
+                if (of == 1) p.c.k_scales[r * p.c.blocks + b] = ratio;
+                if (of == 3) p.c.v_scales[r * p.c.blocks + b] = ratio;
+            }
+        }
+    }
+}
+
+// Tokens a lane of a large call (kv_cache.cu's measurements)
+constexpr int kStoreTokens = 4;
+
+template <typename T, int BITS, bool ROT>
+void launch_store(const StoreParams &p, bool vec, const Shape &s, size_t smem, cudaStream_t stream) {
+    if (!vec)
+        kv_store_kernel<T, BITS, ROT, false, 1><<<s.grid, s.block, smem, stream>>>(p);
+    else if (s.many)
+        kv_store_kernel<T, BITS, ROT, true, kStoreTokens><<<s.grid, s.block, smem, stream>>>(p);
+    else
+        kv_store_kernel<T, BITS, ROT, true, 1><<<s.grid, s.block, smem, stream>>>(p);
+}
+
+}  // namespace kv

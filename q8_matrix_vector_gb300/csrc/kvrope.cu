@@ -1,0 +1,215 @@
+// Rotary positions (../../include/kvrope.h): plan, checks and launch of the rotating
+// variants of kv_store_kernel (kv_store.cuh).
+#include "../../include/kvrope.h"
+#include "kvrope.h"
+
+#include <cmath>
+#include <new>
+
+struct kvrope_s {
+    int device = 0;
+    int head_dim = 0, half = 0, interleaved = 0;
+    float factor = 1.0f;
+    float4 *circle = nullptr;   // 256 points
+    uint64_t *turns = nullptr;  // behind them
+};
+
+namespace kv {
+
+namespace {
+
+// Lanes of one token's q, and how p's blocks are split between storing and rotating.  Half the shared memory of an SM is
+// left to the loads' latency: 32 KB of angles a block at most.
+q8mv_status_t launch(StoreParams p, int bits, int type, bool vec, cudaStream_t stream) {
+    const int e = vec ? 16 / type_size(type) : 1;
+    p.q_items = p.q == nullptr ? 0 : !vec || !p.interleaved ? (p.dim - p.half) / e : p.dim / e;
+    const int64_t q_lanes = static_cast<int64_t>(p.q_items) * p.q_lanes;  // (q_lanes: heads so far)
+    if (q_lanes >= (1LL << 31)) return Q8MV_ERR_INVALID_ARG;
+    p.q_lanes = static_cast<int>(q_lanes);
+    // the blocks' shape is that of the stored lanes, if there are any
+    Shape s = shape(p.lanes > 0 ? p.lanes : p.q_lanes, p.n, kStoreTokens);
+    p.kv_y = p.lanes > 0 ? static_cast<int>(s.grid.y) : 0;
+    const int64_t q_y = ceil_div(p.q_lanes, s.block.x);
+    if (p.kv_y + q_y > 65535) return Q8MV_ERR_INVALID_ARG;
+    const auto bytes = [&](int tokens) { return static_cast<size_t>(s.block.y) * tokens * p.half * 2 * sizeof(float); };
+    if (!vec || bytes(kStoreTokens) > 32768) s.many = false;
+    s.grid = dim3(static_cast<unsigned>(ceil_div(p.n, static_cast<int64_t>(s.block.y) * (s.many ? kStoreTokens : 1))),
+                  static_cast<unsigned>(p.kv_y + q_y));
+    const size_t smem = bytes(s.many ? kStoreTokens : 1);
+    if (bits == 4)
+        launch_rotate_4(p, type, vec, s, smem, stream);
+    else
+        launch_rotate_8(p, type, vec, s, smem, stream);
+    return q8i::cuda_status(cudaGetLastError());
+}
+
+void take(const kvrope_s *plan, StoreParams *p) {
+    p->turns = plan->turns;
+    p->circle = plan->circle;
+    p->factor = plan->factor;
+    p->half = plan->half;
+    p->interleaved = plan->interleaved;
+}
+
+// Whole 16-byte pieces of e elements hold whole pairs, or whole halves of them.
+bool whole_pieces(const StoreParams &p, int64_t e) {
+    return p.dim % e == 0 && (p.interleaved ? 2 * p.half % e == 0 : p.half % e == 0 && (p.dim - 2 * p.half) % e == 0);
+}
+
+q8mv_status_t write(kvrope_s *plan, StoreParams &p, int bits, const kvrope_write_args_t *a, cudaStream_t stream) {
+    if (p.dim != plan->head_dim) return Q8MV_ERR_INVALID_ARG;
+    if (a->n < 0 || a->n >= (1LL << 31) || !valid_type(a->type) || a->heads_q < 0 || a->heads_q > 65535)
+        return Q8MV_ERR_INVALID_ARG;
+    for (int64_t s : {a->q_row, a->q_head, a->k_row, a->k_head, a->v_row, a->v_head, a->out_row, a->out_head})
+        if (!valid_stride(s)) return Q8MV_ERR_INVALID_ARG;
+    if (a->n == 0) return Q8MV_OK;
+    const int size = type_size(a->type);
+    if (!a->k || !a->v || !a->positions || !a->slots || !aligned(a->k, size) || !aligned(a->v, size) ||
+        !aligned(a->positions, 8) || !aligned(a->slots, 8))
+        return Q8MV_ERR_INVALID_ARG;
+    if (a->heads_q > 0 && (!a->q || !a->out || !aligned(a->q, size) || !aligned(a->out, size))) return Q8MV_ERR_INVALID_ARG;
+    take(plan, &p);
+    p.in[0] = a->k;
+    p.in[1] = a->v;
+    p.row[0] = a->k_row;
+    p.row[1] = a->v_row;
+    p.head[0] = a->k_head;
+    p.head[1] = a->v_head;
+    p.slots = a->slots;
+    p.n = a->n;
+    p.lanes = p.c.heads * p.blocks * (size == 4 ? 8 : 4);
+    p.positions = a->positions;
+    const int64_t e = 16 / size;
+    int64_t strides = a->k_row | a->k_head | a->v_row | a->v_head;
+    bool vec = aligned(a->k, 16) && aligned(a->v, 16);
+    if (a->heads_q > 0) {
+        p.q = a->q;
+        p.out = a->out;
+        p.q_row = a->q_row;
+        p.q_head = a->q_head;
+        p.out_row = a->out_row;
+        p.out_head = a->out_head;
+        p.q_lanes = a->heads_q;
+        strides |= a->q_row | a->q_head | a->out_row | a->out_head;
+        vec = vec && aligned(a->q, 16) && aligned(a->out, 16);
+    }
+    return launch(p, bits, a->type, vec && (strides & (e - 1)) == 0 && whole_pieces(p, e), stream);
+}
+
+}  // namespace
+
+}  // namespace kv
+
+extern "C" {
+
+q8mv_status_t kvrope_plan(kvrope_plan_t *out, int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                          const uint64_t *turns, float factor, int device) {
+    if (out == nullptr) return Q8MV_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (head_dim < 2 || head_dim > 65536 || rotary_dim < 2 || rotary_dim > head_dim || rotary_dim > 512 || rotary_dim % 2 != 0)
+        return Q8MV_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || turns == nullptr || !std::isfinite(factor)) return Q8MV_ERR_INVALID_ARG;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(device);
+    if (st != Q8MV_OK) return st;
+    kvrope_s *p = new (std::nothrow) kvrope_s();
+    if (p == nullptr) return Q8MV_ERR_OUT_OF_MEMORY;
+    p->device = scope.device();
+    p->head_dim = head_dim;
+    p->half = rotary_dim / 2;
+    p->interleaved = interleaved;
+    p->factor = factor;
+    float4 circle[256];
+    for (int k = 0; k < 256; ++k) {
+        // from the first eighth, so that the axes' points are exact
+        const int q = k & 63, quarter = k >> 6;
+        const double pi = 3.14159265358979323846;
+        double c = q <= 32 ? std::cos(pi * q / 128) : std::sin(pi * (64 - q) / 128);
+        double s = q <= 32 ? std::sin(pi * q / 128) : std::cos(pi * (64 - q) / 128);
+        for (int i = 0; i < quarter; ++i) {
+            const double t = c;
+            c = -s;
+            s = t;
+        }
+        const float ch = static_cast<float>(c), sh = static_cast<float>(s);
+        circle[k] = make_float4(ch, sh, static_cast<float>(c - ch), static_cast<float>(s - sh));
+    }
+    const size_t bytes = sizeof(uint64_t) * static_cast<size_t>(p->half);
+    cudaError_t e = cudaMalloc(&p->circle, sizeof circle + bytes);
+    if (e == cudaSuccess) {
+        p->turns = reinterpret_cast<uint64_t *>(p->circle + 256);
+        e = cudaMemcpy(p->circle, circle, sizeof circle, cudaMemcpyHostToDevice);
+    }
+    if (e == cudaSuccess) e = cudaMemcpy(p->turns, turns, bytes, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        if (p->circle) cudaFree(p->circle);
+        delete p;
+        return q8i::cuda_status(e);
+    }
+    *out = p;
+    return Q8MV_OK;
+}
+
+q8mv_status_t kvrope_apply(kvrope_plan_t plan, int64_t n, int32_t heads, int32_t type, const void *x, int64_t x_row,
+                           int64_t x_head, const int64_t *positions, void *out, int64_t out_row, int64_t out_head,
+                           int32_t inverse, cudaStream_t stream) {
+    if (plan == nullptr || n < 0 || n >= (1LL << 31) || heads < 0 || heads > 65535 || !kv::valid_type(type))
+        return Q8MV_ERR_INVALID_ARG;
+    if (!kv::valid_stride(x_row) || !kv::valid_stride(x_head) || !kv::valid_stride(out_row) || !kv::valid_stride(out_head))
+        return Q8MV_ERR_INVALID_ARG;
+    if (n == 0 || heads == 0) return Q8MV_OK;
+    const int size = kv::type_size(type);
+    if (!x || !out || !positions || !kv::aligned(x, size) || !kv::aligned(out, size) || !kv::aligned(positions, 8))
+        return Q8MV_ERR_INVALID_ARG;
+    kv::StoreParams p = {};
+    kv::take(plan, &p);
+    p.dim = plan->head_dim;
+    p.n = n;
+    p.q = x;
+    p.out = out;
+    p.q_row = x_row;
+    p.q_head = x_head;
+    p.out_row = out_row;
+    p.out_head = out_head;
+    p.q_lanes = heads;
+    p.positions = positions;
+    p.back = inverse != 0;
+    const int64_t e = 16 / size;
+    const bool vec = kv::aligned(x, 16) && kv::aligned(out, 16) && ((x_row | x_head | out_row | out_head) & (e - 1)) == 0 &&
+                     kv::whole_pieces(p, e);
+    return kv::launch(p, 8, type, vec, stream);
+}
+
+q8mv_status_t kvrope_write_q8(kvrope_plan_t plan, const q8kv_cache_t *cache, const kvrope_write_args_t *args,
+                              cudaStream_t stream) {
+    kv::StoreParams p = {};
+    if (plan == nullptr || args == nullptr || !kv::make_cache(cache, &p.c)) return Q8MV_ERR_INVALID_ARG;
+    p.dim = p.c.dim;
+    p.blocks = p.c.blocks;
+    return kv::write(plan, p, 8, args, stream);
+}
+
+q8mv_status_t kvrope_write_q4(kvrope_plan_t plan, const q4kv_cache_t *cache, const kvrope_write_args_t *args,
+                              cudaStream_t stream) {
+    kv::StoreParams p = {};
+    kv::Cache4 c = {};
+    if (plan == nullptr || args == nullptr || !kv::make_cache4(cache, &c)) return Q8MV_ERR_INVALID_ARG;
+    p.c = c.rows;
+    p.dim = c.dim;
+    p.blocks = c.blocks;
+    return kv::write(plan, p, 4, args, stream);
+}
+
+q8mv_status_t kvrope_destroy(kvrope_plan_t p) {
+    if (p == nullptr) return Q8MV_OK;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(p->device);
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    if (p->circle) cudaFree(p->circle);
+    delete p;
+    return st;
+}
+
+}  // extern "C"

@@ -59,6 +59,7 @@ def _bind(lib: ctypes.CDLL) -> None:
             ("q8kv_cache_write", [ref(CacheDesc), i64, p, p, i32, i64, i64, i64, i64, p, p]),
             ("q8kv_cache_read", [ref(CacheDesc), i64, p, p, p, i32, p]),
             ("q8kv_cache_move", [ref(CacheDesc), i64, i64, p, p, p]),
+            ("kvpage_copy_q8", [ref(CacheDesc), i64, p, p, p, p]),
             ("q8kv_attend_plan", [ref(p), i32, i32, i32, i32, i64, ctypes.c_int]),
             ("q8kv_attend", [p, ref(CacheDesc), p, p]),
             ("q8kv_attend_check", [p, ref(i32)]),
@@ -130,6 +131,41 @@ def _rows(t, tail, device, name):
     raise ValueError(f"{name}'s last axis must be contiguous")
 
 
+def _strides(parts, shape):
+    """The strides in rows of a cache's four arrays, (name, tensor, type, row's elements) each, of [pages, heads,
+    page_size, ...]: each row contiguous, all with the same strides, no two rows in the same place."""
+    device, strides = parts[0][1].get_device(), None
+    if device < 0:
+        raise ValueError(f"{parts[0][0]} must be a CUDA tensor")
+    for name, t, dtype, width in parts:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != (*shape, width):
+            raise ValueError(f"{name} must have shape {(*shape, width)}, got {tuple(t.shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned")
+        stride = t.stride()
+        if (width > 1 and stride[3] != 1) or any(s % width for n, s in zip(t.shape, stride[:3]) if n > 1):
+            raise ValueError(f"{name}'s rows must be contiguous and whole rows apart")
+        if any(s < width for n, s in zip(t.shape, stride[:3]) if n > 1):
+            raise ValueError(f"{name} is expanded: its rows overlap")
+        # the stride of an axis of one element says nothing
+        mine = tuple(s // width if n > 1 else 1 for n, s in zip(t.shape, stride[:3]))
+        if strides is not None and mine != strides:
+            raise ValueError(f"{name} must have the strides of {parts[0][0]}, counted in rows")
+        strides = mine
+    # rows that meet would be written twice
+    order = sorted((s, n) for s, n in zip(strides, shape) if n > 1)
+    reach = 1
+    for s, n in order:
+        if s < reach:
+            raise ValueError("the cache's rows overlap")
+        reach = s * (n - 1) + reach
+    return strides
+
+
 class Cache:
     """A paged Q8_0 key/value cache: int8 codes and one f32 scale per 32 of a row.
 
@@ -137,6 +173,9 @@ class Cache:
     head together, "token" a token's heads); ``Cache.of`` takes existing tensors.  Token slot s is place
     s % page_size of page s // page_size.
     """
+
+    _prefix = "q8kv_cache"  # of its entry points
+    _copier, _fused = "kvpage_copy_q8", "kvrope_write_q8"
 
     def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, device="cuda", layout: str = "head"):
         if layout not in ("head", "token"):
@@ -165,45 +204,23 @@ class Cache:
             raise ValueError(f"k_codes must have 4 axes, got {k_codes.dim()}")
         pages, heads, page_size, dim = k_codes.shape
         blocks = (dim + 31) // 32
-        device, strides = k_codes.get_device(), None
-        if device < 0:
-            raise ValueError("k_codes must be a CUDA tensor")
-        for name, t, dtype, width in (("k_codes", k_codes, torch.int8, dim), ("k_scales", k_scales, torch.float32, blocks),
-                                      ("v_codes", v_codes, torch.int8, dim), ("v_scales", v_scales, torch.float32, blocks)):
-            if t.dtype != dtype:
-                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-            if tuple(t.shape) != (pages, heads, page_size, width):
-                raise ValueError(f"{name} must have shape {(pages, heads, page_size, width)}, got {tuple(t.shape)}")
-            if t.get_device() != device:
-                raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
-            if t.data_ptr() % 16:
-                raise ValueError(f"{name} must be 16-byte aligned")
-            stride = t.stride()
-            if (width > 1 and stride[3] != 1) or any(s % width for n, s in zip(t.shape, stride[:3]) if n > 1):
-                raise ValueError(f"{name}'s rows must be contiguous and whole rows apart")
-            if any(s < width for n, s in zip(t.shape, stride[:3]) if n > 1):
-                raise ValueError(f"{name} is expanded: its rows overlap")
-            # the stride of an axis of one element says nothing
-            mine = tuple(s // width if n > 1 else 1 for n, s in zip(t.shape, stride[:3]))
-            if strides is not None and mine != strides:
-                raise ValueError(f"{name} must have the strides of k_codes, counted in rows")
-            strides = mine
-        # rows that meet would be written twice
-        order = sorted((s, n) for s, n in zip(strides, (pages, heads, page_size)) if n > 1)
-        reach = 1
-        for s, n in order:
-            if s < reach:
-                raise ValueError("the cache's rows overlap")
-            reach = s * (n - 1) + reach
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, dim
-        self.device, self._where = device, k_codes.device
-        self._tail = (heads, dim)
+        strides = _strides((("k_codes", k_codes, torch.int8, dim), ("k_scales", k_scales, torch.float32, blocks),
+                            ("v_codes", v_codes, torch.int8, dim), ("v_scales", v_scales, torch.float32, blocks)),
+                           (pages, heads, page_size))
+        self._keep(k_codes, k_scales, v_codes, v_scales, dim)
         self._desc = CacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), pages,
                                page_size, heads, dim, 0, *strides)
         self._ref = ctypes.byref(self._desc)
-        lib = _library()
-        self._write, self._read, self._move = lib.q8kv_cache_write, lib.q8kv_cache_read, lib.q8kv_cache_move
+
+    def _keep(self, k_codes, k_scales, v_codes, v_scales, dim):
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.pages, self.heads, self.page_size = k_codes.shape[:3]
+        self.head_dim = dim
+        self.device, self._where = k_codes.get_device(), k_codes.device
+        self._tail = (self.heads, dim)
+        lib, prefix = _library(), self._prefix
+        self._write, self._read, self._move = (getattr(lib, f"{prefix}_{n}") for n in ("write", "read", "move"))
+        self._copy = getattr(lib, self._copier)
 
     def write(self, k, v, slots) -> None:
         """Quantise keys and values [n, heads, head_dim] (f32, f16 or bf16) into slots [n] (int64, each once;
@@ -220,7 +237,7 @@ class Cache:
             status = _elsewhere(self._write, device, self._ref, n, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1], vs[0],
                                 vs[1], at)
         if status:
-            _fail(status, "q8kv_cache_write")
+            _fail(status, self._prefix + "_write")
 
     def read(self, slots, dtype=torch.float32, out=None):
         """(k, v) [n, heads, head_dim] of slots [n] (int64) in ``dtype``; zeros for slots outside the cache."""
@@ -244,7 +261,7 @@ class Cache:
         else:
             status = _elsewhere(self._read, device, self._ref, n, at, k.data_ptr(), v.data_ptr(), code)
         if status:
-            _fail(status, "q8kv_cache_read")
+            _fail(status, self._prefix + "_read")
         return k, v
 
     def move(self, src, dst) -> None:
@@ -262,7 +279,23 @@ class Cache:
         else:
             status = _elsewhere(self._move, device, self._ref, batch, path, a, b)
         if status:
-            _fail(status, "q8kv_cache_move")
+            _fail(status, self._prefix + "_move")
+
+    def copy_pages(self, src, dst, count=None) -> None:
+        """Pages dst[i] become copies of pages src[i] ([n] int32), all heads, for the first ``count`` pairs ([1] int32
+        on the device; None: all); pairs with a page outside the cache, as -1, are skipped.  A page may be the source of
+        several; no destination may be another pair's source or destination."""
+        device = self.device
+        a = _ints(src, torch.int32, -1, device, "src")
+        n = src.numel()
+        b = _ints(dst, torch.int32, n, device, "dst")
+        at = _ints(count, torch.int32, 1, device, "count") if count is not None else 0
+        if _current() == device:
+            status = self._copy(self._ref, n, a, b, at, _stream(device))
+        else:
+            status = _elsewhere(self._copy, device, self._ref, n, a, b, at)
+        if status:
+            _fail(status, self._copier)
 
 
 class _Plan:
@@ -300,13 +333,15 @@ class TreeAttention(_Plan):
     and ``max_rows`` query rows.  Use one per concurrent stream."""
 
     _destroy = "q8kv_attend_destroy"
+    _name = "q8kv_attend"
+    _cache = Cache
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, max_requests: int, max_rows: int, device: int = -1):
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self._tail, self._packed = (heads, head_dim), (heads * head_dim, head_dim)
         self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 0.0
-        self._make("q8kv_attend_plan", heads, kv_heads, head_dim, max_requests, max_rows, int(device))
-        self._fn = _library().q8kv_attend
+        self._make(self._name + "_plan", heads, kv_heads, head_dim, max_requests, max_rows, int(device))
+        self._fn = getattr(_library(), self._name)
         self._args = ctypes.create_string_buffer(_ATTEND.size)
 
     def __call__(self, q, cache: Cache, table, lengths, *, starts=None, mask=None, scale=None, out=None, lse=False):
@@ -346,6 +381,8 @@ class TreeAttention(_Plan):
             rows_out, code_out, os = _rows(out, self._tail, device, "out")
             if code_out != code or rows_out != rows:
                 raise ValueError(f"out must have the type and rows of q, got {out.dtype} {tuple(out.shape)}")
+        if cache._prefix != self._cache._prefix:
+            raise TypeError(f"cache must be a {self._cache.__name__}, got {type(cache).__name__}")
         if cache.device != device:
             raise ValueError(f"the cache is on cuda:{cache.device}, the plan on cuda:{device}")
         sums = torch.empty((rows, self.heads), dtype=torch.float32, device=self._where) if lse else None
@@ -357,7 +394,7 @@ class TreeAttention(_Plan):
         else:
             status = _elsewhere(self._fn, device, self._h, cache._ref, self._args)
         if status:
-            _fail(status, "q8kv_attend")
+            _fail(status, self._name)
         return (out, sums) if lse else out
 
     def check(self) -> int:
