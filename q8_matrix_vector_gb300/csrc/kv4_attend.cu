@@ -120,6 +120,9 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     kv::Attend4Params pp = {};
     kv::AttendParams &p = pp.a;
     pp.dim = c.dim;
+    pp.stride_page = static_cast<uint32_t>(r.stride_page);
+    pp.stride_head = static_cast<uint32_t>(r.stride_head);
+    pp.stride_token = static_cast<uint32_t>(r.stride_token);
     p.c = c.rows;
     p.q = a->q;
     p.out = a->out;
@@ -150,7 +153,12 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     // 8 rows at a time or 16, by the mean rows of a request: the fewest that hold them; heads above 128 by 8 alone, as
     // 16 do not fit the registers.
     const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
-    const kv::Attend4Shape v = mean <= 8 || c.blocks > 4 ? kv::k4Rows8 : kv::k4Rows16;
+    const bool wide = mean > 8 && c.blocks <= 4;
+    // Sixteen keys are one stretch of memory where a head's tokens of a page are, and start on 16 bytes.
+    const int scales = 4 * r.blocks;  // bytes of a row's
+    const bool in_turn = r.stride_token == 1 && r.page_size % 16 == 0 && (r.stride_page * scales) % 16 == 0 &&
+                         (r.stride_head * scales) % 16 == 0;
+    const kv::Attend4Shape v = in_turn ? (wide ? kv::k4Rows16InTurn : kv::k4Rows8InTurn) : wide ? kv::k4Rows16 : kv::k4Rows8;
     const kv::Attend4Variant &k = plan->variant[a->type][v];
     k.fn<<<plan->grid[a->type][v], kv::kWarps * 32, k.smem, stream>>>(pp);
     return q8i::cuda_status(cudaGetLastError());

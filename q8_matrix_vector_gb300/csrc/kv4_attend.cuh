@@ -16,21 +16,41 @@
 //   * The order of a row's bytes (q4kv.h) puts what a lane needs of all blocks in one
 //     load: of a key 4 NB bytes (8 elements of each block), of a value 2 NB (4 of each).
 //     Values of two keys are paired by one byte permute a word.
-//   * The 8 is not subtracted from codes.  Of the scores it is the accumulators' initial
-//     value, -8 times the block's sum of q.  Of the values it is a product of its own, a
-//     matrix of -8 (-128 where the codes carry 16) with the same weights, whose result is
-//     the accumulator that the codes' products start from: one more mma a block in place
-//     of eight subtractions.  A step's 32 keys are summed in it and added to the output in
-//     f32 with rounding, so that neither the 8s nor the tensor cores' cut sums pile up.
-// The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents.
+//   * The 8 is not subtracted from codes.  Of the scores it is one more product for all
+//     blocks, the keys' scales times -8 times the blocks' sums of q (two f16 parts), from
+//     which the scores start.  Of the values it is a product of its own, a matrix of -8
+//     (-128 where the codes carry 16) with the same weights, whose result is the accumulator
+//     that the codes' products start from: one more mma a block in place of eight
+//     subtractions.  A step's 32 keys are summed in it and added to the output in f32 with
+//     rounding, so that neither the 8s nor the tensor cores' cut sums pile up.  Sums that
+//     start from 8s keep 5 bits less of small results, which an f32 output would show (its
+//     error was 5e-6 of its norm): for f32 the 8 is subtracted from f16 codes.
+//   * bf16: the weights go to f16 once and are transposed once for all blocks, and then
+//     multiplied by the values' scales in f16, two at a time: two roundings to 11 bits where
+//     the output's own has 8.
+// The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents.  The
+// running maximum moves only when a score is 2^kSlack above it, so that most steps need no
+// maximum over the lanes; f16 has the room.
 #pragma once
 
 #include "kv4_attend.h"
 #include "kv_attend.cuh"
 
+#include <type_traits>
+
 namespace kv {
 
-constexpr int kStages4 = 2;
+#ifndef KV4_CTAS
+#define KV4_CTAS 3
+#endif
+#ifndef KV4_CTAS2
+#define KV4_CTAS2 2
+#endif
+#ifndef KV4_ST
+#define KV4_ST 2
+#endif
+constexpr int kStages4 = KV4_ST;
+constexpr float kSlack = 5.0f;
 
 // Shared memory of one variant: NB stored blocks, NT tiles of 8 query rows, QP parts of q.
 template <int NB, int NT, int QP>
@@ -45,7 +65,7 @@ struct Smem4 {
     static constexpr int kJoin = kWarps * 8 * kJoinPitch * 4;
     static constexpr int kQPitch = 64 * NB + ((64 * NB) % 128 == 64 ? 0 : 64);
     static constexpr int kQ = QP * kRows * kQPitch;
-    static constexpr int kBias = kRows * NB * 4;
+    static constexpr int kBias = kRows * 32;  // 8 pairs of f16 a row
     static constexpr int kTotal = kRing + kJoin + kQ + kBias;
     // where the 16-byte piece `c` of value row r is: spread so that the lanes of a load meet no bank twice
     static __host__ __device__ constexpr int v_piece(int r, int c) {
@@ -125,18 +145,66 @@ __device__ __forceinline__ float scale_of(uint32_t w, int b) {
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-
-// Exponent E for scales whose greatest magnitude is the f16 of these 15 bits: 2^(E + 14) is above it.  (A subnormal
-// counts as 2^-14; an infinity or NaN as any: what sees it is NaN.)
-__device__ __forceinline__ float exponent_of(uint32_t bits) {
-    return static_cast<float>(max(static_cast<int>(bits >> 10), 1) - 15 + 1 - 14);
+// with constant offsets of both
+template <int D, int S>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(dst), "l"(src), "n"(D), "n"(S) : "memory");
 }
 
-template <typename T, int NB, int NT, int QP, int PP>
-__global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 ? 3 : 2)
+// two f32 at a time
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y) {
+    asm("{.reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float u, float v) {  // a = a x + u
+    asm("{.reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mov.b64 r, {%4, %5};\n"
+        " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(u), "f"(v));
+}
+
+// Exponent E for scales whose greatest magnitude is the f16 of these 15 bits: 2^(E + 9) is above it, so that weights of
+// at most 2^(kSlack - E) times scales stay below 2^14.  (A subnormal counts as 2^-14; an infinity or NaN as any: what
+// sees it is NaN.)  LIMITED: at least kLeast, so that the weights themselves fit f16, and most steps need not look.
+template <bool LIMITED>
+__device__ __forceinline__ float exponent_of(uint32_t bits) {
+    return static_cast<float>(max(static_cast<int>(bits >> 10), LIMITED ? 15 : 1) - 15 + 1 - 9);
+}
+constexpr float kLeast = -8.0f;
+
+// Operands of 8 nibbles of the same place in the two halves of a word's nibbles: pairs 0 and 2 as c, 1 and 3 as 16 c, in
+// units of 2^-24, or (EXACT) c - 8 and 16 (c - 8) themselves.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t codes1(uint32_t w) {
+    if constexpr (EXACT) {
+        uint32_t y;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));
+        return y;
+    }
+    return w & 0x000F000Fu;
+}
+template <bool EXACT>
+__device__ __forceinline__ uint32_t codes16(uint32_t w) {
+    if constexpr (EXACT) {
+        uint32_t y;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"((w & 0x00F000F0u) | 0x64006400u), "r"(0x64806480u));
+        return y;
+    }
+    return w & 0x00F000F0u;
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
+template <typename T, int NB, int NT, int QP, int PP, bool SEG>
+__global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? KV4_CTAS : NB <= 4 ? KV4_CTAS2 : 2)
     q4kv_attend_kernel(const Attend4Params pp) {
     using S = Smem4<NB, NT, QP>;
     constexpr int ROWS = S::kRows, KEYS = kStepKeys * kWarps, W = (NB + 1) / 2;
+    constexpr bool EXACT = QP == 2, PACKED = sizeof(T) == 2 && PP == 1;
+    constexpr float kUnit = EXACT ? 1.0f : 16777216.0f;  // codes stand for so many
     const AttendParams &p = pp.a;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t scan_units[kWarps], scan_items[kWarps];
@@ -148,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
     const int g = lane >> 2, c = lane & 3;
     float *jo = reinterpret_cast<float *>(smem + S::kRing);  // [warp][8 rows][kJoinPitch]
     unsigned char *q_sm = smem + S::kRing + S::kJoin;
-    float *bias_sm = reinterpret_cast<float *>(q_sm + S::kQ);  // [row / 2][block][row % 2]
+    unsigned char *bias_sm = q_sm + S::kQ;  // [row][slot][2]: slot part * W + block / 2
 
     // ---- the CTA's share of the line of units (kv_attend.cuh)
     Split split;
@@ -230,29 +298,70 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
 
     // ---- the warp's ring: a stage takes 32 keys, K codes, V codes, K scales, V scales
     unsigned char *ring = smem + warp * (S::kStage * kStages4);
-    for (int i = lane; i < S::kStage * kStages4 / 16; i += 32) reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
-    __syncwarp();
+    // row: of the lane's key, or (SEG) of the first key of the lane's half of the step.  What is not there is not copied:
+    // whatever the ring holds in its place is finite as codes, and its scores and weights are replaced (`partial`).
+    // 32 pieces of 16 bytes at a time, NB a key: the lane's i-th is piece (lane + 32 i) % NB of key (lane + 32 i) / NB.
+    constexpr int kKJump = NB == 8 ? 4 * S::kKPitch : 512;  // from a lane's piece of K to its next, in the ring
+    const uint32_t ring_k = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + lane / NB * S::kKPitch + lane % NB * 16;
+    const uint32_t ring_v = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + kStepKeys * S::kKPitch +
+                            lane / NB * S::kCodes + S::v_piece(lane / NB, lane % NB) * 16;
+    const int8_t *const lane_k = p.c.k_codes + lane * 16, *const lane_v = p.c.v_codes + lane * 16;
     auto issue = [&](bool any, int slot, uint32_t row) {
         if (any) {
-            unsigned char *st = ring + slot * S::kStage;
-            const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(st));
-            const uint32_t sv = sk + kStepKeys * S::kKPitch;
-            const uint32_t ss = sv + kStepKeys * S::kCodes;
+            const uint32_t at = slot * S::kStage, ss = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + at +
+                                                       kStepKeys * (S::kKPitch + S::kCodes);
+            const uint32_t sk = ring_k + at, sv = ring_v + at;
+            if constexpr (SEG) {
+                // 16 keys in a row: 16 NB pieces
+                const uint32_t half[2] = {__shfl_sync(~0u, row, 0), __shfl_sync(~0u, row, 16)};
+                const int8_t *fk[2], *fv[2];
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                // 32 pieces of 16 bytes at a time, NB a key
-                const int i = lane + 32 * j, key = i / NB, piece = i % NB;
-                const uint32_t r = __shfl_sync(~0u, row, key);
-                if (r != kNoRow) {
-                    const uint64_t from = static_cast<uint64_t>(r) * S::kCodes + piece * 16;
-                    cp_async16(sk + key * S::kKPitch + piece * 16, p.c.k_codes + from);
-                    cp_async16(sv + key * S::kCodes + S::v_piece(key, piece) * 16, p.c.v_codes + from);
+                for (int h = 0; h < 2; ++h) {
+                    fk[h] = lane_k + static_cast<uint64_t>(half[h]) * S::kCodes;
+                    fv[h] = lane_v + static_cast<uint64_t>(half[h]) * S::kCodes;
+                }
+                auto both = [&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    if constexpr (j < NB) {
+                        constexpr bool split = 32 * j < 16 * NB && 32 * j + 32 > 16 * NB;  // NB = 3: half of it each
+                        constexpr int h = 32 * j >= 16 * NB ? 1 : 0, from = 512 * j - h * 256 * NB;
+                        if constexpr (split) {
+                            const bool second = lane >= 16;
+                            if (half[second] != kNoRow) {
+                                cp_async16_at<j * kKJump, 0>(sk, fk[second] + (second ? 512 * j - 256 * NB : 512 * j));
+                                cp_async16_at<j * 512, 0>(sv, fv[second] + (second ? 512 * j - 256 * NB : 512 * j));
+                            }
+                        } else if (half[h] != kNoRow) {
+                            cp_async16_at<j * kKJump, from>(sk, fk[h]);
+                            cp_async16_at<j * 512, from>(sv, fv[h]);
+                        }
+                    }
+                };
+                both(std::integral_constant<int, 0>());
+                both(std::integral_constant<int, 1>());
+                both(std::integral_constant<int, 2>());
+                both(std::integral_constant<int, 3>());
+                both(std::integral_constant<int, 4>());
+                both(std::integral_constant<int, 5>());
+                both(std::integral_constant<int, 6>());
+                both(std::integral_constant<int, 7>());
+            } else {
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int i = lane + 32 * j;
+                    const uint32_t r = __shfl_sync(~0u, row, i / NB);
+                    if (r != kNoRow) {
+                        const uint64_t from = static_cast<uint64_t>(r) * S::kCodes + i % NB * 16;
+                        cp_async16(sk + j * kKJump, p.c.k_codes + from);
+                        cp_async16(sv + j * 512, p.c.v_codes + from);
+                    }
                 }
             }
-            const uint32_t dk = ss + lane * S::kScales, dv = dk + kStepKeys * S::kScales;
             if (row != kNoRow) {
-                const char *ks = reinterpret_cast<const char *>(p.c.k_scales) + static_cast<uint64_t>(row) * S::kScales;
-                const char *vs = reinterpret_cast<const char *>(p.c.v_scales) + static_cast<uint64_t>(row) * S::kScales;
+                const uint32_t dk = ss + lane * S::kScales, dv = dk + kStepKeys * S::kScales;
+                const uint64_t from = static_cast<uint64_t>(row) * S::kScales + (SEG ? (lane & 15) * S::kScales : 0);
+                const char *ks = reinterpret_cast<const char *>(p.c.k_scales) + from;
+                const char *vs = reinterpret_cast<const char *>(p.c.v_scales) + from;
                 if constexpr (S::kScales == 16) {
                     cp_async16(dk, ks);
                     cp_async16(dv, vs);
@@ -263,13 +372,6 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                     cp_async4(dk, ks);
                     cp_async4(dv, vs);
                 }
-            } else {
-                // an absent key has scales of 0: whatever codes the ring holds, it adds nothing
-#pragma unroll
-                for (int i = 0; i < S::kScales; i += 4) {
-                    *reinterpret_cast<uint32_t *>(st + (dk - sk) + i) = 0u;
-                    *reinterpret_cast<uint32_t *>(st + (dv - sk) + i) = 0u;
-                }
             }
         }
         cp_commit();
@@ -278,7 +380,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
     // What a CTA does of one item: key tiles kt0 .. kt1 - 1, one step of the warp in each.
     struct Work {
         int64_t kt0, kt1;
-        int base0, n_steps, keys, h;
+        int base0, n_steps, keys;
+        uint32_t head;  // rows before the head's in a page
         const int32_t *table;
     };
     auto work_of = [&](const Place &x) -> Work {
@@ -289,18 +392,19 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
         k.n_steps = static_cast<int>(k.kt1 - k.kt0);
         k.keys = static_cast<int>(min(static_cast<int64_t>(x.prefix) + x.nodes,
                                       static_cast<int64_t>(p.table_cols) * p.c.page_size));
-        k.h = x.h;
+        k.head = static_cast<uint32_t>(x.h) * pp.stride_head;
         k.table = p.table + static_cast<int64_t>(x.b) * p.table_row;
         return k;
     };
-    // row number of the lane's key of step i, or kNoRow
+    // row number of the lane's key of step i (SEG: of its half's first key), or kNoRow
     auto find = [&](const Work &k, int i) -> uint32_t {
-        const int pos = k.base0 + i * KEYS + lane;
+        const int pos = k.base0 + i * KEYS + (SEG ? lane & 16 : lane);
         if (i >= k.n_steps || pos >= k.keys) return kNoRow;
         const uint32_t col = (__umulhi(pos, p.page_mul) + pos) >> p.page_shift;  // pos / page_size
         const int page = __ldg(k.table + col);
         if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
-        return static_cast<uint32_t>(row_of(p.c, page, k.h, pos - static_cast<int>(col) * p.c.page_size));
+        // (rows are numbered in 32 bits: products may be taken modulo 2^32)
+        return static_cast<uint32_t>(page) * pp.stride_page + (pos - col * p.c.page_size) * pp.stride_token + k.head;
     };
     uint32_t row_cur[kStages4];  // rows of the steps in the ring: their lanes' keys are there
     uint32_t row_next;
@@ -365,11 +469,22 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                 for (int b = 0; b < NB; ++b) {
 #pragma unroll
                     for (int d = 1; d < 8; d *= 2) sum[b] += __shfl_xor_sync(~0u, sum[b], d);
-                    if (l8 == 0) bias_sm[((rr >> 1) * NB + b) * 2 + (rr & 1)] = -8.0f / 16777216.0f * sum[b];
+                }
+                if constexpr (!EXACT) {
+                    if (l8 == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float x0 = i < 2 * W ? -8.0f / 16777216.0f * sum[i % W * 2] : 0.0f;
+                            const float x1 = i < 2 * W && i % W * 2 + 1 < NB ? -8.0f / 16777216.0f * sum[i % W * 2 + 1 < NB ? i % W * 2 + 1 : 0] : 0.0f;
+                            const uint32_t hi = pack_half2(x0, x1);
+                            const float2 back = unpack_half2(hi);
+                            reinterpret_cast<uint32_t *>(bias_sm)[rr * 8 + i] = i < W ? hi : pack_half2(x0 - back.x, x1 - back.y);
+                        }
+                    }
                 }
                 // not 0: a score of -inf has to stay that
                 if (l8 == 0)
-                    row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex + 24) << 23) * fabsf(p.scale_log2), 1e-37f);
+                    row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * kUnit * fabsf(p.scale_log2), 1e-37f);
             }
             __syncthreads();
 
@@ -381,14 +496,17 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[t][i][j] = 0.0f;
             // of rows 8 t + 2c and 8 t + 2c + 1; m: running maximum (log2) plus E
-            float m[NT][2], l[NT][2], mul[NT][2];
+            // minus: -m, or 0 while there is none
+            float m[NT][2], minus[NT][2], l[NT][2], mul[NT][2];
+            uint32_t bias[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     m[t][r] = -INFINITY;
-                    l[t][r] = 0.0f;
+                    minus[t][r] = l[t][r] = 0.0f;
                     mul[t][r] = row_mul[8 * t + 2 * c + r];
+                    if constexpr (!EXACT) bias[t][r] = reinterpret_cast<const uint32_t *>(bias_sm)[(8 * t + g) * 8 + 4 * r + c];
                 }
 
             int slot = slot0;
@@ -401,15 +519,29 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                 __syncwarp();
                 const unsigned char *sk = ring + slot * S::kStage, *sv = sk + kStepKeys * S::kKPitch;
                 const unsigned char *ks = sv + kStepKeys * S::kCodes, *vs = ks + kStepKeys * S::kScales;
-                const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow);
                 const int base = k.base0 + i * KEYS;
+                const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow && (!SEG || base + lane < k.keys));
                 if (there != 0) {
-                    // 2^(E + 14) is above the scales of the lane's key, and of all keys
-                    uint32_t top_bits = 0;
+                    // 2^(E + 9) is above the scales of the lane's key, and of all keys: -8, if none is 2 or more
+                    float e_key = kLeast, e_all = kLeast;
+                    uint32_t odd = 0;  // keys with a scale that is not finite
+                    {
+                        uint32_t d[W];
+                        load_scales4<NB>(vs + lane * S::kScales, d);
+                        if constexpr (NB % 2 == 1) d[W - 1] &= 0xFFFFu;
+                        uint32_t any = 0;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        top_bits = max(top_bits, reinterpret_cast<const uint16_t *>(vs + lane * S::kScales)[b] & 0x7FFFu);
-                    const float e_key = exponent_of(top_bits), e_all = exponent_of(__reduce_max_sync(~0u, top_bits));
+                        for (int i = 0; i < W; ++i) any |= d[i];
+                        if (EXACT || __any_sync(~0u, (any & 0x40004000u) != 0)) {
+                            uint32_t top_bits = 0;
+#pragma unroll
+                            for (int i = 0; i < W; ++i) top_bits = max(top_bits, max(d[i] & 0x7FFFu, d[i] >> 16 & 0x7FFFu));
+                            e_key = exponent_of<!EXACT>(top_bits);
+                            // (an absent key's count for nobody)
+                            e_all = exponent_of<!EXACT>(__reduce_max_sync(~0u, top_bits));
+                            odd = __ballot_sync(~0u, top_bits >= 0x7C00u);
+                        }
+                    }
 
                     // ---- scores: s[t][2 j + k][r] of key 16 j + 8 k + place and row 8 t + 2c + r
                     float s[NT][4][2];
@@ -421,19 +553,46 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                         uint32_t x[NB], y[NB];
                         load_key<NB>(sk + (16 * j + place) * S::kKPitch + c * (4 * NB), x);
                         load_key<NB>(sk + (16 * j + 8 + place) * S::kKPitch + c * (4 * NB), y);
+                        // the 8s of all blocks: scales times the rows' sums
+                        float sum[NT][4];
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) s[t][2 * j][r] = s[t][2 * j + 1][r] = 0.0f;
+                            for (int r = 0; r < 4; ++r) sum[t][r] = 0.0f;
+                        if constexpr (!EXACT) {
+                            const unsigned char *k0 = ks + (16 * j + place) * S::kScales, *k1 = k0 + 8 * S::kScales;
+                            uint32_t a[4] = {0u, 0u, 0u, 0u};
+                            a[0] = *reinterpret_cast<const uint32_t *>(k0 + 4 * (c % W));
+                            a[1] = *reinterpret_cast<const uint32_t *>(k1 + 4 * (c % W));
+                            if constexpr (W == 4) {
+                                a[2] = a[0];
+                                a[3] = a[1];
+                            } else if constexpr (W == 3) {
+                                a[2] = *reinterpret_cast<const uint32_t *>(k0 + 4 * ((c + 4) % W));
+                                a[3] = *reinterpret_cast<const uint32_t *>(k1 + 4 * ((c + 4) % W));
+                            }
+                            if constexpr (NB == 3) {  // there is no fourth scale
+                                a[0] &= c & 1 ? 0xFFFFu : ~0u;
+                                a[1] &= c & 1 ? 0xFFFFu : ~0u;
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma_f16(sum[t], a, bias[t][0], bias[t][1], sum[t]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                s[t][2 * j][r] = sum[t][r];
+                                s[t][2 * j + 1][r] = sum[t][2 + r];
+                            }
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             const uint32_t xs = x[b] >> 8, ys = y[b] >> 8;
-                            const uint32_t a0[4] = {x[b] & 0x000F000Fu, y[b] & 0x000F000Fu, x[b] & 0x00F000F0u, y[b] & 0x00F000F0u};
-                            const uint32_t a1[4] = {xs & 0x000F000Fu, ys & 0x000F000Fu, xs & 0x00F000F0u, ys & 0x00F000F0u};
+                            const uint32_t a0[4] = {codes1<EXACT>(x[b]), codes1<EXACT>(y[b]), codes16<EXACT>(x[b]), codes16<EXACT>(y[b])};
+                            const uint32_t a1[4] = {codes1<EXACT>(xs), codes1<EXACT>(ys), codes16<EXACT>(xs), codes16<EXACT>(ys)};
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const float2 z = *reinterpret_cast<const float2 *>(bias_sm + ((4 * t + c) * NB + b) * 2);
-                                float part[4] = {z.x, z.y, z.x, z.y};
+                                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                                 for (int q = 0; q < QP; ++q) {
                                     const uint4 qq = *reinterpret_cast<const uint4 *>(
@@ -452,11 +611,10 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                     // ---- softmax
                     const bool drafts = base + kStepKeys > w.prefix;
                     const bool partial = drafts || there != ~0u;
-                    bool moved = false;
-                    float z[NT][2];
+                    bool above = false;
+                    float top[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        float top[2];
                         if (partial) {
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
@@ -464,37 +622,35 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                                 if (drafts)
                                     see &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
                                                 w.rt * ROWS + 8 * t + 2 * c + r);
-                                top[r] = -INFINITY;
+                                top[t][r] = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const int key = 8 * k + place;
                                     if (((see >> key) & 1u) == 0) s[t][k][r] = -INFINITY;
                                     // a row's E comes from keys that it sees, so that no other's scale matters
-                                    top[r] = fmaxf(top[r], fmaf(s[t][k][r], mul[t][r], __shfl_sync(~0u, e_key, key)));
+                                    top[t][r] = fmaxf(top[t][r], fmaf(s[t][k][r], mul[t][r], __shfl_sync(~0u, e_key, key)));
                                 }
                             }
                         } else {
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
-                                top[r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
+                                top[t][r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
                         }
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-                            for (int d = 4; d < 32; d *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
-                            const float n = fmaxf(m[t][r], top[r]);
-                            moved |= n != m[t][r];
-                            z[t][r] = n;
-                        }
+                        for (int r = 0; r < 2; ++r) above |= top[t][r] > m[t][r] + kSlack;
                     }
-                    if (__any_sync(~0u, moved)) {
+                    if (__any_sync(~0u, above)) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             float f[2];
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                f[r] = ex2(m[t][r] - (z[t][r] == -INFINITY ? 0.0f : z[t][r]));
-                                m[t][r] = z[t][r];
+#pragma unroll
+                                for (int d = 4; d < 32; d *= 2) top[t][r] = fmaxf(top[t][r], __shfl_xor_sync(~0u, top[t][r], d));
+                                const float n = fmaxf(m[t][r], top[t][r]);
+                                minus[t][r] = n == -INFINITY ? 0.0f : -n;
+                                f[r] = ex2(m[t][r] + minus[t][r]);
+                                m[t][r] = n;
                                 l[t][r] *= f[r];
                             }
 #pragma unroll
@@ -509,18 +665,40 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float n = z[t][r] == -INFINITY ? 0.0f : -z[t][r];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                s[t][k][r] = ex2(fmaf(s[t][k][r], mul[t][r], n));
-                                l[t][r] += s[t][k][r];
-                            }
+                        for (int k = 0; k < 4; ++k) {
+                            fma2(s[t][k][0], s[t][k][1], mul[t][0], mul[t][1], minus[t][0], minus[t][1]);
+                            s[t][k][0] = ex2(s[t][k][0]);
+                            s[t][k][1] = ex2(s[t][k][1]);
+                            add2(l[t][0], l[t][1], s[t][k][0], s[t][k][1]);
                         }
-                    // ---- O^T += V^T (P dV)^T, two blocks at a time (a word's halves), 16 keys at a time
-                    uint32_t dv[4][W];
+                    if (odd != 0) {
+                        // A row that sees such a value is NaN; for the others its scale is 0, as their weight is.
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) load_scales4<NB>(vs + (8 * k + place) * S::kScales, dv[k]);
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    if ((odd >> (8 * k + place) & 1u) != 0 && s[t][k][r] != 0.0f) l[t][r] = NAN;
+                        if (odd >> lane & 1u) {
+#pragma unroll
+                            for (int i = 0; i < S::kScales; i += 4)
+                                *reinterpret_cast<uint32_t *>(const_cast<unsigned char *>(vs) + lane * S::kScales + i) = 0u;
+                        }
+                        __syncwarp();
+                    }
+                   // ---- O^T += V^T (P dV)^T, two blocks at a time (a word's halves), 16 keys at a time
+                    uint32_t dv[4][W], p2[NT][4];
+                    if constexpr (PACKED) {
+                        // (the scales of the lane's keys of the second operand are read where they are paired)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) p2[t][k] = transpose8(pack_half2(s[t][k][0], s[t][k][1]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) load_scales4<NB>(vs + (8 * k + place) * S::kScales, dv[k]);
+                    }
                     // the lane's keys 16 j + {2c, 2c + 1, 8 + 2c, 8 + 2c + 1}: places c, 4 + c, 8 + c, 12 + c
                     uint32_t v[2][4][W];
 #pragma unroll
@@ -535,16 +713,23 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                         uint32_t wgt[2][NT][PP][2];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float d = scale_of(dv[k][b / 2], b);
+                            if constexpr (PACKED) {
+                                // scales of keys 8 k + c and 8 k + 4 + c
+                                const unsigned char *at = vs + (8 * k + c) * S::kScales + b / 2 * 4;
+                                const uint32_t d = __byte_perm(*reinterpret_cast<const uint32_t *>(at),
+                                                               *reinterpret_cast<const uint32_t *>(at + 4 * S::kScales),
+                                                               b & 1 ? 0x7632u : 0x5410u);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    wgt[k >> 1][t][0][k & 1] = mul_half2(p2[t][k], d);
+                                }
+                                continue;
+                            }
+                            const float d = PACKED ? 0.0f : scale_of(dv[k][b / 2], b);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
                                 const float(&pr)[2] = s[t][k];
-                                float x0 = pr[0] * d, x1 = pr[1] * d;
-                                if (partial) {
-                                    // a key that the row does not see keeps weight 0 whatever its scale is
-                                    x0 = pr[0] == 0.0f ? 0.0f : x0;
-                                    x1 = pr[1] == 0.0f ? 0.0f : x1;
-                                }
+                                const float x0 = pr[0] * d, x1 = pr[1] * d;
                                 const uint32_t h = pack_half2(x0, x1);
                                 wgt[k >> 1][t][0][k & 1] = transpose8(h);
                                 if constexpr (PP == 2) {
@@ -560,7 +745,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                             const uint32_t eight[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
                             float off[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
+                            for (int j = 0; j < (EXACT ? 0 : 2); ++j)
 #pragma unroll
                                 for (int q = 0; q < PP; ++q) mma_f16(off, eight, wgt[j][t][q][0], wgt[j][t][q][1], off);
 #pragma unroll
@@ -572,8 +757,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
                             const uint32_t x = __byte_perm(v[j][0][b / 2], v[j][1][b / 2], sel);
                             const uint32_t y = __byte_perm(v[j][2][b / 2], v[j][3][b / 2], sel);
                             const uint32_t xs = x >> 8, ys = y >> 8;
-                            const uint32_t a0[4] = {x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u};
-                            const uint32_t a1[4] = {xs & 0x000F000Fu, xs & 0x00F000F0u, ys & 0x000F000Fu, ys & 0x00F000F0u};
+                            const uint32_t a0[4] = {codes1<EXACT>(x), codes16<EXACT>(x), codes1<EXACT>(y), codes16<EXACT>(y)};
+                            const uint32_t a1[4] = {codes1<EXACT>(xs), codes16<EXACT>(xs), codes1<EXACT>(ys), codes16<EXACT>(ys)};
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -587,7 +772,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) o[t][2 * b + e][k] += acc[t][e][k];
+                                for (int k = 0; k < 4; k += 2)
+                                    add2(o[t][2 * b + e][k], o[t][2 * b + e][k + 1], acc[t][e][k], acc[t][e][k + 1]);
                     }
                 }
                 __syncwarp();
@@ -623,8 +809,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float *at = jo + (warp * 8 + 2 * c + r) * S::kJoinPitch;
-                    // elements 4 g + {0 .. 3} of each block, in units of 2^-24, 16 in the odd ones
-                    constexpr float one = 16777216.0f, sixteen = 1048576.0f;
+                    // elements 4 g + {0 .. 3} of each block, in the codes' units, 16 in the odd ones
+                    constexpr float one = kUnit, sixteen = kUnit / 16.0f;
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
                         *reinterpret_cast<float4 *>(at + 32 * b + 4 * g) =
@@ -785,19 +971,20 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 4 : NB <= 4 
 }
 
 template <typename T, int NB, int NT, int QP, int PP>
-Attend4Variant attend4_variant_of() {
-    return {q4kv_attend_kernel<T, NB, NT, QP, PP>, Smem4<NB, NT, QP>::kTotal, 8 * NT};
+Attend4Variant attend4_variant_of(bool rows_in_turn) {
+    return {rows_in_turn ? q4kv_attend_kernel<T, NB, NT, QP, PP, true> : q4kv_attend_kernel<T, NB, NT, QP, PP, false>,
+            Smem4<NB, NT, QP>::kTotal, 8 * NT};
 }
 
 template <typename T, int QP, int PP>
 Attend4Variant attend4_variant_of(int blocks, Attend4Shape shape) {
-    const bool wide = shape == k4Rows16;
+    const bool seg = shape == k4Rows8InTurn || shape == k4Rows16InTurn, wide = shape == k4Rows16 || shape == k4Rows16InTurn;
     switch (blocks) {
-        case 2: return wide ? attend4_variant_of<T, 2, 2, QP, PP>() : attend4_variant_of<T, 2, 1, QP, PP>();
-        case 3: return wide ? attend4_variant_of<T, 3, 2, QP, PP>() : attend4_variant_of<T, 3, 1, QP, PP>();
-        case 4: return wide ? attend4_variant_of<T, 4, 2, QP, PP>() : attend4_variant_of<T, 4, 1, QP, PP>();
-        case 6: return wide ? Attend4Variant{} : attend4_variant_of<T, 6, 1, QP, PP>();
-        case 8: return wide ? Attend4Variant{} : attend4_variant_of<T, 8, 1, QP, PP>();
+        case 2: return wide ? attend4_variant_of<T, 2, 2, QP, PP>(seg) : attend4_variant_of<T, 2, 1, QP, PP>(seg);
+        case 3: return wide ? attend4_variant_of<T, 3, 2, QP, PP>(seg) : attend4_variant_of<T, 3, 1, QP, PP>(seg);
+        case 4: return wide ? attend4_variant_of<T, 4, 2, QP, PP>(seg) : attend4_variant_of<T, 4, 1, QP, PP>(seg);
+        case 6: return wide ? Attend4Variant{} : attend4_variant_of<T, 6, 1, QP, PP>(seg);
+        case 8: return wide ? Attend4Variant{} : attend4_variant_of<T, 8, 1, QP, PP>(seg);
         default: return {};
     }
 }

@@ -11,6 +11,7 @@ namespace kv {
 struct Attend4Params {
     AttendParams a;
     int dim;  // elements of a head
+    uint32_t stride_page, stride_head, stride_token;  // of the cache, modulo 2^32
 };
 
 struct Attend4Variant {
@@ -19,8 +20,9 @@ struct Attend4Variant {
     int rows = 0;  // of an item
 };
 
-// 8 or 16 query rows of one kv head at a time, for NB = 2, 3, 4, 6 or 8 stored blocks.
-enum Attend4Shape { k4Rows8 = 0, k4Rows16, kAttend4Shapes };
+// 8 or 16 query rows of one kv head at a time, for NB = 2, 3, 4, 6 or 8 stored blocks (16: up to 4); a warp's keys one
+// by one, or 16 at a time that follow one another in memory.
+enum Attend4Shape { k4Rows8 = 0, k4Rows16, k4Rows8InTurn, k4Rows16InTurn, kAttend4Shapes };
 
 Attend4Variant attend4_variant_f32(int blocks, Attend4Shape shape);
 Attend4Variant attend4_variant_f16(int blocks, Attend4Shape shape);
