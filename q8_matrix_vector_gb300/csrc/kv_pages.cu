@@ -73,6 +73,10 @@ __device__ __forceinline__ int scan(int x, int *total, int *warp_sums) {
 // Every CTA's number reaches every CTA: the sum of those before this one, and of all.  `box` has a place for each.
 __device__ __forceinline__ int exchange(cg::cluster_group &cluster, int *box, int mine, int *total) {
     const int ranks = cluster.num_blocks(), me = cluster.block_rank();
+    if (ranks == 1) {
+        *total = mine;
+        return 0;
+    }
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < ranks) cluster.map_shared_rank(box, threadIdx.x)[me] = mine;
     cluster.sync();
@@ -99,6 +103,11 @@ __device__ __forceinline__ void load_refs(const int *refs, int p0, int end, int 
     }
 }
 
+// x / page_size; 64-bit divisions take a hundred instructions
+__device__ __forceinline__ int64_t pages_of(const PageParams &p, int64_t x) {
+    return (x >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(p.page_size)) : x / p.page_size;
+}
+
 // A request's span of columns: those that will be written.
 struct Span {
     int64_t length, tokens;
@@ -109,9 +118,9 @@ __device__ __forceinline__ Span span_of(const PageParams &p, int b) {
     s.length = max(p.lengths[b], 0);
     s.tokens = max(p.tokens[b], 0);
     s.held = min(max(p.held[b], 0), p.columns);
-    const int64_t need = s.tokens > 0 ? (s.length + s.tokens + p.page_size - 1) / p.page_size : 0;
+    const int64_t need = s.tokens > 0 ? pages_of(p, s.length + s.tokens + p.page_size - 1) : 0;
     s.need = static_cast<int>(min(need, static_cast<int64_t>(p.columns) + 1));
-    s.first = static_cast<int>(min(s.length / p.page_size, static_cast<int64_t>(s.held)));
+    s.first = static_cast<int>(min(pages_of(p, s.length), static_cast<int64_t>(s.held)));
     return s;
 }
 
@@ -123,7 +132,7 @@ __device__ __forceinline__ bool replaced(const PageParams &p, int b, int c, int 
 }
 
 __device__ __forceinline__ int64_t slot_at(const PageParams &p, int b, int64_t position) {
-    const int64_t c = position / p.page_size;
+    const int64_t c = pages_of(p, position);
     const int64_t page = p.table[static_cast<int64_t>(b) * p.columns + c];
     return page * p.page_size + position - c * p.page_size;
 }
@@ -136,7 +145,14 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.requests + ranks - 1) / ranks;
     const int b0 = min(me * per, p.requests), b1 = min(b0 + per, p.requests);
-    // ---- how many pages each request wants: a warp each
+    // the first refs of the CTA's pages, on their way while the requests are looked at
+    const int share = ((p.pages + ranks - 1) / ranks + kPer - 1) / kPer * kPer;
+    const int p0 = static_cast<int>(min(static_cast<int64_t>(me) * share, static_cast<int64_t>(p.pages)));
+    const int p1 = min(p0 + share, p.pages);
+    int r0[kPer], r[kPer];
+    load_refs(p.refs, p0 + threadIdx.x * kPer, p1, r0);
+    // ---- how many pages each request wants: a warp each (amounts stay here if a tile holds them)
+    const bool few = b1 - b0 <= kThreads;
     int mine = 0;
     for (int b = b0 + warp; b < b1; b += kThreads / 32) {
         const Span s = span_of(p, b);
@@ -150,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
             n = __reduce_add_sync(~0u, n) + max(s.need - s.held, 0);
             mine += n;
         }
-        if (lane == 0) p.amount[b] = n;
+        if (lane == 0) (few ? starts[b - b0] : p.amount[b]) = n;
     }
     int total;
     scan(lane == 0 ? mine : 0, &total, warp_sums);
@@ -159,20 +175,25 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
     const int before = exchange(cluster, box[0], total, &wanted);
     // ---- the lowest free pages in order
     if (wanted > 0) {
-        const int share = ((p.pages + ranks - 1) / ranks + kPer - 1) / kPer * kPer;
-        const int p0 = static_cast<int>(min(static_cast<int64_t>(me) * share, static_cast<int64_t>(p.pages)));
-        const int p1 = min(p0 + share, p.pages);
-        int count = 0, r[kPer];
-        for (int t = p0 + threadIdx.x * kPer; t < p1; t += kTile) {
-            load_refs(p.refs, t, p1, r);
+        int at = 0;
+        if (ranks > 1) {  // how many there are before the CTA's
+            int count = 0;
+            for (int t = p0 + threadIdx.x * kPer; t < p1; t += kTile) {
+                load_refs(p.refs, t, p1, r);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) count += r[i] == 0;
+                for (int i = 0; i < kPer; ++i) count += r[i] == 0;
+            }
+            scan(count, &total, warp_sums);
+            at = exchange(cluster, box[1], total, &free_pages);
         }
-        scan(count, &total, warp_sums);
-        int at = exchange(cluster, box[1], total, &free_pages);
         for (int t0 = p0; t0 < p1 && at < wanted; t0 += kTile) {  // (the same for all threads)
             const int t = t0 + threadIdx.x * kPer;
-            load_refs(p.refs, t, p1, r);
+            if (t0 == p0) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) r[i] = r0[i];
+            } else {
+                load_refs(p.refs, t, p1, r);
+            }
             int n = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) n += r[i] == 0;
@@ -185,13 +206,19 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
                 }
             at += total;
         }
-        cluster.sync();  // the list is there
+        // the list is there
+        if (ranks > 1) {
+            cluster.sync();
+        } else {
+            free_pages = at;  // (at least `wanted`, or all)
+            __syncthreads();
+        }
     }
     // ---- the requests take them
     int served = 0, base = before;
     for (int t0 = b0; t0 < b1; t0 += kThreads) {
         const int b = t0 + threadIdx.x;
-        const int n = b < b1 ? p.amount[b] : 0;
+        const int n = b >= b1 ? 0 : few ? starts[threadIdx.x] : p.amount[b];
         int k = base + scan(max(n, 0), &total, warp_sums);
         const bool fits = n >= 0 && (n == 0 || k + n <= free_pages);
         if (fits && n > 0) served = max(served, k + n);
@@ -204,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
             int from = -1, to = -1;
             if (start >= 0) {
                 int *row = p.table + static_cast<int64_t>(rb) * p.columns;
-                const int64_t part = s.length % p.page_size != 0 ? s.length / p.page_size : -1;
+                const int64_t col = pages_of(p, s.length), part = s.length != col * p.page_size ? col : -1;
                 int done = start;
                 for (int c0 = s.first; c0 < s.need; c0 += 32) {
                     const int c = c0 + lane;
@@ -246,9 +273,11 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) served = max(served, warp_sums[w]);
-    if (static_cast<int>(threadIdx.x) < ranks) cluster.map_shared_rank(box[2], threadIdx.x)[me] = served;
-    cluster.sync();
-    for (int r = 0; r < ranks; ++r) served = max(served, box[2][r]);
+    if (ranks > 1) {
+        if (static_cast<int>(threadIdx.x) < ranks) cluster.map_shared_rank(box[2], threadIdx.x)[me] = served;
+        cluster.sync();
+        for (int i = 0; i < ranks; ++i) served = max(served, box[2][i]);
+    }
     for (int i = me * kThreads + threadIdx.x; i < served; i += ranks * kThreads) {
         p.refs[p.fresh[i]] = 1;
         const int old = p.old[i];

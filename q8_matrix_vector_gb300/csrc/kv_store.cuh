@@ -109,7 +109,7 @@ template <typename T2>
 __device__ __forceinline__ T2 extremes_of_pairs(const uint4 &v) {
     const T2 *p = reinterpret_cast<const T2 *>(&v);
     const T2 a = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
-    const T2 b = __hmax2_nan(__hmax2_nan(__hneg2(p[0]), __hneg2(p[1])), __hmax2_nan(__hneg2(p[2]), __hneg2(p[3])));
+    const T2 b = __hneg2(__hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3])));
     return __hmax2_nan(pair2(a.x, b.x), pair2(a.y, b.y));
 }
 // over the PER lanes of a block
@@ -125,18 +125,23 @@ __device__ __forceinline__ float2 over_block(float2 m) {
 
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
 
-// E codes of 4 bits.  `low`: x / d may be below -8.5 (d is subnormal).
+// E codes of 4 bits.  `low`: x / d may be below -8.5 (d is subnormal).  Codes j and j + E / 2 are cut off at 15 together,
+// as halves of a word.
 template <int E>
 __device__ __forceinline__ uint32_t pack_4(const float (&y)[E], float inv, bool low) {
-    uint32_t w = 0, bias = 0;
+    uint32_t w = 0;
 #pragma unroll
-    for (int j = E - 1; j >= 0; --j) {
-        float z = fminf(__fadd_rn(__fmul_rn(y[j], inv), kRound + 8.0f), kRound + 15.0f);
-        if (low) z = fmaxf(z, kRound);
-        w = w * 16u + __float_as_uint(z);
-        bias = bias * 16u + 0x4B400000u;
+    for (int j = E / 2 - 1; j >= 0; --j) {
+        float z[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            z[i] = __fadd_rn(__fmul_rn(y[j + i * (E / 2)], inv), kRound + 8.0f);
+            if (low) z[i] = fmaxf(z[i], kRound);
+        }
+        w = w * 16u + __vminu2(__byte_perm(__float_as_uint(z[0]), __float_as_uint(z[1]), 0x5410u), 0x000F000Fu);
     }
-    return w - bias;
+    if constexpr (E == 4) w = (w & 0xFFu) | (w >> 8);
+    return w;
 }
 
 // Four codes of 8 bits, for any block: NaN becomes 0 (as kv_cache.cu)
@@ -189,34 +194,65 @@ __device__ __forceinline__ void rotate_pair(T &a, T &b, float c, float s) {
 
 }  // namespace store
 
-// One lane's item of one head of q.
-template <typename T, bool VEC>
-__device__ __forceinline__ void rotate_item(const StoreParams &p, const T *src, T *dst, int item, const float *cs, const float *sn) {
-    constexpr int E = 16 / sizeof(T);
-    using namespace store;
-    if constexpr (VEC) {
-        if (p.interleaved) {
-            const int e0 = item * E;
-            Piece<T> x;
-            x.v = load<T, true>(src + e0);
-            if (e0 < 2 * p.half)
+// N angles' cosines or sines, at 4 N bytes' alignment (16 at most)
+template <int N>
+__device__ __forceinline__ void load_angles(const float *p, float (&c)[N]) {
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-                for (int j = 0; j < E / 2; ++j) rotate_pair(x.t[2 * j], x.t[2 * j + 1], cs[e0 / 2 + j], sn[e0 / 2 + j]);
-            *reinterpret_cast<uint4 *>(dst + e0) = x.v;
-        } else if (item * E < p.half) {
-            const int e0 = item * E;
-            Piece<T> x, y;
-            x.v = load<T, true>(src + e0);
-            y.v = load<T, true>(src + e0 + p.half);
-#pragma unroll
-            for (int j = 0; j < E; ++j) rotate_pair(x.t[j], y.t[j], cs[e0 + j], sn[e0 + j]);
-            *reinterpret_cast<uint4 *>(dst + e0) = x.v;
-            *reinterpret_cast<uint4 *>(dst + e0 + p.half) = y.v;
-        } else {
-            const int e0 = item * E + p.half;
-            *reinterpret_cast<uint4 *>(dst + e0) = load<T, true>(src + e0);
+        for (int j = 0; j < N; j += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + j);
+            c[j] = x.x;
+            c[j + 1] = x.y;
+            c[j + 2] = x.z;
+            c[j + 3] = x.w;
         }
-    } else if (item < p.half) {
+    } else {
+        static_assert(N == 2, "pairs of 2, 4 or 8");
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        c[0] = x.x;
+        c[1] = x.y;
+    }
+}
+
+// One lane's item of one head of q (VEC): a piece, or two that hold each other's pairs (b is of the second, or unused).
+struct Item {
+    int a, b;       // their first elements; b < 0: there is none
+    int first;      // the first pair, below 0: they stay as they are
+};
+template <int E>
+__device__ __forceinline__ Item item_of(const StoreParams &p, int item) {
+    if (p.interleaved) return {item * E, -1, item * E < 2 * p.half ? item * E / 2 : -1};
+    if (item * E < p.half) return {item * E, item * E + p.half, item * E};
+    return {item * E + p.half, -1, -1};
+}
+template <typename T, int E = 16 / sizeof(T)>
+__device__ __forceinline__ void rotate_item(const StoreParams &p, const Item &it, const uint4 &va, const uint4 &vb, T *dst,
+                                            const float *cs, const float *sn) {
+    using namespace store;
+    Piece<T> x, y;
+    x.v = va;
+    y.v = vb;
+    if (it.b >= 0) {
+        float c[E], s[E];
+        load_angles<E>(cs + it.first, c);
+        load_angles<E>(sn + it.first, s);
+#pragma unroll
+        for (int j = 0; j < E; ++j) rotate_pair(x.t[j], y.t[j], c[j], s[j]);
+        *reinterpret_cast<uint4 *>(dst + it.b) = y.v;
+    } else if (it.first >= 0) {
+        float c[E / 2], s[E / 2];
+        load_angles<E / 2>(cs + it.first, c);
+        load_angles<E / 2>(sn + it.first, s);
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) rotate_pair(x.t[2 * j], x.t[2 * j + 1], c[j], s[j]);
+    }
+    *reinterpret_cast<uint4 *>(dst + it.a) = x.v;
+}
+// any alignment: an item is a pair, or an element that stays
+template <typename T>
+__device__ __forceinline__ void rotate_item(const StoreParams &p, const T *src, T *dst, int item, const float *cs, const float *sn) {
+    using namespace store;
+    if (item < p.half) {
         const int a = p.interleaved ? 2 * item : item, b = p.interleaved ? a + 1 : a + p.half;
         T x = src[a], y = src[b];
         rotate_pair(x, y, cs[item], sn[item]);
@@ -232,14 +268,15 @@ template <typename T, int BITS, bool ROT, bool VEC, int U>
 __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
     using namespace store;
     constexpr int E = 16 / sizeof(T), PER = 32 / E;  // elements a lane, lanes a block
-    extern __shared__ float angles[];                // ROT: cos, then sin, [token of the block][pair]
+    extern __shared__ __align__(16) float angles[];  // ROT: cos, then sin, [token of the block][pair]
     __shared__ int64_t rows[8 * U];
     const int tokens = blockDim.y * U, tid = threadIdx.y * blockDim.x + threadIdx.x;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
     const bool stores = static_cast<int>(blockIdx.y) < p.kv_y;
     const int at = (stores ? blockIdx.y : blockIdx.y - p.kv_y) * blockDim.x + threadIdx.x;
 
-    if constexpr (ROT) {
+    // by all threads, once what they load is on its way
+    auto turn_all = [&] {
         const int pairs = static_cast<int>(min(static_cast<int64_t>(tokens), p.n - first)) * p.half;
         for (int i = tid; i < pairs; i += blockDim.x * blockDim.y) {
             const int t = i / p.half, k = i - t * p.half;
@@ -249,18 +286,38 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
             s = __fmul_rn(s, p.factor);
             angles[tokens * p.half + i] = p.back ? -s : s;
         }
+    };
+    if constexpr (ROT) {
         if (!stores) {
-            __syncthreads();
-            if (at >= p.q_lanes) return;
-            const int h = at / p.q_items, item = at - h * p.q_items;
+            const int h = at / max(p.q_items, 1), item = at - h * p.q_items;
+            const T *src = static_cast<const T *>(p.q) + (first + threadIdx.y) * p.q_row + h * p.q_head;
+            T *dst = static_cast<T *>(p.out) + (first + threadIdx.y) * p.out_row + h * p.out_head;
+            const int64_t step = blockDim.y * p.q_row, step_out = blockDim.y * p.out_row;
+            // tokens of this lane
+            const int mine = at < p.q_lanes ? static_cast<int>(min(max((p.n - first - threadIdx.y + blockDim.y - 1) / blockDim.y, int64_t{0}),
+                                                                   static_cast<int64_t>(U))) : 0;
+            if constexpr (VEC) {
+                const Item it = item_of<E>(p, item);
+                uint4 a[U], b[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = u * blockDim.y + threadIdx.y;
-                const int64_t i = first + t;
-                if (i >= p.n) break;
-                const T *src = static_cast<const T *>(p.q) + i * p.q_row + h * p.q_head;
-                T *dst = static_cast<T *>(p.out) + i * p.out_row + h * p.out_head;
-                rotate_item<T, VEC>(p, src, dst, item, angles + t * p.half, angles + (tokens + t) * p.half);
+                for (int u = 0; u < U; ++u) {
+                    a[u] = u < mine ? load<T, true>(src + u * step + it.a) : make_uint4(0, 0, 0, 0);
+                    b[u] = u < mine && it.b >= 0 ? load<T, true>(src + u * step + it.b) : make_uint4(0, 0, 0, 0);
+                }
+                turn_all();
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int t = u * blockDim.y + threadIdx.y;
+                    if (u < mine) rotate_item<T>(p, it, a[u], b[u], dst + u * step_out, angles + t * p.half, angles + (tokens + t) * p.half);
+                }
+            } else {
+                turn_all();
+                __syncthreads();
+                for (int u = 0; u < mine; ++u) {
+                    const int t = u * blockDim.y + threadIdx.y;
+                    rotate_item<T>(p, src + u * step, dst + u * step_out, item, angles + t * p.half, angles + (tokens + t) * p.half);
+                }
             }
             return;
         }
@@ -304,6 +361,7 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
         }
         rows[tid] = r;
     }
+    if constexpr (ROT) turn_all();
     __syncthreads();
     const int lane = threadIdx.x & 31, of = lane & (PER - 1), first_lane = lane - of;  // (blockDim.x: whole warps)
 #pragma unroll
@@ -321,17 +379,23 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
                 const float *cs = angles + t * p.half, *sn = angles + (tokens + t) * p.half;
                 if (VEC && !p.interleaved) {
                     const int i0 = e0 < p.half ? e0 : e0 - p.half;
+                    const uint32_t sign = e0 < p.half ? 0x80000000u : 0u;
+                    float c[E], s[E];
+                    load_angles<E>(cs + i0, c);
+                    load_angles<E>(sn + i0, s);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        const float s = e0 < p.half ? -sn[i0 + j] : sn[i0 + j];
-                        y[0][j] = __fadd_rn(__fmul_rn(y[0][j], cs[i0 + j]), __fmul_rn(to_f32(oth[VEC ? u : 0].t[j]), s));
-                    }
+                    for (int j = 0; j < E; ++j)
+                        y[0][j] = __fadd_rn(__fmul_rn(y[0][j], c[j]),
+                                            __fmul_rn(to_f32(oth[VEC ? u : 0].t[j]), __uint_as_float(__float_as_uint(s[j]) ^ sign)));
                 } else if (VEC) {
+                    float c[E / 2], s[E / 2];
+                    load_angles<E / 2>(cs + e0 / 2, c);
+                    load_angles<E / 2>(sn + e0 / 2, s);
 #pragma unroll
                     for (int j = 0; j < E; j += 2) {
-                        const float c = cs[(e0 + j) / 2], s = sn[(e0 + j) / 2], a = y[0][j], z = y[0][j + 1];
-                        y[0][j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(z, s));
-                        y[0][j + 1] = __fadd_rn(__fmul_rn(z, c), __fmul_rn(a, s));
+                        const float a = y[0][j], z = y[0][j + 1];
+                        y[0][j] = __fsub_rn(__fmul_rn(a, c[j / 2]), __fmul_rn(z, s[j / 2]));
+                        y[0][j + 1] = __fadd_rn(__fmul_rn(z, c[j / 2]), __fmul_rn(a, s[j / 2]));
                     }
                 } else {
                     const T *src = static_cast<const T *>(p.in[0]) + (first + t) * p.row[0] + h * p.head[0];
@@ -455,15 +519,20 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
 
 // Tokens a lane of a large call (kv_cache.cu's measurements)
 constexpr int kStoreTokens = 4;
+// with k's other halves and its angles a lane holds more: 8192 tokens of 8 heads x 128 and 32 of q, bf16: 48.5 us with 4,
+// 46.3 with 2; q alone (f32, 5003 tokens of 12 heads of 80) 7.5 us with 4, 8.9 with 2
+constexpr int kRotateStoreTokens = 2;
 
 template <typename T, int BITS, bool ROT>
 void launch_store(const StoreParams &p, bool vec, const Shape &s, size_t smem, cudaStream_t stream) {
     if (!vec)
         kv_store_kernel<T, BITS, ROT, false, 1><<<s.grid, s.block, smem, stream>>>(p);
-    else if (s.many)
-        kv_store_kernel<T, BITS, ROT, true, kStoreTokens><<<s.grid, s.block, smem, stream>>>(p);
-    else
+    else if (!s.many)
         kv_store_kernel<T, BITS, ROT, true, 1><<<s.grid, s.block, smem, stream>>>(p);
+    else if (ROT && p.kv_y > 0)
+        kv_store_kernel<T, BITS, ROT, true, ROT ? kRotateStoreTokens : kStoreTokens><<<s.grid, s.block, smem, stream>>>(p);
+    else if (!ROT || BITS == 8)  // (what only rotates comes as 8 bits)
+        kv_store_kernel<T, BITS, ROT, true, !ROT || BITS == 8 ? kStoreTokens : 1><<<s.grid, s.block, smem, stream>>>(p);
 }
 
 }  // namespace kv

@@ -27,15 +27,16 @@ q8mv_status_t launch(StoreParams p, int bits, int type, bool vec, cudaStream_t s
     if (q_lanes >= (1LL << 31)) return Q8MV_ERR_INVALID_ARG;
     p.q_lanes = static_cast<int>(q_lanes);
     // the blocks' shape is that of the stored lanes, if there are any
-    Shape s = shape(p.lanes > 0 ? p.lanes : p.q_lanes, p.n, kStoreTokens);
+    const int tokens = p.lanes > 0 ? kRotateStoreTokens : kStoreTokens;
+    Shape s = shape(p.lanes > 0 ? p.lanes : p.q_lanes, p.n, tokens);
     p.kv_y = p.lanes > 0 ? static_cast<int>(s.grid.y) : 0;
     const int64_t q_y = ceil_div(p.q_lanes, s.block.x);
     if (p.kv_y + q_y > 65535) return Q8MV_ERR_INVALID_ARG;
-    const auto bytes = [&](int tokens) { return static_cast<size_t>(s.block.y) * tokens * p.half * 2 * sizeof(float); };
-    if (!vec || bytes(kStoreTokens) > 32768) s.many = false;
-    s.grid = dim3(static_cast<unsigned>(ceil_div(p.n, static_cast<int64_t>(s.block.y) * (s.many ? kStoreTokens : 1))),
+    const auto bytes = [&](int each) { return static_cast<size_t>(s.block.y) * each * p.half * 2 * sizeof(float); };
+    if (!vec || bytes(tokens) > 32768) s.many = false;
+    s.grid = dim3(static_cast<unsigned>(ceil_div(p.n, static_cast<int64_t>(s.block.y) * (s.many ? tokens : 1))),
                   static_cast<unsigned>(p.kv_y + q_y));
-    const size_t smem = bytes(s.many ? kStoreTokens : 1);
+    const size_t smem = bytes(s.many ? tokens : 1);
     if (bits == 4)
         launch_rotate_4(p, type, vec, s, smem, stream);
     else

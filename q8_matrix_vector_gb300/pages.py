@@ -79,7 +79,7 @@ class Pages(_Plan):
         at_lengths = _ints(lengths, torch.int32, n, device, "lengths")
         at_tokens = _ints(tokens, torch.int32, n, device, "tokens")
         slots = torch.empty((n, width), dtype=torch.int64, device=self._where)
-        src, dst, ok = torch.empty(3, n, dtype=torch.int32, device=self._where).unbind()
+        src, dst, ok = torch.empty_like(self.held), torch.empty_like(self.held), torch.empty_like(self.held)
         self._run(self._extend, "kvpage_extend", at_lengths, at_tokens, width, slots.data_ptr(), src.data_ptr(),
                   dst.data_ptr(), ok.data_ptr())
         return slots, src, dst, ok
@@ -98,7 +98,7 @@ class Pages(_Plan):
         """Moves the held pages to the lowest numbers.  Returns (src, dst [pages // 2], count [1], int32): pages
         src[i] are dst[i] now for i < count, -1 behind (call ``copy_pages(src, dst, count)`` of every cache next)."""
         most = self.pages // 2
-        src, dst = torch.empty(2, most, dtype=torch.int32, device=self._where).unbind()
-        count = torch.empty(1, dtype=torch.int32, device=self._where)
+        src = torch.empty(most, dtype=torch.int32, device=self._where)
+        dst, count = torch.empty_like(src), torch.empty(1, dtype=torch.int32, device=self._where)
         self._run(self._compact, "kvpage_compact", src.data_ptr(), dst.data_ptr(), count.data_ptr())
         return src, dst, count
