@@ -69,8 +69,10 @@ q8mv_status_t q4kv_cache_move(const q4kv_cache_t *cache, int64_t batch, int64_t 
  * not seen.  Arithmetic: codes are exact in f16; queries as there; each block's
  * products accumulate in f32 with the 8 taken off, its scale is folded in f32, the
  * softmax runs in f32, and its weights times the values' scales enter the second
- * product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs).  Nothing in
- * it waits.
+ * product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs).  With more than
+ * 32 bf16 query rows a request and kv head (head_dim up to 128), and page tables long
+ * enough, keys enter the first product exactly and values the second with f16's 11
+ * bits.  A scale that is not finite makes all of a row that sees its key NaN.
  */
 typedef struct q4kv_attend_s *q4kv_attend_plan_t;
 
@@ -78,6 +80,9 @@ q8mv_status_t q4kv_attend_plan(q4kv_attend_plan_t *out, int32_t heads_q, int32_t
                                int32_t max_requests, int64_t max_rows, int device);
 q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, const q8kv_attend_args_t *args,
                           cudaStream_t stream);
+/* As q8kv_attend_check and q8kv_attend_set_wait. */
+q8mv_status_t q4kv_attend_check(q4kv_attend_plan_t plan, int32_t *device_error);
+q8mv_status_t q4kv_attend_set_wait(q4kv_attend_plan_t plan, uint64_t wait_ns);
 /* Synchronises the plan's device, then releases its workspace.  NULL is accepted. */
 q8mv_status_t q4kv_attend_destroy(q4kv_attend_plan_t plan);
 

@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 UNITS = [os.path.join(CSRC, name) for name in
          ("q8mv.cu", "batched.cu", "pair.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_f32.cu", "kv_attend_f16.cu",
           "kv_attend_bf16.cu", "kv_attend_tc.cu", "kv_verify.cu", "kv4_cache.cu", "kv4_attend.cu", "kv4_attend_f32.cu",
-          "kv4_attend_f16.cu", "kv4_attend_bf16.cu", "kvrope.cu", "kvrope_4.cu", "kvrope_8.cu", "kv_pages.cu")]
+          "kv4_attend_f16.cu", "kv4_attend_bf16.cu", "kv4_attend_tc.cu", "kvrope.cu", "kvrope_4.cu", "kvrope_8.cu", "kv_pages.cu")]
 SRC = UNITS[0]
 HDR = os.path.join(ROOT, "include", "q8mv.h")
 HDRS = [HDR] + [os.path.join(ROOT, "include", name) for name in ("q8kv.h", "q4kv.h", "kvrope.h", "kvpage.h")]

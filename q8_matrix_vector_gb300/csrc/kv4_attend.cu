@@ -2,6 +2,12 @@
 #include "kv4_attend.h"
 
 #include <algorithm>
+#ifndef TCROWS
+#define TCROWS 32
+#endif
+#ifndef TCTILES
+#define TCTILES 4096
+#endif
 #include <new>
 
 namespace kv {
@@ -19,6 +25,8 @@ Attend4Variant variant4(int dim, int type, Attend4Shape shape) {
 
 }  // namespace kv
 
+static constexpr uint64_t kDefaultWaitNs = 2000000000ull;
+
 struct q4kv_attend_s {
     int device = 0;
     int heads_q = 0, heads_kv = 0, dim = 0;
@@ -26,9 +34,13 @@ struct q4kv_attend_s {
     int64_t max_rows = 0;
     kv::Attend4Variant variant[3][kv::kAttend4Shapes];  // per type
     int grid[3][kv::kAttend4Shapes] = {};               // and their CTAs: every SM full
+    kv::AttendVariant tc;                               // bf16, 128 rows
+    int tc_grid = 0;
     int64_t max_items = 0;
     float *partial = nullptr;
     unsigned *tickets = nullptr;
+    int *err = nullptr;
+    uint64_t wait_ns = kDefaultWaitNs;
 };
 
 extern "C" {
@@ -74,15 +86,27 @@ q8mv_status_t q4kv_attend_plan(q4kv_attend_plan_t *out, int32_t heads_q, int32_t
             tickets = std::max(tickets, items + 2 * kv::ceil_div(p->grid[t][v], kv::kJoinGroup));
             floats = std::max<int64_t>(floats, 2LL * p->grid[t][v] * k.rows * (head_dim + kv::kPartExtra));
         }
+    p->tc = kv::attend4_variant_tc(kv::blocks4(head_dim));
+    if (e == cudaSuccess && p->tc.fn != nullptr) {
+        int ctas = 0;
+        e = cudaFuncSetAttribute(p->tc.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p->tc.smem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, p->tc.fn, p->tc.threads, p->tc.smem);
+        p->tc_grid = sms * std::max(1, ctas);
+        tickets = std::max(tickets, items + 2 * kv::ceil_div(p->tc_grid, kv::kJoinGroup));
+        floats = std::max<int64_t>(floats, 2LL * p->tc_grid * p->tc.part);
+    }
     if (e == cudaSuccess) e = cudaMalloc(&p->partial, sizeof(float) * static_cast<size_t>(floats));
     if (e == cudaSuccess) e = cudaMalloc(&p->tickets, sizeof(unsigned) * static_cast<size_t>(tickets));
     if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, sizeof(unsigned) * static_cast<size_t>(tickets));
+    if (e == cudaSuccess) e = cudaMalloc(&p->err, sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(int));
     // the zeros, before any stream may use them
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaGetLastError();
         if (p->partial) cudaFree(p->partial);
         if (p->tickets) cudaFree(p->tickets);
+        if (p->err) cudaFree(p->err);
         delete p;
         return q8i::cuda_status(e);
     }
@@ -150,10 +174,22 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     p.tickets = plan->tickets;
     p.tickets_n = static_cast<int>(plan->max_items);
     p.group_tickets = plan->tickets + plan->max_items;
+    p.err = plan->err;
+    p.wait_ns = plan->wait_ns;
+    p.dim = c.dim;
+    p.q_vec = kv::aligned(a->q, 16) && ((a->q_row | a->q_head) & 7) == 0;
+    p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;
     // 8 rows at a time or 16, by the mean rows of a request: the fewest that hold them; heads above 128 by 8 alone, as
     // 16 do not fit the registers.
     const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
     const bool wide = mean > 8 && c.blocks <= 4;
+    // 128 bf16 rows at a time where there are more than 32 and enough to do (kv_attend.cu)
+    const int64_t reach = static_cast<int64_t>(a->table_cols) * r.page_size;
+    const double tiles = static_cast<double>(kv::ceil_div(mean, 16) * kv::ceil_div(reach, 128)) * a->requests * r.heads;
+    if (a->type == Q8KV_BF16 && plan->tc.fn != nullptr && mean > TCROWS && tiles >= TCTILES) {
+        plan->tc.fn<<<plan->tc_grid, plan->tc.threads, plan->tc.smem, stream>>>(p);
+        return q8i::cuda_status(cudaGetLastError());
+    }
     // Sixteen keys are one stretch of memory where a head's tokens of a page are, and start on 16 bytes.
     const int scales = 4 * r.blocks;  // bytes of a row's
     const bool in_turn = r.stride_token == 1 && r.page_size % 16 == 0 && (r.stride_page * scales) % 16 == 0 &&
@@ -164,6 +200,27 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     return q8i::cuda_status(cudaGetLastError());
 }
 
+q8mv_status_t q4kv_attend_check(q4kv_attend_plan_t p, int32_t *device_error) {
+    if (p == nullptr || device_error == nullptr) return Q8MV_ERR_INVALID_ARG;
+    kv::DeviceScope scope;
+    q8mv_status_t st = scope.enter(p->device);
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    int word = 0;
+    if (st == Q8MV_OK) st = q8i::cuda_status(cudaMemcpy(&word, p->err, sizeof(int), cudaMemcpyDeviceToHost));
+    if (st == Q8MV_OK && word != 0) {
+        st = q8i::cuda_status(cudaMemset(p->err, 0, sizeof(int)));
+        if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
+    }
+    *device_error = word;
+    return st;
+}
+
+q8mv_status_t q4kv_attend_set_wait(q4kv_attend_plan_t p, uint64_t wait_ns) {
+    if (p == nullptr || wait_ns > 10000000000ull) return Q8MV_ERR_INVALID_ARG;
+    p->wait_ns = wait_ns == 0 ? kDefaultWaitNs : wait_ns;
+    return Q8MV_OK;
+}
+
 q8mv_status_t q4kv_attend_destroy(q4kv_attend_plan_t p) {
     if (p == nullptr) return Q8MV_OK;
     kv::DeviceScope scope;
@@ -171,6 +228,7 @@ q8mv_status_t q4kv_attend_destroy(q4kv_attend_plan_t p) {
     if (st == Q8MV_OK) st = q8i::cuda_status(cudaDeviceSynchronize());
     if (p->partial) cudaFree(p->partial);
     if (p->tickets) cudaFree(p->tickets);
+    if (p->err) cudaFree(p->err);
     delete p;
     return st;
 }

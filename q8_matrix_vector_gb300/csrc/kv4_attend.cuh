@@ -27,7 +27,8 @@
 //     error was 5e-6 of its norm): for f32 the 8 is subtracted from f16 codes.
 //   * bf16: the weights go to f16 once and are transposed once for all blocks, and then
 //     multiplied by the values' scales in f16, two at a time: two roundings to 11 bits where
-//     the output's own has 8.
+//     the output's own has 8.  f16: the same with the weights in two f16 parts, whose products
+//     are again two, to 2^-22.  f32: products in f32, then two parts.
 // The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents.  The
 // running maximum moves only when a score is 2^kSlack above it, so that most steps need no
 // maximum over the lanes; f16 has the room.
@@ -142,9 +143,6 @@ __device__ __forceinline__ float scale_of(uint32_t w, int b) {
     return b & 1 ? __high2float(h) : __low2float(h);
 }
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 // with constant offsets of both
 template <int D, int S>
 __device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src) {
@@ -192,6 +190,11 @@ __device__ __forceinline__ uint32_t codes16(uint32_t w) {
     return w & 0x00F000F0u;
 }
 
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t y;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    return y;
+}
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     uint32_t y;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? KV4_CTAS : N
     q4kv_attend_kernel(const Attend4Params pp) {
     using S = Smem4<NB, NT, QP>;
     constexpr int ROWS = S::kRows, KEYS = kStepKeys * kWarps, W = (NB + 1) / 2;
-    constexpr bool EXACT = QP == 2, PACKED = sizeof(T) == 2 && PP == 1;
+    constexpr bool EXACT = QP == 2, PACKED = !EXACT;
     constexpr float kUnit = EXACT ? 1.0f : 16777216.0f;  // codes stand for so many
     const AttendParams &p = pp.a;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -688,13 +691,20 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? KV4_CTAS : N
                         __syncwarp();
                     }
                    // ---- O^T += V^T (P dV)^T, two blocks at a time (a word's halves), 16 keys at a time
-                    uint32_t dv[4][W], p2[NT][4];
+                    uint32_t dv[4][W], p2[NT][PP][4];
                     if constexpr (PACKED) {
                         // (the scales of the lane's keys of the second operand are read where they are paired)
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) p2[t][k] = transpose8(pack_half2(s[t][k][0], s[t][k][1]));
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t h = pack_half2(s[t][k][0], s[t][k][1]);
+                                p2[t][0][k] = transpose8(h);
+                                if constexpr (PP == 2) {
+                                    const float2 back = unpack_half2(h);
+                                    p2[t][PP - 1][k] = transpose8(pack_half2(s[t][k][0] - back.x, s[t][k][1] - back.y));
+                                }
+                            }
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) load_scales4<NB>(vs + (8 * k + place) * S::kScales, dv[k]);
@@ -721,7 +731,11 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? KV4_CTAS : N
                                                                b & 1 ? 0x7632u : 0x5410u);
 #pragma unroll
                                 for (int t = 0; t < NT; ++t) {
-                                    wgt[k >> 1][t][0][k & 1] = mul_half2(p2[t][k], d);
+                                    const uint32_t h = mul_half2(p2[t][0][k], d);
+                                    wgt[k >> 1][t][0][k & 1] = h;
+                                    // what that rounded off, and the lower part's product
+                                    if constexpr (PP == 2)
+                                        wgt[k >> 1][t][PP - 1][k & 1] = fma_half2(p2[t][PP - 1][k], d, fma_half2(p2[t][0][k], d, h ^ 0x80008000u));
                                 }
                                 continue;
                             }

@@ -27,5 +27,7 @@ enum Attend4Shape { k4Rows8 = 0, k4Rows16, k4Rows8InTurn, k4Rows16InTurn, kAtten
 Attend4Variant attend4_variant_f32(int blocks, Attend4Shape shape);
 Attend4Variant attend4_variant_f16(int blocks, Attend4Shape shape);
 Attend4Variant attend4_variant_bf16(int blocks, Attend4Shape shape);
+// 128 bf16 query rows at a time (kv_attend_tc.cuh), up to four blocks
+AttendVariant attend4_variant_tc(int blocks);
 
 }  // namespace kv

@@ -151,6 +151,7 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     p.tickets_n = static_cast<int>(plan->max_items);
     p.group_tickets = plan->tickets + plan->max_items;
     p.err = plan->err;
+    p.dim = p.c.dim;
     p.wait_ns = plan->wait_ns;
     p.q_vec = kv::aligned(a->q, 16) && ((a->q_row | a->q_head) & 7) == 0;
     p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;

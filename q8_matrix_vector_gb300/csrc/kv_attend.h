@@ -37,6 +37,7 @@ struct AttendParams {
     unsigned *group_tickets;  // two per kJoinGroup CTAs
     int *err;           // the plan's error word, and the bound on waits (kRows128)
     uint64_t wait_ns;
+    int dim;            // elements of a head (kRows128; the Q4_0 cache's rows are shorter)
     int q_vec, out_vec; // 16-byte loads of eight queries, stores of eight outputs are aligned (kRows128)
 };
 

@@ -4,8 +4,8 @@
 namespace kv {
 
 AttendVariant attend_variant_tc(int dim) {
-    if (dim <= 64) return {q8kv_attend_tc_kernel<64>, TcSmem<64>::kTotal, kTcThreads, TcSmem<64>::kPart};
-    if (dim <= 128) return {q8kv_attend_tc_kernel<128>, TcSmem<128>::kTotal, kTcThreads, TcSmem<128>::kPart};
+    if (dim <= 64) return {q8kv_attend_tc_kernel<64, 0>, TcSmem<64, 0>::kTotal, kTcThreads, TcSmem<64, 0>::kPart};
+    if (dim <= 128) return {q8kv_attend_tc_kernel<128, 0>, TcSmem<128, 0>::kTotal, kTcThreads, TcSmem<128, 0>::kPart};
     return {};
 }
 

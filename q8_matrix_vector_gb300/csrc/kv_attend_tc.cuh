@@ -1,5 +1,5 @@
-// Attention of wide draft trees over a Q8_0 cache on the 5th-generation tensor
-// cores (../../include/q8kv.h): up to 128 query rows (node, head of the group) of
+// Attention of wide draft trees over a Q8_0 cache (NB4 = 0) or a Q4_0 one of NB4
+// stored blocks on the 5th-generation tensor cores (../../include/q8kv.h, q4kv.h): up to 128 query rows (node, head of the group) of
 // one kv head at a time, bf16 queries and outputs.
 //
 //     S[r, j] = q[r] . K[j],   O[r] += P[r, j] V[j],   P = exp2(scale log2(e) S + E - M)
@@ -35,6 +35,7 @@
 // CTA's first scores are there and 10 us of joining cut items at the end.
 #pragma once
 
+#include "kv4_attend.h"
 #include "kv_attend.cuh"
 
 namespace kv {
@@ -53,16 +54,17 @@ constexpr int kTcItemUnits = 4;                 // an item's fixed cost in tiles
                                                 // 149, 114, 88.4, 86.5, 86.0, 89.6 us with 1 .. 6; 24 of 300 .. 3000, 68 rows: 83.1 with 4,
                                                 // 83.6 with 5)
 
-template <int DP>
+template <int DP, int NB4>
 struct TcSmem {
     static constexpr int kTile = DP / 64 * kTcHalf;   // one operand of 128 rows: 64 e after 64 e
     static constexpr int kQ = 0, kK = kTile, kLo = 2 * kTile, kV = 3 * kTile, kMeta = 4 * kTile;
     static constexpr int kMetaTile = kTcKeys * 16;    // per key: K's factor, E, 2^-E, flag
     // a convert warp's keys of a tile as they are in the cache: codes of K and V, scales of both
     // (a row's pitch is 16 mod 128 bytes: 8 lanes read 16 bytes of 8 rows)
-    static constexpr int kRaw = kMeta + 4 * kMetaTile, kRawPitch = DP + 16;
+    static constexpr int kRaw = kMeta + 4 * kMetaTile, kRawPitch = NB4 == 0 ? DP + 16 : NB4 == 3 ? 80 : 16 * NB4 + 16;
+    static constexpr int kScales = NB4 == 0 ? DP / 32 * 4 : NB4 == 2 ? 4 : 8;  // bytes of a row's
     static constexpr int kRawV = kTcWarpKeys * kRawPitch, kRawS = 2 * kTcWarpKeys * kRawPitch;
-    static constexpr int kRawWarp = 2 * kTcWarpKeys * kRawPitch + 2 * kTcWarpKeys * (DP / 32) * 4;
+    static constexpr int kRawWarp = 2 * kTcWarpKeys * kRawPitch + 2 * kTcWarpKeys * kScales;
     static constexpr int kUsed = kRaw + 2 * kTcConvWarps * kRawWarp;  // of two tiles
     static constexpr int kTotal = kUsed + 1024;  // the swizzled tiles begin on 1024 bytes
     static constexpr int kPart = kTcRows * (DP + 2);  // floats of a partial result: O by 4 columns x 128 rows, m, l
@@ -194,6 +196,45 @@ __device__ __forceinline__ uint32_t tc_scaled(uint32_t codes, uint32_t hi, uint3
     return y;
 }
 
+// 8 N4 bytes of a Q4_0 row
+template <int N4>
+__device__ __forceinline__ void tc_load4(const unsigned char *at, uint32_t (&w)[2 * N4]) {
+    if constexpr (N4 == 3) {
+#pragma unroll
+        for (int i = 0; i < 2 * N4; i += 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(at + 4 * i);
+            w[i] = x.x;
+            w[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * N4; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(at + 4 * i);
+            w[i] = x.x;
+            w[i + 1] = x.y;
+            w[i + 2] = x.z;
+            w[i + 3] = x.w;
+        }
+    }
+}
+// Eight codes of a word times their scale: pairs (0, 4), (1, 5), (2, 6), (3, 7), the order in which they come out of it; q's
+// elements and the output's have it in their eights as well.  A code times a scale of 11 bits has 15: exact in two parts.
+template <bool REST>
+__device__ __forceinline__ void tc_eight4(uint32_t x, float scale, uint32_t *o, uint32_t *rest) {
+    const uint32_t d = pack_half2(scale, scale);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t y = j < 2 ? x : x >> 8;
+        uint32_t c;
+        if (j & 1)  // (1024 + 16 c) / 16 - 72
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c) : "r"((y & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+        else
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"((y & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(c), "r"(d));
+        if constexpr (REST) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest[j]) : "r"(c), "r"(d), "r"(o[j] ^ 0x80008000u));
+    }
+}
+
 // power of two with exponent e
 __device__ __forceinline__ float tc_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -223,10 +264,10 @@ struct TcTile {
     bool any;
 };
 
-template <int DP>
+template <int DP, int NB4>
 __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const AttendParams p) {
     using T = __nv_bfloat16;
-    using S = TcSmem<DP>;
+    using S = TcSmem<DP, NB4>;
     constexpr int PARTS = DP / 16, KPL = 32 / PARTS, NL = kTcWarpKeys / KPL;  // 16-byte pieces of a row, keys of a load, loads
     constexpr int NB = DP / 32, WK = kTcWarpKeys;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -436,7 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
     } else if (warp >= kTcSoftWarps) {
         // ================ convert
         const int cw = warp - kTcSoftWarps, part = lane % PARTS, sub = lane / PARTS;
-        const bool live = part * 16 < p.c.dim;
+        const bool live = part * 16 < p.dim;
         const int ct = tid - kTcSoftWarps * 32;  // thread among the convert warps
         unsigned char *const raws = smem + S::kRaw + cw * (2 * S::kRawWarp);  // by tile % 2: K, V, scales of K [key][NB], of V
         for (int i = lane; i < 2 * S::kRawWarp / 16; i += 32) reinterpret_cast<uint4 *>(raws)[i] = make_uint4(0, 0, 0, 0);
@@ -482,6 +523,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         };
         const bool wide_scales = NB == 4 && p.c.blocks == 4;
         auto codes = [&](const int8_t *from, uint32_t to, uint32_t row) {  // the warp's rows of one array
+            if constexpr (NB4 != 0) {
+#pragma unroll
+                for (int j = 0; j < (WK * NB4 + 31) / 32; ++j) {
+                    const int i = lane + 32 * j, key = min(i / (NB4 != 0 ? NB4 : 1), WK - 1), piece = i % (NB4 != 0 ? NB4 : 1);
+                    const uint32_t r = __shfl_sync(~0u, row, key);
+                    if (r != kNoRow && i < WK * NB4)
+                        cp_async16(to + key * S::kRawPitch + piece * 16, from + static_cast<uint64_t>(r) * (16 * NB4) + piece * 16);
+                }
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
                 const uint32_t r = __shfl_sync(~0u, row, j * KPL + sub);
@@ -493,8 +544,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             unsigned char *raw = raws + (g & 1) * S::kRawWarp;
             float *raw_s = reinterpret_cast<float *>(raw + S::kRawS);
             codes(p.c.k_codes, tc_smem(raw), row);
-            const uint32_t at = tc_smem(raw_s) + lane * (NB * 4);
-            if (row != kNoRow) {
+            const uint32_t at = tc_smem(raw_s) + lane * S::kScales;
+            if constexpr (NB4 != 0) {
+                if (row != kNoRow) {
+                    const char *ks = reinterpret_cast<const char *>(p.c.k_scales) + static_cast<uint64_t>(row) * S::kScales;
+                    const char *vs = reinterpret_cast<const char *>(p.c.v_scales) + static_cast<uint64_t>(row) * S::kScales;
+                    if constexpr (S::kScales == 8) {
+                        cp_async8(at, ks);
+                        cp_async8(at + WK * S::kScales, vs);
+                    } else {
+                        cp_async4(at, ks);
+                        cp_async4(at + WK * S::kScales, vs);
+                    }
+                } else if (lane < WK) {
+#pragma unroll
+                    for (int b = 0; b < S::kScales / 4; ++b)
+                        raw_s[lane * (S::kScales / 4) + b] = raw_s[WK * (S::kScales / 4) + lane * (S::kScales / 4) + b] = 0.0f;
+                }
+            } else if (row != kNoRow) {
                 const float *ks = p.c.k_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
                 const float *vs = p.c.v_scales + static_cast<uint64_t>(row) * static_cast<uint32_t>(p.c.blocks);
                 if (wide_scales) {
@@ -541,6 +608,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 o[i] = tc_scaled(unbias(__byte_perm(in[i / 2], 0x64646464u, i % 2 ? 0x4342u : 0x4140u)), h2, l2, rest ? &(*rest)[i] : nullptr);
             store(tile, piece, o);
         };
+        // Q4_0: half of the lane's key's blocks
+        constexpr int N4 = NB4 != 0 ? NB4 : 2;
+        auto convert4_k = [&](const unsigned char *from, const float(&scale)[NB]) {
+            uint32_t w[2 * N4];
+            tc_load4<N4>(from + key * S::kRawPitch + odd_piece * 8 * N4, w);
+#pragma unroll
+            for (int b = 0; b < N4; ++b) {
+                uint32_t o[8], rest[8];
+                tc_eight4<true>(w[b], scale[b], o, rest);
+                tc_eight4<true>(w[N4 + b], scale[b], o + 4, rest + 4);
+                store(base + S::kK, 2 * b + odd_piece, o);
+                store(base + S::kLo, 2 * b + odd_piece, rest);
+            }
+        };
+        auto convert4_v = [&](const unsigned char *from, const float(&scale)[NB]) {
+            uint32_t w[2 * N4];
+            tc_load4<N4>(from + key * S::kRawPitch + odd_piece * 8 * N4, w);
+#pragma unroll
+            for (int b = 0; b < N4; ++b) {
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // units 2 i and 2 i + 1 of 16 bits
+                    const int k0 = 2 * i * N4 + b, k1 = k0 + N4;
+                    tc_eight4<false>(__byte_perm(w[k0 / 2], w[k1 / 2], (k0 & 1 ? 0x32u : 0x10u) | (k1 & 1 ? 0x7600u : 0x5400u)), scale[b],
+                                     o + 4 * i, nullptr);
+                }
+                store(base + S::kV, 2 * b + odd_piece, o);
+            }
+        };
         auto waited = [&](uint64_t *bar, int64_t phase) -> bool {  // whole warps
             if (!tc_wait(bar, static_cast<uint32_t>(phase) & 1u, leaving, p.wait_ns)) bad = true;
             bad = __any_sync(~0u, bad);
@@ -570,7 +667,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     const int e = 8 * (g0 + k);
                     Eight y;
                     y.u = make_uint4(0, 0, 0, 0);
-                    if (r < rows && e < p.c.dim) {
+                    if (r < rows && e < p.dim) {
                         if (p.q_vec) {
                             y.u = __ldg(reinterpret_cast<const uint4 *>(src + e));
                         } else {
@@ -596,7 +693,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     const Eight y = eight(k);
                     uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(to_f32(y.t[2 * e]) * down, to_f32(y.t[2 * e + 1]) * down);
+                    for (int e = 0; e < 4; ++e) {
+                        const int e0 = NB4 == 0 ? 2 * e : e, e1 = NB4 == 0 ? e0 + 1 : e + 4;
+                        o[e] = pack_half2(to_f32(y.t[e0]) * down, to_f32(y.t[e1]) * down);
+                    }
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + tc_place(r, g0 + k)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
                 }
                 if (g0 == 0)
@@ -619,8 +719,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 uint32_t bk = 0, bv = 0;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    k_scale[b] = raw_s[key * NB + b];
-                    v_scale[b] = raw_s[WK * NB + key * NB + b];
+                    if constexpr (NB4 != 0) {
+                        constexpr int SB = S::kScales / 2;
+                        const __half *hs = reinterpret_cast<const __half *>(raw_s) + key * SB;
+                        k_scale[b] = b < NB4 ? __half2float(hs[b < NB4 ? b : 0]) : 0.0f;
+                        v_scale[b] = b < NB4 ? __half2float(hs[WK * SB + (b < NB4 ? b : 0)]) : 0.0f;
+                    } else {
+                        k_scale[b] = raw_s[key * NB + b];
+                        v_scale[b] = raw_s[WK * NB + key * NB + b];
+                    }
                     bk = max(bk, __float_as_uint(k_scale[b]) & 0x7FFFFFFFu);
                     bv = max(bv, __float_as_uint(v_scale[b]) & 0x7FFFFFFFu);
                 }
@@ -641,8 +748,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             }
             // ---- K
             const uint32_t kb = base + S::kK;
+            if constexpr (NB4 != 0) convert4_k(raw, k_scale);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
+            for (int b = 0; b < (NB4 != 0 ? 0 : NB); ++b) {
                 uint32_t rest[8];
                 convert(kb, 2 * b + odd_piece, raw, k_scale[b], &rest);
                 store(base + S::kLo, 2 * b + odd_piece, rest);
@@ -663,14 +771,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             cp_wait<3>();  // K of g + 1 .. g + 2 and V of g + 1 may be on their way
             __syncwarp();
             if (g >= 1 && !waited(v_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
+            if constexpr (NB4 != 0) convert4_v(raws + (g & 1) * S::kRawWarp + S::kRawV, scale);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) convert(base + S::kV, 2 * b + odd_piece, raws + (g & 1) * S::kRawWarp + S::kRawV, scale[b], nullptr);
+            for (int b = 0; b < (NB4 != 0 ? 0 : NB); ++b) convert(base + S::kV, 2 * b + odd_piece, raws + (g & 1) * S::kRawWarp + S::kRawV, scale[b], nullptr);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc_arrive(&v_full);
             issue_b(row_after, g + 2);
             return true;
         };
+        if constexpr (NB4 == 3) {  // there is no fourth block: it stays 0
+            const uint32_t none[8] = {};
+            store(base + S::kK, 6 + odd_piece, none);
+            store(base + S::kLo, 6 + odd_piece, none);
+            store(base + S::kV, 6 + odd_piece, none);
+        }
         if (lane == 0) {
             TcTile t;
             t.w = w;
@@ -912,13 +1027,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     if (r >= rows) return;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        if (e0 + e < p.c.dim) {
+                        if (e0 + e < p.dim) {
                             union {
                                 uint4 u;
                                 T t[8];
                             } y;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) y.t[k] = from_f32<T>(v[e + k] * inv);
+                            for (int k = 0; k < 8; ++k) y.t[k] = from_f32<T>(v[e + (NB4 == 0 ? k : k < 4 ? 2 * k : 2 * k - 7)] * inv);
                             if (p.out_vec) {
                                 *reinterpret_cast<uint4 *>(out + e0 + e) = y.u;
                             } else {

@@ -400,16 +400,16 @@ class TreeAttention(_Plan):
     def check(self) -> int:
         """Synchronise and return (and clear) whether a bounded wait of the plan's kernels ran out (1, else 0)."""
         word = ctypes.c_int32()
-        status = _library().q8kv_attend_check(self._h, ctypes.byref(word))
+        status = getattr(_library(), self._name + "_check")(self._h, ctypes.byref(word))
         if status:
-            _fail(status, "q8kv_attend_check")
+            _fail(status, self._name + "_check")
         return word.value
 
     def set_wait(self, wait_ns: int = 0) -> None:
         """For tests of the bounded waits: their bound (0: the default)."""
-        status = _library().q8kv_attend_set_wait(self._h, int(wait_ns))
+        status = getattr(_library(), self._name + "_set_wait")(self._h, int(wait_ns))
         if status:
-            _fail(status, "q8kv_attend_set_wait")
+            _fail(status, self._name + "_set_wait")
 
 
 class TreeVerify(_Plan):

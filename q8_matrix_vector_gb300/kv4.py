@@ -28,6 +28,8 @@ def _bind(lib: ctypes.CDLL) -> None:
             ("kvpage_copy_q4", [ref(CacheDesc), i64, p, p, p, p]),
             ("q4kv_attend_plan", [ref(p), i32, i32, i32, i32, i64, ctypes.c_int]),
             ("q4kv_attend", [p, ref(CacheDesc), p, p]),
+            ("q4kv_attend_check", [p, ref(i32)]),
+            ("q4kv_attend_set_wait", [p, ctypes.c_uint64]),
             ("q4kv_attend_destroy", [p])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
@@ -91,11 +93,8 @@ class Cache4(Cache):
 
 
 class TreeAttention4(TreeAttention):
-    """Attention of draft trees over a ``Cache4``: the arguments and results of ``TreeAttention``.  Its kernels wait for
-    nothing, so there is nothing to check."""
+    """Attention of draft trees over a ``Cache4``: the calls, arguments and results of ``TreeAttention``."""
 
     _destroy = "q4kv_attend_destroy"
     _name = "q4kv_attend"
     _cache = Cache4
-
-    check = set_wait = None

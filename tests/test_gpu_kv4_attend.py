@@ -262,3 +262,77 @@ def test_refusals(q8mv):
     with pytest.raises(q8mv.Q8mvError):
         q8mv.TreeAttention4(4, 2, 72, 2, 8)
     assert c.plan(c.q[:0], c.cache, table, lengths).shape == (0, 4, 64)
+
+
+def wide(q8mv, seed, lengths, nodes, **more):
+    """A case that 128 rows at a time take: more than 32 bf16 rows a request, and a table that reaches far."""
+    return Case(q8mv, seed, lengths, nodes, dtype="bfloat16", cols=131072 // more.get("page", 16), **more)
+
+
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 112, 128])
+@pytest.mark.parametrize("layout", ["head", "token"])
+@pytest.mark.parametrize("nodes,group", [([40, 0, 33, 64], 3), ([31, 31], 4), ([200, 7], 2)])
+def test_128_rows_at_a_time(q8mv, dim, layout, nodes, group):
+    lengths = [700, 3, 129, 0][:len(nodes)]
+    wide(q8mv, dim + nodes[0], lengths, nodes, group=group, dim=dim, layout=layout, page=32).check()
+
+
+def test_128_rows_cut_over_many_ctas(q8mv):
+    c = wide(q8mv, 31, [5000, 1300], [31, 31], heads=3, group=4, dim=128, page=16)
+    c.check()
+    out, lse = c.run()
+    for _ in range(3):
+        again = c.run()
+        assert (out == again[0]).all() and (lse == again[1]).all()
+    assert c.plan.check() == 0
+
+
+def test_128_rows_of_nothing_and_of_what_is_not_finite(q8mv):
+    import torch
+
+    wide(q8mv, 32, [0, 0], [40, 40], dim=128, density=0.0).check()
+    wide(q8mv, 33, [300, 0], [40, 40], dim=96, tree=False).check()
+    c = wide(q8mv, 34, [300, 60], [40, 40], dim=128)
+    for b in range(2):
+        c.seen[b][:, 1] = False
+    mask = c.mask.cpu().numpy().view(np.uint32)
+    mask[:, 0] &= ~np.uint32(2)
+    c.mask = torch.from_numpy(mask.view(np.int32)).cuda()
+    c.device()
+    for b, value in ((0, np.inf), (1, np.nan)):
+        pos = int(c.lengths[b]) + 1
+        for s in (c.cache.k_scales, c.cache.v_scales):
+            s[int(c.table[b, pos // 16]), :, pos % 16] = value
+    c.check(c.run())
+    # a prefix key that everyone sees
+    c.cache.v_scales[int(c.table[0, 2]), 1, 3] = float("inf")
+    out, _ = c.run()
+    assert torch.isnan(out[:40, 2:]).all() and not torch.isnan(out[:40, :2]).any() and not torch.isnan(out[40:]).any()
+
+
+def test_128_rows_strided(q8mv):
+    import torch
+
+    c = wide(q8mv, 35, [200, 70], [36, 40], heads=2, group=3, dim=80)
+    q = torch.zeros(c.rows, 7, 83, dtype=torch.bfloat16, device="cuda")
+    q[:, 1:, 2:82] = c.q
+    c.q = q[:, 1:, 2:82]
+    out = torch.full((c.rows + 1, 8, 85), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = c.run(out=out[:c.rows, 1:7, 3:83], scale=-0.2)
+    c.check(got, scale=-0.2)
+    out[:c.rows, 1:7, 3:83] = 7
+    assert (out == 7).all()
+
+
+def test_a_wait_that_runs_out_is_reported(q8mv):
+    """A bound of one nanosecond: the call ends, the plan says so, and its next call is as ever."""
+    c = wide(q8mv, 36, [3000, 1300], [31, 31], heads=3, group=4, dim=128)
+    want = [x.clone() for x in c.run()]
+    assert c.plan.check() == 0
+    c.plan.set_wait(1)
+    c.run()
+    assert c.plan.check() in (0, 1)  # (a wait may be over before its bound is looked at)
+    assert c.plan.check() == 0
+    c.plan.set_wait(0)
+    again = c.run()
+    assert (want[0] == again[0]).all() and (want[1] == again[1]).all() and c.plan.check() == 0
