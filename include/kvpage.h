@@ -30,7 +30,7 @@ typedef struct {
     int32_t *held;
 } kvpage_state_t;
 
-/* pages 1 .. 2^30, page_size 1 .. 65536, requests 1 .. 65536, columns 1 .. 2^24, requests * columns <= 2^30 */
+/* pages 1 .. 2^28, page_size 1 .. 65536, requests 1 .. 65535, columns 1 .. 2^24, requests * columns <= 2^28 */
 q8mv_status_t kvpage_plan(kvpage_plan_t *out, int64_t pages, int32_t page_size, int32_t requests, int32_t columns,
                           int device);
 
@@ -82,9 +82,9 @@ q8mv_status_t kvpage_destroy(kvpage_plan_t plan);
  * another's source or destination.  0 <= n < 2^31.
  */
 q8mv_status_t kvpage_copy_q8(const q8kv_cache_t *cache, int64_t n, const int32_t *src, const int32_t *dst,
-                                    const int32_t *count, cudaStream_t stream);
+                             const int32_t *count, cudaStream_t stream);
 q8mv_status_t kvpage_copy_q4(const q4kv_cache_t *cache, int64_t n, const int32_t *src, const int32_t *dst,
-                                    const int32_t *count, cudaStream_t stream);
+                             const int32_t *count, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

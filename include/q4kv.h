@@ -70,7 +70,7 @@ q8mv_status_t q4kv_cache_move(const q4kv_cache_t *cache, int64_t batch, int64_t 
  * products accumulate in f32 with the 8 taken off, its scale is folded in f32, the
  * softmax runs in f32, and its weights times the values' scales enter the second
  * product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs).  With more than
- * 32 bf16 query rows a request and kv head (head_dim up to 128), and page tables long
+ * 48 bf16 query rows a request and kv head (head_dim up to 128), and page tables long
  * enough, keys enter the first product exactly and values the second with f16's 11
  * bits.  A scale that is not finite makes all of a row that sees its key NaN.
  */

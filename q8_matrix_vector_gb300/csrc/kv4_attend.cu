@@ -2,12 +2,6 @@
 #include "kv4_attend.h"
 
 #include <algorithm>
-#ifndef TCROWS
-#define TCROWS 32
-#endif
-#ifndef TCTILES
-#define TCTILES 4096
-#endif
 #include <new>
 
 namespace kv {
@@ -179,18 +173,23 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     p.dim = c.dim;
     p.q_vec = kv::aligned(a->q, 16) && ((a->q_row | a->q_head) & 7) == 0;
     p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;
-    // 8 rows at a time or 16, by the mean rows of a request: the fewest that hold them; heads above 128 by 8 alone, as
-    // 16 do not fit the registers.
+    // 8 rows at a time or 16, by the mean rows of a request: the fewest that hold them (16 requests of 700 .. 4000 tokens, 8
+    // heads of 128, bf16: 12 rows 28.3 us by 16; one token each of groups of 8 is 8 rows); heads above 128 by 8 alone, as 16 do
+    // not fit the registers.
     const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
     const bool wide = mean > 8 && c.blocks <= 4;
-    // 128 bf16 rows at a time where there are more than 32 and enough to do (kv_attend.cu)
+    // 128 bf16 rows at a time where there are more than 48 and enough to do, in tiles of 16 rows x 128 keys of the tables'
+    // reach (kv_attend.cu): the 16 requests above, 48 rows 59.6 us by 16 and 69.1 by 128, 64 rows 75.9 and 70.6; one request
+    // of 124 rows over 8000 tokens (4032 tiles) 34.2 and 43.4, over 16000 (8064) 55.7 and 53.0; four over 2000 (4096) 36.7
+    // and 35.4, over 4000 (8192) 58.0 and 45.5; four of 64 rows over 8000 (8064) 55.3 and 57.3.
     const int64_t reach = static_cast<int64_t>(a->table_cols) * r.page_size;
     const double tiles = static_cast<double>(kv::ceil_div(mean, 16) * kv::ceil_div(reach, 128)) * a->requests * r.heads;
-    if (a->type == Q8KV_BF16 && plan->tc.fn != nullptr && mean > TCROWS && tiles >= TCTILES) {
+    if (a->type == Q8KV_BF16 && plan->tc.fn != nullptr && mean > 48 && tiles >= 8192) {
         plan->tc.fn<<<plan->tc_grid, plan->tc.threads, plan->tc.smem, stream>>>(p);
         return q8i::cuda_status(cudaGetLastError());
     }
-    // Sixteen keys are one stretch of memory where a head's tokens of a page are, and start on 16 bytes.
+    // Sixteen keys are one stretch of memory where a head's tokens of a page are, and start on 16 bytes (64 requests of 180 ..
+    // 8100 tokens: 85.9 us, key by key 89.2).
     const int scales = 4 * r.blocks;  // bytes of a row's
     const bool in_turn = r.stride_token == 1 && r.page_size % 16 == 0 && (r.stride_page * scales) % 16 == 0 &&
                          (r.stride_head * scales) % 16 == 0;

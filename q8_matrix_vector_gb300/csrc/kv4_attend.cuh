@@ -41,16 +41,10 @@
 
 namespace kv {
 
-#ifndef KV4_CTAS
-#define KV4_CTAS 3
-#endif
-#ifndef KV4_CTAS2
-#define KV4_CTAS2 2
-#endif
-#ifndef KV4_ST
-#define KV4_ST 2
-#endif
-constexpr int kStages4 = KV4_ST;
+// Steps in flight a warp, and CTAs an SM.  8 rows of up to 128: three CTAs (168 registers a thread); with four the registers
+// spill in the loop (two requests of 300k .. 524k tokens, bf16: 233 and 236 us; 64 of 180 .. 8100: 84.8 and 89.1), and
+// three steps with three CTAs gain nothing (233.0 and 233.0; 64 requests of 8000: 143.4 and 144.3).
+constexpr int kStages4 = 2;
 constexpr float kSlack = 5.0f;
 
 // Shared memory of one variant: NB stored blocks, NT tiles of 8 query rows, QP parts of q.
@@ -202,7 +196,7 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 }
 
 template <typename T, int NB, int NT, int QP, int PP, bool SEG>
-__global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? KV4_CTAS : NB <= 4 ? KV4_CTAS2 : 2)
+__global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
     q4kv_attend_kernel(const Attend4Params pp) {
     using S = Smem4<NB, NT, QP>;
     constexpr int ROWS = S::kRows, KEYS = kStepKeys * kWarps, W = (NB + 1) / 2;

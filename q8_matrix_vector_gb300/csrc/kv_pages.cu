@@ -666,14 +666,14 @@ q8mv_status_t kvpage_destroy(kvpage_plan_t p) {
 }
 
 q8mv_status_t kvpage_copy_q8(const q8kv_cache_t *cache, int64_t n, const int32_t *src, const int32_t *dst,
-                                    const int32_t *count, cudaStream_t stream) {
+                             const int32_t *count, cudaStream_t stream) {
     kv::Cache c;
     if (!kv::make_cache(cache, &c)) return Q8MV_ERR_INVALID_ARG;
     return kv::copy_pages(c, n, src, dst, count, stream);
 }
 
 q8mv_status_t kvpage_copy_q4(const q4kv_cache_t *cache, int64_t n, const int32_t *src, const int32_t *dst,
-                                    const int32_t *count, cudaStream_t stream) {
+                             const int32_t *count, cudaStream_t stream) {
     kv::Cache4 c = {};
     if (!kv::make_cache4(cache, &c)) return Q8MV_ERR_INVALID_ARG;
     return kv::copy_pages(c.rows, n, src, dst, count, stream);
