@@ -37,8 +37,8 @@ q8mv_status_t kvpage_plan(kvpage_plan_t *out, int64_t pages, int32_t page_size, 
 /*
  * Pages for tokens[b] (below 0: 0) tokens past lengths[b] (below 0: 0).  With P =
  * page_size, columns lengths / P .. ceil((lengths + tokens) / P) - 1 get a fresh page
- * if they are past held, or if the page there is shared (refs > 1): the other
- * requests keep it.  If the first of them already has tokens (lengths % P > 0) and was
+ * if they are past held (and so do any between held and lengths / P), or if the page
+ * there is shared (refs > 1): the other requests keep it.  If the first of them already has tokens (lengths % P > 0) and was
  * shared, its page has to be copied: src[b] -> dst[b], both -1 for a request
  * without.  Fresh pages are the lowest that were free before the call, in order of
  * request, then column.  ok[b] = 1, or 0 for a request that would pass the columns,

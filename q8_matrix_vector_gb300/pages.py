@@ -48,14 +48,17 @@ class Pages(_Plan):
     def __init__(self, pages: int, page_size: int, requests: int, columns: int, device: int = -1):
         self.pages, self.page_size, self.requests, self.columns = pages, page_size, requests, columns
         self._make("kvpage_plan", pages, page_size, requests, columns, int(device))
-        self.refs = torch.zeros(pages, dtype=torch.int32, device=self._where)
-        self.table = torch.full((requests, columns), -1, dtype=torch.int32, device=self._where)
-        self.held = torch.zeros(requests, dtype=torch.int32, device=self._where)
-        self._state = State(self.refs.data_ptr(), self.table.data_ptr(), self.held.data_ptr())
+        self._refs = torch.zeros(pages, dtype=torch.int32, device=self._where)
+        self._table = torch.full((requests, columns), -1, dtype=torch.int32, device=self._where)
+        self._held = torch.zeros(requests, dtype=torch.int32, device=self._where)
+        self._state = State(self._refs.data_ptr(), self._table.data_ptr(), self._held.data_ptr())
         self._ref = ctypes.byref(self._state)
         lib = _library()
         self._extend, self._fork, self._free, self._compact = (getattr(lib, "kvpage_" + n) for n in
                                                                ("extend", "fork", "free", "compact"))
+
+    # the library has their addresses: they are written to, not replaced
+    refs, table, held = (property(lambda self, n=n: getattr(self, n)) for n in ("_refs", "_table", "_held"))
 
     def _run(self, fn, what, *args):
         device = self.device
@@ -67,7 +70,8 @@ class Pages(_Plan):
             _fail(status, what)
 
     def extend(self, lengths, tokens, width: int):
-        """Pages for tokens[b] more tokens past the first lengths[b] ([requests] int32 each) of each request.
+        """Pages for tokens[b] more tokens past the first lengths[b] ([requests] int32 each) of each request: fresh ones,
+        the lowest free, past those that it holds, and in place of shared ones that these tokens are written to.
 
         Returns (slots [requests, width] int64, src, dst, ok [requests] int32): the slots of the first ``width`` new
         tokens, -1 behind the last; a page that was shared and is about to be written, and its copy, -1 for none (call
@@ -79,7 +83,8 @@ class Pages(_Plan):
         at_lengths = _ints(lengths, torch.int32, n, device, "lengths")
         at_tokens = _ints(tokens, torch.int32, n, device, "tokens")
         slots = torch.empty((n, width), dtype=torch.int64, device=self._where)
-        src, dst, ok = torch.empty_like(self.held), torch.empty_like(self.held), torch.empty_like(self.held)
+        held = self._held
+        src, dst, ok = torch.empty_like(held), torch.empty_like(held), torch.empty_like(held)
         self._run(self._extend, "kvpage_extend", at_lengths, at_tokens, width, slots.data_ptr(), src.data_ptr(),
                   dst.data_ptr(), ok.data_ptr())
         return slots, src, dst, ok

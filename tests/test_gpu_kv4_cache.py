@@ -190,3 +190,37 @@ def test_many_copies(q8mv):
     want[dst[:1400].long()] = want[src[:1400].long()]
     cache.copy_pages(src, dst)
     assert torch.equal(cache.v_codes, want)
+
+
+def test_offsets_past_32_bits(q8mv):
+    """A cache of 2^32 bytes of codes and more: its last pages are written, read, attended, moved and copied."""
+    import torch
+
+    pages, page, heads, dim = 70000, 128, 8, 128  # 71.7 million rows of 64 bytes
+    cache = q8mv.Cache4(pages, page, heads, dim)
+    assert cache.k_codes.numel() > 2 ** 32
+    g = torch.Generator("cuda").manual_seed(3)
+    n = 3 * page
+    k, v = (torch.randn(n, heads, dim, generator=g, device="cuda") for _ in range(2))
+    last = torch.arange((pages - 3) * page, pages * page, device="cuda")
+    first = torch.arange(n, device="cuda")
+    small = q8mv.Cache4(3, page, heads, dim)
+    for c, slots in ((cache, last), (small, first)):
+        c.write(k, v, slots)
+    for a, b in zip(cache.read(last), small.read(first)):
+        assert torch.equal(a, b)
+    q = torch.randn(1, 32, dim, generator=g, device="cuda")
+    attend = q8mv.TreeAttention4(32, heads, dim, 1, 1)
+    lengths = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    tables = [torch.arange(x, x + 3, dtype=torch.int32, device="cuda").view(1, 3) for x in (pages - 3, 0)]
+    assert torch.equal(attend(q, cache, tables[0], lengths), attend(q, small, tables[1], lengths))
+    assert not cache.k_codes[:pages - 3].any()  # nothing went anywhere else
+    cache.copy_pages(tables[0].view(-1), tables[1].view(-1))
+    assert torch.equal(cache.v_codes[:3], small.v_codes)
+    cache.move(last[:5].clone(), torch.arange(5, device="cuda") + 10 * page)
+    assert torch.equal(cache.read(torch.arange(5, device="cuda") + 10 * page)[1], small.read(first[:5].clone())[1])
+    rotary = q8mv.Rotary(dim)
+    for c, slots in ((cache, last), (small, first)):
+        rotary.write(c, None, k, v, first, slots)
+    for a, b in zip(cache.read(last), small.read(first)):
+        assert torch.equal(a, b)
