@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 512, kPer = 4;  // of a CTA that counts; pages a thread takes at a time
 constexpr int kCluster = 8;
 constexpr int kTile = kThreads * kPer;
+constexpr int kFewColumns = 4;  // a thread looks at so many alone
 
 struct PageParams {
     int *refs, *table, *held;
@@ -137,7 +138,7 @@ __device__ __forceinline__ int64_t slot_at(const PageParams &p, int b, int64_t p
     return page * p.page_size + position - c * p.page_size;
 }
 
-__global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParams p) {
+__global__ void __launch_bounds__(kThreads, 1) kvpage_extend_kernel(const PageParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();  // waited for before the first exchange: nobody's shared memory is written before it runs
     __shared__ int warp_sums[kThreads / 32], box[3][kCluster], starts[kThreads];
@@ -151,25 +152,39 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
     const int p1 = min(p0 + share, p.pages);
     int r0[kPer], r[kPer];
     load_refs(p.refs, p0 + threadIdx.x * kPer, p1, r0);
-    // ---- how many pages each request wants: a warp each (amounts stay here if a tile holds them)
+    // ---- how many pages each request wants: a thread each, or its warp where many columns are to be looked at (amounts
+    // stay here if a tile holds them)
     const bool few = b1 - b0 <= kThreads;
     int mine = 0;
-    for (int b = b0 + warp; b < b1; b += kThreads / 32) {
-        const Span s = span_of(p, b);
-        int n = -1;
-        if (s.need <= p.columns) {
-            n = 0;
-            for (int c = s.first + lane; c < min(s.held, s.need); c += 32) {
-                int page;
-                n += replaced(p, b, c, &page);
+    for (int t0 = b0; t0 < b1; t0 += kThreads) {
+        const int b = t0 + threadIdx.x;
+        int n = 0, first = 0, end = 0;  // held columns first .. end - 1 may be replaced
+        if (b < b1) {
+            const Span s = span_of(p, b);
+            if (s.need <= p.columns) {
+                n = max(s.need - s.held, 0);
+                first = s.first;
+                end = max(min(s.held, s.need), first);
+            } else {
+                n = -1;
             }
-            n = __reduce_add_sync(~0u, n) + max(s.need - s.held, 0);
-            mine += n;
         }
-        if (lane == 0) (few ? starts[b - b0] : p.amount[b]) = n;
+        int page;
+        if (end - first <= kFewColumns)
+            for (int c = first; c < end; ++c) n += replaced(p, b, c, &page);
+        for (unsigned many = __ballot_sync(~0u, end - first > kFewColumns); many != 0; many &= many - 1) {
+            const int who = __ffs(many) - 1, rb = t0 + warp * 32 + who;
+            const int c0 = __shfl_sync(~0u, first, who), c1 = __shfl_sync(~0u, end, who);
+            int k = 0;
+            for (int c = c0 + lane; c < c1; c += 32) k += replaced(p, rb, c, &page);
+            k = __reduce_add_sync(~0u, k);
+            if (lane == who) n += k;
+        }
+        if (b < b1) (few ? starts[threadIdx.x] : p.amount[b]) = n;
+        mine += max(n, 0);
     }
     int total;
-    scan(lane == 0 ? mine : 0, &total, warp_sums);
+    scan(mine, &total, warp_sums);
     cluster.barrier_wait();
     int wanted, free_pages = 0;
     const int before = exchange(cluster, box[0], total, &wanted);
@@ -224,45 +239,60 @@ __global__ void __launch_bounds__(kThreads) kvpage_extend_kernel(const PageParam
         if (fits && n > 0) served = max(served, k + n);
         starts[threadIdx.x] = fits ? k : -1;
         base += total;
-        __syncthreads();
-        for (int i = warp; i < min(kThreads, b1 - t0); i += kThreads / 32) {
-            const int rb = t0 + i, start = starts[i];
-            const Span s = span_of(p, rb);
-            int from = -1, to = -1;
-            if (start >= 0) {
-                int *row = p.table + static_cast<int64_t>(rb) * p.columns;
-                const int64_t col = pages_of(p, s.length), part = s.length != col * p.page_size ? col : -1;
-                int done = start;
-                for (int c0 = s.first; c0 < s.need; c0 += 32) {
-                    const int c = c0 + lane;
-                    int page = -1;
-                    const bool fresh = c < s.need && (c >= s.held || replaced(p, rb, c, &page));
-                    const unsigned all = __ballot_sync(~0u, fresh);
-                    if (fresh) {
-                        const int at = done + __popc(all & ((1u << lane) - 1u)), x = p.fresh[at];
-                        row[c] = x;
-                        p.old[at] = page;
-                        if (c == part && page >= 0) {
-                            from = page;
-                            to = x;
-                        }
-                    }
-                    done += __popc(all);
-                }
-                if (lane == 0 && s.need > s.held) p.held[rb] = s.need;
-                __syncwarp();
+        Span s = {};
+        if (b < b1) s = span_of(p, b);
+        const bool goes = b < b1 && fits && s.need > s.first;
+        const int64_t col = pages_of(p, s.length);
+        const int part = s.length != col * p.page_size && col < p.columns ? static_cast<int>(col) : -1;  // its page has tokens
+        int from = -1, to = -1;
+        // column c gets page p.fresh[at]
+        auto give = [&](int rb, int c, int at, int old, int part_c, int *f, int *g) {
+            const int x = p.fresh[at];
+            p.table[static_cast<int64_t>(rb) * p.columns + c] = x;
+            p.old[at] = old;
+            if (c == part_c && old >= 0) {
+                *f = old;
+                *g = x;
             }
-            from = __reduce_max_sync(~0u, from);
-            to = __reduce_max_sync(~0u, to);
-            if (lane == 0) {
-                p.src[rb] = from;
-                p.dst[rb] = to;
-                p.ok[rb] = start >= 0;
+        };
+        if (goes && s.need - s.first <= kFewColumns)
+            for (int c = s.first; c < s.need; ++c) {
+                int page = -1;
+                if (c >= s.held || replaced(p, b, c, &page)) give(b, c, k++, page, part, &from, &to);
             }
-            if (p.slots_here)
-                for (int w = lane; w < p.width; w += 32)
-                    p.slots[static_cast<int64_t>(rb) * p.width + w] = start >= 0 && w < s.tokens ? slot_at(p, rb, s.length + w) : -1;
+        for (unsigned many = __ballot_sync(~0u, goes && s.need - s.first > kFewColumns); many != 0; many &= many - 1) {
+            const int who = __ffs(many) - 1, rb = t0 + warp * 32 + who;
+            const int first = __shfl_sync(~0u, s.first, who), need = __shfl_sync(~0u, s.need, who), held = __shfl_sync(~0u, s.held, who);
+            const int part_c = __shfl_sync(~0u, part, who);
+            int done = __shfl_sync(~0u, k, who), f = -1, g = -1;
+            for (int c0 = first; c0 < need; c0 += 32) {
+                const int c = c0 + lane;
+                int page = -1;
+                const bool fresh = c < need && (c >= held || replaced(p, rb, c, &page));
+                const unsigned all = __ballot_sync(~0u, fresh);
+                if (fresh) give(rb, c, done + __popc(all & ((1u << lane) - 1u)), page, part_c, &f, &g);
+                done += __popc(all);
+            }
+            f = __reduce_max_sync(~0u, f);
+            g = __reduce_max_sync(~0u, g);
+            if (lane == who) {
+                from = f;
+                to = g;
+            }
         }
+        if (b < b1) {
+            if (goes && s.need > s.held) p.held[b] = s.need;
+            p.src[b] = from;
+            p.dst[b] = to;
+            p.ok[b] = fits;
+        }
+        __syncthreads();  // the tile's rows and starts are there
+        if (p.slots_here)
+            for (int i = threadIdx.x; i < min(kThreads, b1 - t0) * p.width; i += kThreads) {
+                const int r = i / p.width, w = i - r * p.width, rb = t0 + r;
+                const bool there = starts[r] >= 0 && w < p.tokens[rb];
+                p.slots[static_cast<int64_t>(rb) * p.width + w] = there ? slot_at(p, rb, static_cast<int64_t>(max(p.lengths[rb], 0)) + w) : -1;
+            }
         __syncthreads();
     }
     if (wanted == 0) return;  // (no CTA waits for another, or writes to it, from here)
@@ -338,7 +368,7 @@ __global__ void __launch_bounds__(256) kvpage_free_kernel(const PageParams p) {
 }
 
 // compact, first: who moves where (p.fresh: a page's new number, -1 for one past the dense part that nobody holds)
-__global__ void __launch_bounds__(kThreads) kvpage_compact_kernel(const PageParams p) {
+__global__ void __launch_bounds__(kThreads, 1) kvpage_compact_kernel(const PageParams p) {
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();
     __shared__ int warp_sums[kThreads / 32], box[3][kCluster];
@@ -545,9 +575,10 @@ bool take(const kvpage_s *plan, const kvpage_state_t *s, PageParams *p) {
     return true;
 }
 
-// One CTA for a small pool, whose work is a few round trips; a cluster for more.
-q8mv_status_t launch_cluster(void (*kernel)(PageParams), const PageParams &p, cudaStream_t stream) {
-    const int ctas = p.pages > 2 * kTile || p.requests > 2 * kThreads / 32 ? kCluster : 1;
+// One CTA for up to `pages` pages, whose work is a few round trips; a cluster, whose barriers are round trips of their own,
+// for more (extend, 144 requests and 4096 pages: 11.0 us by a cluster, 6.8 by one; compact, 16384 pages: 8.4 and 16.8).
+q8mv_status_t launch_cluster(void (*kernel)(PageParams), const PageParams &p, int pages, cudaStream_t stream) {
+    const int ctas = p.pages > pages || p.requests > kThreads ? kCluster : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -616,7 +647,7 @@ q8mv_status_t kvpage_extend(kvpage_plan_t plan, const kvpage_state_t *state, con
     p.dst = dst;
     p.ok = ok;
     p.slots_here = width <= 64;
-    const q8mv_status_t st = kv::launch_cluster(kv::kvpage_extend_kernel, p, stream);
+    const q8mv_status_t st = kv::launch_cluster(kv::kvpage_extend_kernel, p, 16384, stream);
     if (st != Q8MV_OK || p.slots_here) return st;
     kv::kvpage_slots_kernel<<<dim3(static_cast<unsigned>(kv::ceil_div(width, 256)), static_cast<unsigned>(p.requests)), 256, 0,
                               stream>>>(p);
@@ -648,7 +679,7 @@ q8mv_status_t kvpage_compact(kvpage_plan_t plan, const kvpage_state_t *state, in
     p.src = src;
     p.dst = dst;
     p.count = count;
-    const q8mv_status_t st = kv::launch_cluster(kv::kvpage_compact_kernel, p, stream);
+    const q8mv_status_t st = kv::launch_cluster(kv::kvpage_compact_kernel, p, 4096, stream);
     if (st != Q8MV_OK) return st;
     kv::kvpage_follow_kernel<<<dim3(static_cast<unsigned>(kv::ceil_div(p.columns, 256)), static_cast<unsigned>(p.requests)), 256,
                                0, stream>>>(p);

@@ -112,14 +112,23 @@ __device__ __forceinline__ T2 extremes_of_pairs(const uint4 &v) {
     const T2 b = __hneg2(__hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3])));
     return __hmax2_nan(pair2(a.x, b.x), pair2(a.y, b.y));
 }
-// over the PER lanes of a block
-template <int PER>
+// The largest |x|, twice.
+template <int E>
+__device__ __forceinline__ float2 magnitude(const float (&y)[E]) {
+    float m = fabsf(y[0]);
+#pragma unroll
+    for (int j = 1; j < E; ++j) m = max_nan(m, fabsf(y[j]));
+    return make_float2(m, m);
+}
+// over the PER lanes of a block; ONE: both numbers are the same
+template <int PER, bool ONE>
 __device__ __forceinline__ float2 over_block(float2 m) {
 #pragma unroll
     for (int d = 1; d < PER; d *= 2) {
         m.x = max_nan(m.x, __shfl_xor_sync(~0u, m.x, d));
-        m.y = max_nan(m.y, __shfl_xor_sync(~0u, m.y, d));
+        if (!ONE) m.y = max_nan(m.y, __shfl_xor_sync(~0u, m.y, d));
     }
+    if (ONE) m.y = m.x;
     return m;
 }
 
@@ -135,6 +144,7 @@ __device__ __forceinline__ uint32_t pack_4(const float (&y)[E], float inv, bool 
         float z[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            // (not as f32x2: its product and sum come out fused)
             z[i] = __fadd_rn(__fmul_rn(y[j + i * (E / 2)], inv), kRound + 8.0f);
             if (low) z[i] = fmaxf(z[i], kRound);
         }
@@ -263,6 +273,65 @@ __device__ __forceinline__ void rotate_item(const StoreParams &p, const T *src, 
     }
 }
 
+// The angles of a block's tokens, by all its threads
+__device__ __forceinline__ void turn_all(const StoreParams &p, float *angles, int tokens, int64_t first, int tid) {
+    const int pairs = static_cast<int>(min(static_cast<int64_t>(tokens), p.n - first)) * p.half;
+    for (int i = tid; i < pairs; i += blockDim.x * blockDim.y) {
+        const int t = i / p.half, k = i - t * p.half;
+        float c, s;
+        store::turn(static_cast<uint64_t>(__ldg(p.positions + first + t)) * __ldg(p.turns + k), p.circle, &c, &s);
+        angles[i] = __fmul_rn(c, p.factor);
+        s = __fmul_rn(s, p.factor);
+        angles[tokens * p.half + i] = p.back ? -s : s;
+    }
+}
+
+// Lane `at` of q's, U tokens: loads, then the angles, then the rest.
+template <typename T, bool VEC, int U>
+__device__ __forceinline__ void rotate_q(const StoreParams &p, float *angles, int at, int64_t first, int tid) {
+    constexpr int E = 16 / sizeof(T);
+    const int tokens = blockDim.y * U;
+    const int h = at / max(p.q_items, 1), item = at - h * p.q_items;
+    const T *src = static_cast<const T *>(p.q) + (first + threadIdx.y) * p.q_row + h * p.q_head;
+    T *dst = static_cast<T *>(p.out) + (first + threadIdx.y) * p.out_row + h * p.out_head;
+    const int64_t step = blockDim.y * p.q_row, step_out = blockDim.y * p.out_row;
+    // tokens of this lane
+    const int64_t left = p.n - first - threadIdx.y;
+    const int mine = at >= p.q_lanes || left <= 0 ? 0 : left > (U - 1) * static_cast<int64_t>(blockDim.y) ? U
+                                                        : static_cast<int>((left + blockDim.y - 1) / blockDim.y);
+    if constexpr (VEC) {
+        const Item it = item_of<E>(p, item);
+        uint4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u] = u < mine ? store::load<T, true>(src + u * step + it.a) : make_uint4(0, 0, 0, 0);
+            b[u] = u < mine && it.b >= 0 ? store::load<T, true>(src + u * step + it.b) : make_uint4(0, 0, 0, 0);
+        }
+        turn_all(p, angles, tokens, first, tid);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = u * blockDim.y + threadIdx.y;
+            if (u < mine) rotate_item<T>(p, it, a[u], b[u], dst + u * step_out, angles + t * p.half, angles + (tokens + t) * p.half);
+        }
+    } else {
+        turn_all(p, angles, tokens, first, tid);
+        __syncthreads();
+        for (int u = 0; u < mine; ++u) {
+            const int t = u * blockDim.y + threadIdx.y;
+            rotate_item<T>(p, src + u * step, dst + u * step_out, item, angles + t * p.half, angles + (tokens + t) * p.half);
+        }
+    }
+}
+
+// q alone: of the registers that keys and values take, it has none.
+template <typename T, bool VEC, int U>
+__global__ void __launch_bounds__(256) kv_rotate_kernel(const StoreParams p) {
+    extern __shared__ __align__(16) float angles[];  // cos, then sin, [token of the block][pair]
+    rotate_q<T, VEC, U>(p, angles, blockIdx.y * blockDim.x + threadIdx.x, static_cast<int64_t>(blockIdx.x) * (blockDim.y * U),
+                        threadIdx.y * blockDim.x + threadIdx.x);
+}
+
 // U tokens a lane.
 template <typename T, int BITS, bool ROT, bool VEC, int U>
 __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
@@ -275,50 +344,9 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
     const bool stores = static_cast<int>(blockIdx.y) < p.kv_y;
     const int at = (stores ? blockIdx.y : blockIdx.y - p.kv_y) * blockDim.x + threadIdx.x;
 
-    // by all threads, once what they load is on its way
-    auto turn_all = [&] {
-        const int pairs = static_cast<int>(min(static_cast<int64_t>(tokens), p.n - first)) * p.half;
-        for (int i = tid; i < pairs; i += blockDim.x * blockDim.y) {
-            const int t = i / p.half, k = i - t * p.half;
-            float c, s;
-            turn(static_cast<uint64_t>(__ldg(p.positions + first + t)) * __ldg(p.turns + k), p.circle, &c, &s);
-            angles[i] = __fmul_rn(c, p.factor);
-            s = __fmul_rn(s, p.factor);
-            angles[tokens * p.half + i] = p.back ? -s : s;
-        }
-    };
     if constexpr (ROT) {
         if (!stores) {
-            const int h = at / max(p.q_items, 1), item = at - h * p.q_items;
-            const T *src = static_cast<const T *>(p.q) + (first + threadIdx.y) * p.q_row + h * p.q_head;
-            T *dst = static_cast<T *>(p.out) + (first + threadIdx.y) * p.out_row + h * p.out_head;
-            const int64_t step = blockDim.y * p.q_row, step_out = blockDim.y * p.out_row;
-            // tokens of this lane
-            const int mine = at < p.q_lanes ? static_cast<int>(min(max((p.n - first - threadIdx.y + blockDim.y - 1) / blockDim.y, int64_t{0}),
-                                                                   static_cast<int64_t>(U))) : 0;
-            if constexpr (VEC) {
-                const Item it = item_of<E>(p, item);
-                uint4 a[U], b[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    a[u] = u < mine ? load<T, true>(src + u * step + it.a) : make_uint4(0, 0, 0, 0);
-                    b[u] = u < mine && it.b >= 0 ? load<T, true>(src + u * step + it.b) : make_uint4(0, 0, 0, 0);
-                }
-                turn_all();
-                __syncthreads();
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int t = u * blockDim.y + threadIdx.y;
-                    if (u < mine) rotate_item<T>(p, it, a[u], b[u], dst + u * step_out, angles + t * p.half, angles + (tokens + t) * p.half);
-                }
-            } else {
-                turn_all();
-                __syncthreads();
-                for (int u = 0; u < mine; ++u) {
-                    const int t = u * blockDim.y + threadIdx.y;
-                    rotate_item<T>(p, src + u * step, dst + u * step_out, item, angles + t * p.half, angles + (tokens + t) * p.half);
-                }
-            }
+            rotate_q<T, VEC, U>(p, angles, at, first, tid);
             return;
         }
     }
@@ -361,7 +389,7 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
         }
         rows[tid] = r;
     }
-    if constexpr (ROT) turn_all();
+    if constexpr (ROT) turn_all(p, angles, tokens, first, tid);
     __syncthreads();
     const int lane = threadIdx.x & 31, of = lane & (PER - 1), first_lane = lane - of;  // (blockDim.x: whole warps)
 #pragma unroll
@@ -412,18 +440,19 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
             }
         }
         float2 m[2];
-        if constexpr (sizeof(T) == 2 && !ROT) {
-            using T2 = decltype(pair2(raw[0][0].t[0], raw[0][0].t[0]));
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                T2 x = extremes_of_pairs<T2>(raw[u][s].v);
+        for (int s = 0; s < 2; ++s) {
+            if (sizeof(T) == 2 && !(ROT && s == 0)) {  // (as they came)
+                if constexpr (sizeof(T) == 2) {
+                    using T2 = decltype(pair2(raw[0][0].t[0], raw[0][0].t[0]));
+                    T2 x = extremes_of_pairs<T2>(raw[u][s].v);
 #pragma unroll
-                for (int d = 1; d < PER; d *= 2) x = __hmax2_nan(x, __shfl_xor_sync(~0u, x, d));
-                m[s] = make_float2(to_f32(x.x), to_f32(x.y));
+                    for (int d = 1; d < PER; d *= 2) x = __hmax2_nan(x, __shfl_xor_sync(~0u, x, d));
+                    m[s] = make_float2(to_f32(x.x), to_f32(x.y));
+                }
+            } else {
+                m[s] = BITS == 8 ? over_block<PER, true>(magnitude(y[s])) : over_block<PER, false>(extremes(y[s]));
             }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) m[s] = over_block<PER>(extremes(y[s]));
         }
         const bool nan = m[0].x != m[0].x || m[1].x != m[1].x || m[0].y != m[0].y || m[1].y != m[1].y;
         if (__any_sync(~0u, nan)) {  // of those that are numbers
@@ -435,7 +464,7 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
                     m[s].x = fmaxf(m[s].x, y[s][j]);
                     m[s].y = fmaxf(m[s].y, -y[s][j]);
                 }
-                m[s] = over_block<PER>(m[s]);
+                m[s] = over_block<PER, false>(m[s]);
             }
         }
         if constexpr (BITS == 4) {
@@ -517,22 +546,18 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
     }
 }
 
-// Tokens a lane of a large call (kv_cache.cu's measurements)
+// Tokens a lane of a large call: of writes (kv_cache.cu's measurements: 40.4 us for 8190 tokens of 32 heads x 128 in bf16, 42.0
+// with two), and of what only rotates (f32, 5003 tokens of 12 heads of 80: 7.5 us, 8.9 with two)
 constexpr int kStoreTokens = 4;
-// with k's other halves and its angles a lane holds more: 8192 tokens of 8 heads x 128 and 32 of q, bf16: 48.5 us with 4,
-// 46.3 with 2; q alone (f32, 5003 tokens of 12 heads of 80) 7.5 us with 4, 8.9 with 2
-constexpr int kRotateStoreTokens = 2;
 
 template <typename T, int BITS, bool ROT>
 void launch_store(const StoreParams &p, bool vec, const Shape &s, size_t smem, cudaStream_t stream) {
     if (!vec)
         kv_store_kernel<T, BITS, ROT, false, 1><<<s.grid, s.block, smem, stream>>>(p);
-    else if (!s.many)
+    else if (ROT || !s.many)
         kv_store_kernel<T, BITS, ROT, true, 1><<<s.grid, s.block, smem, stream>>>(p);
-    else if (ROT && p.kv_y > 0)
-        kv_store_kernel<T, BITS, ROT, true, ROT ? kRotateStoreTokens : kStoreTokens><<<s.grid, s.block, smem, stream>>>(p);
-    else if (!ROT || BITS == 8)  // (what only rotates comes as 8 bits)
-        kv_store_kernel<T, BITS, ROT, true, !ROT || BITS == 8 ? kStoreTokens : 1><<<s.grid, s.block, smem, stream>>>(p);
+    else
+        kv_store_kernel<T, BITS, ROT, true, ROT ? 1 : kStoreTokens><<<s.grid, s.block, smem, stream>>>(p);
 }
 
 }  // namespace kv

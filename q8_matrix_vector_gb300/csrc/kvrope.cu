@@ -18,29 +18,56 @@ namespace kv {
 
 namespace {
 
-// Lanes of one token's q, and how p's blocks are split between storing and rotating.  Half the shared memory of an SM is
-// left to the loads' latency: 32 KB of angles a block at most.
+// Shape and shared memory of `lanes` lanes a token; 32 KB of angles a block at most.
+Shape shape_of(const StoreParams &p, int lanes, int tokens, bool vec, size_t *smem) {
+    Shape s = shape(lanes, p.n, tokens);
+    const auto bytes = [&](int each) { return static_cast<size_t>(s.block.y) * each * p.half * 2 * sizeof(float); };
+    if (!vec || bytes(tokens) > 32768) s.many = false;
+    s.grid.x = static_cast<unsigned>(ceil_div(p.n, static_cast<int64_t>(s.block.y) * (s.many ? tokens : 1)));
+    *smem = bytes(s.many ? tokens : 1);
+    return s;
+}
+
+template <typename T>
+void launch_q(const StoreParams &p, bool vec, const Shape &s, size_t smem, cudaStream_t stream) {
+    if (!vec)
+        kv_rotate_kernel<T, false, 1><<<s.grid, s.block, smem, stream>>>(p);
+    else if (!s.many)
+        kv_rotate_kernel<T, true, 1><<<s.grid, s.block, smem, stream>>>(p);
+    else
+        kv_rotate_kernel<T, true, kStoreTokens><<<s.grid, s.block, smem, stream>>>(p);
+}
+
+// q_lanes comes as q's heads.  One launch, whose blocks along y rotate q behind those that store, a token a lane: with k's
+// other halves and the angles two or four take more registers than they are worth, and q in a launch of its own, four
+// tokens a lane, gains less than the launch costs (8192 tokens of 8 heads x 128 and 32 of q, bf16: 43.8 us; with two 46.4,
+// four 48.5; two launches 45.0).
 q8mv_status_t launch(StoreParams p, int bits, int type, bool vec, cudaStream_t stream) {
     const int e = vec ? 16 / type_size(type) : 1;
     p.q_items = p.q == nullptr ? 0 : !vec || !p.interleaved ? (p.dim - p.half) / e : p.dim / e;
-    const int64_t q_lanes = static_cast<int64_t>(p.q_items) * p.q_lanes;  // (q_lanes: heads so far)
+    const int64_t q_lanes = static_cast<int64_t>(p.q_items) * p.q_lanes;
     if (q_lanes >= (1LL << 31)) return Q8MV_ERR_INVALID_ARG;
     p.q_lanes = static_cast<int>(q_lanes);
-    // the blocks' shape is that of the stored lanes, if there are any
-    const int tokens = p.lanes > 0 ? kRotateStoreTokens : kStoreTokens;
-    Shape s = shape(p.lanes > 0 ? p.lanes : p.q_lanes, p.n, tokens);
-    p.kv_y = p.lanes > 0 ? static_cast<int>(s.grid.y) : 0;
-    const int64_t q_y = ceil_div(p.q_lanes, s.block.x);
-    if (p.kv_y + q_y > 65535) return Q8MV_ERR_INVALID_ARG;
-    const auto bytes = [&](int each) { return static_cast<size_t>(s.block.y) * each * p.half * 2 * sizeof(float); };
-    if (!vec || bytes(tokens) > 32768) s.many = false;
-    s.grid = dim3(static_cast<unsigned>(ceil_div(p.n, static_cast<int64_t>(s.block.y) * (s.many ? tokens : 1))),
-                  static_cast<unsigned>(p.kv_y + q_y));
-    const size_t smem = bytes(s.many ? tokens : 1);
-    if (bits == 4)
-        launch_rotate_4(p, type, vec, s, smem, stream);
-    else
-        launch_rotate_8(p, type, vec, s, smem, stream);
+    size_t smem;
+    Shape s = shape_of(p, p.lanes > 0 ? p.lanes : p.q_lanes, p.lanes > 0 ? 1 : kStoreTokens, vec, &smem);
+    if (p.lanes > 0) {
+        p.kv_y = static_cast<int>(s.grid.y);
+        const int64_t y = p.kv_y + ceil_div(p.q_lanes, s.block.x);
+        if (y > 65535) return Q8MV_ERR_INVALID_ARG;
+        s.grid.y = static_cast<unsigned>(y);
+        if (bits == 4)
+            launch_rotate_4(p, type, vec, s, smem, stream);
+        else
+            launch_rotate_8(p, type, vec, s, smem, stream);
+    } else {
+        if (s.grid.y > 65535u) return Q8MV_ERR_INVALID_ARG;
+        if (type == Q8KV_F32)
+            launch_q<float>(p, vec, s, smem, stream);
+        else if (type == Q8KV_F16)
+            launch_q<__half>(p, vec, s, smem, stream);
+        else
+            launch_q<__nv_bfloat16>(p, vec, s, smem, stream);
+    }
     return q8i::cuda_status(cudaGetLastError());
 }
 
