@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
     __shared__ int64_t scan_units[kWarps], scan_items[kWarps];
     __shared__ int64_t start_b, start_item, start_unit;
     __shared__ float row_mul[ROWS];
+    __shared__ int ahead[kWarps][2][32];  // pages of the next item's first two steps
     __shared__ int is_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -393,15 +394,22 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         k.table = p.table + static_cast<int64_t>(x.b) * p.table_row;
         return k;
     };
-    // row number of the lane's key of step i (SEG: of its half's first key), or kNoRow
-    auto find = [&](const Work &k, int i) -> uint32_t {
-        const int pos = k.base0 + i * KEYS + (SEG ? lane & 16 : lane);
-        if (i >= k.n_steps || pos >= k.keys) return kNoRow;
-        const uint32_t col = (__umulhi(pos, p.page_mul) + pos) >> p.page_shift;  // pos / page_size
-        const int page = __ldg(k.table + col);
+    // position of the lane's key of step i (SEG: of its half's first key) and its column of the table; false if there is none
+    auto seek = [&](const Work &k, int i, int *pos, uint32_t *col) -> bool {
+        *pos = k.base0 + i * KEYS + (SEG ? lane & 16 : lane);
+        *col = (__umulhi(*pos, p.page_mul) + *pos) >> p.page_shift;  // pos / page_size
+        return i < k.n_steps && *pos < k.keys;
+    };
+    // its row number, or kNoRow
+    auto row_at = [&](const Work &k, int pos, uint32_t col, int page) -> uint32_t {
         if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
         // (rows are numbered in 32 bits: products may be taken modulo 2^32)
         return static_cast<uint32_t>(page) * pp.stride_page + (pos - col * p.c.page_size) * pp.stride_token + k.head;
+    };
+    auto find = [&](const Work &k, int i) -> uint32_t {
+        int pos;
+        uint32_t col;
+        return seek(k, i, &pos, &col) ? row_at(k, pos, col, __ldg(k.table + col)) : kNoRow;
     };
     uint32_t row_cur[kStages4];  // rows of the steps in the ring: their lanes' keys are there
     uint32_t row_next;
@@ -414,6 +422,41 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         }
         row_next = find(k, kStages4 - 1);
     };
+    // The same for an item whose pages are on their way to `ahead` since `look`, so that its first keys wait for no table.
+    auto look = [&](const Work &k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int pos;
+            uint32_t col;
+            if (seek(k, i, &pos, &col)) cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&ahead[warp][i][lane])), k.table + col);
+        }
+    };
+    auto begin_ahead = [&](const Work &k) {
+        uint32_t row[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int pos;
+            uint32_t col;
+            row[i] = seek(k, i, &pos, &col) ? row_at(k, pos, col, ahead[warp][i][lane]) : kNoRow;
+        }
+        row_cur[0] = row[0];
+        issue(k.n_steps > 0, slot0, row[0]);
+        row_next = row[1];
+    };
+    // The thread's elements of an item's q: l8 + 8 i of row tid / 8
+    static_assert(ROWS <= kWarps * 4, "a row for every 8 threads");
+    const int q_row = tid >> 3, l8 = tid & 7;
+    T q_raw[4 * NB];
+    auto load_q = [&](const Place &x) {
+        const int idx = x.rt * ROWS + q_row, node = idx / p.group, hq = x.h * p.group + idx - node * p.group;
+        const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(x.row0) + node) * p.q_row + hq * p.q_head;
+        const bool live = q_row < min(ROWS, x.nodes * p.group - x.rt * ROWS);
+#pragma unroll
+        for (int i = 0; i < 4 * NB; ++i) {
+            const int e = l8 + 8 * i;
+            q_raw[i] = live && e < pp.dim ? src[e] : from_f32<T>(0.0f);
+        }
+    };
     // Row g of an octet of the operands is place (g & 1) * 4 + g / 2 of eight keys, so that the four keys 2c, 2c + 1 of a
     // lane's values, over c, are neighbours in shared memory.
     const int place = (g & 1) * 4 + (g >> 1);
@@ -421,21 +464,18 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
     Work k = work_of(w);
     begin(k);
     bool first_item = true;  // that has tiles here
+    load_q(w);
     for (;;) {
         const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
         if (k.n_steps > 0) {
-            // ---- q rows to shared memory: a power of two per row, then f16 parts.  16 threads a row: a thread's elements
-            // are pairs e, e + 4 of one word, as the operands have them
-            for (int rr = tid >> 3; rr < ROWS; rr += kWarps * 4) {
-                const int l8 = tid & 7;
-                const int idx = w.rt * ROWS + rr, node = idx / p.group, hq = w.h * p.group + idx - node * p.group;
-                const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(w.row0) + node) * p.q_row + hq * p.q_head;
+            // ---- q rows to shared memory: a power of two per row, then f16 parts
+            if (q_row < ROWS) {  // whole warps
+                const int rr = q_row;
                 float x[4 * NB];
                 float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4 * NB; ++i) {
-                    const int e = l8 + 8 * i;
-                    x[i] = rr < rows && e < pp.dim ? to_f32(src[e]) : 0.0f;
+                    x[i] = to_f32(q_raw[i]);
                     top = fmaxf(top, fabsf(x[i]));
                 }
 #pragma unroll
@@ -484,6 +524,12 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                     row_mul[rr] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * kUnit * fabsf(p.scale_log2), 1e-37f);
             }
             __syncthreads();
+            const bool more = w.first + w.tiles_k < u_end;
+            if (more) {
+                Place next = w;
+                advance(next);
+                look(work_of(next));
+            }
 
             float o[NT][NB * 2][4];
 #pragma unroll
@@ -790,14 +836,15 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                 for (int j = 0; j + 1 < kStages4; ++j) row_cur[j] = row_cur[j + 1];
             }
             slot0 = slot;
-            // ---- the next item's first keys are on their way while the warps of this one are joined
+            // ---- the next item's first keys and q are on their way while the warps of this one are joined
             const Place done = w;
             const Work did = k;
-            const bool more = w.first + w.tiles_k < u_end;
             if (more) {
                 advance(w);
                 k = work_of(w);
-                begin(k);
+                cp_wait<0>();
+                begin_ahead(k);
+                load_q(w);
             }
             const bool whole = did.kt0 == 0 && did.kt1 == done.tiles_k;
             const int pitch = pp.dim + kPartExtra;
@@ -973,6 +1020,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
             advance(w);
             k = work_of(w);
             begin(k);
+            load_q(w);
         }
         __syncthreads();  // the join's reads, before the next item's q
     }
