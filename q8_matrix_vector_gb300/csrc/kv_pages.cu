@@ -579,6 +579,10 @@ bool take(const kvpage_s *plan, const kvpage_state_t *s, PageParams *p) {
 // for more (extend, 144 requests and 4096 pages: 11.0 us by a cluster, 6.8 by one; compact, 16384 pages: 8.4 and 16.8).
 q8mv_status_t launch_cluster(void (*kernel)(PageParams), const PageParams &p, int pages, cudaStream_t stream) {
     const int ctas = p.pages > pages || p.requests > kThreads ? kCluster : 1;
+    if (ctas == 1) {  // (a cluster of its own)
+        kernel<<<1, kThreads, 0, stream>>>(p);
+        return q8i::cuda_status(cudaGetLastError());
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
