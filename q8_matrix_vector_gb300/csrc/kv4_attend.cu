@@ -193,7 +193,13 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     const int scales = 4 * r.blocks;  // bytes of a row's
     const bool in_turn = r.stride_token == 1 && r.page_size % 16 == 0 && (r.stride_page * scales) % 16 == 0 &&
                          (r.stride_head * scales) % 16 == 0;
-    const kv::Attend4Shape v = in_turn ? (wide ? kv::k4Rows16InTurn : kv::k4Rows8InTurn) : wide ? kv::k4Rows16 : kv::k4Rows8;
+    // With 8 rows, and a token's heads side by side, each warp can take a head of its own, so that a CTA reads longer stretches
+    // than one head's 64 bytes (kv_attend.cu).  But four heads' parts are to be joined instead of one's, so only where the
+    // tables reach 150 MB: 69 MB of two requests 30 us by one head and 43 by four, 138 MB 57 and 59, 276 MB 104 and 87, 1.1 GB
+    // 455 and 256; 295 MB of 64 requests 109 and 86; heads of 256 (590 MB) 191 and 143.
+    const double bytes = static_cast<double>(reach) * a->requests * r.heads * 2.0 * (r.dim + scales);
+    const bool side_by_side = r.stride_head < r.stride_token && r.heads % kv::kWarps == 0 && bytes >= 1.5e8;
+    const kv::Attend4Shape v = side_by_side && mean <= 8 ? kv::k4Heads4 : in_turn ? (wide ? kv::k4Rows16InTurn : kv::k4Rows8InTurn) : wide ? kv::k4Rows16 : kv::k4Rows8;
     const kv::Attend4Variant &k = plan->variant[a->type][v];
     k.fn<<<plan->grid[a->type][v], kv::kWarps * 32, k.smem, stream>>>(pp);
     return q8i::cuda_status(cudaGetLastError());

@@ -4,8 +4,8 @@
 //     out[r, e] = sum_j P[r, j] * dV[j, b(e)] * (cV[j, e] - 8) / sum_j P[r, j],   P = exp(s - max)
 //
 // Work is cut and joined as in kv_attend.cuh: (request, kv head, 8 or 16 query rows)
-// items on one line of units, equal shares of it a CTA, parts joined by the last to
-// come.  A warp takes 32 keys of a tile of 128, keeps its own maximum, sum and
+// items, or 8 rows of four heads, on one line of units, equal shares of it a CTA, parts
+// joined by the last to come.  A warp takes 32 keys of a tile of 128, keeps its own maximum, sum and
 // accumulators, and fills its own ring with cp.async.  The cache is the first operand
 // of mma.sync m16n8k16, 8 rows the second.  What four bits change:
 //   * A nibble where it lies in a half word is, as an f16's bits, c 2^-24 or 16 c 2^-24,
@@ -43,25 +43,31 @@ namespace kv {
 
 // Steps in flight a warp, and CTAs an SM.  8 rows of up to 128: three CTAs (168 registers a thread); with four the registers
 // spill in the loop (two requests of 300k .. 524k tokens, bf16: 233 and 236 us; 64 of 180 .. 8100: 84.8 and 89.1), and
-// three steps with three CTAs gain nothing (233.0 and 233.0; 64 requests of 8000: 143.4 and 144.3).
+// three steps with three CTAs gain nothing (233.0 and 233.0; 64 requests of 8000: 143.4 and 144.3).  Heads of 64: four (64
+// of 180 .. 8100: 56.9 us with three, 52.4 with four).
 constexpr int kStages4 = 2;
 constexpr float kSlack = 5.0f;
 
-// Shared memory of one variant: NB stored blocks, NT tiles of 8 query rows, QP parts of q.
-template <int NB, int NT, int QP>
+// Shared memory of one variant: NB stored blocks, NT tiles of 8 query rows, QP parts of q, HW kv heads (the warps' own,
+// or one for all warps).
+template <int NB, int NT, int QP, int HW>
 struct Smem4 {
     static constexpr int kRows = 8 * NT;
+    static constexpr int kTileKeys = kStepKeys * kWarps / HW;
     static constexpr int kCodes = 16 * NB;                       // of a row
     static constexpr int kKPitch = NB == 8 ? kCodes + 16 : kCodes;  // 8: rows two apart would share banks
     static constexpr int kScales = NB == 2 ? 4 : NB <= 4 ? 8 : 16;  // bytes of a row's scales
     static constexpr int kStage = kStepKeys * (kKPitch + kCodes + 2 * kScales);
     static constexpr int kRing = kStage * kStages4 * kWarps;
     static constexpr int kJoinPitch = 32 * NB + 4;
-    static constexpr int kJoin = kWarps * 8 * kJoinPitch * 4;
+    // 8 rows of a warp's results, f32, in the stage that is free when an item ends
+    static_assert(8 * kJoinPitch * 4 <= kStage, "a stage holds them");
     static constexpr int kQPitch = 64 * NB + ((64 * NB) % 128 == 64 ? 0 : 64);
-    static constexpr int kQ = QP * kRows * kQPitch;
-    static constexpr int kBias = kRows * 32;  // 8 pairs of f16 a row
-    static constexpr int kTotal = kRing + kJoin + kQ + kBias;
+    static constexpr int kQHead = QP * kRows * kQPitch;
+    static constexpr int kQ = HW * kQHead;
+    static constexpr int kBiasHead = kRows * 32;  // 8 pairs of f16 a row
+    static constexpr int kBias = HW * kBiasHead;
+    static constexpr int kTotal = kRing + kQ + kBias;
     // where the 16-byte piece `c` of value row r is: spread so that the lanes of a load meet no bank twice
     static __host__ __device__ constexpr int v_piece(int r, int c) {
         return NB == 4 ? c ^ (r & 2) : NB == 8 ? c ^ ((r & 3) << 1) : c;
@@ -195,25 +201,26 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     return y;
 }
 
-template <typename T, int NB, int NT, int QP, int PP, bool SEG>
-__global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
+template <typename T, int NB, int NT, int QP, int PP, bool SEG, int HW>
+__global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 && NT == 1 ? 3 : 2)
     q4kv_attend_kernel(const Attend4Params pp) {
-    using S = Smem4<NB, NT, QP>;
-    constexpr int ROWS = S::kRows, KEYS = kStepKeys * kWarps, W = (NB + 1) / 2;
+    using S = Smem4<NB, NT, QP, HW>;
+    static_assert(HW == 1 || (HW == kWarps && NT == 1), "one head for all warps, or one each with 8 rows");
+    constexpr int ROWS = S::kRows, KEYS = S::kTileKeys, W = (NB + 1) / 2;
+    constexpr int TILES = HW == 1 ? NT : HW;  // of 8 rows in a partial result
     constexpr bool EXACT = QP == 2, PACKED = !EXACT;
     constexpr float kUnit = EXACT ? 1.0f : 16777216.0f;  // codes stand for so many
     const AttendParams &p = pp.a;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t scan_units[kWarps], scan_items[kWarps];
     __shared__ int64_t start_b, start_item, start_unit;
-    __shared__ float row_mul[ROWS];
+    __shared__ float row_mul[HW * ROWS];
     __shared__ int ahead[kWarps][2][32];  // pages of the next item's first two steps
     __shared__ int is_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    float *jo = reinterpret_cast<float *>(smem + S::kRing);  // [warp][8 rows][kJoinPitch]
-    unsigned char *q_sm = smem + S::kRing + S::kJoin;
+    unsigned char *q_sm = smem + S::kRing;
     unsigned char *bias_sm = q_sm + S::kQ;  // [row][slot][2]: slot part * W + block / 2
 
     // ---- the CTA's share of the line of units (kv_attend.cuh)
@@ -226,8 +233,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         int64_t units = 0, items = 0;
         for (int b = b0; b < b1; ++b) {
             load_request<ROWS, KEYS>(p, b, w);
-            units += units_of<1>(p, w);
-            items += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+            units += units_of<HW>(p, w);
+            items += static_cast<int64_t>(p.c.heads / HW) * w.tiles_r;
         }
         int64_t iu = units, ii = items;  // inclusive over the warp
 #pragma unroll
@@ -264,10 +271,10 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
             int b = b0;
             for (; b < b1; ++b) {
                 load_request<ROWS, KEYS>(p, b, w);
-                const int64_t n = units_of<1>(p, w);
+                const int64_t n = units_of<HW>(p, w);
                 if (u < before_u + n) break;
                 before_u += n;
-                before_i += static_cast<int64_t>(p.c.heads) * w.tiles_r;
+                before_i += static_cast<int64_t>(p.c.heads / HW) * w.tiles_r;
             }
             start_b = b;
             start_unit = before_u;
@@ -278,6 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         const int64_t k = (u - start_unit) / (w.tiles_k + kItemUnits);  // item within the request
         w.h = static_cast<int>(k / w.tiles_r);
         w.rt = static_cast<int>(k - static_cast<int64_t>(w.h) * w.tiles_r);
+        w.h *= HW;
         w.item = start_item + k;
         w.first = start_unit + k * (w.tiles_k + kItemUnits) + kItemUnits;
     }
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         ++x.item;
         if (++x.rt == x.tiles_r) {
             x.rt = 0;
-            if (++x.h == p.c.heads) {
+            if ((x.h += HW) == p.c.heads) {
                 x.h = 0;
                 do load_request<ROWS, KEYS>(p, x.b + 1, x);
                 while (x.tiles_r == 0);
@@ -386,11 +394,11 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         Work k;
         k.kt0 = max(u, x.first) - x.first;
         k.kt1 = max(min(u_end, x.first + x.tiles_k) - x.first, k.kt0);
-        k.base0 = static_cast<int>(k.kt0) * KEYS + warp * kStepKeys;
+        k.base0 = static_cast<int>(k.kt0) * KEYS + (HW == 1 ? warp * kStepKeys : 0);
         k.n_steps = static_cast<int>(k.kt1 - k.kt0);
         k.keys = static_cast<int>(min(static_cast<int64_t>(x.prefix) + x.nodes,
                                       static_cast<int64_t>(p.table_cols) * p.c.page_size));
-        k.head = static_cast<uint32_t>(x.h) * pp.stride_head;
+        k.head = static_cast<uint32_t>(x.h + (HW == 1 ? 0 : warp)) * pp.stride_head;
         k.table = p.table + static_cast<int64_t>(x.b) * p.table_row;
         return k;
     };
@@ -443,18 +451,22 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         issue(k.n_steps > 0, slot0, row[0]);
         row_next = row[1];
     };
-    // The thread's elements of an item's q: l8 + 8 i of row tid / 8
-    static_assert(ROWS <= kWarps * 4, "a row for every 8 threads");
+    // The thread's elements of an item's q: l8 + 8 i of rows tid / 8 and, with four heads, 16 behind it
+    constexpr int PASSES = (HW * ROWS + kWarps * 4 - 1) / (kWarps * 4);
     const int q_row = tid >> 3, l8 = tid & 7;
-    T q_raw[4 * NB];
+    T q_raw[PASSES][4 * NB];
     auto load_q = [&](const Place &x) {
-        const int idx = x.rt * ROWS + q_row, node = idx / p.group, hq = x.h * p.group + idx - node * p.group;
-        const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(x.row0) + node) * p.q_row + hq * p.q_head;
-        const bool live = q_row < min(ROWS, x.nodes * p.group - x.rt * ROWS);
 #pragma unroll
-        for (int i = 0; i < 4 * NB; ++i) {
-            const int e = l8 + 8 * i;
-            q_raw[i] = live && e < pp.dim ? src[e] : from_f32<T>(0.0f);
+        for (int s = 0; s < PASSES; ++s) {
+            const int rr = q_row + s * (kWarps * 4), hw = rr / ROWS, r = rr % ROWS;
+            const int idx = x.rt * ROWS + r, node = idx / p.group, hq = (x.h + hw) * p.group + idx - node * p.group;
+            const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(x.row0) + node) * p.q_row + hq * p.q_head;
+            const bool live = rr < HW * ROWS && r < min(ROWS, x.nodes * p.group - x.rt * ROWS);
+#pragma unroll
+            for (int i = 0; i < 4 * NB; ++i) {
+                const int e = l8 + 8 * i;
+                q_raw[s][i] = live && e < pp.dim ? src[e] : from_f32<T>(0.0f);
+            }
         }
     };
     // Row g of an octet of the operands is place (g & 1) * 4 + g / 2 of eight keys, so that the four keys 2c, 2c + 1 of a
@@ -469,13 +481,15 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
         const int rows = min(ROWS, w.nodes * p.group - w.rt * ROWS);
         if (k.n_steps > 0) {
             // ---- q rows to shared memory: a power of two per row, then f16 parts
-            if (q_row < ROWS) {  // whole warps
-                const int rr = q_row;
+#pragma unroll
+            for (int pass = 0; pass < PASSES; ++pass) {
+                const int rr = q_row + pass * (kWarps * 4);
+                if (rr >= HW * ROWS) break;  // whole warps
                 float x[4 * NB];
                 float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4 * NB; ++i) {
-                    x[i] = to_f32(q_raw[i]);
+                    x[i] = to_f32(q_raw[pass][i]);
                     top = fmaxf(top, fabsf(x[i]));
                 }
 #pragma unroll
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                 for (int i = 0; i < 4 * NB; ++i) {
                     const float y = x[i] * down * part16;
                     const __half hi = __float2half_rn(y);
-                    __half *dst = reinterpret_cast<__half *>(q_sm + rr * S::kQPitch) + 8 * i + 2 * (l8 & 3) + (l8 >> 2);
+                    __half *dst = reinterpret_cast<__half *>(q_sm + rr / ROWS * S::kQHead + rr % ROWS * S::kQPitch) + 8 * i + 2 * (l8 & 3) + (l8 >> 2);
                     *dst = hi;
                     float used = __half2float(hi);
                     if constexpr (QP == 2) {
@@ -548,10 +562,12 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                 for (int r = 0; r < 2; ++r) {
                     m[t][r] = -INFINITY;
                     minus[t][r] = l[t][r] = 0.0f;
-                    mul[t][r] = row_mul[8 * t + 2 * c + r];
-                    if constexpr (!EXACT) bias[t][r] = reinterpret_cast<const uint32_t *>(bias_sm)[(8 * t + g) * 8 + 4 * r + c];
+                    mul[t][r] = row_mul[(HW == 1 ? 0 : warp * ROWS) + 8 * t + 2 * c + r];
+                    if constexpr (!EXACT)
+                        bias[t][r] = reinterpret_cast<const uint32_t *>(bias_sm)[((HW == 1 ? 0 : warp * ROWS) + 8 * t + g) * 8 + 4 * r + c];
                 }
 
+            const unsigned char *my_q = q_sm + (HW == 1 ? 0 : warp * S::kQHead);
             int slot = slot0;
             for (int i = 0; i < k.n_steps; ++i) {
                 // row_cur[0] is step i's; the next free stage takes step i + kStages4 - 1
@@ -639,7 +655,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
 #pragma unroll
                                 for (int q = 0; q < QP; ++q) {
                                     const uint4 qq = *reinterpret_cast<const uint4 *>(
-                                        q_sm + (q * ROWS + 8 * t + g) * S::kQPitch + b * 64 + c * 16);
+                                        my_q + (q * ROWS + 8 * t + g) * S::kQPitch + b * 64 + c * 16);
                                     mma_f16(part, a0, qq.x, qq.y, part);
                                     mma_f16(part, a1, qq.z, qq.w, part);
                                 }
@@ -852,20 +868,65 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
             first_item = false;
             // tile t, row r8 of the item's results: its output row and query head
             auto place_row = [&](int t, int r8, int64_t *row, int *hq) -> bool {
-                const int r = 8 * t + r8;
+                const int r = HW == 1 ? 8 * t + r8 : r8;
                 const int idx = done.rt * ROWS + r, node = idx / p.group;
                 *row = static_cast<int64_t>(done.row0) + node;
-                *hq = done.h * p.group + idx - node * p.group;
+                *hq = (done.h + (HW == 1 ? 0 : t)) * p.group + idx - node * p.group;
                 return r < rows;
+            };
+            // elements 4 g + {0 .. 3} of each block, in the codes' units, 16 in the odd ones
+            constexpr float one = kUnit, sixteen = kUnit / 16.0f;
+            if constexpr (HW > 1) {
+                // each warp has whole results of its head
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int r8 = 2 * c + r;
+                    int64_t row;
+                    int hq;
+                    const bool live = place_row(warp, r8, &row, &hq);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) l[0][r] += __shfl_xor_sync(~0u, l[0][r], d);
+                    if (live) {
+                        T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
+                        float *part = p.partial + (slot_p * (8 * TILES) + warp * 8 + r8) * pitch;
+                        const float sum = l[0][r], inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const int e = 32 * b + 4 * g;
+                            const float4 x = make_float4(o[0][2 * b][r] * one, o[0][2 * b][2 + r] * sixteen, o[0][2 * b + 1][r] * one,
+                                                         o[0][2 * b + 1][2 + r] * sixteen);
+                            if (e < pp.dim) {
+                                if (whole) {
+                                    out[e] = from_f32<T>(x.x * inv);
+                                    out[e + 1] = from_f32<T>(x.y * inv);
+                                    out[e + 2] = from_f32<T>(x.z * inv);
+                                    out[e + 3] = from_f32<T>(x.w * inv);
+                                } else {
+                                    *reinterpret_cast<float4 *>(part + e) = x;
+                                }
+                            }
+                        }
+                        if (g == 0) {
+                            if (!whole) {
+                                part[pp.dim] = m[0][r];
+                                part[pp.dim + 1] = sum;
+                            } else if (p.lse) {
+                                p.lse[row * p.heads_q + hq] = (-minus[0][r] + log2f(sum)) * 0.693147180559945f;
+                            }
+                        }
+                    }
+                }
+            } else {
+            // row r8 of warp q: [kJoinPitch], its maximum and sum behind its elements
+            auto joined = [&](int q, int r8) {
+                return reinterpret_cast<float *>(smem + q * (S::kStage * kStages4) + (slot0 ^ 1) * S::kStage) + r8 * S::kJoinPitch;
             };
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (t > 0) __syncthreads();
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float *at = jo + (warp * 8 + 2 * c + r) * S::kJoinPitch;
-                    // elements 4 g + {0 .. 3} of each block, in the codes' units, 16 in the odd ones
-                    constexpr float one = kUnit, sixteen = kUnit / 16.0f;
+                    float *at = joined(warp, 2 * c + r);
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
                         *reinterpret_cast<float4 *>(at + 32 * b + 4 * g) =
@@ -884,11 +945,11 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                 const int r8 = tid / TPR, lr = tid % TPR;
                 float f[kWarps], top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                for (int q = 0; q < kWarps; ++q) top = fmaxf(top, jo[(q * 8 + r8) * S::kJoinPitch + 32 * NB]);
+                for (int q = 0; q < kWarps; ++q) top = fmaxf(top, joined(q, r8)[32 * NB]);
                 const float z = top == -INFINITY ? 0.0f : top;
 #pragma unroll
                 for (int q = 0; q < kWarps; ++q) {
-                    const float *x = jo + (q * 8 + r8) * S::kJoinPitch;
+                    const float *x = joined(q, r8);
                     f[q] = ex2(x[32 * NB] - z);
                     sum = fmaf(f[q], x[32 * NB + 1], sum);
                 }
@@ -896,7 +957,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                 int hq;
                 if (place_row(t, r8, &row, &hq)) {
                     T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
-                    float *part = p.partial + (slot_p * ROWS + 8 * t + r8) * pitch;
+                    float *part = p.partial + (slot_p * (8 * TILES) + 8 * t + r8) * pitch;
                     const float inv = sum > 0.0f ? __frcp_rn(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
 #pragma unroll
                     for (int q = 0; q < 32 * NB / TPR; ++q) {
@@ -904,7 +965,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                         if (e < pp.dim) {
                             float x = 0.0f;
 #pragma unroll
-                            for (int v = 0; v < kWarps; ++v) x = fmaf(f[v], jo[(v * 8 + r8) * S::kJoinPitch + e], x);
+                            for (int v = 0; v < kWarps; ++v) x = fmaf(f[v], joined(v, r8)[e], x);
                             if (whole)
                                 out[e] = from_f32<T>(x * inv);
                             else
@@ -921,9 +982,10 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                     }
                 }
             }
+            }
             // (an item past the tickets exists only if `starts` is not ascending: it has no output)
             if (!whole && done.item < p.tickets_n) {
-                constexpr int TPR = kWarps * 32 / ROWS, V = (8 * NB + TPR - 1) / TPR;  // threads a row, float4 a thread
+                constexpr int PR = 8 * TILES, TPR = kWarps * 32 / PR, V = (8 * NB + TPR - 1) / TPR;  // rows, threads a row, float4 a thread
                 const int pr = tid / TPR, lr = tid % TPR;
                 int64_t row;
                 int hq;
@@ -931,8 +993,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                 // Adds n parts, the first at slot `head`, the i-th at slot `at + i * step`: to the output, or to the
                 // first part's place.
                 auto join = [&](int n, int64_t head, int64_t at, int64_t step, bool last) {
-                    const float *from = p.partial + (at * ROWS + pr) * pitch, *from0 = p.partial + (head * ROWS + pr) * pitch;
-                    step *= ROWS * pitch;
+                    const float *from = p.partial + (at * PR + pr) * pitch, *from0 = p.partial + (head * PR + pr) * pitch;
+                    step *= PR * pitch;
                     float top = -INFINITY, sum = 0.0f, x[V][4];
 #pragma unroll
                     for (int q = 0; q < V; ++q)
@@ -972,7 +1034,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
                         if (lr == 0 && p.lse)
                             p.lse[row * p.heads_q + hq] = ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.693147180559945f;
                     } else if (live) {
-                        float *to = p.partial + (head * ROWS + pr) * pitch;
+                        float *to = p.partial + (head * PR + pr) * pitch;
 #pragma unroll
                         for (int q = 0; q < V; ++q)
                             if (4 * (lr + TPR * q) < pp.dim)
@@ -1026,21 +1088,34 @@ __global__ void __launch_bounds__(kWarps * 32, NB <= 4 && NT == 1 ? 3 : 2)
     }
 }
 
-template <typename T, int NB, int NT, int QP, int PP>
+template <typename T, int NB, int NT, int QP, int PP, int HW>
 Attend4Variant attend4_variant_of(bool rows_in_turn) {
-    return {rows_in_turn ? q4kv_attend_kernel<T, NB, NT, QP, PP, true> : q4kv_attend_kernel<T, NB, NT, QP, PP, false>,
-            Smem4<NB, NT, QP>::kTotal, 8 * NT};
+    constexpr int smem = Smem4<NB, NT, QP, HW>::kTotal, rows = 8 * (HW == 1 ? NT : HW);
+    if constexpr (HW == 1)
+        if (rows_in_turn) return {q4kv_attend_kernel<T, NB, NT, QP, PP, true, HW>, smem, rows};
+    return {q4kv_attend_kernel<T, NB, NT, QP, PP, false, HW>, smem, rows};
+}
+
+template <typename T, int NB, int QP, int PP>
+Attend4Variant attend4_variant_of(Attend4Shape shape) {
+    switch (shape) {
+        case k4Rows8: return attend4_variant_of<T, NB, 1, QP, PP, 1>(false);
+        case k4Rows8InTurn: return attend4_variant_of<T, NB, 1, QP, PP, 1>(true);
+        case k4Heads4: return attend4_variant_of<T, NB, 1, QP, PP, kWarps>(false);
+        default: break;
+    }
+    if constexpr (NB <= 4) return attend4_variant_of<T, NB, 2, QP, PP, 1>(shape == k4Rows16InTurn);
+    return {};
 }
 
 template <typename T, int QP, int PP>
 Attend4Variant attend4_variant_of(int blocks, Attend4Shape shape) {
-    const bool seg = shape == k4Rows8InTurn || shape == k4Rows16InTurn, wide = shape == k4Rows16 || shape == k4Rows16InTurn;
     switch (blocks) {
-        case 2: return wide ? attend4_variant_of<T, 2, 2, QP, PP>(seg) : attend4_variant_of<T, 2, 1, QP, PP>(seg);
-        case 3: return wide ? attend4_variant_of<T, 3, 2, QP, PP>(seg) : attend4_variant_of<T, 3, 1, QP, PP>(seg);
-        case 4: return wide ? attend4_variant_of<T, 4, 2, QP, PP>(seg) : attend4_variant_of<T, 4, 1, QP, PP>(seg);
-        case 6: return wide ? Attend4Variant{} : attend4_variant_of<T, 6, 1, QP, PP>(seg);
-        case 8: return wide ? Attend4Variant{} : attend4_variant_of<T, 8, 1, QP, PP>(seg);
+        case 2: return attend4_variant_of<T, 2, QP, PP>(shape);
+        case 3: return attend4_variant_of<T, 3, QP, PP>(shape);
+        case 4: return attend4_variant_of<T, 4, QP, PP>(shape);
+        case 6: return attend4_variant_of<T, 6, QP, PP>(shape);
+        case 8: return attend4_variant_of<T, 8, QP, PP>(shape);
         default: return {};
     }
 }

@@ -21,8 +21,8 @@ struct Attend4Variant {
 };
 
 // 8 or 16 query rows of one kv head at a time, for NB = 2, 3, 4, 6 or 8 stored blocks (16: up to 4); a warp's keys one
-// by one, or 16 at a time that follow one another in memory.
-enum Attend4Shape { k4Rows8 = 0, k4Rows16, k4Rows8InTurn, k4Rows16InTurn, kAttend4Shapes };
+// by one, or 16 at a time that follow one another in memory; or 8 rows of four kv heads, one for each warp.
+enum Attend4Shape { k4Rows8 = 0, k4Rows16, k4Rows8InTurn, k4Rows16InTurn, k4Heads4, kAttend4Shapes };
 
 Attend4Variant attend4_variant_f32(int blocks, Attend4Shape shape);
 Attend4Variant attend4_variant_f16(int blocks, Attend4Shape shape);

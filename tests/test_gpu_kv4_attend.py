@@ -336,3 +336,47 @@ def test_a_wait_that_runs_out_is_reported(q8mv):
     c.plan.set_wait(0)
     again = c.run()
     assert (want[0] == again[0]).all() and (want[1] == again[1]).all() and c.plan.check() == 0
+
+
+def side_by_side(q8mv, seed, lengths, nodes, **more):
+    """A case that four heads a CTA take: a token's heads side by side, a table that reaches far, at most 8 rows."""
+    return Case(q8mv, seed, lengths, nodes, layout="token", cols=2 ** 20 // more.get("page", 16), **more)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("dim", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("heads,group,nodes", [(4, 8, [1, 1, 1, 0]), (8, 1, [3, 1, 0, 8]), (4, 3, [2, 2, 1, 3])])
+def test_four_heads_a_cta(q8mv, dtype, dim, heads, group, nodes):
+    side_by_side(q8mv, dim + group, [300, 1, 77, 0], nodes, heads=heads, group=group, dim=dim, dtype=dtype, page=24).check()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_four_heads_a_cta_cut_over_many(q8mv, dtype):
+    c = side_by_side(q8mv, 41, [9000, 40], [1, 2], heads=4, group=2, dim=128, dtype=dtype, page=64)
+    c.check()
+    out, lse = c.run()
+    for _ in range(3):
+        again = c.run()
+        assert (out == again[0]).all() and (lse == again[1]).all()
+
+
+def test_four_heads_a_cta_masks_and_what_is_not_finite(q8mv):
+    import torch
+
+    side_by_side(q8mv, 42, [0, 0], [3, 3], heads=4, group=2, dim=128, density=0.0).check()
+    c = side_by_side(q8mv, 43, [100, 30], [4, 4], heads=8, group=1, dim=96, dtype="bfloat16")
+    for b in range(2):
+        c.seen[b][:, 1] = False
+    mask = c.mask.cpu().numpy().view(np.uint32) & ~np.uint32(2)
+    c.mask = torch.from_numpy(mask.view(np.int32)).cuda()
+    c.device()
+    for b, value in ((0, np.inf), (1, np.nan)):
+        pos = int(c.lengths[b]) + 1
+        for s in (c.cache.k_scales, c.cache.v_scales):
+            s[int(c.table[b, pos // 16]), :, pos % 16] = value
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("nodes", [[1, 1], [40, 40]])
+def test_tables_without_columns(q8mv, nodes):
+    Case(q8mv, 44, [30, 0], nodes, cols=0, dim=128, dtype="bfloat16").check()

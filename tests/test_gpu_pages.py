@@ -259,3 +259,44 @@ def test_refusals(q8mv):
         cache.copy_pages(good, good.long())
     with pytest.raises(TypeError):
         cache.copy_pages(good, good, torch.zeros(1, device="cuda"))
+
+
+def test_more_requests_than_a_cluster_keeps(q8mv):
+    """Amounts of more than 512 requests a CTA go through the workspace."""
+    rng = np.random.default_rng(5)
+    n = 5000
+    pair = Pair(q8mv, 9000, 4, n, 6)
+    lengths = np.zeros(n, int)
+    for _ in range(3):
+        tokens = rng.integers(0, 9, n)
+        _, _, _, ok = pair.extend(lengths, tokens, 8)
+        lengths = np.where(ok == 1, lengths + tokens, lengths)
+        parents = np.arange(n)
+        parents[rng.random(n) < 0.2] = rng.integers(n)
+        pair.fork(parents)
+        lengths = lengths[parents]
+    pair.compact()
+
+
+def test_a_captured_cluster(q8mv):
+    import torch
+
+    pool, plain = q8mv.Pages(40000, 8, 20, 40), ref.Pool(40000, 8, 20, 40)
+    lengths = torch.zeros(20, dtype=torch.int32, device="cuda")
+    tokens = torch.full_like(lengths, 100)
+    pool.refs[:39000] = 1  # held by nobody here
+    plain.refs[:39000] = 1
+    pool.extend(lengths, torch.zeros_like(lengths), 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pool.extend(lengths, tokens, 70)  # (and slots by a kernel of their own)
+        moves = pool.compact()
+    host = np.zeros(20, int)
+    for _ in range(3):
+        graph.replay()
+        want = plain.extend(host, [100] * 20, 70)
+        want_moves = plain.compact()
+        for a, b in (*zip(out, want), *zip(moves, want_moves), *zip((pool.refs, pool.table, pool.held), plain.state())):
+            assert np.array_equal(a.cpu().numpy(), b)
+        host += 100
+        lengths.add_(tokens)
