@@ -9,7 +9,7 @@
  * unsigned integers, so that no position is too far for the angle to be exact:
  *     c = f32(cos) * factor,  s = f32(sin) * factor
  *     y[a] = x[a] c - x[b] s,  y[b] = x[b] c + x[a] s     (a, b the pair)
- * in f32, every step rounded.  cos and sin are within 2^-35 of the angle's before
+ * in f32, every step rounded.  cos and sin are within 2^-42 of the angle's before
  * their rounding to f32.  A frequency f, in radians a position, has turns
  * round(f / (2 pi) * 2^64).  Frequencies that are scaled for long contexts, by any
  * rule, are other turns.

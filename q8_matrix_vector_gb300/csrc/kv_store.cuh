@@ -14,10 +14,11 @@
 //     its threads, into shared memory, for all heads.  p * turns modulo 2^64 is the
 //     angle to the last bit at any position.  Its top 8 bits pick one of 256 points of
 //     the circle, kept as two f32 each; the rest, below pi / 256, is a two-term f32 number,
-//     and sin r = r - r^3/6 + r^5/120, cos r - 1 = -r^2/2 + r^4/24 have terms so small
-//     that f32 is enough; the angles' sum adds up to 2^-35.  The rounding to f32 is then
-//     as good as always that of the exact value, so that rotated keys get the codes that
-//     a program in 64 bits gives them.
+//     and sin r = r - r^3/6 + r^5/120, cos r = 1 - r^2/2 + r^4/24 have small terms for which
+//     f32 is enough; the great ones keep what their roundings lose.  That adds up to 2^-42, so
+//     that the rounding to f32 is as good as always that of the exact value, and rotated keys
+//     get the codes that a program in 64 bits gives them (at 2^-35 a code of a prompt of
+//     8192 tokens differed now and then).
 //     For q a lane takes both halves of its pairs, so that q may be rotated in place;
 //     k's other half is read by the lane that needs it (it is in L1).
 #pragma once
@@ -76,20 +77,24 @@ __device__ __forceinline__ void turn(uint64_t t, const float4 *circle, float *c,
     // 2 pi / 2^39 in two parts
     constexpr float k1 = 0x1.921fb6p-37f, k2 = -0x1.777a5cp-62f;
     const float x = __fmul_rn(h, k1);
-    const float x2 = __fmul_rn(x, x);
-    const float low = __fadd_rn(__fmaf_rn(h, k1, -x), __fmaf_rn(l, k1, __fmul_rn(h, k2)));
-    const float sl = __fmaf_rn(__fmul_rn(x2, x), __fmaf_rn(x2, 1.0f / 120.0f, -1.0f / 6.0f), low);  // sin = x + sl
-    const float cm = __fmaf_rn(-x, low, __fmul_rn(x2, __fmaf_rn(x2, 1.0f / 24.0f, -0.5f)));         // cos = 1 + cm
-    // C cos - S sin, S cos + C sin: the great terms with their roundings' errors
-    const float p = __fmul_rn(z.y, x), q = __fmul_rn(z.x, x);
-    const float pe = __fmaf_rn(z.y, x, -p), qe = __fmaf_rn(z.x, x, -q);
-    const float a = __fsub_rn(z.x, p), b = __fadd_rn(z.y, q);
-    // (|C| is above |S x| or 0, and so the other way about: the difference of a sum is exact)
-    const float ae = __fsub_rn(__fsub_rn(z.x, a), p), be = __fadd_rn(__fsub_rn(z.y, b), q);
-    const float ar = __fmaf_rn(z.x, cm, __fmaf_rn(-z.y, sl, __fmaf_rn(-z.w, x, __fsub_rn(z.z, pe))));
-    const float br = __fmaf_rn(z.y, cm, __fmaf_rn(z.x, sl, __fmaf_rn(z.z, x, __fadd_rn(z.w, qe))));
-    *c = __fadd_rn(a, __fadd_rn(ae, ar));
-    *s = __fadd_rn(b, __fadd_rn(be, br));
+    const float low = __fadd_rn(__fmaf_rn(h, k1, -x), __fmaf_rn(l, k1, __fmul_rn(h, k2)));  // the angle is x + low
+    // cos = 1 + n + g, sin = x + sl: n exact, the others below 4e-7
+    const float x2 = __fmul_rn(x, x), n = -0.5f * x2;
+    const float g = __fmaf_rn(__fmul_rn(x2, x2), 1.0f / 24.0f, -0.5f * __fmaf_rn(2.0f * x, low, __fmaf_rn(x, x, -x2)));
+    const float sl = __fmaf_rn(__fmul_rn(x2, x), __fmaf_rn(x2, 1.0f / 120.0f, -1.0f / 6.0f), low);
+    // C cos - S sin = C - S x + C n + ..., S cos + C sin = S + C x + S n + ...: the great terms with what their roundings
+    // lose, in falling order (or the first is 0 and the third with it), so that a sum less its first term is exact
+    const float C = z.x, S = z.y;
+    const float p = __fmul_rn(S, x), q = __fmul_rn(C, x), u = __fmul_rn(C, n), v = __fmul_rn(S, n);
+    const float a = __fsub_rn(C, p), b = __fadd_rn(S, q);
+    const float c1 = __fadd_rn(a, u), s1 = __fadd_rn(b, v);
+    const float ce = __fadd_rn(__fsub_rn(__fsub_rn(C, a), p), __fsub_rn(u, __fsub_rn(c1, a)));
+    const float se = __fadd_rn(__fadd_rn(__fsub_rn(S, b), q), __fsub_rn(v, __fsub_rn(s1, b)));
+    const float pe = __fsub_rn(__fmaf_rn(C, n, -u), __fmaf_rn(S, x, -p)), qe = __fadd_rn(__fmaf_rn(S, n, -v), __fmaf_rn(C, x, -q));
+    const float cr = __fmaf_rn(C, g, __fmaf_rn(-S, sl, __fmaf_rn(z.z, n, __fmaf_rn(-z.w, x, z.z))));
+    const float sr = __fmaf_rn(S, g, __fmaf_rn(C, sl, __fmaf_rn(z.w, n, __fmaf_rn(z.z, x, z.w))));
+    *c = __fadd_rn(c1, __fadd_rn(__fadd_rn(ce, pe), cr));
+    *s = __fadd_rn(s1, __fadd_rn(__fadd_rn(se, qe), sr));
 }
 
 // The largest x and the largest -x (and 0) of a lane's elements, NaN if one is.
