@@ -32,6 +32,13 @@
 // The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents.  The
 // running maximum moves only when a score is 2^kSlack above it, so that most steps need no
 // maximum over the lanes; f16 has the room.
+//
+// Measured on GB300, groups of 4 or 8 heads of 128, bf16 (copy rate 6792 GB/s): two requests
+// of 300k and 524k tokens 225 us, 5.0 TB/s of the cache; f16 280, f32 336.  64 requests of
+// 180 .. 8100 tokens 81 us, 3.6 TB/s; 64 of 8000 139 us, 4.9 TB/s.  What bounds the loop is
+// issue: 589 instructions a warp's 32 keys, a third of them masks, shifts and permutes on the
+// half-rate pipe, with three warps a scheduler; in the mixed batch an item's start, end and
+// join take a quarter of the time.
 #pragma once
 
 #include "kv4_attend.h"

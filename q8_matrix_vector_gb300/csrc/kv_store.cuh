@@ -21,6 +21,11 @@
 //     8192 tokens differed now and then).
 //     For q a lane takes both halves of its pairs, so that q may be rotated in place;
 //     k's other half is read by the lane that needs it (it is in L1).
+//
+// Measured on GB300 (copy rate 6792 GB/s): 8190 tokens of 32 heads of 128, bf16, to Q4_0
+// 37.9 us, 4.5 TB/s, issue (0.7 of the cycles).  8192 tokens, 8 heads to Q8_0 with 32 of q
+// rotated, 43.8 us, 4.3 TB/s, the latency of angles and loads (0.5 of the cycles issue); q
+// alone 24.6 us, 5.5 TB/s.
 #pragma once
 
 #include "kv4.h"
