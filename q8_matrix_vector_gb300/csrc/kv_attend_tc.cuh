@@ -29,11 +29,11 @@
 // recorded in the plan's error word and the CTA leaves, once its MMAs have ended and
 // its parts of cut items are counted: the tickets are whole after every call.
 //
-// 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 87.3 us,
-// 239 TFLOP/s of the two products, 1.2 TB/s of cache.  A tile takes 5600 cycles, of
-// which the MMAs run 1400; turning its codes into operands bounds it, then 8 us until a
-// CTA's first scores are there and 10 us of joining cut items at the end.
-// Over the Q4_0 cache 84 us: half of the bytes, as many operands to form.
+// 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 79.0 us,
+// 264 TFLOP/s of the two products, 1.3 TB/s of cache; over the Q4_0 cache 68.4 us.
+// A Q4_0 tile takes a convert warp 4600 cycles, of which the MMAs run 1400: K's operands
+// 1400, V's 700, waits 800, the copies and places of tiles to come 1000.  That bounds it,
+// then 8 us until a CTA's first scores are there and 10 us of joining cut items at the end.
 #pragma once
 
 #include "kv4_attend.h"
@@ -257,12 +257,11 @@ static __device__ __noinline__ void tc_count(const Split split, unsigned *ticket
     }
 }
 
-// A convert warp's place: an item, and which of its tiles here.
+// A convert warp's place: an item, and the first and the number of its tiles here.
 struct TcTile {
     Place w;
     int64_t kt;
-    int n, i;  // the item's tiles of this CTA, and which of them
-    bool any;
+    int n;  // 0: no item is left
 };
 
 template <int DP, int NB4>
@@ -479,48 +478,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         // ================ convert
         const int cw = warp - kTcSoftWarps, part = lane % PARTS, sub = lane / PARTS;
         const bool live = part * 16 < p.dim;
-        const int ct = tid - kTcSoftWarps * 32;  // thread among the convert warps
         unsigned char *const raws = smem + S::kRaw + cw * (2 * S::kRawWarp);  // by tile % 2: K, V, scales of K [key][NB], of V
         for (int i = lane; i < 2 * S::kRawWarp / 16; i += 32) reinterpret_cast<uint4 *>(raws)[i] = make_uint4(0, 0, 0, 0);
         __syncwarp();
-        // A tile of the CTA: its item and its number there.  The warp keeps two in shared memory, this one and the
-        // next but one: in registers they would push the codes out.
-        TcTile *const here = tiles[cw], *const ahead = tiles[cw] + 1;
+        // A tile of the CTA: its item in shared memory, its number there and how many are left with it in registers.  The
+        // warp keeps two, this one and the next but one.
+        struct Walk {
+            TcTile *item;
+            int64_t kt;
+            int left;  // tiles of the item, with this one; 0: the CTA has no more
+            bool fresh;
+        };
+        Walk here = {tiles[cw], 0, 0, true}, ahead = {tiles[cw] + 1, 0, 0, true};
         auto settle = [&](TcTile &t) {  // to the first item with tiles, from t.w on
             for (;;) {
                 t.n = tiles_of(t.w, &t.kt);
-                t.i = 0;
-                t.any = t.n > 0;
-                if (t.any || !more(t.w)) return;
+                if (t.n > 0 || !more(t.w)) return;
                 advance(t.w);
             }
         };
-        auto step = [&](TcTile *at) {
+        auto enter = [&](Walk &at) {
             __syncwarp();
-            if (lane == 0 && at->any) {
-                ++at->kt;
-                if (++at->i == at->n) {
-                    at->any = more(at->w);
-                    if (at->any) {
-                        TcTile t = *at;
-                        advance(t.w);
-                        settle(t);
-                        *at = t;
-                    }
-                }
-            }
-            __syncwarp();
+            at.kt = at.item->kt;
+            at.left = at.item->n;
+            at.fresh = true;
         };
-        // row of the lane's key in a tile, or kNoRow
-        auto find = [&](const TcTile *t) -> uint32_t {
-            if (!t->any) return kNoRow;
-            const int64_t pos = t->kt * kTcKeys + cw * WK + lane;
-            const int64_t keys = min(static_cast<int64_t>(t->w.prefix) + t->w.nodes, static_cast<int64_t>(p.table_cols) * p.c.page_size);
-            if (lane >= WK || pos >= keys) return kNoRow;
-            const uint32_t at = static_cast<uint32_t>(pos), col = (__umulhi(at, p.page_mul) + at) >> p.page_shift;
-            const int page = __ldg(p.table + static_cast<int64_t>(t->w.b) * p.table_row + col);
-            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
-            return static_cast<uint32_t>(row_of(p.c, page, t->w.h, static_cast<int>(at - col * p.c.page_size)));
+        auto step = [&](Walk &at) {
+            if (at.left == 0) return;
+            ++at.kt;
+            at.fresh = false;
+            if (--at.left > 0) return;
+            __syncwarp();
+            if (lane == 0) {
+                TcTile t = *at.item;
+                if (more(t.w)) {
+                    advance(t.w);
+                    settle(t);
+                } else {
+                    t.n = 0;
+                }
+                *at.item = t;
+            }
+            enter(at);
+        };
+        // The row of the lane's key in a tile, or kNoRow, in two steps, so that nothing waits for the table (which, with the
+        // walk in shared memory, cost 5 us of 79): the page, as it is loaded, and what the row is further than its page's first.
+        struct Found {
+            int page;
+            uint32_t rest;
+        };
+        auto find = [&](const Walk &at) -> Found {
+            Found f = {-1, 0};
+            if (at.left == 0) return f;
+            const Place &x = at.item->w;
+            const int64_t pos = at.kt * kTcKeys + cw * WK + lane;
+            const int64_t keys = min(static_cast<int64_t>(x.prefix) + x.nodes, static_cast<int64_t>(p.table_cols) * p.c.page_size);
+            if (lane >= WK || pos >= keys) return f;
+            const uint32_t i = static_cast<uint32_t>(pos), col = (__umulhi(i, p.page_mul) + i) >> p.page_shift;
+            f.rest = static_cast<uint32_t>(row_of(p.c, 0, x.h, static_cast<int>(i - col * p.c.page_size)));
+            f.page = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_row + col);
+            return f;
+        };
+        auto row_there = [&](const Found &f) -> uint32_t {
+            if (static_cast<uint32_t>(f.page) >= static_cast<uint32_t>(p.c.pages)) return kNoRow;
+            return static_cast<uint32_t>(row_of(p.c, f.page, 0, 0)) + f.rest;
         };
         const bool wide_scales = NB == 4 && p.c.blocks == 4;
         auto codes = [&](const int8_t *from, uint32_t to, uint32_t row) {  // the warp's rows of one array
@@ -648,60 +669,60 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
         int item_no = -1;
         float v_scale[NB] = {};  // the lane's key's scales of V, normalised, of the tile whose K was converted last
         // q and K of tile g
-        auto do_k = [&](int64_t g, uint32_t row, uint32_t row_after) -> bool {
-            const TcTile &t = *here;
+        auto do_k = [&](int64_t g, uint32_t row, const Found &after, uint32_t *row_after) -> bool {
+            const Place &t = here.item->w;
             // the scores of the tile before, which end its use of q and K (and tile g - 4's of the rings' entries)
             if (g > 0 && !waited(k_free + ((g - 1) & 1), (g - 1) >> 1)) return false;
-            const bool all_before = t.kt * kTcKeys + (cw + 1) * WK <= t.w.prefix;
-            if (t.i == 0) {
+            const bool all_before = here.kt * kTcKeys + (cw + 1) * WK <= t.prefix;
+            if (here.fresh) {
                 ++item_no;
-                constexpr int TPR = kTcConvWarps * 32 / kTcRows, H = DP / 8 / TPR;  // threads a row, a thread's groups of 8
-                const int r = ct / TPR, g0 = ct % TPR * H;
-                const int rows = min(kTcRows, t.w.nodes * p.group - t.w.rt * kTcRows);
-                const int idx = t.w.rt * kTcRows + r, node = idx / p.group, hq = t.w.h * p.group + idx - node * p.group;
-                const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(t.w.row0) + node) * p.q_row + hq * p.q_head;
+                // A warp takes 16 rows, LR lanes a row, 16 bytes of q each; four loads are on their way.
+                constexpr int LR = DP / 8, PER = 32 / LR, STEPS = kTcRows / kTcConvWarps / PER;
+                const int c = lane % LR, r0 = cw * (kTcRows / kTcConvWarps) + lane / LR;
+                const int rows = min(kTcRows, t.nodes * p.group - t.rt * kTcRows);
+                const uint32_t group = p.group, first = t.rt * kTcRows;
                 union Eight {
                     uint4 u;
                     T t[8];
                 };
-                auto eight = [&](int k) -> Eight {  // the k-th of the thread's groups
-                    const int e = 8 * (g0 + k);
-                    Eight y;
-                    y.u = make_uint4(0, 0, 0, 0);
-                    if (r < rows && e < p.dim) {
-                        if (p.q_vec) {
-                            y.u = __ldg(reinterpret_cast<const uint4 *>(src + e));
-                        } else {
+#pragma unroll 1
+                for (int k0 = 0; k0 < STEPS; k0 += 4) {
+                    Eight ys[4];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) y.t[j] = src[e + j];
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = r0 + (k0 + k) * PER;
+                        ys[k].u = make_uint4(0, 0, 0, 0);
+                        if (r < rows && 8 * c < p.dim) {
+                            const uint32_t idx = first + r, node = idx / group, hq = t.h * group + idx - node * group;
+                            const T *src = static_cast<const T *>(p.q) + (static_cast<int64_t>(t.row0) + node) * p.q_row + hq * p.q_head + 8 * c;
+                            if (p.q_vec) {
+                                ys[k].u = __ldg(reinterpret_cast<const uint4 *>(src));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) ys[k].t[j] = src[j];
+                            }
                         }
                     }
-                    return y;
-                };
-                uint32_t top = 0;
-#pragma unroll 4
-                for (int k = 0; k < H; ++k) {
-                    const Eight y = eight(k);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(y.t[j])) & 0x7FFFFFFFu);
-                }
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = r0 + (k0 + k) * PER;
+                        uint32_t top = 0;
 #pragma unroll
-                for (int d = 1; d < TPR; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
-                const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
-                const float down = copysignf(tc_pow2(-ex), p.scale_log2);
-#pragma unroll 4
-                for (int k = 0; k < H; ++k) {
-                    const Eight y = eight(k);
-                    uint32_t o[4];
+                        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(to_f32(ys[k].t[j])) & 0x7FFFFFFFu);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int e0 = NB4 == 0 ? 2 * e : e, e1 = NB4 == 0 ? e0 + 1 : e + 4;
-                        o[e] = pack_half2(to_f32(y.t[e0]) * down, to_f32(y.t[e1]) * down);
+                        for (int d = 1; d < LR; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
+                        const int ex = min(max(static_cast<int>(top >> 23) - 127 - 10, -100), 100);
+                        const float down = copysignf(tc_pow2(-ex), p.scale_log2);
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int e0 = NB4 == 0 ? 2 * e : e, e1 = NB4 == 0 ? e0 + 1 : e + 4;
+                            o[e] = pack_half2(to_f32(ys[k].t[e0]) * down, to_f32(ys[k].t[e1]) * down);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + tc_place(r, c)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                        if (c == 0) row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
                     }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + S::kQ + tc_place(r, g0 + k)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
                 }
-                if (g0 == 0)
-                    row_mul[item_no & 3][r] = fmaxf(tc_pow2(ex) * fabsf(p.scale_log2), 1e-37f);
             }
             if (g <= 2)
                 cp_wait<2>();
@@ -764,7 +785,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             __syncwarp();
             if (lane == 0) tc_arrive(k_full + x);
             // (after the fence, which would wait for these copies: 2000 cycles a tile)
-            issue_a(row_after, g + 2);
+            *row_after = row_there(after);
+            issue_a(*row_after, g + 2);
             return true;
         };
         // V of tile g
@@ -791,29 +813,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
             TcTile t;
             t.w = w;
             settle(t);
-            *here = t;
-            *ahead = t;
+            *here.item = t;
+            *ahead.item = t;
         }
-        __syncwarp();
-        if (here->any) {
-            // r0, r1, r2: rows of the tiles g + 1, g + 2 and g + 3 of the loop below; `here` is tile g + 1, `ahead` g + 3
+        enter(here);
+        enter(ahead);
+        if (here.left > 0) {
+            // r0, r1 and f2: rows of the tiles g + 1, g + 2 and g + 3 of the loop below; `here` is tile g + 1, `ahead` g + 3
             // (g = -1: only the first tile's K)
-            uint32_t r0 = find(here);
+            const Found f0 = find(ahead);
+            step(ahead);
+            const Found f1 = find(ahead);
+            step(ahead);
+            Found f2 = find(ahead);
+            uint32_t r0 = row_there(f0);
             issue_a(r0, 0);
             issue_b(r0, 0);
-            step(ahead);
-            uint32_t r1 = find(ahead);
+            uint32_t r1 = row_there(f1), r2 = kNoRow;
             issue_a(r1, 1);
             issue_b(r1, 1);
-            step(ahead);
-            uint32_t r2 = find(ahead);
             int64_t keys = 0;  // tiles whose K is converted
             for (int64_t g = -1;; ++g) {
                 float scale[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) scale[b] = v_scale[b];
-                if (here->any) {
-                    if (!do_k(keys++, r0, r2)) break;
+                if (here.left > 0) {
+                    if (!do_k(keys++, r0, f2, &r2)) break;
                 } else {
                     cp_commit();  // in the place of K's group
                 }
@@ -823,7 +848,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 step(ahead);
                 r0 = r1;
                 r1 = r2;
-                r2 = find(ahead);
+                f2 = find(ahead);
             }
         }
         cp_wait<0>();
@@ -1023,11 +1048,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                 T *out = static_cast<T *>(p.out) + row * p.out_row + hq * p.out_head;
                 const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_item ? 0 : 1);
                 first_item = false;
-                auto finish = [&](int e0, const float (&v)[32], float total) {  // columns e0 .. e0 + 31
+                auto finish = [&](int e0, const auto &v, float total) {  // the columns from e0 on
                     const float inv = total > 0.0f ? __frcp_rn(total) : total == 0.0f ? 0.0f : total;
                     if (r >= rows) return;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
+                    for (int e = 0; e < static_cast<int>(sizeof(v) / sizeof(v[0])); e += 8) {
                         if (e0 + e < p.dim) {
                             union {
                                 uint4 u;
@@ -1084,30 +1109,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                     auto join = [&](int parts, int64_t head, int64_t at, int64_t step, bool last) {
                         if (bad) return;
                         auto part_of = [&](int i) { return p.partial + (i == 0 ? head : at + i * step) * pitch; };
+                        // three parts at a time, so that their loads travel together (a part that is not there weighs 0)
+                        auto ml_of = [&](int i) {
+                            return i < parts ? __ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r) : make_float2(-INFINITY, 0.0f);
+                        };
                         float up = -INFINITY, total = 0.0f;
-                        for (int i = 0; i < parts; ++i) up = fmaxf(up, __ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r).x);
+#pragma unroll 1
+                        for (int i = 0; i < parts; i += 3) {
+                            const float2 a = ml_of(i), b = ml_of(i + 1), c = ml_of(i + 2);
+                            up = fmaxf(fmaxf(up, a.x), fmaxf(b.x, c.x));
+                        }
                         const float zz = up == -INFINITY ? 0.0f : up;
-                        for (int i = 0; i < parts; ++i) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r);
-                            total = fmaf(ex2(ml.x - zz), ml.y, total);
+#pragma unroll 1
+                        for (int i = 0; i < parts; i += 3) {
+                            float2 ml[3];
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) ml[k] = ml_of(i + k);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k)
+                                if (i + k < parts) total = fmaf(ex2(ml[k].x - zz), ml[k].y, total);
                         }
 #pragma unroll 1
-                        for (int q = 0; q < DP / 64; ++q) {
-                            const int e0 = x * (DP / 2) + 32 * q;
-                            float v[32];
+                        for (int q = 0; q < DP / 32; ++q) {
+                            const int e0 = x * (DP / 2) + 16 * q;
+                            float v[16];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-                            for (int i = 0; i < parts; ++i) {
-                                const float f = ex2(__ldcg(reinterpret_cast<const float2 *>(part_of(i) + kTcRows * DP) + r).x - zz);
-                                const float4 *src = reinterpret_cast<const float4 *>(part_of(i)) + e0 / 4 * kTcRows + r;
+                            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+#pragma unroll 1
+                            for (int i = 0; i < parts; i += 3) {
+                                float4 y[3][4];
+                                float2 ml[3];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    if (e == 4) asm volatile("" ::: "memory");
-                                    const float4 y = __ldcg(src + e * kTcRows);
-                                    v[4 * e] = fmaf(f, y.x, v[4 * e]);
-                                    v[4 * e + 1] = fmaf(f, y.y, v[4 * e + 1]);
-                                    v[4 * e + 2] = fmaf(f, y.z, v[4 * e + 2]);
-                                    v[4 * e + 3] = fmaf(f, y.w, v[4 * e + 3]);
+                                for (int k = 0; k < 3; ++k) {
+                                    ml[k] = ml_of(i + k);
+                                    const float4 *src = reinterpret_cast<const float4 *>(part_of(i + k)) + e0 / 4 * kTcRows + r;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) y[k][e] = i + k < parts ? __ldcg(src + e * kTcRows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 3; ++k) {
+                                    const float f = ex2(ml[k].x - zz);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        v[4 * e] = fmaf(f, y[k][e].x, v[4 * e]);
+                                        v[4 * e + 1] = fmaf(f, y[k][e].y, v[4 * e + 1]);
+                                        v[4 * e + 2] = fmaf(f, y[k][e].z, v[4 * e + 2]);
+                                        v[4 * e + 3] = fmaf(f, y[k][e].w, v[4 * e + 3]);
+                                    }
                                 }
                             }
                             if (last) {
@@ -1115,7 +1163,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q8kv_attend_tc_kernel(const Att
                             } else {
                                 float4 *to4 = reinterpret_cast<float4 *>(p.partial + head * pitch) + e0 / 4 * kTcRows + r;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) to4[e * kTcRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                                for (int e = 0; e < 4; ++e) to4[e * kTcRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                             }
                         }
                         if (last) {
