@@ -18,7 +18,7 @@
 //     f32 is enough; the great ones keep what their roundings lose.  That adds up to 2^-42, so
 //     that the rounding to f32 is as good as always that of the exact value, and rotated keys
 //     get, but for one in millions, the codes that a program in 64 bits gives them (at 2^-35
-//     some codes of a prompt of 8192 tokens differed in most draws).
+//     some codes of a prompt of 8192 tokens differed in some draws).
 //     For q a lane takes both halves of its pairs, so that q may be rotated in place;
 //     k's other half is read by the lane that needs it (it is in L1).
 //
