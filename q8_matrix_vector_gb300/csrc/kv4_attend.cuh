@@ -590,22 +590,29 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                 if (there != 0) {
                     // 2^(E + 9) is above the scales of the lane's key, and of all keys: -8, if none is 2 or more
                     float e_key = kLeast, e_all = kLeast;
-                    uint32_t odd = 0;  // keys with a scale that is not finite
+                    uint32_t odd = 0;  // keys with a scale, of K or V, that is not finite (or whatever the ring holds for an absent one)
                     {
-                        uint32_t d[W];
+                        uint32_t d[W], dk[W];
                         load_scales4<NB>(vs + lane * S::kScales, d);
-                        if constexpr (NB % 2 == 1) d[W - 1] &= 0xFFFFu;
+                        load_scales4<NB>(ks + lane * S::kScales, dk);
+                        if constexpr (NB % 2 == 1) {
+                            d[W - 1] &= 0xFFFFu;
+                            dk[W - 1] &= 0xFFFFu;
+                        }
                         uint32_t any = 0;
 #pragma unroll
-                        for (int i = 0; i < W; ++i) any |= d[i];
+                        for (int i = 0; i < W; ++i) any |= d[i] | dk[i];
                         if (EXACT || __any_sync(~0u, (any & 0x40004000u) != 0)) {
-                            uint32_t top_bits = 0;
+                            uint32_t top_bits = 0, top_k = 0;
 #pragma unroll
-                            for (int i = 0; i < W; ++i) top_bits = max(top_bits, max(d[i] & 0x7FFFu, d[i] >> 16 & 0x7FFFu));
+                            for (int i = 0; i < W; ++i) {
+                                top_bits = max(top_bits, max(d[i] & 0x7FFFu, d[i] >> 16 & 0x7FFFu));
+                                top_k = max(top_k, max(dk[i] & 0x7FFFu, dk[i] >> 16 & 0x7FFFu));
+                            }
                             e_key = exponent_of<!EXACT>(top_bits);
                             // (an absent key's count for nobody)
                             e_all = exponent_of<!EXACT>(__reduce_max_sync(~0u, top_bits));
-                            odd = __ballot_sync(~0u, top_bits >= 0x7C00u);
+                            odd = __ballot_sync(~0u, max(top_bits, top_k) >= 0x7C00u);
                         }
                     }
 
@@ -688,6 +695,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                                 if (drafts)
                                     see &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
                                                 w.rt * ROWS + 8 * t + 2 * c + r);
+                                // whoever sees a scale that is not finite is NaN, however little its key weighs
+                                if ((see & odd) != 0) l[t][r] = NAN;
                                 top[t][r] = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
@@ -699,8 +708,10 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                             }
                         } else {
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
+                            for (int r = 0; r < 2; ++r) {
+                                if (odd != 0) l[t][r] = NAN;
                                 top[t][r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
+                            }
                         }
 #pragma unroll
                         for (int r = 0; r < 2; ++r) above |= top[t][r] > m[t][r] + kSlack;
@@ -738,14 +749,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                             add2(l[t][0], l[t][1], s[t][k][0], s[t][k][1]);
                         }
                     if (odd != 0) {
-                        // A row that sees such a value is NaN; for the others its scale is 0, as their weight is.
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                for (int r = 0; r < 2; ++r)
-                                    if ((odd >> (8 * k + place) & 1u) != 0 && s[t][k][r] != 0.0f) l[t][r] = NAN;
+                        // the rows that see it are NaN; for the others its values' scales are 0, as their weights are
                         if (odd >> lane & 1u) {
 #pragma unroll
                             for (int i = 0; i < S::kScales; i += 4)
