@@ -69,10 +69,12 @@ q8mv_status_t q4kv_cache_move(const q4kv_cache_t *cache, int64_t batch, int64_t 
  * not seen.  Arithmetic: codes are exact in f16; queries as there; each block's
  * products accumulate in f32 with the 8 taken off, its scale is folded in f32, the
  * softmax runs in f32, and its weights times the values' scales enter the second
- * product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs).  With more than
- * 48 bf16 query rows a request and kv head (head_dim up to 128), and page tables long
- * enough, keys enter the first product exactly and values the second with f16's 11
- * bits.  A scale that is not finite makes all of a row that sees its key NaN.
+ * product as two f16 parts (f32 and f16 outputs) or one (bf16 outputs), each of them
+ * to 2^-24 of the row's largest weight times the largest scale near it, whatever the
+ * values' size.  With more than 48 bf16 query rows a request and kv head (head_dim up
+ * to 128), and page tables long enough, keys enter the first product exactly and values
+ * the second with f16's 11 bits.  A scale that is not finite makes all of a row that
+ * sees its key NaN.
  */
 typedef struct q4kv_attend_s *q4kv_attend_plan_t;
 

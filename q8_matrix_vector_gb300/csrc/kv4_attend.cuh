@@ -29,7 +29,8 @@
 //     multiplied by the values' scales in f16, two at a time: two roundings to 11 bits where
 //     the output's own has 8.  f16: the same with the weights in two f16 parts, whose products
 //     are again two, to 2^-22.  f32: products in f32, then two parts.
-// The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents.  The
+// The weights' scale 2^E (kv_attend.cuh) is taken from the f16 scales' exponents; with 16-bit
+// weights small scales are brought up by a power of two first, for all keys of a step.  The
 // running maximum moves only when a score is 2^kSlack above it, so that most steps need no
 // maximum over the lanes; f16 has the room.
 //
@@ -167,15 +168,18 @@ __device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float
         : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(u), "f"(v));
 }
 
-// Exponent E for scales whose greatest magnitude is the f16 of these 15 bits: 2^(E + 9) is above it, so that weights of
-// at most 2^(kSlack - E) times scales stay below 2^14.  (A subnormal counts as 2^-14; an infinity or NaN as any: what
-// sees it is NaN.)  LIMITED: at least kLeast, so that the weights themselves fit f16, and most steps need not look.
-template <bool LIMITED>
-__device__ __forceinline__ float exponent_of(uint32_t bits) {
-    return static_cast<float>(max(static_cast<int>(bits >> 10), LIMITED ? 15 : 1) - 15 + 1 - 9);
-}
-constexpr float kLeast = -8.0f;
-
+// Scales whose greatest has the f16 exponent field f (0 counts as 1) are below 2^(E + 9), E = f - 23, so that weights of at
+// most 2^(kSlack - E) times scales stay below 2^14.
+__device__ __forceinline__ int field_of(uint32_t bits) { return max(static_cast<int>(bits >> 10), 1); }
+__device__ __forceinline__ float exponent_of(int field) { return static_cast<float>(field - 23); }
+// PACKED: weights, and their products with scales, are f16 themselves.  The field counts as 15 at least, which keeps
+// weights at 2^(kSlack + 8) at most; but where it is more than kFine below, the scales are brought up to 15 instead, exactly,
+// by 2^-G, and the weights are taken times 2^G, so that small values' products do not end in f16's last bits.  Bringing them up
+// takes 3 in a hundred of the time (two requests of 300k .. 524k: 231.5 and 239 us), so it is left out where the largest
+// weight times the step's largest scale is 2 or more without it: then a product's own 2^-25 is 2^-24 of the largest or less.
+constexpr int kFine = 7;
+__device__ __forceinline__ int counted(int field) { return field >= 15 - kFine ? max(field, 15) : field; }
+__device__ __forceinline__ int shift_of(int counted_field) { return min(counted_field - 15, 0); }
 // Operands of 8 nibbles of the same place in the two halves of a word's nibbles: pairs 0 and 2 as c, 1 and 3 as 16 c, in
 // units of 2^-24, or (EXACT) c - 8 and 16 (c - 8) themselves.
 template <bool EXACT>
@@ -588,34 +592,6 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                 const int base = k.base0 + i * KEYS;
                 const uint32_t there = __ballot_sync(~0u, row_cur[0] != kNoRow && (!SEG || base + lane < k.keys));
                 if (there != 0) {
-                    // 2^(E + 9) is above the scales of the lane's key, and of all keys: -8, if none is 2 or more
-                    float e_key = kLeast, e_all = kLeast;
-                    uint32_t odd = 0;  // keys with a scale, of K or V, that is not finite (or whatever the ring holds for an absent one)
-                    {
-                        uint32_t d[W], dk[W];
-                        load_scales4<NB>(vs + lane * S::kScales, d);
-                        load_scales4<NB>(ks + lane * S::kScales, dk);
-                        if constexpr (NB % 2 == 1) {
-                            d[W - 1] &= 0xFFFFu;
-                            dk[W - 1] &= 0xFFFFu;
-                        }
-                        uint32_t any = 0;
-#pragma unroll
-                        for (int i = 0; i < W; ++i) any |= d[i] | dk[i];
-                        if (EXACT || __any_sync(~0u, (any & 0x40004000u) != 0)) {
-                            uint32_t top_bits = 0, top_k = 0;
-#pragma unroll
-                            for (int i = 0; i < W; ++i) {
-                                top_bits = max(top_bits, max(d[i] & 0x7FFFu, d[i] >> 16 & 0x7FFFu));
-                                top_k = max(top_k, max(dk[i] & 0x7FFFu, dk[i] >> 16 & 0x7FFFu));
-                            }
-                            e_key = exponent_of<!EXACT>(top_bits);
-                            // (an absent key's count for nobody)
-                            e_all = exponent_of<!EXACT>(__reduce_max_sync(~0u, top_bits));
-                            odd = __ballot_sync(~0u, max(top_bits, top_k) >= 0x7C00u);
-                        }
-                    }
-
                     // ---- scores: s[t][2 j + k][r] of key 16 j + 8 k + place and row 8 t + 2c + r
                     float s[NT][4][2];
 #pragma unroll
@@ -681,9 +657,73 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                             }
                         }
                     }
-                    // ---- softmax
+                    // ---- which keys each row sees
                     const bool drafts = base + kStepKeys > w.prefix;
                     const bool partial = drafts || there != ~0u;
+                    uint32_t see[NT][2];
+                    if (partial) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                see[t][r] = there;
+                                if (drafts)
+                                    see[t][r] &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
+                                                      w.rt * ROWS + 8 * t + 2 * c + r);
+                            }
+                    }
+                    // ---- the values' scales
+                    int f_all = 15, f_key = 1;  // exponent fields: that all keys count with, the lane's key's own
+                    uint32_t odd = 0;  // keys with a scale, of K or V, that is not finite (or whatever the ring holds for an absent one)
+                    {
+                        uint32_t d[W], dk[W], any = 0, any_k = 0;
+                        load_scales4<NB>(vs + lane * S::kScales, d);
+                        load_scales4<NB>(ks + lane * S::kScales, dk);
+                        if constexpr (NB % 2 == 1) {
+                            d[W - 1] &= 0xFFFFu;
+                            dk[W - 1] &= 0xFFFFu;
+                        }
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            any |= d[i];
+                            any_k |= dk[i];
+                        }
+                        // Most steps: every row sees every key, and every key has scales of V below 2 and one of 2^-7 or more (a
+                        // bit each of the field).  Of K, 0x7C00 and 0x0400 are 0x8000.
+                        const bool plain = (any & 0x40004000u) == 0 && (any & 0x20002000u) != 0 &&
+                                           (((any_k & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u) == 0;
+                        if (EXACT || partial || !__all_sync(~0u, plain)) {
+                            uint32_t most = 0, most_k = 0;
+#pragma unroll
+                            for (int i = 0; i < W; ++i) {
+                                most = __vmaxu2(most, d[i] & 0x7FFF7FFFu);
+                                most_k = __vmaxu2(most_k, dk[i] & 0x7FFF7FFFu);
+                            }
+                            const uint32_t top_bits = max(most & 0xFFFFu, most >> 16);
+                            odd = __ballot_sync(~0u, max(top_bits, max(most_k & 0xFFFFu, most_k >> 16)) >= 0x7C00u);
+                            uint32_t counting = ~odd;
+                            if (partial) {  // what no row sees does not count
+                                uint32_t by_any = 0;
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) by_any |= see[t][0] | see[t][1];
+                                counting &= __reduce_or_sync(~0u, by_any);
+                            }
+                            const bool counts = (counting >> lane & 1u) != 0;
+                            f_key = field_of(top_bits);
+                            f_all = __reduce_max_sync(~0u, counts ? f_key : 1);
+                            if (PACKED) f_all = counted(f_all);
+                            if (odd != 0 || (PACKED && f_all < 15)) {
+                                // (rows that see an odd key are NaN; for the others its values' scales are 0, as their weights are)
+                                const uint32_t up = static_cast<uint32_t>(15 - (PACKED ? shift_of(f_all) : 0)) * 0x04000400u;
+#pragma unroll
+                                for (int i = 0; i < W; ++i)
+                                    reinterpret_cast<uint32_t *>(const_cast<unsigned char *>(vs) + lane * S::kScales)[i] =
+                                        counts ? mul_half2(d[i], up) : 0u;
+                                __syncwarp();
+                            }
+                        }
+                    }
+                    // ---- softmax
                     bool above = false;
                     float top[NT][2];
 #pragma unroll
@@ -691,26 +731,22 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                         if (partial) {
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                uint32_t see = there;
-                                if (drafts)
-                                    see &= sees(p.mask, p.mask_row, p.mask_words, p.group, w.nodes, w.row0, base - w.prefix,
-                                                w.rt * ROWS + 8 * t + 2 * c + r);
                                 // whoever sees a scale that is not finite is NaN, however little its key weighs
-                                if ((see & odd) != 0) l[t][r] = NAN;
+                                if ((see[t][r] & odd) != 0) l[t][r] = NAN;
                                 top[t][r] = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const int key = 8 * k + place;
-                                    if (((see >> key) & 1u) == 0) s[t][k][r] = -INFINITY;
-                                    // a row's E comes from keys that it sees, so that no other's scale matters
-                                    top[t][r] = fmaxf(top[t][r], fmaf(s[t][k][r], mul[t][r], __shfl_sync(~0u, e_key, key)));
+                                    if (((see[t][r] >> key) & 1u) == 0) s[t][k][r] = -INFINITY;
+                                    // f32: a row's E comes from keys that it sees, so that no other's scale matters
+                                    top[t][r] = fmaxf(top[t][r], fmaf(s[t][k][r], mul[t][r], exponent_of(EXACT ? __shfl_sync(~0u, f_key, key) : f_all)));
                                 }
                             }
                         } else {
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 if (odd != 0) l[t][r] = NAN;
-                                top[t][r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], e_all);
+                                top[t][r] = fmaf(fmaxf(fmaxf(s[t][0][r], s[t][1][r]), fmaxf(s[t][2][r], s[t][3][r])), mul[t][r], exponent_of(f_all));
                             }
                         }
 #pragma unroll
@@ -739,23 +775,25 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 2 && NT == 1 ? 4 : NB <= 4 
                             }
                         }
                     }
+                    {
+                        // weights, times 2^G if the scales were brought up by as much; their sum without
+                        const int g = PACKED ? shift_of(f_all) : 0;
+                        const float add = static_cast<float>(g), up = __uint_as_float(static_cast<uint32_t>(127 - g) << 23);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                        for (int t = 0; t < NT; ++t) {
+                            float sum[2] = {0.0f, 0.0f};
+                            const float from[2] = {minus[t][0] + add, minus[t][1] + add};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            fma2(s[t][k][0], s[t][k][1], mul[t][0], mul[t][1], minus[t][0], minus[t][1]);
-                            s[t][k][0] = ex2(s[t][k][0]);
-                            s[t][k][1] = ex2(s[t][k][1]);
-                            add2(l[t][0], l[t][1], s[t][k][0], s[t][k][1]);
+                            for (int k = 0; k < 4; ++k) {
+                                fma2(s[t][k][0], s[t][k][1], mul[t][0], mul[t][1], from[0], from[1]);
+                                s[t][k][0] = ex2(s[t][k][0]);
+                                s[t][k][1] = ex2(s[t][k][1]);
+                                add2(sum[0], sum[1], s[t][k][0], s[t][k][1]);
+                            }
+                            fma2(sum[0], sum[1], up, up, l[t][0], l[t][1]);
+                            l[t][0] = sum[0];
+                            l[t][1] = sum[1];
                         }
-                    if (odd != 0) {
-                        // the rows that see it are NaN; for the others its values' scales are 0, as their weights are
-                        if (odd >> lane & 1u) {
-#pragma unroll
-                            for (int i = 0; i < S::kScales; i += 4)
-                                *reinterpret_cast<uint32_t *>(const_cast<unsigned char *>(vs) + lane * S::kScales + i) = 0u;
-                        }
-                        __syncwarp();
                     }
                    // ---- O^T += V^T (P dV)^T, two blocks at a time (a word's halves), 16 keys at a time
                     uint32_t dv[4][W], p2[NT][PP][4];
