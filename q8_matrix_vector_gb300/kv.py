@@ -46,7 +46,8 @@ class VerifyArgs(ctypes.Structure):
                 ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-# one pack_into instead of an attribute store per field
+# One pack instead of an attribute store per field, into bytes of the call's own: the library reads them without the
+# interpreter's lock, while another thread may make a call of the same object.
 _ATTEND = struct.Struct("=3Qii5q3QqiiQqf4x")
 _VERIFY = struct.Struct("=10Q3qiiii")
 assert _ATTEND.size == ctypes.sizeof(AttendArgs) and _VERIFY.size == ctypes.sizeof(VerifyArgs)
@@ -342,7 +343,6 @@ class TreeAttention(_Plan):
         self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 0.0
         self._make(self._name + "_plan", heads, kv_heads, head_dim, max_requests, max_rows, int(device))
         self._fn = getattr(_library(), self._name)
-        self._args = ctypes.create_string_buffer(_ATTEND.size)
 
     def __call__(self, q, cache: Cache, table, lengths, *, starts=None, mask=None, scale=None, out=None, lse=False):
         """out [rows, heads, head_dim] (the type of q); with ``lse`` also the log of each row's sum [rows, heads] f32.
@@ -386,13 +386,13 @@ class TreeAttention(_Plan):
         if cache.device != device:
             raise ValueError(f"the cache is on cuda:{cache.device}, the plan on cuda:{device}")
         sums = torch.empty((rows, self.heads), dtype=torch.float32, device=self._where) if lse else None
-        _ATTEND.pack_into(self._args, 0, q.data_ptr(), out.data_ptr(), sums.data_ptr() if lse else 0, code, requests, rows,
-                          qs[0], qs[1], os[0], os[1], at_starts, at_len, at_table, cols, cols, words, at_mask, words,
-                          self._scale if scale is None else scale)
+        args = _ATTEND.pack(q.data_ptr(), out.data_ptr(), sums.data_ptr() if lse else 0, code, requests, rows, qs[0], qs[1],
+                            os[0], os[1], at_starts, at_len, at_table, cols, cols, words, at_mask, words,
+                            self._scale if scale is None else scale)
         if _current() == device:
-            status = self._fn(self._h, cache._ref, self._args, _stream(device))
+            status = self._fn(self._h, cache._ref, args, _stream(device))
         else:
-            status = _elsewhere(self._fn, device, self._h, cache._ref, self._args)
+            status = _elsewhere(self._fn, device, self._h, cache._ref, args)
         if status:
             _fail(status, self._name)
         return (out, sums) if lse else out
@@ -422,7 +422,6 @@ class TreeVerify(_Plan):
         self.vocab, self.max_requests = vocab, max_requests
         self._make("q8kv_verify_plan", max_requests, max_rows, vocab, int(device))
         self._fn = _library().q8kv_verify
-        self._args = ctypes.create_string_buffer(_VERIFY.size)
         self._tail = (vocab,)
 
     def __call__(self, logits, tokens, parents, uniforms, *, temperature=None, draft_probs=None, starts=None,
@@ -463,13 +462,13 @@ class TreeVerify(_Plan):
             at_draft, draft_row = draft_probs.data_ptr(), ds[0]
         path, count, token = torch.empty(rows + 2 * requests, dtype=torch.int32, device=self._where).split(
             (rows, requests, requests))
-        _VERIFY.pack_into(self._args, 0, logits.data_ptr(), at_draft, at_tokens, at_parents, at_uniforms, at_temperature,
-                          at_starts, path.data_ptr(), count.data_ptr(), token.data_ptr(), ls[0], draft_row, rows, requests,
-                          self.vocab, code, 0)
+        args = _VERIFY.pack(logits.data_ptr(), at_draft, at_tokens, at_parents, at_uniforms, at_temperature, at_starts,
+                            path.data_ptr(), count.data_ptr(), token.data_ptr(), ls[0], draft_row, rows, requests, self.vocab,
+                            code, 0)
         if _current() == device:
-            status = self._fn(self._h, self._args, _stream(device))
+            status = self._fn(self._h, args, _stream(device))
         else:
-            status = _elsewhere(self._fn, device, self._h, self._args)
+            status = _elsewhere(self._fn, device, self._h, args)
         if status:
             _fail(status, "q8kv_verify")
         return path, count, token

@@ -131,7 +131,6 @@ class Rotary(_Plan):
                    self.factor, int(device))
         lib = _library()
         self._apply, self._fused = lib.kvrope_apply, {n: getattr(lib, n) for n in ("kvrope_write_q8", "kvrope_write_q4")}
-        self._args = ctypes.create_string_buffer(_WRITE.size)
 
     def _out(self, x, out, name):
         """(out, its strides): x's shape and type."""
@@ -186,13 +185,14 @@ class Rotary(_Plan):
                 raise ValueError("q must have the type and number of tokens of k")
             out, os = self._out(q, out, "out")
             heads, q_at, out_at = q.shape[1], q.data_ptr(), out.data_ptr()
-        _WRITE.pack_into(self._args, 0, q_at, k.data_ptr(), v.data_ptr(), out_at, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
-                         os[0], os[1], at, at_slots, n, heads, code)
+        # (in bytes of the call's own: another thread may make a call while the library reads them)
+        args = _WRITE.pack(q_at, k.data_ptr(), v.data_ptr(), out_at, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], at,
+                           at_slots, n, heads, code)
         fn = self._fused[cache._fused]
         if _current() == device:
-            status = fn(self._h, cache._ref, self._args, _stream(device))
+            status = fn(self._h, cache._ref, args, _stream(device))
         else:
-            status = _elsewhere(fn, device, self._h, cache._ref, self._args)
+            status = _elsewhere(fn, device, self._h, cache._ref, args)
         if status:
             _fail(status, cache._fused)
         return None if q is None else out
