@@ -32,8 +32,10 @@ q8mv_status_t kvrope_plan(kvrope_plan_t *out, int32_t head_dim, int32_t rotary_d
 /*
  * out = x rotated by positions[n] (or back, inverse != 0: the transpose, which is
  * the gradient's way).  Row r, head h at x + r * x_row + h * x_head elements, the last
- * axis contiguous, any alignment of the type; out may be x itself with its strides,
- * or must not overlap it.  Negative positions turn the other way.  0 <= n < 2^31.
+ * axis contiguous, any alignment of the type; out may be x itself with its strides.
+ * Else it must not overlap x or positions, nor its own rows one another: calls whose
+ * memory does, or whose rows are differently far apart in the same stretch of it, are
+ * refused.  Negative positions turn the other way.  0 <= n < 2^31.
  */
 q8mv_status_t kvrope_apply(kvrope_plan_t plan, int64_t n, int32_t heads, int32_t type, const void *x, int64_t x_row,
                            int64_t x_head, const int64_t *positions, void *out, int64_t out_row, int64_t out_head,
@@ -43,7 +45,9 @@ q8mv_status_t kvrope_apply(kvrope_plan_t plan, int64_t n, int32_t heads, int32_t
  * One call for a layer's step: out = q rotated (heads_q = 0: no q), k rotated and,
  * without a rounding to its type between, quantised with v into slots, as
  * q8kv_cache_write or q4kv_cache_write would.  A slot outside the cache skips its
- * token's k and v, not its q.  The plan's head_dim is the cache's.
+ * token's k and v, not its q.  The plan's head_dim is the cache's.  out is refused as
+ * in kvrope_apply where it overlaps q (unless it is q), k, v, positions or slots; it may
+ * lie between them, as q's part of one tensor that holds all three.
  */
 typedef struct {
     const void *q, *k, *v;

@@ -2,6 +2,7 @@
 // variants of kv_store_kernel (kv_store.cuh).
 #include "../../include/kvrope.h"
 #include "kvrope.h"
+#include "strided.h"
 
 #include <cmath>
 #include <new>
@@ -84,6 +85,17 @@ bool whole_pieces(const StoreParams &p, int64_t e) {
     return p.dim % e == 0 && (p.interleaved ? 2 * p.half % e == 0 : p.half % e == 0 && (p.dim - 2 * p.half) % e == 0);
 }
 
+// Memory of [n, heads, dim] elements, and of n whole numbers.
+Strided tensor(const void *at, int64_t n, int64_t row, int64_t heads, int64_t head, int64_t dim, int size) {
+    return {at, n, row * size, heads, head * size, dim * size};
+}
+Strided numbers(const int64_t *at, int64_t n) { return {at, 1, 0, 1, 0, 8 * n}; }
+
+// Whether `out` is `in` itself, to be rotated in place.
+bool same(const Strided &out, const Strided &in) {
+    return out.at == in.at && (out.rows == 1 || out.row == in.row) && (out.heads == 1 || out.head == in.head);
+}
+
 q8mv_status_t write(kvrope_s *plan, StoreParams &p, int bits, const kvrope_write_args_t *a, cudaStream_t stream) {
     if (p.dim != plan->head_dim) return Q8MV_ERR_INVALID_ARG;
     if (a->n < 0 || a->n >= (1LL << 31) || !valid_type(a->type) || a->heads_q < 0 || a->heads_q > 65535)
@@ -95,7 +107,16 @@ q8mv_status_t write(kvrope_s *plan, StoreParams &p, int bits, const kvrope_write
     if (!a->k || !a->v || !a->positions || !a->slots || !aligned(a->k, size) || !aligned(a->v, size) ||
         !aligned(a->positions, 8) || !aligned(a->slots, 8))
         return Q8MV_ERR_INVALID_ARG;
-    if (a->heads_q > 0 && (!a->q || !a->out || !aligned(a->q, size) || !aligned(a->out, size))) return Q8MV_ERR_INVALID_ARG;
+    if (a->heads_q > 0) {
+        if (!a->q || !a->out || !aligned(a->q, size) || !aligned(a->out, size)) return Q8MV_ERR_INVALID_ARG;
+        const Strided out = tensor(a->out, a->n, a->out_row, a->heads_q, a->out_head, p.dim, size);
+        const Strided q = tensor(a->q, a->n, a->q_row, a->heads_q, a->q_head, p.dim, size);
+        if (folds(out) || (!same(out, q) && meet(out, q)) ||
+            meet(out, tensor(a->k, a->n, a->k_row, p.c.heads, a->k_head, p.dim, size)) ||
+            meet(out, tensor(a->v, a->n, a->v_row, p.c.heads, a->v_head, p.dim, size)) ||
+            meet(out, numbers(a->positions, a->n)) || meet(out, numbers(a->slots, a->n)))
+            return Q8MV_ERR_INVALID_ARG;
+    }
     take(plan, &p);
     p.in[0] = a->k;
     p.in[1] = a->v;
@@ -190,6 +211,10 @@ q8mv_status_t kvrope_apply(kvrope_plan_t plan, int64_t n, int32_t heads, int32_t
     if (n == 0 || heads == 0) return Q8MV_OK;
     const int size = kv::type_size(type);
     if (!x || !out || !positions || !kv::aligned(x, size) || !kv::aligned(out, size) || !kv::aligned(positions, 8))
+        return Q8MV_ERR_INVALID_ARG;
+    const kv::Strided to = kv::tensor(out, n, out_row, heads, out_head, plan->head_dim, size);
+    const kv::Strided from = kv::tensor(x, n, x_row, heads, x_head, plan->head_dim, size);
+    if (kv::folds(to) || (!kv::same(to, from) && kv::meet(to, from)) || kv::meet(to, kv::numbers(positions, n)))
         return Q8MV_ERR_INVALID_ARG;
     kv::StoreParams p = {};
     kv::take(plan, &p);

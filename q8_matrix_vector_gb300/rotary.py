@@ -146,7 +146,7 @@ class Rotary(_Plan):
 
     def __call__(self, x, positions, *, out=None, inverse: bool = False):
         """x [n, heads, head_dim] (f32, f16 or bf16) turned by positions [n] (int64), or back with ``inverse`` (the
-        gradient of the forward turn).  ``out`` may be x itself."""
+        gradient of the forward turn).  ``out`` may be x itself; memory that overlaps otherwise is refused."""
         device = self.device
         if x.dim() != 3:
             raise ValueError(f"x must be [n, heads, {self.head_dim}], got {tuple(x.shape)}")
@@ -160,7 +160,7 @@ class Rotary(_Plan):
         return out
 
     def write(self, cache, q, k, v, positions, slots, *, out=None):
-        """One call for a layer's step: q [n, heads, head_dim] turned (into ``out``, which may be q), k
+        """One call for a layer's step: q [n, heads, head_dim] turned (into ``out``, which may be q but must not meet it otherwise, nor k or v), k
         [n, kv heads, head_dim] turned and, without a rounding between, quantised with v into ``cache`` (``Cache`` or
         ``Cache4``) at slots [n] (int64, each once; outside the cache, as -1: skipped).  Returns the turned q (None for
         q None)."""
