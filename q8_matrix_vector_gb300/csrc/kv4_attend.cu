@@ -174,29 +174,33 @@ q8mv_status_t q4kv_attend(q4kv_attend_plan_t plan, const q4kv_cache_t *cache, co
     p.q_vec = kv::aligned(a->q, 16) && ((a->q_row | a->q_head) & 7) == 0;
     p.out_vec = kv::aligned(a->out, 16) && ((a->out_row | a->out_head) & 7) == 0;
     // 8 rows at a time or 16, by the mean rows of a request: the fewest that hold them (16 requests of 700 .. 4000 tokens, 8
-    // heads of 128, bf16: 12 rows 28.3 us by 16; one token each of groups of 8 is 8 rows); heads above 128 by 8 alone, as 16 do
+    // heads of 128, bf16: 12 rows 29.1 us by 16; one token each of groups of 8 is 8 rows); heads above 128 by 8 alone, as 16 do
     // not fit the registers.
     const int64_t mean = (a->rows + a->requests - 1) / a->requests * p.group;
     const bool wide = mean > 8 && c.blocks <= 4;
     // 128 bf16 rows at a time where there are more than 48 and enough to do, in tiles of 16 rows x 128 keys of the tables'
-    // reach (kv_attend.cu): the 16 requests above, 48 rows 59.6 us by 16 and 69.1 by 128, 64 rows 75.9 and 70.6; one request
-    // of 124 rows over 8000 tokens (4032 tiles) 34.2 and 43.4, over 16000 (8064) 55.7 and 53.0; four over 2000 (4096) 36.7
-    // and 35.4, over 4000 (8192) 58.0 and 45.5; four of 64 rows over 8000 (8064) 55.3 and 57.3.
+    // reach (kv_attend.cu): the 16 requests above, 48 rows 61.0 us by 16 and 67.2 by 128, 52 rows 77.9 and 69.2, 64 rows 77.9
+    // and 69.4.  One request of 124 rows over 8000 tokens (4032 tiles) 34.6 and 40.3, over 16000 (8064) 57.1 and 49.2; four
+    // over 2000 (4096) 37.5 and 34.4, over 4000 (8192) 59.4 and 43.4; four of 64 rows over 4000 (4096) 35.7 and 42.6, over 8000
+    // (8064) 57.1 and 55.6; 16 of 64 rows over 1000 (4096) 41.8 and 43.4, over 2000 (8192) 62.4 and 55.1.  The host knows the
+    // tables' reach, not the lengths: under columns for 131072 tokens one request of 124 rows over 1000 takes 34.8 us and not
+    // 16.2, four of them 32.2 and not 28.5.
     const int64_t reach = static_cast<int64_t>(a->table_cols) * r.page_size;
     const double tiles = static_cast<double>(kv::ceil_div(mean, 16) * kv::ceil_div(reach, 128)) * a->requests * r.heads;
-    if (a->type == Q8KV_BF16 && plan->tc.fn != nullptr && mean > 48 && tiles >= 8192) {
+    if (a->type == Q8KV_BF16 && plan->tc.fn != nullptr && mean > 48 && tiles >= 6144) {
         plan->tc.fn<<<plan->tc_grid, plan->tc.threads, plan->tc.smem, stream>>>(p);
         return q8i::cuda_status(cudaGetLastError());
     }
     // Sixteen keys are one stretch of memory where a head's tokens of a page are, and start on 16 bytes (64 requests of 180 ..
-    // 8100 tokens: 85.9 us, key by key 89.2).
+    // 8100 tokens: 82.7 us, key by key 85.8).
     const int scales = 4 * r.blocks;  // bytes of a row's
     const bool in_turn = r.stride_token == 1 && r.page_size % 16 == 0 && (r.stride_page * scales) % 16 == 0 &&
                          (r.stride_head * scales) % 16 == 0;
     // With 8 rows, and a token's heads side by side, each warp can take a head of its own, so that a CTA reads longer stretches
     // than one head's 64 bytes (kv_attend.cu).  But four heads' parts are to be joined instead of one's, so only where the
-    // tables reach 150 MB: 69 MB of two requests 30 us by one head and 43 by four, 138 MB 57 and 59, 276 MB 104 and 87, 1.1 GB
-    // 455 and 256; 295 MB of 64 requests 109 and 86; heads of 256 (590 MB) 191 and 143.
+    // tables reach 150 MB: 69 MB of two requests 30 us by one head and 43 by four, 138 MB 57 and 58, 277 MB 102 and 87, 1.2 GB
+    // 425 and 259; of 64 requests 297 MB 82 and 81, 598 MB 106 and 88; heads of 256 (595 MB) 153 and 147.  (Short sequences
+    // under columns for 131072 tokens: one request of 511, 32 heads, 16.5 us and not 10.9, eight of 600 19.7 and not 17.6.)
     const double bytes = static_cast<double>(reach) * a->requests * r.heads * 2.0 * (r.dim + scales);
     const bool side_by_side = r.stride_head < r.stride_token && r.heads % kv::kWarps == 0 && bytes >= 1.5e8;
     const kv::Attend4Shape v = side_by_side && mean <= 8 ? kv::k4Heads4 : in_turn ? (wide ? kv::k4Rows16InTurn : kv::k4Rows8InTurn) : wide ? kv::k4Rows16 : kv::k4Rows8;

@@ -168,11 +168,12 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     const int64_t reach = static_cast<int64_t>(a->table_cols) * p.c.page_size;
     const double bytes = static_cast<double>(reach) * a->requests * p.c.heads * (2.0 * p.c.dim + 8.0 * p.c.blocks);
     const bool side_by_side = p.c.stride_head < p.c.stride_token && p.c.heads % kv::kWarps == 0 && bytes >= 5e8;
-    // 128 bf16 rows at a time where there are more than 32 (36 rows of the 16 requests above: 75 us, by 16 rows 83;
-    // 128 rows: 86 and 189; but 32 rows: 75 and 60), and enough to do: its tiles of 128 keys take longer to fill and to
-    // join.  In tiles of 16 rows x 128 keys of the tables' reach, one request of 124 rows: 2048 tiles 45 us, by 16
-    // rows 31; four of 64 rows: 4096 tiles 50 and 49; four of 124 rows: 8192 tiles 53 and 82.  (Under columns for 131072
-    // tokens one request of 124 rows over 1000 tokens takes 41 us and not 19.6, four of them 36.6 and not 33.7.)
+    // 128 bf16 rows at a time where there are more than 32 (36 rows of the 16 requests above: 79 us, by 16 rows 80; 52
+    // rows: 80 and 102; 124 rows: 83 and 190; but 32 rows: 78 and 59), and enough to do: its tiles of 128 keys take longer
+    // to fill and to join.  In tiles of 16 rows x 128 keys of the tables' reach, one request of 124 rows: 2048 tiles 39 us,
+    // by 16 rows 31, 4032 43 and 45; four of 64 rows: 3072 tiles 40 and 40, 4096 46 and 46, 8064 63 and 75; four of 124
+    // rows: 2304 tiles 34 and 34, 8192 47 and 79.  (Under columns for 131072 tokens one request of 124 rows over 1000
+    // tokens takes 36 us and not 19.2.)
     const double tiles = static_cast<double>(kv::ceil_div(mean, 16) * kv::ceil_div(reach, 128)) * a->requests * p.c.heads;
     const bool wide = a->type == Q8KV_BF16 && p.c.dim <= 128 && mean > 32 && tiles >= 4096;
     const kv::AttendShape v = wide                         ? kv::kRows128

@@ -51,9 +51,10 @@ constexpr int kTcErrWait = 1;
 constexpr uint64_t kTcDrainNs = 2000000000ull;  // for MMAs that were issued: they end by themselves, whatever a plan's waits are
 constexpr float kTcTop = 7.0f;                  // log2 of P at the row's maximum when that is taken
 constexpr float kTcSlack = 15.0f;               // and how far P may grow before it is taken anew (f16 ends at 2^16)
-constexpr int kTcItemUnits = 4;                 // an item's fixed cost in tiles (16 requests of 700 .. 5000 tokens, 124 rows, Q8_0:
-                                                // 90.3, 91.0, 93.0, 95.6 us with 3 .. 6; four of 4000: 48.5, 48.5, 46.7, 46.8;
-                                                // Q4_0: 78.4, 79.0, 79.6, 81.7 and 44.9, 44.9, 43.4, 43.5)
+constexpr int kTcItemUnits = 4;                 // An item's fixed cost in tiles: no number is best everywhere.  With 3 .. 6, 124 rows:
+                                                // 16 requests of 700 .. 5000 tokens, Q8_0 90.0, 90.8, 92.6, 94.7 us, Q4_0 78.4,
+                                                // 79.3, 79.1, 80.8; of 700 .. 4000 82.0, 82.0, 84.1, 84.7 and 72.7, 71.0, 72.4, 72.5;
+                                                // four of 4000 47.3, 47.3, 46.2, 46.1 and 43.6, 43.4, 42.6, 42.7
 
 template <int DP, int NB4>
 struct TcSmem {

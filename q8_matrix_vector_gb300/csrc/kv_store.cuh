@@ -18,14 +18,14 @@
 //     f32 is enough; the great ones keep what their roundings lose.  That adds up to 2^-42, so
 //     that the rounding to f32 is as good as always that of the exact value, and rotated keys
 //     get the codes that a program in 64 bits gives them (2^-35, a last bit off in one value of
-//     some thousands, took 41.3 us where this takes 43.8).
+//     some thousands, took 41.3 us where this takes 43.2).
 //     For q a lane takes both halves of its pairs, so that q may be rotated in place;
 //     k's other half is read by the lane that needs it (it is in L1).
 //
 // Measured on GB300 (copy rate 6792 GB/s): 8190 tokens of 32 heads of 128, bf16, to Q4_0
-// 37.9 us, 4.5 TB/s, issue (0.7 of the cycles).  8192 tokens, 8 heads to Q8_0 with 32 of q
-// rotated, 43.8 us, 4.3 TB/s, the latency of angles and loads (0.5 of the cycles issue); q
-// alone 24.6 us, 5.5 TB/s.
+// 38.9 us, 4.4 TB/s, issue (0.7 of the cycles).  8192 tokens, 8 heads to Q8_0 with 32 of q
+// rotated, 43.2 us, 4.3 TB/s, the latency of angles and loads (0.5 of the cycles issue); to
+// Q4_0 44.0 us; q alone 25.4 us, 5.3 TB/s.
 #pragma once
 
 #include "kv4.h"
@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(256) kv_rotate_kernel(const StoreParams p) {
                         threadIdx.y * blockDim.x + threadIdx.x);
 }
 
-// U tokens a lane.  Six blocks an SM with one (40 registers, a few bytes spilled): 8192 tokens rotated and written 41.3 us;
-// five 43.2, four 49.4, eight 52.0.
+// U tokens a lane.  Six blocks an SM with one (40 registers, a few bytes spilled): 8192 tokens rotated and written to Q8_0
+// 43.2 us; five 43.9, four 49.7, eight 52.7 (to Q4_0 44.0, 43.5, 49.4, 51.7).
 template <typename T, int BITS, bool ROT, bool VEC, int U>
 __global__ void __launch_bounds__(256, U == 1 ? 6 : 1) kv_store_kernel(const StoreParams p) {
     using namespace store;
@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(256, U == 1 ? 6 : 1) kv_store_kernel(const Sto
     }
 }
 
-// Tokens a lane of a large call: of writes (kv_cache.cu's measurements: 40.4 us for 8190 tokens of 32 heads x 128 in bf16, 42.0
-// with two), and of what only rotates (f32, 5003 tokens of 12 heads of 80: 7.5 us, 8.9 with two)
+// Tokens a lane of a large call: of writes (8190 tokens of 32 heads x 128 in bf16: 38.9 us, 41.0 with two, 46.6 with one), and
+// of what only rotates (f32, 5003 tokens of 12 heads of 80: 7.2 us, 8.4 with two, 8.9 with one)
 constexpr int kStoreTokens = 4;
 
 template <typename T, int BITS, bool ROT>

@@ -41,8 +41,8 @@ void launch_q(const StoreParams &p, bool vec, const Shape &s, size_t smem, cudaS
 
 // q_lanes comes as q's heads.  One launch, whose blocks along y rotate q behind those that store, a token a lane: with k's
 // other halves and the angles two or four take more registers than they are worth, and q in a launch of its own, four
-// tokens a lane, gains less than the launch costs (8192 tokens of 8 heads x 128 and 32 of q, bf16, five blocks an SM: 43.8 us;
-// with two 46.4, four 48.5; two launches 45.0).
+// tokens a lane, gains less than the launch costs (8192 tokens of 8 heads x 128 and 32 of q, bf16, with five blocks an SM and
+// cosines to 2^-35: 43.4 us; with two 46.4, four 48.5; two launches 45.0.  As it is now 43.2).
 q8mv_status_t launch(StoreParams p, int bits, int type, bool vec, cudaStream_t stream) {
     const int e = vec ? 16 / type_size(type) : 1;
     p.q_items = p.q == nullptr ? 0 : !vec || !p.interleaved ? (p.dim - p.half) / e : p.dim / e;
