@@ -30,8 +30,8 @@ q8mv_status_t kvrope_plan(kvrope_plan_t *out, int32_t head_dim, int32_t rotary_d
                           const uint64_t *turns, float factor, int device);
 
 /*
- * out = x rotated by positions[n] (or back, inverse != 0: the transpose, which is
- * the gradient's way).  Row r, head h at x + r * x_row + h * x_head elements, the last
+ * out = x rotated by positions[n] (inverse != 0: by the transpose, which is the
+ * gradient's way, and back but for the square of a factor that is not 1).  Row r, head h at x + r * x_row + h * x_head elements, the last
  * axis contiguous, any alignment of the type; out may be x itself with its strides.
  * Else it must not overlap x or positions, nor its own rows one another: calls whose
  * memory does, or whose rows are differently far apart in the same stretch of it, are

@@ -35,8 +35,8 @@
 // maximum over the lanes; f16 has the room.
 //
 // Measured on GB300, groups of 4 or 8 heads of 128, bf16 (copy rate 6792 GB/s): two requests
-// of 300k and 524k tokens 225 us, 5.0 TB/s of the cache; f16 280, f32 336.  64 requests of
-// 180 .. 8100 tokens 81 us, 3.6 TB/s; 64 of 8000 139 us, 4.9 TB/s.  What bounds the loop is
+// of 300k .. 524k tokens 231 us, 4.9 TB/s of the cache; f16 286, f32 343.  64 requests of
+// 180 .. 8100 tokens 82 us, 3.7 TB/s; 64 of 8000 141 us, 4.2 TB/s.  What bounds the loop is
 // issue: 589 instructions a warp's 32 keys, a third of them masks, shifts and permutes on the
 // half-rate pipe, with three warps a scheduler; in the mixed batch an item's start, end and
 // join take a quarter of the time.
@@ -50,9 +50,9 @@
 namespace kv {
 
 // Steps in flight a warp, and CTAs an SM.  8 rows of up to 128: three CTAs (168 registers a thread); with four the registers
-// spill in the loop (two requests of 300k .. 524k tokens, bf16: 233 and 236 us; 64 of 180 .. 8100: 84.8 and 89.1), and
-// three steps with three CTAs gain nothing (233.0 and 233.0; 64 requests of 8000: 143.4 and 144.3).  Heads of 64: four (64
-// of 180 .. 8100: 56.9 us with three, 52.4 with four).
+// spill in the loop (two requests of 300k .. 524k tokens, bf16: 231 and 242 us; 64 of 180 .. 8100: 82 and 85), and
+// three steps with three CTAs gained nothing (an earlier loop: 233.0 and 233.0; 64 requests of 8000: 143.4 and 144.3).  Heads
+// of 64: four (64 of 180 .. 8100: 57.6 us with three, 54.7 with four).
 constexpr int kStages4 = 2;
 constexpr float kSlack = 5.0f;
 

@@ -30,7 +30,7 @@
 // its parts of cut items are counted: the tickets are whole after every call.
 //
 // 16 requests of 700 .. 5000 tokens, trees of 31 nodes, 32 heads over 8 of 128: 79.0 us,
-// 264 TFLOP/s of the two products, 1.3 TB/s of cache; over the Q4_0 cache 68.4 us.
+// 264 TFLOP/s of the two products, 1.3 TB/s of cache; over the Q4_0 cache 71.1 us.
 // A Q4_0 tile takes a convert warp 4600 cycles, of which the MMAs run 1400: K's operands
 // 1400, V's 700, waits 800, the copies and places of tiles to come 1000.  That bounds it,
 // then 8 us until a CTA's first scores are there and 10 us of joining cut items at the end.

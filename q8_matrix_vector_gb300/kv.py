@@ -331,7 +331,8 @@ class _Plan:
 
 class TreeAttention(_Plan):
     """Attention of draft trees over a ``Cache``; owns the workspace of calls with up to ``max_requests`` requests
-    and ``max_rows`` query rows.  Use one per concurrent stream."""
+    and ``max_rows`` query rows.  Use one per concurrent stream: calls of one object must be ordered on the device,
+    whichever threads make them."""
 
     _destroy = "q8kv_attend_destroy"
     _name = "q8kv_attend"
@@ -350,7 +351,8 @@ class TreeAttention(_Plan):
         q [rows, heads, head_dim] f32, f16 or bf16: all requests' nodes one after another, ``starts`` [requests + 1]
         int32 their first rows (None: as many for each request).  lengths [requests] int32: cached tokens before the
         nodes; node j's own key and value are at position lengths + j.  table [requests, columns] int32: the
-        requests' pages.  mask [rows, words] int32: bit j % 32 of word j // 32 lets a node see node j of its request
+        requests' pages (the kernel is chosen by how far the table reaches, as the lengths are not known to the host:
+        columns far past the longest request cost time, and may change last bits).  mask [rows, words] int32: bit j % 32 of word j // 32 lets a node see node j of its request
         (None: nodes up to itself).  ``scale`` defaults to 1 / sqrt(head_dim).
         """
         device = self.device
@@ -414,7 +416,7 @@ class TreeAttention(_Plan):
 
 class TreeVerify(_Plan):
     """Verification of drafted tokens for up to ``max_requests`` requests and ``max_rows`` nodes; use one per
-    concurrent stream."""
+    concurrent stream (calls of one object must be ordered on the device, whichever threads make them)."""
 
     _destroy = "q8kv_verify_destroy"
 

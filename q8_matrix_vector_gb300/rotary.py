@@ -107,7 +107,8 @@ def frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict | None = N
 class Rotary(_Plan):
     """Rotary positions of the first ``rotary_dim`` (None: all) elements of heads of ``head_dim``: pairs (2 i, 2 i + 1)
     if ``interleaved``, else (i, i + rotary_dim / 2).  ``scaling`` as ``frequencies``, or give ``turning`` (radians a
-    position of each pair) and ``factor`` (of cos and sin) yourself.  Angles are exact at any position."""
+    position of each pair) and ``factor`` (of cos and sin) yourself.  Frequencies are rounded to 2^-64 of a turn; their
+    multiples are exact at any position.  One object may be called by several threads and on several streams at once."""
 
     _destroy = "kvrope_destroy"
 
@@ -145,8 +146,8 @@ class Rotary(_Plan):
         return out, stride
 
     def __call__(self, x, positions, *, out=None, inverse: bool = False):
-        """x [n, heads, head_dim] (f32, f16 or bf16) turned by positions [n] (int64), or back with ``inverse`` (the
-        gradient of the forward turn).  ``out`` may be x itself; memory that overlaps otherwise is refused."""
+        """x [n, heads, head_dim] (f32, f16 or bf16) turned by positions [n] (int64), or with ``inverse`` by the transpose,
+        which is the gradient of the forward turn (and its way back, times the square of ``factor`` where that is not 1).  ``out`` may be x itself; memory that overlaps otherwise is refused."""
         device = self.device
         if x.dim() != 3:
             raise ValueError(f"x must be [n, heads, {self.head_dim}], got {tuple(x.shape)}")
