@@ -55,7 +55,7 @@ def frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict | None = N
         fastest stays;
       * dict(kind="yarn", factor, original, fast=32, slow=1, attention=None): pairs that turn more than ``fast`` times in
         ``original`` positions stay, those that turn less than ``slow`` times are divided by factor, linear in the pair's
-        number between; cos and sin times ``attention``, 0.1 ln(factor) + 1 if not given;
+        number between; cos and sin times ``attention``, 0.1 ln(factor) + 1 if not given (1 for factors up to 1);
       * dict(kind="bands", factor, original, low=1, high=4): pairs that turn more than ``high`` times in ``original``
         positions stay, those below ``low`` are divided by factor, linear in the number of turns between.
     """
