@@ -171,7 +171,7 @@ q8mv_status_t q8kv_attend(q8kv_attend_plan_t plan, const q8kv_cache_t *cache, co
     // 128 bf16 rows at a time where there are more than 32 (36 rows of the 16 requests above: 79 us, by 16 rows 80; 52
     // rows: 80 and 102; 124 rows: 83 and 190; but 32 rows: 78 and 59), and enough to do: its tiles of 128 keys take longer
     // to fill and to join.  In tiles of 16 rows x 128 keys of the tables' reach, one request of 124 rows: 2048 tiles 39 us,
-    // by 16 rows 31, 4032 43 and 45; four of 64 rows: 3072 tiles 40 and 40, 4096 46 and 46, 8064 63 and 75; four of 124
+    // by 16 rows 31, 4032 43 and 45; four of 64 rows: 4096 tiles 46 and 46, 8064 63 and 75; four of 124
     // rows: 2304 tiles 34 and 34, 8192 47 and 79.  (Under columns for 131072 tokens one request of 124 rows over 1000
     // tokens takes 36 us and not 19.2.)
     const double tiles = static_cast<double>(kv::ceil_div(mean, 16) * kv::ceil_div(reach, 128)) * a->requests * p.c.heads;
